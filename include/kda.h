@@ -256,10 +256,145 @@ int kda_prefill_noalloc(const void* q, const void* k, const void* v, const float
                         const kda_options* opt, kda_stream_t stream);
 
 /*
+ * The gated delta rule in the form of the layers named after it ("Kimi K3",
+ * section "Forgetting different features at different rates": Gated DeltaNet
+ * shrinks the whole state by one factor per head).  It differs from kda_prefill
+ * with KDA_DECAY_HEAD in what it takes: fewer query / key heads than value
+ * heads, values wider or narrower than keys, decays without a floor or from a
+ * softplus of their logit, rows inside a wider projection, states in a pool.
+ * Its states are exact to fp32 whatever the data type.  Per sequence, per value
+ * head h (query / key head h / (H_v / H_k)), per token t:
+ *
+ *     q, k <- q / sqrt(|q|^2 + eps_l2), k / sqrt(|k|^2 + eps_l2)   (optional)
+ *     beta <- sigmoid(beta)                                         (optional)
+ *     g    =  min(log_alpha, 0)  or  -A_h softplus(z + b_h)
+ *     S_t  =  (I - beta k k^T) e^g S_{t-1} + beta k v^T        [d_k x d_v]
+ *     o_t  =  q_scale * S_t^T q
+ *
+ * Head sizes: d_k in {32, 64, 128}, d_v in {32, 64, 128, 256}; H_v a multiple
+ * of H_k.  Log decays below -200 (minus infinity among them) act as -200: their
+ * factor is 0 in fp32.
+ */
+typedef struct kda_gdr_options {
+  int l2norm_qk;         /* 1 (default): L2-normalise q and k per head per token */
+  int beta_is_logit;     /* 0 (default): beta is already in (0,1); 1: sigmoid    */
+  int decay_from_logit;  /* 0 (default): log_alpha holds log decays.  1: it holds
+                            logits z, and the log decay is -A_h softplus(z + b_h) */
+  const float* decay_scale; /* with decay_from_logit: A [H_v] fp32, NULL = ones  */
+  const float* decay_bias;  /* with decay_from_logit: b [H_v] fp32, NULL = zeros */
+  float q_scale;         /* read-out multiplier, default 1                       */
+  float eps_l2;          /* L2-norm epsilon, default 1e-6                        */
+  long long ldq, ldk, ldv; /* elements between the rows of successive tokens in
+                            q, k, v; 0 = dense (H_k d_k, H_k d_k, H_v d_v).  A
+                            multiple of 16 bytes                               */
+  const int32_t* slots;  /* NULL: the state of sequence n is matrix n.  Else int32
+                            [N] on the device: it is matrix slots[n] of a pool of
+                            n_slots.  A negative slot leaves its sequence out:
+                            neither its o rows nor any state is touched.  A slot
+                            of n_slots or more, or one that an earlier sequence
+                            has, leaves it out too and sets the status word to
+                            KDA_ERR_SHAPE                                      */
+  int n_slots;           /* matrices in the pool, with slots                     */
+  float* snapshots;      /* kda_gdr_decode_step only: NULL, or fp32
+                            [N][L][H_v][d_k][d_v] that receives the state after
+                            each token (of proposed tokens, some of which are
+                            taken), rows of sequences left out untouched       */
+  int max_seqlen;        /* host-side bound on the longest sequence, 0 = T_total */
+  int impl;              /* kda_gdr_prefill: KDA_IMPL_AUTO, KDA_IMPL_SIMT (token
+                            by token on the CUDA cores) or KDA_IMPL_TC (chunks
+                            of 64 on the tensor cores, bf16 data only)         */
+  void* workspace;       /* device scratch, >= kda_gdr_prefill_workspace_size()  */
+  size_t workspace_bytes;
+} kda_gdr_options;
+
+/* Fill *opt with the defaults listed above. */
+void kda_gdr_options_init(kda_gdr_options* opt);
+
+/*
+ * kda_gdr_prefill -- the gated delta rule over packed sequences.
+ *
+ *   q, k        [T_total][H_k][d_k] dtype (token strides in opt)
+ *   v           [T_total][H_v][d_v] dtype
+ *   log_alpha   [T_total][H_v] fp32, 4-byte aligned
+ *   beta        [T_total][H_v] dtype
+ *   S0          [N or n_slots][H_v][d_k][d_v] fp32 initial states, NULL = zeros
+ *   cu_seqlens  as in kda_prefill
+ *   o           [T_total][H_v][d_v] dtype out
+ *   S_T         as S0, final states out (may be S0)
+ *
+ * opt NULL: the defaults.  q, k, v, S0, S_T, o 16-byte aligned.  o must not
+ * overlap an input.  KDA_ERR_WORKSPACE where the workspace is too small; the
+ * workspace holds nothing between calls, but calls that can overlap on the GPU
+ * need one each.
+ */
+int kda_gdr_prefill(const void* q, const void* k, const void* v, const float* log_alpha,
+                    const void* beta, const float* S0, const int32_t* cu_seqlens, int N, void* o,
+                    float* S_T, int T_total, int H_k, int H_v, int d_k, int d_v, int dtype,
+                    const kda_gdr_options* opt, kda_stream_t stream);
+
+/* Bytes of device workspace kda_gdr_prefill needs (0: none). */
+size_t kda_gdr_prefill_workspace_size(int T_total, int N, int H_k, int H_v, int d_k, int d_v,
+                                      int dtype, const kda_gdr_options* opt);
+
+/* The implementation kda_gdr_prefill runs for these sizes and options:
+ * KDA_IMPL_SIMT or KDA_IMPL_TC, or a negative status if it would reject them. */
+int kda_gdr_prefill_path(int T_total, int N, int H_k, int H_v, int d_k, int d_v, int dtype,
+                         const kda_gdr_options* opt);
+
+/*
+ * kda_gdr_decode_step -- L recurrent tokens for each of N sequences, states
+ * updated in place: each is read once and written once.
+ *
+ *   q, k        [N][L][H_k][d_k] dtype (token strides in opt)
+ *   v           [N][L][H_v][d_v] dtype
+ *   log_alpha   [N][L][H_v] fp32
+ *   beta        [N][L][H_v] dtype
+ *   S           [N or n_slots][H_v][d_k][d_v] fp32, read and overwritten
+ *   o           [N][L][H_v][d_v] dtype out
+ */
+int kda_gdr_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                        const void* beta, float* S, void* o, int N, int L, int H_k, int H_v,
+                        int d_k, int d_v, int dtype, const kda_gdr_options* opt,
+                        kda_stream_t stream);
+
+/* Activations of kda_linear. */
+enum {
+  KDA_ACT_NONE = 0,
+  KDA_ACT_RELU = 1,      /* max(x, 0)                                        */
+  KDA_ACT_SILU = 2,      /* x sigmoid(x)                                     */
+  KDA_ACT_GELU = 3,      /* x Phi(x), Phi the normal distribution            */
+  KDA_ACT_GELU_TANH = 4, /* x (1 + tanh(sqrt(2/pi)(x + 0.044715 x^3))) / 2   */
+  KDA_ACT_SIGMOID = 5
+};
+
+/*
+ * kda_linear -- a projection: y = act(x w^T + bias) + residual, the products
+ * that make q, k, v, beta, the decay logits and the gate, and the one that
+ * takes a layer's output back to the residual stream.
+ *
+ *   x         [M][K] dtype, rows ldx elements apart (0 = K)
+ *   w         [N][K] dtype, rows ldw elements apart (0 = K)
+ *   bias      [N] dtype or NULL
+ *   residual  [M][N] dtype, rows ldr elements apart (0 = N), or NULL
+ *   y         [M][N] dtype out, rows ldy elements apart (0 = N); may be the
+ *             residual itself (same address and stride), else overlaps no input
+ *
+ * Sums, bias, activation and residual are in fp32, rounded once to dtype.
+ * Pointers need the alignment of their elements; bf16 products run on the
+ * tensor cores where x and w are 16-byte aligned with rows a multiple of 16
+ * bytes apart, on the CUDA cores otherwise, and so do fp32 products.  M, N or
+ * K may be 0 (K = 0: y = act(bias) + residual).
+ */
+int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
+               const void* residual, long long ldr, void* y, long long ldy, int M, int N, int K,
+               int act, int dtype, kda_stream_t stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: KDA_OK, KDA_ERR_TIMEOUT (a bounded device wait gave up),
- * KDA_ERR_SHAPE (a kernel found cu_seqlens out of range and skipped that
- * sequence), or KDA_ERR_CUDA if the stream itself reports an error.
+ * KDA_ERR_SHAPE (a kernel found cu_seqlens or a state slot out of range, or a
+ * slot taken twice, and skipped that sequence), or KDA_ERR_CUDA if the stream
+ * itself reports an error.
  */
 int kda_get_last_error(kda_stream_t stream);
 

@@ -63,6 +63,29 @@ class kda_options(ctypes.Structure):
     ]
 
 
+class kda_gdr_options(ctypes.Structure):
+    """Mirror of ``struct kda_gdr_options`` (field order and types as in kda.h)."""
+    _fields_ = [
+        ("l2norm_qk", ctypes.c_int),
+        ("beta_is_logit", ctypes.c_int),
+        ("decay_from_logit", ctypes.c_int),
+        ("decay_scale", ctypes.c_void_p),
+        ("decay_bias", ctypes.c_void_p),
+        ("q_scale", ctypes.c_float),
+        ("eps_l2", ctypes.c_float),
+        ("ldq", ctypes.c_longlong),
+        ("ldk", ctypes.c_longlong),
+        ("ldv", ctypes.c_longlong),
+        ("slots", ctypes.c_void_p),
+        ("n_slots", ctypes.c_int),
+        ("snapshots", ctypes.c_void_p),
+        ("max_seqlen", ctypes.c_int),
+        ("impl", ctypes.c_int),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -73,7 +96,9 @@ _LIB = None
 EXPORTS = ("kda_options_init", "kda_prefill", "kda_prefill_noalloc",
            "kda_prefill_workspace_size", "kda_prefill_path",
            "kda_decode_step", "kda_gated_rmsnorm", "kda_get_last_error", "kda_status_string",
-           "kda_abi_version")
+           "kda_abi_version", "kda_gdr_options_init", "kda_gdr_prefill",
+           "kda_gdr_prefill_workspace_size", "kda_gdr_prefill_path", "kda_gdr_decode_step",
+           "kda_linear")
 PATH_NAMES = {1: "simt", 2: "tc"}
 
 
@@ -111,6 +136,21 @@ def load(path: str | None = None):
     lib.kda_abi_version.restype = ci
     lib.kda_prefill_noalloc.argtypes = lib.kda_prefill.argtypes
     lib.kda_prefill_noalloc.restype = ci
+    pg, cl = ctypes.POINTER(kda_gdr_options), ctypes.c_longlong
+    lib.kda_gdr_options_init.argtypes = [pg]
+    lib.kda_gdr_options_init.restype = None
+    lib.kda_gdr_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, vp, vp, ci, ci, ci, ci, ci,
+                                    ci, pg, vp]
+    lib.kda_gdr_prefill.restype = ci
+    lib.kda_gdr_prefill_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci, ci, pg]
+    lib.kda_gdr_prefill_workspace_size.restype = ctypes.c_size_t
+    lib.kda_gdr_prefill_path.argtypes = [ci, ci, ci, ci, ci, ci, ci, pg]
+    lib.kda_gdr_prefill_path.restype = ci
+    lib.kda_gdr_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci,
+                                        pg, vp]
+    lib.kda_gdr_decode_step.restype = ci
+    lib.kda_linear.argtypes = [vp, cl, vp, cl, vp, vp, cl, vp, cl, ci, ci, ci, ci, ci, vp]
+    lib.kda_linear.restype = ci
     if path == _build.LIB or _LIB is None:
         _LIB = lib
     return lib
@@ -374,3 +414,237 @@ def kda_prefill_noalloc(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: i
     if rc != KDA_OK:
         raise KdaError(rc, "kda_prefill_noalloc")
     return o, S_T
+
+
+# ------------------------------------------------- the gated delta rule
+def kda_gdr_options_init(**overrides) -> kda_gdr_options:
+    """Default options (C kda_gdr_options_init), then keyword overrides."""
+    opt = kda_gdr_options()
+    load().kda_gdr_options_init(ctypes.byref(opt))
+    for key, val in overrides.items():
+        if key == "impl" and isinstance(val, str):
+            val = IMPLS[val]
+        setattr(opt, key, val)
+    return opt
+
+
+def _on_device(first, *ts):
+    """Every tensor on the device of `first`, and that the current device: the
+    launch goes to a stream of the current one."""
+    import torch
+    if not first.is_cuda:
+        raise ValueError("libkda takes CUDA tensors (device memory)")
+    dev = first.get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("libkda takes tensors on one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current CUDA device: wrap the call in "
+                         "torch.cuda.device(tensor.device)")
+
+
+def _token_stride(x, name: str) -> int:
+    """Elements between the rows of successive tokens of x [..., H, d]: heads and
+    channels are dense, tokens evenly spaced (so that x may be a slice of a wider
+    projection)."""
+    *rows, H, d = x.shape
+    st = x.stride()
+    if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
+        raise ValueError(f"{name}: each token's heads and channels have to be contiguous")
+    if len(rows) == 2 and rows[0] > 1 and rows[1] > 1 and st[0] != rows[1] * st[1]:
+        raise ValueError(f"{name}: tokens have to be evenly spaced")
+    if len(rows) == 2:
+        return st[1] if rows[1] > 1 else st[0] if rows[0] > 1 else H * d
+    return st[0] if rows[0] > 1 else H * d
+
+
+def _expect(x, name, shape, dtype):
+    """x as the library reads it: this shape and type, contiguous."""
+    if tuple(x.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name}: {x.dtype}, expected {dtype}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: libkda takes contiguous tensors")
+
+
+def _gdr_call(q, k, v, log_alpha, beta, states, slots, o, decay_scale, decay_bias, N, l2norm_qk,
+              beta_is_logit, decay_from_logit, q_scale, eps_l2):
+    """Checks what the two entry points share; returns (o, options, sizes)."""
+    import torch
+    f32 = torch.float32
+    _on_device(q, k, v, log_alpha, beta, slots, o, decay_scale, decay_bias, *states)
+    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("q and k [..., H_k, d_k] and v [..., H_v, d_v] of the same tokens")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v of one dtype")
+    Hk, dk = q.shape[-2:]
+    Hv, dv = v.shape[-2:]
+    rows = tuple(q.shape[:-2])
+    _expect(log_alpha, "log_alpha", (*rows, Hv), f32)
+    _expect(beta, "beta", (*rows, Hv), q.dtype)
+    if o is None:
+        o = torch.empty((*rows, Hv, dv), dtype=q.dtype, device=q.device)
+    else:
+        _expect(o, "o", (*rows, Hv, dv), q.dtype)
+    n_slots = N
+    if slots is not None:
+        _expect(slots, "slots", (N,), torch.int32)
+        n_slots = states[0].shape[0] if states[0] is not None else states[-1].shape[0]
+    for S in states:
+        if S is not None:
+            _expect(S, "state", (n_slots, Hv, dk, dv), f32)
+    for x, name in ((decay_scale, "decay_scale"), (decay_bias, "decay_bias")):
+        if x is not None:
+            _expect(x, name, (Hv,), f32)
+    opt = kda_gdr_options(
+        int(bool(l2norm_qk)), int(bool(beta_is_logit)), int(bool(decay_from_logit)),
+        _ptr(decay_scale), _ptr(decay_bias), q_scale, eps_l2, _token_stride(q, "q"),
+        _token_stride(k, "k"), _token_stride(v, "v"), _ptr(slots), n_slots)
+    return o, opt, (Hk, Hv, dk, dv)
+
+
+def kda_gdr_prefill_workspace_size(T_total: int, N: int, H_k: int, H_v: int, d_k: int, d_v: int,
+                                   dtype: int = KDA_BF16,
+                                   opt: kda_gdr_options | None = None) -> int:
+    o = opt if opt is not None else kda_gdr_options_init()
+    return int(load().kda_gdr_prefill_workspace_size(T_total, N, H_k, H_v, d_k, d_v, dtype,
+                                                     ctypes.byref(o)))
+
+
+def kda_gdr_prefill_path(T_total: int, N: int, H_k: int, H_v: int, d_k: int, d_v: int,
+                         dtype: int = KDA_BF16, opt: kda_gdr_options | None = None) -> str:
+    """The implementation kda_gdr_prefill uses for these sizes: "simt" or "tc"."""
+    o = opt if opt is not None else kda_gdr_options_init()
+    rc = load().kda_gdr_prefill_path(T_total, N, H_k, H_v, d_k, d_v, dtype, ctypes.byref(o))
+    if rc < 0:
+        raise KdaError(rc, "kda_gdr_prefill_path")
+    return PATH_NAMES[rc]
+
+
+def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int | None = None,
+                    o=None, S_T=None, *, slots=None, l2norm_qk: bool = True,
+                    beta_is_logit: bool = False, decay_from_logit: bool = False, decay_scale=None,
+                    decay_bias=None, q_scale: float = 1.0, eps_l2: float = 1e-6,
+                    max_seqlen: int = 0, impl="auto", workspace=None, stream=None):
+    """The gated delta rule over packed sequences (C ``kda_gdr_prefill``).
+
+    q, k [T, H_k, d_k]; v [T, H_v, d_v]; each token's heads contiguous, tokens any
+    even distance apart (slices of one projection).  log_alpha [T, H_v] fp32;
+    beta [T, H_v]; S0 [N, H_v, d_k, d_v] fp32 or None (zeros); cu_seqlens [N+1]
+    int32 on the device, or None for N sequences of T / N tokens.  Returns
+    (o, S_T).  With ``slots`` [N] int32, S0 and S_T are pools
+    [n_slots, H_v, d_k, d_v] and sequence n's state is matrix slots[n]; S_T has
+    to be given (it may be S0).  ``decay_from_logit``: log_alpha holds logits z,
+    the log decay is -A softplus(z + b) with decay_scale A [H_v] and decay_bias
+    b [H_v] (fp32, None = ones / zeros)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q [T, H_k, d_k]")
+    T = q.shape[0]
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        _on_device(q, cu_seqlens)
+        _expect(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
+    N = N or 1
+    if S_T is None:
+        if slots is not None:
+            raise ValueError("with slots, S_T is the pool that the states are written to")
+        S_T = torch.empty((N, v.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32,
+                          device=q.device)
+    o, opt, sizes = _gdr_call(q, k, v, log_alpha, beta, (S0, S_T), slots, o, decay_scale,
+                              decay_bias, N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale,
+                              eps_l2)
+    dt = _dtype_code(q)
+    opt.max_seqlen = int(max_seqlen)
+    opt.impl = IMPLS[impl] if isinstance(impl, str) else int(impl)
+    need = load().kda_gdr_prefill_workspace_size(T, N, *sizes, dt, ctypes.byref(opt))
+    if need > 0:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _on_device(q, workspace)
+        opt.workspace = _ptr(workspace)
+        opt.workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = load().kda_gdr_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S0),
+                                _ptr(cu_seqlens), N, _ptr(o), _ptr(S_T), T, *sizes, dt,
+                                ctypes.byref(opt), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_gdr_prefill")
+    return o, S_T
+
+
+def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snapshots=None,
+                        l2norm_qk: bool = True, beta_is_logit: bool = False,
+                        decay_from_logit: bool = False, decay_scale=None, decay_bias=None,
+                        q_scale: float = 1.0, eps_l2: float = 1e-6, stream=None):
+    """L recurrent tokens for each of N sequences (C ``kda_gdr_decode_step``).
+
+    q, k [N, L, H_k, d_k]; v [N, L, H_v, d_v]; log_alpha, beta [N, L, H_v]; or all
+    without L for one token.  S [N, H_v, d_k, d_v] fp32 (a pool
+    [n_slots, H_v, d_k, d_v] with ``slots`` [N] int32) is updated in place.
+    Returns o [N, (L,) H_v, d_v].  ``snapshots``: True or a tensor
+    [N, L, H_v, d_k, d_v] fp32 for the state after each token; then returns
+    (o, snapshots)."""
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError("q [N, H_k, d_k] or [N, L, H_k, d_k]")
+    N, L = q.shape[0], q.shape[1] if q.dim() == 4 else 1
+    o, opt, sizes = _gdr_call(q, k, v, log_alpha, beta, (S,), slots, o, decay_scale, decay_bias,
+                              N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale, eps_l2)
+    if snapshots is False:
+        snapshots = None
+    if snapshots is not None:
+        shape = (N, L, sizes[1], sizes[2], sizes[3])
+        if snapshots is True:
+            snapshots = torch.empty(shape, dtype=torch.float32, device=q.device)
+        _on_device(q, snapshots)
+        _expect(snapshots, "snapshots", shape, torch.float32)
+        opt.snapshots = _ptr(snapshots)
+    rc = load().kda_gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
+                                    _ptr(S), _ptr(o), N, L, *sizes, _dtype_code(q),
+                                    ctypes.byref(opt), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_gdr_decode_step")
+    return o if snapshots is None else (o, snapshots)
+
+
+# ------------------------------------------------- projections
+# KDA_ACT_*
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
+
+
+def _rows(x, name: str, width: int) -> int:
+    """Elements between the rows of x [M, width], columns dense."""
+    if x.dim() != 2 or x.shape[1] != width:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [.., {width}]")
+    if width > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: each row has to be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else 0
+
+
+def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none", stream=None):
+    """y = act(x w^T + bias) + residual (C ``kda_linear``).
+
+    x [M, K], w [N, K], bias [N] or None, residual [M, N] or None, all of one
+    dtype; rows contiguous, any distance apart.  ``act``: a key of ``ACTS``.
+    y [M, N] may be the residual itself."""
+    import torch
+    _on_device(x, w, bias, residual, y)
+    N, K = w.shape
+    M = x.shape[0]
+    ldx, ldw = _rows(x, "x", K), _rows(w, "w", K)
+    if y is None:
+        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    for t in (w, bias, residual, y):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError("x, w, bias, residual and y of one dtype")
+    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
+        raise ValueError(f"y and residual [{M}, {N}]")
+    if bias is not None:
+        _expect(bias, "bias", (N,), x.dtype)
+    rc = load().kda_linear(_ptr(x), ldx, _ptr(w), ldw, _ptr(bias), _ptr(residual),
+                           0 if residual is None else _rows(residual, "residual", N), _ptr(y),
+                           _rows(y, "y", N), M, N, K, ACTS[act], _dtype_code(x), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_linear")
+    return y
