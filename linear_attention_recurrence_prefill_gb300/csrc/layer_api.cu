@@ -170,7 +170,15 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
   a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
   a.ldx = ldx; a.ldw = ldw; a.ldr = ldr; a.ldy = ldy;
   a.M = M; a.N = N; a.K = K; a.act = act;
-  const cudaError_t e = launch_linear_simt(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (linear_tc_takes(a, dtype)) {
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    e = launch_linear_tc(a, status, s);
+  } else {
+    e = launch_linear_simt(a, dtype, s);
+  }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

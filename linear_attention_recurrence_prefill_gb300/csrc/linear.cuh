@@ -29,6 +29,18 @@ __device__ __forceinline__ float activate(float x, int act) {
   }
 }
 
+// What one thread of an epilogue does to the sum of element (m, n).
+template <typename T>
+__device__ __forceinline__ void finish(const LinearArgs& a, float z, float bias, long long m,
+                                       int n) {
+  z = activate(z + bias, a.act);
+  if (a.residual) z += to_f32(static_cast<const T*>(a.residual)[m * a.ldr + n]);
+  static_cast<T*>(a.y)[m * a.ldy + n] = from_f32<T>(z);
+}
+
 cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, cudaStream_t s);
+// bf16 with x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
+bool linear_tc_takes(const LinearArgs& a, int dtype);
+cudaError_t launch_linear_tc(const LinearArgs& a, int* status, cudaStream_t s);
 
 }  // namespace kda

@@ -43,8 +43,6 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a) {
     __syncthreads();
   }
   const T* bias = static_cast<const T*>(a.bias);
-  const T* res = static_cast<const T*>(a.residual);
-  T* y = static_cast<T*>(a.y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const long long m = m0 + ty * 4 + i;
@@ -53,11 +51,7 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a) {
     for (int j = 0; j < 4; ++j) {
       const int n = n0 + tx * 4 + j;
       if (n >= a.N) break;
-      float z = acc[i][j];
-      if (bias) z += to_f32(bias[n]);
-      z = activate(z, a.act);
-      if (res) z += to_f32(res[m * a.ldr + n]);
-      y[m * a.ldy + n] = from_f32<T>(z);
+      finish<T>(a, acc[i][j], bias ? to_f32(bias[n]) : 0.f, m, n);
     }
   }
 }
