@@ -45,23 +45,32 @@ __device__ __forceinline__ float gdr_inv_norm(float sum_sq, float eps) {
   return s > 0.f ? 1.0f / sqrtf(s) : 0.f;
 }
 
+// Offset i of the packed sequences (cu_seqlens, or equal lengths).
+__device__ __forceinline__ int gdr_offset(const GdrArgs& a, int i) {
+  return a.cu_seqlens ? a.cu_seqlens[i] : i * (a.T_total / a.N);
+}
+
 // The token range and the state matrix of sequence n, found by one whole warp
 // (every lane gets the answer).  False: the sequence is left out, because its
 // slot is negative, or (status word set) because its slot is out of range or
-// taken by an earlier sequence, or its tokens are out of range.
+// taken by an earlier sequence, its tokens are out of range, or the offsets
+// decrease at it or before it.
 __device__ __forceinline__ bool gdr_sequence(const GdrArgs& a, int n, int& t0, int& t1,
                                              int& slot) {
+  const int lane = threadIdx.x & 31;
   seq_range(a.cu_seqlens, a.N, a.T_total, n, t0, t1);
   slot = n;
-  bool bad = t0 < 0 || t1 < t0 || t1 > a.T_total;
+  bool bad = t0 < 0 || t1 < t0 || t1 > a.T_total, found = false;
+  if (a.cu_seqlens)
+    for (int i = lane; i < n; i += 32) found |= a.cu_seqlens[i] > a.cu_seqlens[i + 1];
   if (a.slots) {
     slot = a.slots[n];
     if (slot < 0) return false;
-    bool taken = false;
-    for (int i = threadIdx.x & 31; i < n; i += 32) taken |= a.slots[i] == slot;
-    bad |= slot >= a.n_slots || __any_sync(0xffffffffu, taken);
+    bad |= slot >= a.n_slots;
+    for (int i = lane; i < n; i += 32) found |= a.slots[i] == slot;
   }
-  if (bad && (threadIdx.x & 31) == 0) atomicExch(a.status, KDA_ERR_SHAPE);
+  bad |= __any_sync(0xffffffffu, found);
+  if (bad && lane == 0) atomicExch(a.status, KDA_ERR_SHAPE);
   return !bad;
 }
 

@@ -93,14 +93,19 @@ int kda_gdr_prefill_path(int T_total, int N, int H_k, int H_v, int d_k, int d_v,
   const int rc = check_gdr_sizes(N, T_total, H_k, H_v, d_k, d_v, dtype, op);
   if (rc != KDA_OK) return rc;
   if (op->max_seqlen < 0 || op->max_seqlen > T_total) return KDA_ERR_SHAPE;
-  if (op->impl < KDA_IMPL_AUTO || op->impl > KDA_IMPL_TC) return KDA_ERR_UNSUPPORTED;
-  if (op->impl == KDA_IMPL_TC) return KDA_ERR_UNSUPPORTED;
-  return KDA_IMPL_SIMT;
+  const bool tc = gdr_chunked_supported(d_k, d_v, dtype);
+  switch (op->impl) {
+    case KDA_IMPL_SIMT: return KDA_IMPL_SIMT;
+    case KDA_IMPL_TC: return tc ? KDA_IMPL_TC : KDA_ERR_UNSUPPORTED;
+    case KDA_IMPL_AUTO: return tc && T_total > 0 ? KDA_IMPL_TC : KDA_IMPL_SIMT;
+    default: return KDA_ERR_UNSUPPORTED;
+  }
 }
 
 size_t kda_gdr_prefill_workspace_size(int T_total, int N, int H_k, int H_v, int d_k, int d_v,
                                       int dtype, const kda_gdr_options* opt) {
-  return 0;
+  const int path = kda_gdr_prefill_path(T_total, N, H_k, H_v, d_k, d_v, dtype, opt);
+  return path == KDA_IMPL_TC ? gdr_chunked_workspace_bytes(T_total, N, H_v) : 0;
 }
 
 int kda_gdr_prefill(const void* q, const void* k, const void* v, const float* log_alpha,
@@ -117,12 +122,19 @@ int kda_gdr_prefill(const void* q, const void* k, const void* v, const float* lo
   if (!cu_seqlens && T_total % N != 0) return KDA_ERR_SHAPE;
   if (!aligned(cu_seqlens, 4)) return KDA_ERR_ALIGN;
   if (op->snapshots) return KDA_ERR_UNSUPPORTED;
+  if (path == KDA_IMPL_TC) {
+    if (!op->workspace || op->workspace_bytes < gdr_chunked_workspace_bytes(T_total, N, H_v))
+      return KDA_ERR_WORKSPACE;
+    if (!aligned(op->workspace, 16)) return KDA_ERR_ALIGN;
+  }
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GdrArgs a = gdr_args(q, k, v, log_alpha, beta, S0, S_T, o, N, T_total, H_k, H_v, d_k, d_v, op,
                        status);
   a.cu_seqlens = cu_seqlens;
-  const cudaError_t e = launch_gdr_recurrent(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = path == KDA_IMPL_TC ? launch_gdr_chunked(a, op->workspace, s)
+                                            : launch_gdr_recurrent(a, dtype, s);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -15,16 +15,31 @@ struct LinearArgs {
   int M, N, K, act;
 };
 
+// kFast, for results that are rounded to bf16: the exponential and the division
+// by their approximate instructions, off by a few 2^-23, not by half a step of bf16
+// (2^-9 and more).
+template <bool kFast>
+__device__ __forceinline__ float over_1_plus_exp(float x, float y) {  // x / (1 + e^y)
+  if constexpr (kFast) {
+    const float d = 1.f + __expf(y);
+    // __fdividef is 0 for divisors beyond 2^126, where x / d is below 2^-126 x anyway; x
+    // infinite there is the quotient's NaN
+    return __fdividef(x, d);
+  }
+  return x / (1.f + expf(y));
+}
+
+template <bool kFast>
 __device__ __forceinline__ float activate(float x, int act) {
   switch (act) {
     case KDA_ACT_RELU: return x < 0.f ? 0.f : x;
-    case KDA_ACT_SILU: return x / (1.f + expf(-x));
+    case KDA_ACT_SILU: return over_1_plus_exp<kFast>(x, -x);
     // x Phi(x) = x erfc(-x / sqrt 2) / 2: no cancellation in the left tail
     case KDA_ACT_GELU: return 0.5f * x * erfcf(-0.70710678118654752f * x);
     // (1 + tanh y) / 2 = 1 / (1 + e^-2y), sqrt(2 / pi) = 0.79788456
     case KDA_ACT_GELU_TANH:
-      return x / (1.f + expf(-1.5957691216057308f * (x + 0.044715f * x * x * x)));
-    case KDA_ACT_SIGMOID: return sigmoidf_(x);
+      return over_1_plus_exp<kFast>(x, -1.5957691216057308f * (x + 0.044715f * x * x * x));
+    case KDA_ACT_SIGMOID: return over_1_plus_exp<kFast>(1.f, -x);
     default: return x;
   }
 }
@@ -33,7 +48,7 @@ __device__ __forceinline__ float activate(float x, int act) {
 template <typename T>
 __device__ __forceinline__ void finish(const LinearArgs& a, float z, float bias, long long m,
                                        int n) {
-  z = activate(z + bias, a.act);
+  z = activate<sizeof(T) == 2>(z + bias, a.act);
   if (a.residual) z += to_f32(static_cast<const T*>(a.residual)[m * a.ldr + n]);
   static_cast<T*>(a.y)[m * a.ldy + n] = from_f32<T>(z);
 }

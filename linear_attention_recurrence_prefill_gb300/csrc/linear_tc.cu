@@ -43,6 +43,45 @@ struct Tc {
   int n_tiles, m_tiles, k_blocks;
 };
 
+// The epilogue of output channel n for the 32 tokens from m on, of which `cols` exist.
+// All of the residual is fetched before the first store: y may be the residual, so the
+// compiler would not move a load over a store by itself.
+__device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r)[32], float bias,
+                                         long long m, int n, int cols) {
+  const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.residual) + m * a.ldr + n;
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + m * a.ldy + n;
+  __nv_bfloat16 add[32];
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < cols) add[j] = res[j * a.ldr];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) add[j] = __ushort_as_bfloat16(0);
+  }
+  float z[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]) + bias;
+  // the activation chosen once for all
+  auto all = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) z[j] = f(z[j]);
+  };
+  switch (a.act) {
+    case KDA_ACT_RELU: all([](float x) { return activate<true>(x, KDA_ACT_RELU); }); break;
+    case KDA_ACT_SILU: all([](float x) { return activate<true>(x, KDA_ACT_SILU); }); break;
+    case KDA_ACT_GELU: all([](float x) { return activate<true>(x, KDA_ACT_GELU); }); break;
+    case KDA_ACT_GELU_TANH:
+      all([](float x) { return activate<true>(x, KDA_ACT_GELU_TANH); });
+      break;
+    case KDA_ACT_SIGMOID: all([](float x) { return activate<true>(x, KDA_ACT_SIGMOID); }); break;
+    default: break;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < cols) y[j * a.ldy] = __float2bfloat16_rn(z[j] + __bfloat162float(add[j]));
+}
+
 template <int BN, int kStages>
 constexpr uint32_t smem_bytes() {
   return 1024 + kStages * (kRowsA + BN) * kBlockK * 2;
@@ -177,12 +216,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[acc]);
           }
-          if (n < t.a.N) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < cols)
-                finish<__nv_bfloat16>(t.a, __uint_as_float(r[j]), b, m0 + c + j, n);
-          }
+          if (n < t.a.N) finish32(t.a, r, b, m0 + c, n, cols - c);
         }
       }
     }

@@ -428,39 +428,84 @@ def kda_gdr_options_init(**overrides) -> kda_gdr_options:
     return opt
 
 
-def _on_device(first, *ts):
-    """Every tensor on the device of `first`, and that the current device: the
-    launch goes to a stream of the current one."""
-    import torch
-    if not first.is_cuda:
-        raise ValueError("libkda takes CUDA tensors (device memory)")
+class _Host:
+    """What every call needs, looked up once: a call's own work on the host is a few
+    microseconds, as long as the smallest kernels run."""
+
+    def __init__(self):
+        import torch
+        lib = load()
+        self.linear, self.step, self.prefill = (lib.kda_linear, lib.kda_gdr_decode_step,
+                                                lib.kda_gdr_prefill)
+        self.codes = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+        self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
+        self.empty = torch.empty
+        self.current_device = torch._C._cuda_getDevice
+        # (device) -> address of the current stream
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+
+
+_HOST = None
+
+
+def _host() -> _Host:
+    global _HOST
+    if _HOST is None:
+        _HOST = _Host()
+    return _HOST
+
+
+def _code(host, dtype) -> int:
+    code = host.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: use bfloat16 or float32")
+    return code
+
+
+def _one_device(host, first, *ts) -> int:
+    """The device of `first`, which has to be everyone's and the current one: the
+    launch goes to a stream of the current device."""
     dev = first.get_device()
+    if dev < 0:
+        raise ValueError("libkda takes CUDA tensors (device memory)")
     for t in ts:
         if t is not None and t.get_device() != dev:
             raise ValueError("libkda takes tensors on one device")
-    if dev != torch.cuda.current_device():
+    if dev != host.current_device():
         raise ValueError("the tensors are not on the current CUDA device: wrap the call in "
                          "torch.cuda.device(tensor.device)")
+    return dev
+
+
+def _stream_of(host, stream, dev: int) -> int:
+    if stream is None:
+        return host.current_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _token_stride(x, name: str) -> int:
     """Elements between the rows of successive tokens of x [..., H, d]: heads and
     channels are dense, tokens evenly spaced (so that x may be a slice of a wider
-    projection)."""
+    projection); 0 for dense rows."""
+    if x.is_contiguous():
+        return 0
     *rows, H, d = x.shape
     st = x.stride()
     if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
         raise ValueError(f"{name}: each token's heads and channels have to be contiguous")
     if len(rows) == 2 and rows[0] > 1 and rows[1] > 1 and st[0] != rows[1] * st[1]:
         raise ValueError(f"{name}: tokens have to be evenly spaced")
-    if len(rows) == 2:
-        return st[1] if rows[1] > 1 else st[0] if rows[0] > 1 else H * d
-    return st[0] if rows[0] > 1 else H * d
+    if max(rows, default=1) < 2:
+        return 0
+    ld = st[0] if len(rows) == 1 or rows[1] < 2 else st[1]
+    if ld < H * d:  # a broadcast token, or tokens that overlap
+        raise ValueError(f"{name}: tokens have to lie apart")
+    return ld
 
 
 def _expect(x, name, shape, dtype):
     """x as the library reads it: this shape and type, contiguous."""
-    if tuple(x.shape) != shape:
+    if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
     if x.dtype != dtype:
         raise TypeError(f"{name}: {x.dtype}, expected {dtype}")
@@ -468,37 +513,37 @@ def _expect(x, name, shape, dtype):
         raise ValueError(f"{name}: libkda takes contiguous tensors")
 
 
-def _gdr_call(q, k, v, log_alpha, beta, states, slots, o, decay_scale, decay_bias, N, l2norm_qk,
-              beta_is_logit, decay_from_logit, q_scale, eps_l2):
+def _gdr_call(host, q, k, v, log_alpha, beta, S0, S_T, slots, o, decay_scale, decay_bias, N,
+              l2norm_qk, beta_is_logit, decay_from_logit, q_scale, eps_l2):
     """Checks what the two entry points share; returns (o, options, sizes)."""
-    import torch
-    f32 = torch.float32
-    _on_device(q, k, v, log_alpha, beta, slots, o, decay_scale, decay_bias, *states)
-    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
+    shape, dtype = q.shape, q.dtype
+    if k.shape != shape or v.shape[:-2] != shape[:-2]:
         raise ValueError("q and k [..., H_k, d_k] and v [..., H_v, d_v] of the same tokens")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v of one dtype")
-    Hk, dk = q.shape[-2:]
+    Hk, dk = shape[-2:]
     Hv, dv = v.shape[-2:]
-    rows = tuple(q.shape[:-2])
-    _expect(log_alpha, "log_alpha", (*rows, Hv), f32)
-    _expect(beta, "beta", (*rows, Hv), q.dtype)
+    rows = tuple(shape[:-2])
+    _expect(log_alpha, "log_alpha", (*rows, Hv), host.f32)
+    _expect(beta, "beta", (*rows, Hv), dtype)
     if o is None:
-        o = torch.empty((*rows, Hv, dv), dtype=q.dtype, device=q.device)
+        o = host.empty((*rows, Hv, dv), dtype=dtype, device=q.device)
     else:
-        _expect(o, "o", (*rows, Hv, dv), q.dtype)
+        _expect(o, "o", (*rows, Hv, dv), dtype)
     n_slots = N
     if slots is not None:
-        _expect(slots, "slots", (N,), torch.int32)
-        n_slots = states[0].shape[0] if states[0] is not None else states[-1].shape[0]
-    for S in states:
-        if S is not None:
-            _expect(S, "state", (n_slots, Hv, dk, dv), f32)
-    for x, name in ((decay_scale, "decay_scale"), (decay_bias, "decay_bias")):
-        if x is not None:
-            _expect(x, name, (Hv,), f32)
+        _expect(slots, "slots", (N,), host.i32)
+        n_slots = S_T.shape[0]
+    states = (n_slots, Hv, dk, dv)
+    _expect(S_T, "state", states, host.f32)
+    if S0 is not None and S0 is not S_T:
+        _expect(S0, "S0", states, host.f32)
+    if decay_scale is not None:
+        _expect(decay_scale, "decay_scale", (Hv,), host.f32)
+    if decay_bias is not None:
+        _expect(decay_bias, "decay_bias", (Hv,), host.f32)
     opt = kda_gdr_options(
-        int(bool(l2norm_qk)), int(bool(beta_is_logit)), int(bool(decay_from_logit)),
+        1 if l2norm_qk else 0, 1 if beta_is_logit else 0, 1 if decay_from_logit else 0,
         _ptr(decay_scale), _ptr(decay_bias), q_scale, eps_l2, _token_stride(q, "q"),
         _token_stride(k, "k"), _token_stride(v, "v"), _ptr(slots), n_slots)
     return o, opt, (Hk, Hv, dk, dv)
@@ -538,36 +583,37 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
     to be given (it may be S0).  ``decay_from_logit``: log_alpha holds logits z,
     the log decay is -A softplus(z + b) with decay_scale A [H_v] and decay_bias
     b [H_v] (fp32, None = ones / zeros)."""
-    import torch
-    if q.dim() != 3:
-        raise ValueError("q [T, H_k, d_k]")
+    host = _host()
+    dev = _one_device(host, q, k, v, log_alpha, beta, S0, cu_seqlens, o, S_T, slots, decay_scale,
+                      decay_bias, workspace)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k [T, H_k, d_k] and v [T, H_v, d_v]")
     T = q.shape[0]
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
-        _on_device(q, cu_seqlens)
-        _expect(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
-    N = N or 1
+        _expect(cu_seqlens, "cu_seqlens", (N + 1,), host.i32)
+    elif N is None:
+        N = 1
     if S_T is None:
         if slots is not None:
             raise ValueError("with slots, S_T is the pool that the states are written to")
-        S_T = torch.empty((N, v.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32,
-                          device=q.device)
-    o, opt, sizes = _gdr_call(q, k, v, log_alpha, beta, (S0, S_T), slots, o, decay_scale,
+        S_T = host.empty((max(N, 0), v.shape[1], q.shape[2], v.shape[2]), dtype=host.f32,
+                         device=q.device)
+    o, opt, sizes = _gdr_call(host, q, k, v, log_alpha, beta, S0, S_T, slots, o, decay_scale,
                               decay_bias, N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale,
                               eps_l2)
-    dt = _dtype_code(q)
-    opt.max_seqlen = int(max_seqlen)
+    dt = _code(host, q.dtype)
+    opt.max_seqlen = max_seqlen
     opt.impl = IMPLS[impl] if isinstance(impl, str) else int(impl)
-    need = load().kda_gdr_prefill_workspace_size(T, N, *sizes, dt, ctypes.byref(opt))
+    need = load().kda_gdr_prefill_workspace_size(T, N, *sizes, dt, opt)
     if need > 0:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _on_device(q, workspace)
-        opt.workspace = _ptr(workspace)
+            workspace = host.empty(need, dtype=host.u8, device=q.device)
+        opt.workspace = workspace.data_ptr()
         opt.workspace_bytes = workspace.numel() * workspace.element_size()
-    rc = load().kda_gdr_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S0),
-                                _ptr(cu_seqlens), N, _ptr(o), _ptr(S_T), T, *sizes, dt,
-                                ctypes.byref(opt), _stream(stream))
+    rc = host.prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
+                      beta.data_ptr(), _ptr(S0), _ptr(cu_seqlens), N, o.data_ptr(),
+                      S_T.data_ptr(), T, *sizes, dt, opt, _stream_of(host, stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_gdr_prefill")
     return o, S_T
@@ -585,24 +631,27 @@ def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snap
     Returns o [N, (L,) H_v, d_v].  ``snapshots``: True or a tensor
     [N, L, H_v, d_k, d_v] fp32 for the state after each token; then returns
     (o, snapshots)."""
-    import torch
-    if q.dim() not in (3, 4):
-        raise ValueError("q [N, H_k, d_k] or [N, L, H_k, d_k]")
+    host = _host()
+    dev = _one_device(host, q, k, v, log_alpha, beta, S, o, slots, decay_scale, decay_bias)
+    if q.dim() not in (3, 4) or v.dim() != q.dim():
+        raise ValueError("q, k and v [N, H, d] or [N, L, H, d]")
     N, L = q.shape[0], q.shape[1] if q.dim() == 4 else 1
-    o, opt, sizes = _gdr_call(q, k, v, log_alpha, beta, (S,), slots, o, decay_scale, decay_bias,
-                              N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale, eps_l2)
+    o, opt, sizes = _gdr_call(host, q, k, v, log_alpha, beta, None, S, slots, o, decay_scale,
+                              decay_bias, N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale,
+                              eps_l2)
     if snapshots is False:
         snapshots = None
     if snapshots is not None:
-        shape = (N, L, sizes[1], sizes[2], sizes[3])
+        shape = (N, L, *sizes[1:])
         if snapshots is True:
-            snapshots = torch.empty(shape, dtype=torch.float32, device=q.device)
-        _on_device(q, snapshots)
-        _expect(snapshots, "snapshots", shape, torch.float32)
-        opt.snapshots = _ptr(snapshots)
-    rc = load().kda_gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                                    _ptr(S), _ptr(o), N, L, *sizes, _dtype_code(q),
-                                    ctypes.byref(opt), _stream(stream))
+            snapshots = host.empty(shape, dtype=host.f32, device=q.device)
+        else:
+            _one_device(host, q, snapshots)
+            _expect(snapshots, "snapshots", shape, host.f32)
+        opt.snapshots = snapshots.data_ptr()
+    rc = host.step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
+                   beta.data_ptr(), S.data_ptr(), o.data_ptr(), N, L, *sizes,
+                   _code(host, q.dtype), opt, _stream_of(host, stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_gdr_decode_step")
     return o if snapshots is None else (o, snapshots)
@@ -613,13 +662,19 @@ def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snap
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 
 
-def _rows(x, name: str, width: int) -> int:
-    """Elements between the rows of x [M, width], columns dense."""
-    if x.dim() != 2 or x.shape[1] != width:
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [.., {width}]")
+def _rows(x, name: str, rows: int, width: int) -> int:
+    """Elements between the rows of x [rows, width], columns dense; 0 for dense rows."""
+    if x.shape != (rows, width):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(rows, width)}")
+    if x.is_contiguous():
+        return 0
     if width > 1 and x.stride(1) != 1:
         raise ValueError(f"{name}: each row has to be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else 0
+    if rows < 2:
+        return 0
+    if x.stride(0) < width:  # a broadcast row, or rows that overlap
+        raise ValueError(f"{name}: rows have to lie apart")
+    return x.stride(0)
 
 
 def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none", stream=None):
@@ -628,23 +683,30 @@ def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none", stream=Non
     x [M, K], w [N, K], bias [N] or None, residual [M, N] or None, all of one
     dtype; rows contiguous, any distance apart.  ``act``: a key of ``ACTS``.
     y [M, N] may be the residual itself."""
-    import torch
-    _on_device(x, w, bias, residual, y)
-    N, K = w.shape
-    M = x.shape[0]
-    ldx, ldw = _rows(x, "x", K), _rows(w, "w", K)
-    if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    for t in (w, bias, residual, y):
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError("x, w, bias, residual and y of one dtype")
-    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
-        raise ValueError(f"y and residual [{M}, {N}]")
+    host = _host()
+    dev = _one_device(host, x, w, bias, residual, y)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x [M, K] and w [N, K]")
+    M, (N, K), dtype = x.shape[0], w.shape, x.dtype
+    code = _code(host, dtype)
+    ldx, ldw, ldr, ldy, b, r = _rows(x, "x", M, K), _rows(w, "w", N, K), 0, 0, None, None
+    if w.dtype != dtype:
+        raise TypeError("x, w, bias, residual and y of one dtype")
     if bias is not None:
-        _expect(bias, "bias", (N,), x.dtype)
-    rc = load().kda_linear(_ptr(x), ldx, _ptr(w), ldw, _ptr(bias), _ptr(residual),
-                           0 if residual is None else _rows(residual, "residual", N), _ptr(y),
-                           _rows(y, "y", N), M, N, K, ACTS[act], _dtype_code(x), _stream(stream))
+        _expect(bias, "bias", (N,), dtype)
+        b = bias.data_ptr()
+    if residual is not None:
+        ldr, r = _rows(residual, "residual", M, N), residual.data_ptr()
+        if residual.dtype != dtype:
+            raise TypeError("x, w, bias, residual and y of one dtype")
+    if y is None:
+        y = host.empty((M, N), dtype=dtype, device=x.device)
+    else:
+        ldy = _rows(y, "y", M, N)
+        if y.dtype != dtype:
+            raise TypeError("x, w, bias, residual and y of one dtype")
+    rc = host.linear(x.data_ptr(), ldx, w.data_ptr(), ldw, b, r, ldr, y.data_ptr(), ldy, M, N, K,
+                     ACTS[act], code, _stream_of(host, stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_linear")
     return y

@@ -173,9 +173,13 @@ def test_binding_refuses():
         kda._token_stride(torch.zeros(4, 2, 32).transpose(0, 1), "q")
     with pytest.raises(ValueError):  # [N, L] rows that are not evenly spaced
         kda._token_stride(torch.zeros(3, 8, 2, 32)[:, :4], "q")
+    for x in (torch.zeros(1, 2, 32).expand(4, 2, 32), torch.zeros(3, 1, 2, 32).expand(3, 4, 2, 32)):
+        with pytest.raises(ValueError):  # one token broadcast
+            kda._token_stride(x, "q")
     assert kda._token_stride(torch.zeros(9, 6, 32)[:, 2:4], "q") == 6 * 32
     assert kda._token_stride(torch.zeros(3, 4, 6, 32)[..., :2, :], "q") == 6 * 32
-    assert kda._token_stride(torch.zeros(3, 1, 2, 32), "q") == 64
+    assert kda._token_stride(torch.zeros(3, 1, 6, 32)[:, :, 1:3], "q") == 6 * 32
+    assert kda._token_stride(torch.zeros(3, 1, 2, 32), "q") == 0
     with pytest.raises(ValueError):
         kda._expect(torch.zeros(3, 2), "x", (3, 3), F32)
     with pytest.raises(TypeError):
@@ -185,15 +189,7 @@ def test_binding_refuses():
 
 
 # ------------------------------------------------------------------ prefill on the GPU
-IMPL = [("simt", F32), ("simt", BF16)]
-
-
-def _skip_unbuilt(impl, dk, dv):
-    if impl == "tc":
-        try:
-            kda.kda_gdr_prefill_path(64, 1, 1, 1, dk, dv, kda.KDA_BF16, kda.kda_gdr_options_init(impl="tc"))
-        except kda.KdaError:
-            pytest.skip("no chunked kernel for these head sizes")
+IMPL = [("simt", F32), ("simt", BF16), ("tc", BF16)]
 
 
 @gpu
@@ -203,7 +199,6 @@ def _skip_unbuilt(impl, dk, dv):
     (1, 2, 64, 64, [200, 16]), (2, 2, 32, 32, [77]), (1, 4, 64, 256, [70]), (1, 2, 128, 256, [100]),
     (2, 2, 32, 128, [129]), (1, 1, 128, 32, [65]), (1, 3, 128, 64, [150]), (4, 4, 64, 32, [17, 17])])
 def test_prefill(impl, dtype, Hk, Hv, dk, dv, lens):
-    _skip_unbuilt(impl, dk, dv)
     args = draw((sum(lens),), Hk, Hv, dk, dv, dtype)
     S0 = pool(len(lens), Hv, dk, dv)
     o, S = kda.kda_gdr_prefill(*args, S0, cu_of(lens), impl=impl)

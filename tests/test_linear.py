@@ -62,10 +62,13 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         kda.kda_linear(x, w)
     with pytest.raises(ValueError):
-        kda._rows(x.T, "x", 4)
+        kda._rows(x.T, "x", 8, 4)
     with pytest.raises(ValueError):
-        kda._rows(x, "x", 9)
-    assert kda._rows(torch.zeros(5, 20)[:, 4:12], "x", 8) == 20
+        kda._rows(x, "x", 4, 9)
+    with pytest.raises(ValueError):
+        kda._rows(x[:1].expand(4, 8), "x", 4, 8)
+    assert kda._rows(torch.zeros(5, 20)[:, 4:12], "x", 5, 8) == 20
+    assert kda._rows(x, "x", 4, 8) == 0
 
 
 def test_plain_bound_holds_for_fp32():
