@@ -13,11 +13,12 @@
 // Two kernels.  prep: T, P and the vectors of every chunk, all chunks in
 // parallel.  chain: the state's walk over the chunks of a sequence.
 //
-// Precision: the final states are fp32 results, so no operand may be rounded to
-// bf16.  K, Q and V are bf16 as they come and enter the products unscaled (norms
-// and decays multiply rows of results or fp32 operands); everything else (the state,
-// V - e^g K S, U, T, P) enters as two bf16 parts, x = hi + lo to 2^-16, one product for
-// each pair of parts but lo * lo.
+// Precision: the final states are fp32 results, so no operand on the state's way may be
+// rounded to bf16.  K, Q and V are bf16 as they come and enter the products unscaled (norms
+// and decays multiply rows of results or fp32 operands).  Everything else enters as a sum of
+// bf16 parts: the state, V - e^g K S, U and T as three (24 bits, an fp32 value), of whose
+// products those of order 2^-24 are left out; what only o sees (Q S and P U, rounded to bf16
+// in the end) as two.
 #include "gdr.cuh"
 #include "umma.cuh"
 
@@ -29,11 +30,11 @@ using namespace umma;
 constexpr int kC = 64;                 // tokens per chunk
 constexpr long long kSpins = 4000000000LL;  // ~2 s of clock cycles
 
-// One (chunk, value head) of the workspace: T and P as bf16 parts [row][64], 128-byte
-// rows whose 16-byte groups are XORed with the row's low three bits, then the vectors.
+// One (chunk, value head) of the workspace: the bf16 parts of T and P as tiles [row][64] of
+// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.
 constexpr uint32_t kTile = kC * kC * 2;
-constexpr uint32_t kTHi = 0, kTLo = kTile, kPHi = 2 * kTile, kPLo = 3 * kTile;
-constexpr uint32_t kVec = 4 * kTile;  // floats: a[64], b[64], ku[64], e^{g_C}
+constexpr uint32_t kT = 0, kP = 3 * kTile;  // T: three parts, P: two
+constexpr uint32_t kVec = 5 * kTile;        // floats: a[64], b[64], ku[64], e^{g_C}
 constexpr uint32_t kBlock = kVec + 1024;
 
 __host__ __device__ constexpr uint32_t tile_at(uint32_t row, uint32_t col) {
@@ -67,67 +68,64 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x, y as two bf16 parts each
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf162(x, y);
-  lo = pack_bf162(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+// x, y as sums of bf16 parts, packed
+__device__ __forceinline__ uint32_t part(float& x, float& y) {  // takes the next part off
+  const uint32_t p = pack_bf162(x, y);
+  x -= __uint_as_float(p << 16);
+  y -= __uint_as_float(p & 0xffff0000u);
+  return p;
+}
+template <int kParts>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[kParts]) {
+#pragma unroll
+  for (int i = 0; i < kParts - 1; ++i) p[i] = part(x, y);
+  p[kParts - 1] = pack_bf162(x, y);
 }
 // The accumulators of two neighbouring 16 x 8 tiles as the parts of a 16 x 16 A operand: the
 // layouts agree element by element.
+template <int kParts>
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4],
-                                        uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split2(c0[0], c0[1], hi[0], lo[0]);
-  split2(c0[2], c0[3], hi[1], lo[1]);
-  split2(c1[0], c1[1], hi[2], lo[2]);
-  split2(c1[2], c1[3], hi[3], lo[3]);
+                                        uint32_t (&p)[kParts][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[kParts];
+    split2<kParts>((i < 2 ? c0 : c1)[2 * (i & 1)], (i < 2 ? c0 : c1)[2 * (i & 1) + 1], w);
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) p[k][i] = w[k];
+  }
 }
 
 // ------------------------------------------------------------------ prep
+// One CTA per (chunk, query / key head): the two Grams once, then for each value head its
+// decays, A, P and the inverse of I + A:
+//   the four 16 x 16 diagonal blocks by forward substitution (a warp each, a lane per column),
+//   then twice [X00 0; X10 X11] with X10 = -X11 (A10 X00), from 16 to 32 and from 32 to 64,
+// all in fp32.  The operands are laid out in shared memory as the chain reads them and leave by
+// bulk copies.
 constexpr int kPrepThreads = 128;
-constexpr int kAtPitch = kC + 4;
+constexpr int kPitchA = kC + 4;  // floats
+constexpr int kScan = 4;         // heads whose decays are summed up at once, one per warp
 
 template <int DK>
 struct PrepSmem {
   static constexpr int kPitch = DK * 2 + 16;  // bytes: rows 16 bytes past a multiple of 128
-  __nv_bfloat16 k[kC * kPitch / 2], q[kC * kPitch / 2];
-  float at[2][kC][kAtPitch];                  // A transposed, two heads
+  union {
+    struct {
+      __nv_bfloat16 k[kC * kPitch / 2], q[kC * kPitch / 2];
+    };
+    struct {
+      float A[kC][kPitchA], X[kC][kPitchA];  // behind the Grams
+    };
+  };
+  // staging: T's first two parts take A's place, the rest of the block lies here
+  alignas(16) uint8_t rest[kBlock - 2 * kTile];
   float ik[kC], iq[kC];
-  float ghi[2][kC], glo[2][kC], beta[2][kC];
-  int n, c, t0, t1;
+  float ghi[kScan][kC], glo[kScan][kC], beta[kScan][kC];
+  int n, t0, t1;
 };
 
-// Column j of (I + A)^-1, rows k0 on (rows before k0 are zero: j >= k0), in x[.] as pairs:
-// x_j = 1, then as soon as x_k is known it leaves every later sum.
-template <int kK0>
-__device__ __forceinline__ void solve_column(const float (*at)[kAtPitch], int j,
-                                             unsigned long long (&x)[kC / 2]) {
-#pragma unroll
-  for (int i = 0; i < kC / 2; ++i)
-    x[i] = ((unsigned long long)__float_as_uint(j == 2 * i + 1 ? 1.f : 0.f) << 32) |
-           __float_as_uint(j == 2 * i ? 1.f : 0.f);
-#pragma unroll
-  for (int k = kK0; k < kC - 1; ++k) {
-    const uint32_t xk = k & 1 ? (uint32_t)(x[k / 2] >> 32) : (uint32_t)x[k / 2];
-    const uint32_t m = xk ^ 0x80000000u;
-    const unsigned long long m2 = ((unsigned long long)m << 32) | m;
-#pragma unroll
-    for (int i = (k + 1) & ~3; i < kC; i += 4) {  // entries up to row k are zero
-      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&at[k][i]);
-      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(x[i / 2]) : "l"(a.x), "l"(m2));
-      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(x[i / 2 + 1]) : "l"(a.y), "l"(m2));
-    }
-  }
-}
-
-__device__ __forceinline__ void store_parts(uint8_t* hi_tile, uint8_t* lo_tile, uint32_t at,
-                                            float v) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  *reinterpret_cast<__nv_bfloat16*>(hi_tile + at) = h;
-  *reinterpret_cast<__nv_bfloat16*>(lo_tile + at) = __float2bfloat16_rn(v - __bfloat162float(h));
-}
-
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrArgs a, uint8_t* ws) {
+__global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, uint8_t* ws) {
   using Smem = PrepSmem<DK>;
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
@@ -177,8 +175,44 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrArgs a, uint8
       cp_async16(smem_u32(s.q) + r * Smem::kPitch + g * 16, q + t * a.ldq + g * 8, r < len ? 16 : 0);
     }
     cp_async_commit();
-    cp_async_wait_all();
   }
+  // running sums of the log decays of heads h0 .., one per warp, in 64 bits: differences of
+  // them are taken
+  const __nv_bfloat16* beta = static_cast<const __nv_bfloat16*>(a.beta);
+  auto scan = [&](int h0) {
+    if (h0 + warp >= G) return;
+    const int h = hk * G + h0 + warp;
+    double g2[2];
+    float be[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane * 2 + i;
+      const size_t at = (size_t)(t0 + (r < len ? r : 0)) * a.Hv + h;
+      const float la = a.log_alpha[at], b = to_f32(beta[at]);
+      g2[i] = r < len ? (double)gdr_log_decay(a, la, h) : 0.0;
+      be[i] = r < len ? (a.beta_is_logit ? sigmoidf_(b) : b) : 0.f;
+    }
+    double sum = g2[0] + g2[1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const double other = __shfl_up_sync(0xffffffffu, sum, m);
+      if (lane >= m) sum += other;
+    }
+    const double g[2] = {sum - g2[1], sum};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane * 2 + i;
+      const float hi = (float)g[i];
+      s.ghi[warp][r] = hi;
+      s.glo[warp][r] = (float)(g[i] - (double)hi);
+      s.beta[warp][r] = be[i];
+    }
+  };
+  scan(0);
+  // the blocks of P above its diagonal stay zero
+  for (int i = tid; i < (int)sizeof(s.rest) / 16; i += kPrepThreads)
+    reinterpret_cast<uint4*>(s.rest)[i] = make_uint4(0, 0, 0, 0);
+  cp_async_wait_all();
   __syncthreads();
 
   // norms: two threads per row
@@ -236,92 +270,158 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(GdrArgs a, uint8
   }
   __syncthreads();
 
-  const __nv_bfloat16* beta = static_cast<const __nv_bfloat16*>(a.beta);
-  for (int h0 = 0; h0 < G; h0 += 2) {
-    if (warp < 2 && h0 + warp < G) {
-      // running sums of the log decays, in 64 bits: differences of them are taken
-      const int h = hk * G + h0 + warp;
-      uint8_t* out = ws + ((size_t)blk * a.Hv + h) * kBlock;
-      double g2[2];
-      float be[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = lane * 2 + i;
-        const size_t at = (size_t)(t0 + r) * a.Hv + h;
-        g2[i] = r < len ? (double)gdr_log_decay(a, a.log_alpha[at], h) : 0.0;
-        const float b = r < len ? to_f32(beta[at]) : 0.f;
-        be[i] = r < len && a.beta_is_logit ? sigmoidf_(b) : b;
-      }
-      double sum = g2[0] + g2[1];
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const double other = __shfl_up_sync(0xffffffffu, sum, m);
-        if (lane >= m) sum += other;
-      }
-      const double last = __shfl_sync(0xffffffffu, sum, 31);
-      const double g[2] = {sum - g2[1], sum};
-      float* vec = reinterpret_cast<float*>(out + kVec);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = lane * 2 + i;
-        const float hi = (float)g[i];
-        s.ghi[warp][r] = hi;
-        s.glo[warp][r] = (float)(g[i] - (double)hi);
-        s.beta[warp][r] = be[i];
-        const float e = expf(hi);
-        vec[r] = e * s.ik[r];
-        vec[64 + r] = e * s.iq[r];
-        vec[128 + r] = expf((float)(last - g[i])) * s.ik[r];
-      }
-      if (lane == 0) vec[192] = expf((float)last);
+  for (int hg = 0; hg < G; ++hg) {
+    const int x = hg % kScan;
+    uint8_t* out = ws + ((size_t)blk * a.Hv + hk * G + hg) * kBlock;
+    if (hg > 0) {
+      if (tid == 0) bulk_wait_read();  // the last head's block has left shared memory
+      if (x == 0) scan(hg);
+      __syncthreads();
     }
-    __syncthreads();
+    // A and P, from the Grams in registers; the vectors
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (h0 + x >= G) break;
-      uint8_t* out = ws + ((size_t)blk * a.Hv + hk * G + h0 + x) * kBlock;
+    for (int half = 0; half < 2; ++half) {
+      const int i = warp * 16 + (lane >> 2) + half * 8;
+      const float gh = s.ghi[x][i], gl = s.glo[x][i], ak = s.beta[x][i] * s.ik[i], pq = s.iq[i];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = warp * 16 + (lane >> 2) + half * 8;
-        const float gh = s.ghi[x][i], gl = s.glo[x][i], ak = s.beta[x][i] * s.ik[i], pq = s.iq[i];
+      for (int nt = 0; nt < 8; ++nt) {
+        if (nt > 2 * warp + 1) break;
+        float m[2], p[2];
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-          if (nt > 2 * warp + 1) break;
-          float p[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = nt * 8 + (lane & 3) * 2 + e;
-            const float d = (gh - s.ghi[x][j]) + (gl - s.glo[x][j]);
-            const float w = j <= i ? expf(fminf(d, 0.f)) * s.ik[j] : 0.f;
-            s.at[x][j][i] = j < i ? ak * w * kk[nt][half * 2 + e] : 0.f;
-            p[e] = j <= i ? pq * w * qk[nt][half * 2 + e] : 0.f;
-          }
-          uint32_t hi, lo;
-          split2(p[0], p[1], hi, lo);
-          const uint32_t at = tile_at(i, nt * 8 + (lane & 3) * 2);
-          *reinterpret_cast<uint32_t*>(out + kPHi + at) = hi;
-          *reinterpret_cast<uint32_t*>(out + kPLo + at) = lo;
+        for (int e = 0; e < 2; ++e) {
+          const int j = nt * 8 + (lane & 3) * 2 + e;
+          const float d = (gh - s.ghi[x][j]) + (gl - s.glo[x][j]);
+          const float w = j <= i ? expf(fminf(d, 0.f)) * s.ik[j] : 0.f;
+          m[e] = j < i ? ak * w * kk[nt][half * 2 + e] : 0.f;
+          p[e] = j <= i ? pq * w * qk[nt][half * 2 + e] : 0.f;
         }
+        const int j0 = nt * 8 + (lane & 3) * 2;
+        *reinterpret_cast<float2*>(&s.A[i][j0]) = make_float2(m[0], m[1]);
+        uint32_t w[2];
+        split2<2>(p[0], p[1], w);
+        uint8_t* dst = s.rest + (kP - 2 * kTile) + tile_at(i, j0);
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+        *reinterpret_cast<uint32_t*>(dst + kTile) = w[1];
+      }
+    }
+    if (tid < kC) {
+      float* vec = reinterpret_cast<float*>(s.rest + (kVec - 2 * kTile));
+      const float gh = s.ghi[x][tid], gl = s.glo[x][tid], e = expf(gh);
+      const float Gh = s.ghi[x][kC - 1], Gl = s.glo[x][kC - 1];
+      vec[tid] = e * s.ik[tid];
+      vec[64 + tid] = e * s.iq[tid];
+      vec[128 + tid] = expf((Gh - gh) + (Gl - gl)) * s.ik[tid];
+      if (tid == 0) vec[192] = expf(Gh);
+    }
+    __syncthreads();
+
+    // diagonal blocks: column c of block `warp`, x_i = -sum_k A_ik x_k
+    if (lane < 16) {
+      const int b0 = warp * 16;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float sum = i == lane ? 1.f : 0.f;
+#pragma unroll
+        for (int k = 0; k < i; ++k) sum = fmaf(-s.A[b0 + i][b0 + k], v[k], sum);
+        v[i] = sum;
+        s.X[b0 + i][b0 + lane] = sum;
       }
     }
     __syncthreads();
+    // 16 -> 32: blocks (1, 0) and (3, 2), 64 threads each, four columns of a row per thread;
+    // A10 X00 lies for the time being in the block above the diagonal
     {
-      const int x = warp >> 1, j = (warp & 1) * 32 + lane;
-      if (h0 + x < G) {
-        uint8_t* out = ws + ((size_t)blk * a.Hv + hk * G + h0 + x) * kBlock;
-        unsigned long long col[kC / 2];
-        if (warp & 1) solve_column<32>(s.at[x], j, col);
-        else solve_column<0>(s.at[x], j, col);
-        const float b = s.beta[x][j];
+      const int b0 = (tid >> 6) * 32, r = (tid >> 2) & 15, c = (tid & 3) * 4;
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kC; ++i) {
-          const float v = b * __uint_as_float(i & 1 ? (uint32_t)(col[i / 2] >> 32) : (uint32_t)col[i / 2]);
-          if (i >= (j & ~15)) store_parts(out + kTHi, out + kTLo, tile_at(i, j), v);
-        }
+      for (int k = 0; k < 16; ++k) {
+        const float m = s.A[b0 + 16 + r][b0 + k];
+        const float4 y = *reinterpret_cast<const float4*>(&s.X[b0 + k][b0 + c]);
+        z.x = fmaf(m, y.x, z.x); z.y = fmaf(m, y.y, z.y);
+        z.z = fmaf(m, y.z, z.z); z.w = fmaf(m, y.w, z.w);
       }
+      *reinterpret_cast<float4*>(&s.X[b0 + r][b0 + 16 + c]) = z;
+      __syncthreads();
+      z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float m = -s.X[b0 + 16 + r][b0 + 16 + k];
+        const float4 y = *reinterpret_cast<const float4*>(&s.X[b0 + k][b0 + 16 + c]);
+        z.x = fmaf(m, y.x, z.x); z.y = fmaf(m, y.y, z.y);
+        z.z = fmaf(m, y.z, z.z); z.w = fmaf(m, y.w, z.w);
+      }
+      *reinterpret_cast<float4*>(&s.X[b0 + 16 + r][b0 + c]) = z;
     }
     __syncthreads();
+    // 32 -> 64, eight columns of a row per thread; entries above the diagonals count as zero
+    {
+      const int r = tid >> 2, c = (tid & 3) * 8;
+      float z[8] = {};
+      auto step = [&](float m, const float* y) {
+        const float4 y0 = *reinterpret_cast<const float4*>(y);
+        const float4 y1 = *reinterpret_cast<const float4*>(y + 4);
+        z[0] = fmaf(m, y0.x, z[0]); z[1] = fmaf(m, y0.y, z[1]);
+        z[2] = fmaf(m, y0.z, z[2]); z[3] = fmaf(m, y0.w, z[3]);
+        z[4] = fmaf(m, y1.x, z[4]); z[5] = fmaf(m, y1.y, z[5]);
+        z[6] = fmaf(m, y1.z, z[6]); z[7] = fmaf(m, y1.w, z[7]);
+      };
+      if (c < 16)
+#pragma unroll 8
+        for (int k = 0; k < 16; ++k) step(s.A[32 + r][k], &s.X[k][c]);
+#pragma unroll 8
+      for (int k = 16; k < 32; ++k) step(s.A[32 + r][k], &s.X[k][c]);
+      *reinterpret_cast<float4*>(&s.X[r][32 + c]) = make_float4(z[0], z[1], z[2], z[3]);
+      *reinterpret_cast<float4*>(&s.X[r][36 + c]) = make_float4(z[4], z[5], z[6], z[7]);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < 16; ++k) step(-s.X[32 + r][32 + k], &s.X[k][32 + c]);
+      if (r >= 16)
+#pragma unroll 8
+        for (int k = 16; k < 32; ++k) step(-s.X[32 + r][32 + k], &s.X[k][32 + c]);
+      *reinterpret_cast<float4*>(&s.X[32 + r][c]) = make_float4(z[0], z[1], z[2], z[3]);
+      *reinterpret_cast<float4*>(&s.X[32 + r][c + 4]) = make_float4(z[4], z[5], z[6], z[7]);
+    }
+    __syncthreads();
+    // T = (I + A)^-1 Diag(beta) in three parts, eight columns at a time; A is done with
+#pragma unroll 1
+    for (int i = tid; i < kC * 8; i += kPrepThreads) {
+      const int r = i >> 3, c = (i & 7) * 8;
+      uint4 w[3] = {};
+      if (c <= r) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(&s.X[r][c + e]);
+          const float4 be = *reinterpret_cast<const float4*>(&s.beta[x][c + e]);
+          v[e] = y.x * be.x; v[e + 1] = y.y * be.y; v[e + 2] = y.z * be.z; v[e + 3] = y.w * be.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c + e <= r ? v[e] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t p[3];
+          split2<3>(v[2 * e], v[2 * e + 1], p);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) (&w[k].x)[e] = p[k];
+        }
+      }
+      uint8_t* t01 = reinterpret_cast<uint8_t*>(s.A) + tile_at(r, c);
+      *reinterpret_cast<uint4*>(t01) = w[0];
+      *reinterpret_cast<uint4*>(t01 + kTile) = w[1];
+      *reinterpret_cast<uint4*>(s.rest + tile_at(r, c)) = w[2];
+    }
+    fence_proxy_async();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_s2g(out, s.A, 2 * kTile);
+      bulk_s2g(out + 2 * kTile, s.rest, kBlock - 2 * kTile);
+      bulk_commit();
+    }
   }
+  if (tid == 0) bulk_wait_all();
 }
 
 // ------------------------------------------------------------------ chain
@@ -429,22 +529,22 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
     float X[8][4] = {}, Y[8][4] = {};
 #pragma unroll
     for (int x = 0; x < DK / 16; ++x) {
-      uint32_t hi[4], lo[4];
-      split_a(S[2 * x], S[2 * x + 1], hi, lo);
+      uint32_t f[3][4];
+      split_a<3>(S[2 * x], S[2 * x + 1], f);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t fk[4], fq[4];
         const uint32_t at = (p * 16 + nb) * Smem::kPitch + x * 32 + kb * 16;
         ldsm4(fk, sk + at);
         ldsm4(fq, sq + at);
-        mma(X[2 * p], hi, fk[0], fk[1]);
-        mma(X[2 * p + 1], hi, fk[2], fk[3]);
-        mma(Y[2 * p], hi, fq[0], fq[1]);
-        mma(Y[2 * p + 1], hi, fq[2], fq[3]);
-        mma(X[2 * p], lo, fk[0], fk[1]);
-        mma(X[2 * p + 1], lo, fk[2], fk[3]);
-        mma(Y[2 * p], lo, fq[0], fq[1]);
-        mma(Y[2 * p + 1], lo, fq[2], fq[3]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          mma(X[2 * p], f[i], fk[0], fk[1]);
+          mma(X[2 * p + 1], f[i], fk[2], fk[3]);
+          if (i == 2) break;
+          mma(Y[2 * p], f[i], fq[0], fq[1]);
+          mma(Y[2 * p + 1], f[i], fq[2], fq[3]);
+        }
       }
     }
     // V^T - e^g X^T (ik in a); e^g Y^T
@@ -469,39 +569,41 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
     float U[8][4] = {};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      uint32_t hi[4], lo[4];
-      split_a(X[2 * x], X[2 * x + 1], hi, lo);
+      uint32_t f[3][4];
+      split_a<3>(X[2 * x], X[2 * x + 1], f);
 #pragma unroll
       for (int p = x; p < 4; ++p) {
-        uint32_t fh[4], fl[4];
-        const uint32_t at = tile_at(p * 16 + nb, x * 16 + kb * 8);
-        ldsm4(fh, sb + kTHi + at);
-        ldsm4(fl, sb + kTLo + at);
-        mma(U[2 * p], hi, fh[0], fh[1]);
-        mma(U[2 * p + 1], hi, fh[2], fh[3]);
-        mma(U[2 * p], lo, fh[0], fh[1]);
-        mma(U[2 * p + 1], lo, fh[2], fh[3]);
-        mma(U[2 * p], hi, fl[0], fl[1]);
-        mma(U[2 * p + 1], hi, fl[2], fl[3]);
+        const uint32_t at = sb + kT + tile_at(p * 16 + nb, x * 16 + kb * 8);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          uint32_t m[4];
+          ldsm4(m, at + j * kTile);
+#pragma unroll
+          for (int i = 0; i < 3 - j; ++i) {
+            mma(U[2 * p], f[i], m[0], m[1]);
+            mma(U[2 * p + 1], f[i], m[2], m[3]);
+          }
+        }
       }
     }
     // O^T = e^g Y^T + U^T P^T
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      uint32_t hi[4], lo[4];
-      split_a(U[2 * x], U[2 * x + 1], hi, lo);
+      uint32_t f[2][4];
+      split_a<2>(U[2 * x], U[2 * x + 1], f);
 #pragma unroll
       for (int p = x; p < 4; ++p) {
-        uint32_t fh[4], fl[4];
-        const uint32_t at = tile_at(p * 16 + nb, x * 16 + kb * 8);
-        ldsm4(fh, sb + kPHi + at);
-        ldsm4(fl, sb + kPLo + at);
-        mma(Y[2 * p], hi, fh[0], fh[1]);
-        mma(Y[2 * p + 1], hi, fh[2], fh[3]);
-        mma(Y[2 * p], lo, fh[0], fh[1]);
-        mma(Y[2 * p + 1], lo, fh[2], fh[3]);
-        mma(Y[2 * p], hi, fl[0], fl[1]);
-        mma(Y[2 * p + 1], hi, fl[2], fl[3]);
+        const uint32_t at = sb + kP + tile_at(p * 16 + nb, x * 16 + kb * 8);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t m[4];
+          ldsm4(m, at + j * kTile);
+#pragma unroll
+          for (int i = 0; i < 2 - j; ++i) {
+            mma(Y[2 * p], f[i], m[0], m[1]);
+            mma(Y[2 * p + 1], f[i], m[2], m[3]);
+          }
+        }
       }
     }
     // S^T <- e^{g_C} S^T + (e^{g_C - g} U)^T K
@@ -519,16 +621,17 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
           float(&uu)[4] = U[2 * x + u];
           uu[0] *= ku.x; uu[1] *= ku.y; uu[2] *= ku.x; uu[3] *= ku.y;
         }
-        uint32_t hi[4], lo[4];
-        split_a(U[2 * x], U[2 * x + 1], hi, lo);
+        uint32_t f[3][4];
+        split_a<3>(U[2 * x], U[2 * x + 1], f);
 #pragma unroll
         for (int p = 0; p < DK / 16; ++p) {
-          uint32_t f[4];  // tokens 16 x + (0-7, 8-15) x channels 16 p + (0-7, 8-15)
-          ldsm4t(f, sk + (x * 16 + tr) * Smem::kPitch + p * 32 + tc * 16);
-          mma(S[2 * p], hi, f[0], f[1]);
-          mma(S[2 * p + 1], hi, f[2], f[3]);
-          mma(S[2 * p], lo, f[0], f[1]);
-          mma(S[2 * p + 1], lo, f[2], f[3]);
+          uint32_t m[4];  // tokens 16 x + (0-7, 8-15) x channels 16 p + (0-7, 8-15)
+          ldsm4t(m, sk + (x * 16 + tr) * Smem::kPitch + p * 32 + tc * 16);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            mma(S[2 * p], f[i], m[0], m[1]);
+            mma(S[2 * p + 1], f[i], m[2], m[3]);
+          }
         }
       }
     }
