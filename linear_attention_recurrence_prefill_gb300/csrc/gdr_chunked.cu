@@ -19,32 +19,12 @@
 // bf16 parts: the state, V - e^g K S, U and T as three (24 bits, an fp32 value), of whose
 // products those of order 2^-24 are left out; what only o sees (Q S and P U, rounded to bf16
 // in the end) as two.
-#include "gdr.cuh"
-#include "umma.cuh"
+#include "gdr_chunked.cuh"
 
 namespace kda {
 namespace {
 
 using namespace umma;
-
-constexpr int kC = 64;                 // tokens per chunk
-constexpr long long kSpins = 4000000000LL;  // ~2 s of clock cycles
-
-// One (chunk, value head) of the workspace: the bf16 parts of T and P as tiles [row][64] of
-// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.
-constexpr uint32_t kTile = kC * kC * 2;
-constexpr uint32_t kT = 0, kP = 3 * kTile;  // T: three parts, P: two
-constexpr uint32_t kVec = 5 * kTile;        // floats: a[64], b[64], ku[64], e^{g_C}
-constexpr uint32_t kBlock = kVec + 1024;
-
-__host__ __device__ constexpr uint32_t tile_at(uint32_t row, uint32_t col) {
-  return row * 128u + ((((col >> 3) ^ row) & 7u) << 4) + (col & 7u) * 2u;
-}
-
-// Chunk c of sequence n has block (t0 / 64 + n) + c: floor((t0 + len) / 64) + 1 is at
-// least floor(t0 / 64) + ceil(len / 64), so that sequences never share a block, and no
-// prefix sum over the sequences is needed.
-__host__ __device__ constexpr int block_base(int t0, int n) { return t0 / kC + n; }
 
 // ------------------------------------------------------------------ fragments
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -67,19 +47,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// x, y as sums of bf16 parts, packed
-__device__ __forceinline__ uint32_t part(float& x, float& y) {  // takes the next part off
-  const uint32_t p = pack_bf162(x, y);
-  x -= __uint_as_float(p << 16);
-  y -= __uint_as_float(p & 0xffff0000u);
-  return p;
-}
-template <int kParts>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[kParts]) {
-#pragma unroll
-  for (int i = 0; i < kParts - 1; ++i) p[i] = part(x, y);
-  p[kParts - 1] = pack_bf162(x, y);
 }
 // The accumulators of two neighbouring 16 x 8 tiles as the parts of a 16 x 16 A operand: the
 // layouts agree element by element.
@@ -477,7 +444,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
     int c = 0;
     for (; c < chunks; ++c) {
       const int b = c & 1;
-      if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&s.empty[b], (c / 2 - 1) & 1, kSpins));
+      if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&s.empty[b], (c / 2 - 1) & 1, kGdrSpins));
       if (!ok) break;
       auto& st = s.stage[b];
       const int len = min(kC, t1 - t0 - c * kC);
@@ -494,7 +461,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
       }
     }
     // loads in flight land before shared memory is released
-    for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&s.full[j & 1], (j / 2) & 1, kSpins);
+    for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&s.full[j & 1], (j / 2) & 1, kGdrSpins);
     if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
     return;
   }
@@ -518,7 +485,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
   bool ok = true;
   for (int c = 0; c < chunks; ++c) {
     const int b = c & 1;
-    ok = __all_sync(0xffffffffu, mbar_wait(&s.full[b], (c / 2) & 1, kSpins));
+    ok = __all_sync(0xffffffffu, mbar_wait(&s.full[b], (c / 2) & 1, kGdrSpins));
     if (!ok) break;
     auto& st = s.stage[b];
     const uint32_t sk = smem_u32(st.k), sq = smem_u32(st.q), sv = smem_u32(st.v);
@@ -690,6 +657,7 @@ cudaError_t launch_dk(const GdrArgs& a, uint8_t* ws, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   gdr_prep_kernel<DK><<<dim3(a.T_total / kC + a.N, a.Hk), kPrepThreads, bytes, s>>>(a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (gdr_chain_tc_takes(a)) return launch_gdr_chain_tc(a, ws, s);
   if (a.dv % 128 == 0) return launch_chain<DK, 8>(a, ws, s);
   if (a.dv == 64) return launch_chain<DK, 4>(a, ws, s);
   return launch_chain<DK, 2>(a, ws, s);
