@@ -6,17 +6,18 @@
 //
 // S^T stays in the registers of eight warps (thread = lane of TMEM = row of S^T, two warpgroups
 // for the two halves of d_k); the A operands of every product are written to TMEM, the B
-// operands lie in shared memory as prep and TMA put them there.  A chunk is a chain of four
-// dependent steps, each a conversion by the eight warps and products by the tensor cores:
-//     S -> parts | X (then Y) | V - a X -> parts | U | ku U -> parts | S's update
-// While the tensor cores work on X the warps store the last chunk's o, while they work on U
-// the warps scale Y, and P U runs behind the update.
+// operands lie in shared memory as prep and TMA put them there.  A chunk is a chain of
+// dependent steps, conversions by the eight warps and products by the tensor cores in turn:
+//     S -> parts | X and Y | V - a X -> parts | U | ku U -> parts | S's update
+// While the tensor cores work on X and Y the warps store the last chunk's o, while they work on
+// U the warps scale Y, and P U runs behind the update.  A product costs what its A operand takes to be fetched, N = 64 as much
+// as N = 128, so X and Y are one product against [K; Q].
 //
-// TMEM columns: the parts of S, whose place the update's product takes when X and Y are done;
-// X; two regions that Y and U take in turn (the parts of U lie in U's own place; the last
-// chunk's o is read from its Y while the next Y is built in the other); the parts of V - a X,
-// then of ku U.  Warpgroup h writes and reads only its own columns of each, so that no barrier
-// between the warps is needed.
+// TMEM columns (d_k = 128): 0-191 the parts of S, the first two of which lie where the same
+// warpgroup's half of the update's product comes (0-127), the third (128-191) where V - a X and
+// ku U go with 192-223; from 224 two regions in turn: X, then U, then its parts; Y, then o.
+// A warpgroup writes and reads only its own columns, so that no barrier between the warps is
+// needed.
 #include <cuda.h>
 
 #include <mutex>
@@ -31,22 +32,32 @@ using namespace umma;
 constexpr int kStateWarps = 8, kWarpLoad = 8, kWarpMma = 9;
 constexpr int kThreads = 320;
 constexpr uint32_t kDv = 128;
-constexpr uint32_t kXCol = 192, kYuCol = 256, kWCol = 384;  // X; two of 64; 96
+constexpr uint32_t kVCol = 128, kVCol2 = 192, kXyCol = 224;
 
 template <int DK>
 struct Layout {
-  static constexpr uint32_t kHalf = DK / 2;            // channels of a warpgroup
-  static constexpr uint32_t kSpHalf = 3 * kHalf / 2;   // its columns of S's parts
-  // the update's product: 128 channels in the places of the parts, 64 beside them
-  static constexpr uint32_t kDCol = DK == 128 ? 0 : 96, kDHalf = DK == 128 ? kSpHalf : kHalf;
-  static constexpr uint32_t kRows = kC * DK * 2;        // bytes of a K or Q tile
-  static constexpr uint32_t kKAt = kBlock, kQAt = kKAt + kRows, kVAt = kQAt + kRows;
-  static constexpr uint32_t kStage = kVAt + kC * kDv * 2;
-  static constexpr uint32_t kSmem = 2 * kStage + 1024;
+  static constexpr uint32_t kHalf = DK / 2;        // channels of a warpgroup
+  static constexpr uint32_t kPart = kHalf / 2;     // TMEM columns of one part of them
+  static constexpr uint32_t kThird = 2 * DK / 2;   // where the third parts of S begin
+  static constexpr uint32_t kRows = kC * 128;      // bytes of 64 rows of 64 channels
+  static constexpr uint32_t kKqAt = kBlock;        // 64 channels of K, then of Q; the next 64
+  static constexpr uint32_t kVAt = kKqAt + 2 * (DK / 64) * kRows;
+  static constexpr uint32_t kStage = kVAt + 2 * kRows;
+  static constexpr uint32_t kOAt = 2 * kStage;     // o [token][channel], bf16
+  static constexpr uint32_t kSmem = kOAt + kC * kDv * 2 + 1024;
+  // column of part k of the channels from 16 s on
+  static constexpr uint32_t s_col(uint32_t s, uint32_t k) {
+    const uint32_t half = s / (DK / 32), at = s % (DK / 32) * 8;
+    return (k < 2 ? half * 2 * kPart + k * kPart : kThird + half * kPart) + at;
+  }
 };
+// column of part k of V - a X or ku U, tokens from 16 s on
+__host__ __device__ constexpr uint32_t v_col(uint32_t s, uint32_t k) {
+  return (k < 2 ? kVCol + (s >> 1) * 32 + k * 16 : kVCol2 + (s >> 1) * 16) + (s & 1) * 8;
+}
 
 struct Chain {
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;
   GdrArgs a;
   const uint8_t* ws;
 };
@@ -66,19 +77,15 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// 2 N values as parts of N columns each, kStep columns apart
-template <int kParts, int N>
-__device__ __forceinline__ void store_parts(uint32_t col, uint32_t step, const float* x) {
-  uint32_t p[kParts][N];
+// 2 N values as three parts of N columns each
+template <int N>
+__device__ __forceinline__ void store_parts3(uint32_t col0, uint32_t col1, uint32_t col2, const float* x) {
+  uint32_t p[3][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t w[kParts];
-    split2<kParts>(x[2 * i], x[2 * i + 1], w);
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) p[k][i] = w[k];
-  }
-#pragma unroll
-  for (int k = 0; k < kParts; ++k) tmem_store<N>(col + k * step, p[k]);
+  for (int i = 0; i < N; ++i) split3(x[2 * i], x[2 * i + 1], p[0][i], p[1][i], p[2][i]);
+  tmem_store<N>(col0, p[0]);
+  tmem_store<N>(col1, p[1]);
+  tmem_store<N>(col2, p[2]);
 }
 
 template <int DK>
@@ -86,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
   using L = Layout<DK>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[2], empty[2], sp[2], x_done, y_done, v_ready, u_done, y_scaled, ku_ready,
-      u_ready, d_done, o_done, drained;
+  __shared__ uint64_t full[2], empty[2], sp[2], xy_done, v_ready, u_done, y_scaled, ku_ready, u_ready,
+      d_done, o_done, drained;
   __shared__ uint32_t tmem_base;
 
   const GdrArgs& a = t.a;
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       mbar_init(&empty[i], 1);
       mbar_init(&sp[i], kStateWarps);
     }
-    for (uint64_t* b : {&x_done, &y_done, &u_done, &d_done, &o_done, &drained}) mbar_init(b, 1);
+    for (uint64_t* b : {&xy_done, &u_done, &d_done, &o_done, &drained}) mbar_init(b, 1);
     for (uint64_t* b : {&v_ready, &y_scaled, &ku_ready, &u_ready}) mbar_init(b, kStateWarps);
     mbar_fence_init();
   }
@@ -131,80 +138,86 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       mbar_arrive_expect_tx(&full[b], L::kStage);
       const int row = t0 + c * kC;
 #pragma unroll
-      for (int i = 0; i < DK / 64; ++i)
-        tma_load_3d(st + L::kKAt + i * 8192, &t.tm_k, i * 64, hk, row, &full[b]);
+      for (int i = 0; i < DK / 64; ++i) {
+        tma_load_3d(st + L::kKqAt + 2 * i * L::kRows, &t.tm_k, i * 64, hk, row, &full[b]);
+        tma_load_3d(st + L::kKqAt + (2 * i + 1) * L::kRows, &t.tm_q, i * 64, hk, row, &full[b]);
+      }
       bulk_g2s(st, t.ws + ((size_t)(base + c) * a.Hv + h) * kBlock, kBlock, &full[b]);
 #pragma unroll
-      for (int i = 0; i < DK / 64; ++i)
-        tma_load_3d(st + L::kQAt + i * 8192, &t.tm_q, i * 64, hk, row, &full[b]);
-#pragma unroll
       for (int i = 0; i < 2; ++i)
-        tma_load_3d(st + L::kVAt + i * 8192, &t.tm_v, slice * (int)kDv + i * 64, h, row, &full[b]);
+        tma_load_3d(st + L::kVAt + i * L::kRows, &t.tm_v, slice * (int)kDv + i * 64, h, row, &full[b]);
     }
     // loads in flight land before shared memory is released
     if (!ok)
       for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&full[j & 1], (j / 2) & 1, kGdrSpins);
-  } else if (warp == kWarpMma && lane == 0) {
-    constexpr uint32_t idesc = idesc_f16(128, 64, true), idesc_d = idesc_f16(128, 64, true, false, true);
+  } else if (warp == kWarpMma) {
+    const uint32_t lead = elect_leader();
+    constexpr uint32_t idesc_xy = idesc_f16(128, 128, true), idesc = idesc_f16(128, 64, true),
+                       idesc_d = idesc_f16(128, DK, true, false, true);
     constexpr uint32_t kSteps = DK / 16;
     auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && mbar_wait(bar, parity, kGdrSpins);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
       fence_after_sync();
       return ok;
     };
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, ph = c & 1;
       const uint32_t st = smem_u32(stages + b * L::kStage);
-      const uint32_t ycol = tmem + kYuCol + (c & 1) * 64, ucol = tmem + kYuCol + (1 - (c & 1)) * 64;
+      const uint32_t xcol = tmem + kXyCol + (c & 1) * 128, ycol = xcol + 64;
+      // descriptors: the address is their low 14 bits, in units of 16 bytes
+      const uint64_t kq = desc_k_sw128(st + L::kKqAt, 0), tt = desc_k_sw128(st + kT, 0),
+                     pp = desc_k_sw128(st + kP, 0), km = desc_mn_sw128(st + L::kKqAt, 0, 2 * L::kRows);
       if (!wait(&full[b], (c / 2) & 1)) break;
-      // X and Y: K step s = channels 16 s ..; half the channels of each warpgroup at a time
-      auto product = [&](uint32_t d, uint32_t rows, uint32_t s, uint32_t k, bool add) {
-        const uint32_t half = s / (kSteps / 2), col = half * L::kSpHalf + k * (L::kHalf / 2) + (s % (kSteps / 2)) * 8;
-        mma_ts(d, tmem + col, desc_k_sw128(st + rows + (s >> 2) * 8192, (s & 3) * 32), idesc, add);
-      };
-      bool first = true;
-      for (int part_of = 0; part_of < 2 && ok; ++part_of) {
+      // X and Y, half of each warpgroup's channels at a time
+#pragma unroll
+      for (uint32_t part_of = 0; part_of < 2; ++part_of) {
         if (!wait(&sp[part_of], ph)) break;
+#pragma unroll
         for (uint32_t half = 0; half < 2; ++half)
+#pragma unroll
           for (uint32_t i = 0; i < kSteps / 4; ++i)
+#pragma unroll
             for (uint32_t k = 0; k < 3; ++k) {
-              product(tmem + kXCol, L::kKAt, half * (kSteps / 2) + part_of * (kSteps / 4) + i, k, !first);
-              first = false;
+              const uint32_t s = half * (kSteps / 2) + part_of * (kSteps / 4) + i;
+              mma_ts_if(lead, xcol, tmem + L::s_col(s, k), kq + (((s >> 2) * 2 * L::kRows + (s & 3) * 32) >> 4),
+                     idesc_xy, part_of + half + i + k > 0);
             }
       }
       if (!ok) break;
-      mma_commit(&x_done);
-      for (uint32_t s = 0; s < kSteps; ++s)
-        for (uint32_t k = 0; k < 2; ++k) product(ycol, L::kQAt, s, k, s + k > 0);
-      mma_commit(&y_done);
+      mma_commit_if(lead, &xy_done);
       // U: tokens 16 s .. of V - a X against T's columns
       if (!wait(&v_ready, ph)) break;
+#pragma unroll
       for (uint32_t s = 0; s < 4; ++s)
+#pragma unroll
         for (uint32_t j = 0; j < 3; ++j)
+#pragma unroll
           for (uint32_t k = 0; k < 3 - j; ++k)
-            mma_ts(ucol, tmem + kWCol + (s >> 1) * 48 + k * 16 + (s & 1) * 8,
-                   desc_k_sw128(st + kT + j * kTile, s * 32), idesc, s + j + k > 0);
-      mma_commit(&u_done);
+            mma_ts_if(lead, xcol, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4), idesc, s + j + k > 0);
+      mma_commit_if(lead, &u_done);
       // the update: ku U against K, tokens contracted
       if (!wait(&ku_ready, ph)) break;
-      for (uint32_t half = 0; half < DK / 64; ++half)
-        for (uint32_t s = 0; s < 4; ++s)
-          for (uint32_t k = 0; k < 3; ++k)
-            mma_ts(tmem + L::kDCol + half * L::kDHalf, tmem + kWCol + (s >> 1) * 48 + k * 16 + (s & 1) * 8,
-                   desc_mn_sw128(st + L::kKAt + half * 8192, s, 8192), idesc_d, s + k > 0);
-      mma_commit(&d_done);
+#pragma unroll
+      for (uint32_t s = 0; s < 4; ++s)
+#pragma unroll
+        for (uint32_t k = 0; k < 3; ++k)
+          mma_ts_if(lead, tmem, tmem + v_col(s, k), km + (s * 2048 >> 4), idesc_d, s + k > 0);
+      mma_commit_if(lead, &d_done);
       // P U onto b Y
       if (!wait(&y_scaled, ph) || !wait(&u_ready, ph)) break;
+#pragma unroll
       for (uint32_t s = 0; s < 4; ++s)
+#pragma unroll
         for (uint32_t j = 0; j < 2; ++j)
+#pragma unroll
           for (uint32_t k = 0; k < 2 - j; ++k)
-            mma_ts(ycol, ucol + (s >> 1) * 32 + k * 16 + (s & 1) * 8,
-                   desc_k_sw128(st + kP + j * kTile, s * 32), idesc, 1);
-      mma_commit(&o_done);
-      mma_commit(&empty[b]);
+            mma_ts_if(lead, ycol, xcol + (s >> 1) * 32 + k * 16 + (s & 1) * 8, pp + ((j * kTile + s * 32) >> 4),
+                   idesc, 1);
+      mma_commit_if(lead, &o_done);
+      mma_commit_if(lead, &empty[b]);
     }
     // products in flight end before shared memory and TMEM are released
-    mma_commit(&drained);
+    mma_commit_if(lead, &drained);
     mbar_wait(&drained, 0, kGdrSpins);
   } else if (warp < kStateWarps) {
     const int quarter = warp & 3, half = warp >> 2;
@@ -212,106 +225,119 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     const uint32_t lanes = taddr(tmem, quarter * 32, 0);
     const size_t mat = ((size_t)slot * a.Hv + h) * DK * a.dv + (size_t)(half * L::kHalf) * a.dv +
                        slice * kDv + dv;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (size_t)h * a.dv + slice * kDv + dv;
-    const size_t token = (size_t)a.Hv * a.dv;
     float S[L::kHalf];
 #pragma unroll
     for (uint32_t i = 0; i < L::kHalf; ++i) S[i] = a.S0 ? a.S0[mat + (size_t)i * a.dv] : 0.f;
     float eG = 1.f;
+    // A wait that gave up: the warp goes on without waiting, so that it meets the others at the
+    // named barriers, and stores nothing more to global memory.
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
       fence_after_sync();
-      return ok;
     };
-    // S <- e^{g_C} S + the update's product, 32 (or 16) channels from i on
-    auto update = [&](uint32_t i) {
-      if constexpr (DK == 128) {
+    // S <- e^{g_C} S + the update's product
+    auto update = [&] {
+#pragma unroll
+      for (uint32_t i = 0; i < L::kHalf; i += 32) {
         uint32_t r[32];
-        tmem_ld32(lanes + L::kDCol + half * L::kDHalf + i, r);
+        tmem_ld32(lanes + half * L::kHalf + i, r);
         tmem_wait_ld();
 #pragma unroll
         for (uint32_t j = 0; j < 32; ++j) S[i + j] = fmaf(eG, S[i + j], __uint_as_float(r[j]));
-      } else {
-        uint32_t r[16];
-        tmem_ld16(lanes + L::kDCol + half * L::kDHalf + i, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (uint32_t j = 0; j < 16; ++j) S[i + j] = fmaf(eG, S[i + j], __uint_as_float(r[j]));
       }
     };
-    // o of chunk c: this warpgroup's 32 tokens, lanes = neighbouring channels
+    // o of chunk c, this warpgroup's 32 tokens, through shared memory: two boxes of 64 channels,
+    // or row by row where the sequence ends among them (what follows is another's)
+    uint8_t* so = stages + L::kOAt + half * 2 * 4096;
     auto write_o = [&](int c) {
       uint32_t r[32];
-      tmem_ld32(lanes + kYuCol + (c & 1) * 64 + half * 32, r);
+      tmem_ld32(lanes + kXyCol + (c & 1) * 128 + 64 + half * 32, r);
+      if (quarter == 0) bulk_wait_read();  // the rows before have left
+      named_sync(1 + half, 128);
       tmem_wait_ld();
-      const int row = t0 + c * kC + half * 32;
+      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(so + (dv >> 6) * 4096) + (dv & 63);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (row + i < t1) o[(size_t)(row + i) * token] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      for (int i = 0; i < 32; ++i) to[i * 64] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      fence_proxy_async();
+      named_sync(1 + half, 128);
+      const int row = t0 + c * kC + half * 32;
+      if (quarter == 0 && ok) {
+        if (row + 32 <= t1) {
+          if (lane < 2) tma_store_3d(&t.tm_o, so + lane * 4096, slice * (int)kDv + lane * 64, h, row);
+        } else if (row + lane < t1) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(row + lane) * a.Hv + h) * a.dv + slice * kDv;
+          bulk_s2g(o, so + lane * 128, 128);
+          bulk_s2g(o + 64, so + 4096 + lane * 128, 128);
+        }
+        bulk_commit();
+      }
     };
-
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, ph = c & 1;
       uint8_t* st = stages + b * L::kStage;
       const float* vec = reinterpret_cast<const float*>(st + kVec) + half * 32;
       const int len = min(kC, t1 - t0 - c * kC);
-      if (c > 0 && !wait(&d_done, (c - 1) & 1)) break;
+      // V, and zeros behind the last token: there the rows are the next sequence's (the products
+      // see them behind the hand-over below)
+      wait(&full[b], (c / 2) & 1);
+      uint32_t vp[16];
+      {
+        const uint16_t* vs = reinterpret_cast<const uint16_t*>(st + L::kVAt + (dv >> 6) * L::kRows) +
+                             half * 32 * 64 + (dv & 63);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const uint32_t lo = half * 32 + i < len ? vs[i * 64] : 0, hi = half * 32 + i + 1 < len ? vs[i * 64 + 64] : 0;
+          vp[i / 2] = lo | hi << 16;
+        }
+      }
       if (len < kC) {
-        // rows behind the last token belong to the next sequence: zeros in their place, seen by
-        // the products behind the hand-over below
-        if (!wait(&full[b], (c / 2) & 1)) break;
         for (int i = threadIdx.x; i < (kC - len) * 8 * (DK / 64) * 2; i += kStateWarps * 32) {
           const int tile = i / ((kC - len) * 8), j = i % ((kC - len) * 8);
-          *reinterpret_cast<uint4*>(st + L::kKAt + tile * 8192 + (len + (j >> 3)) * 128 + (j & 7) * 16) =
+          *reinterpret_cast<uint4*>(st + L::kKqAt + tile * L::kRows + (len + (j >> 3)) * 128 + (j & 7) * 16) =
               make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
       }
-      // the whole product is read before the parts take its place
+      // S as parts, in two halves so that the products start on the first; the update's whole
+      // product is read before the parts take its place
       if (c > 0) {
-        update(0);
-        update(L::kHalf / 2);
+        wait(&d_done, (c - 1) & 1);
+        update();
       }
-      // S as parts, in two halves so that the products start on the first
 #pragma unroll
       for (uint32_t i = 0; i < 2; ++i) {
-        store_parts<3, L::kHalf / 4>(lanes + half * L::kSpHalf + i * (L::kHalf / 4), L::kHalf / 2,
-                                     &S[i * L::kHalf / 2]);
+        store_parts3<L::kHalf / 4>(lanes + half * 2 * L::kPart + i * (L::kPart / 2),
+                                   lanes + half * 2 * L::kPart + L::kPart + i * (L::kPart / 2),
+                                   lanes + L::kThird + half * L::kPart + i * (L::kPart / 2),
+                                   &S[i * L::kHalf / 2]);
         hand_over(&sp[i], lane);
       }
       if (c > 0) {
-        if (!wait(&o_done, (c - 1) & 1)) break;
+        wait(&o_done, (c - 1) & 1);
         write_o(c - 1);
       }
       // V - a X
-      if (!wait(&full[b], (c / 2) & 1)) break;
+      wait(&xy_done, ph);
       float v[32];
       {
-        const __nv_bfloat16* vs = reinterpret_cast<const __nv_bfloat16*>(st + L::kVAt + (dv >> 6) * 8192) +
-                                  half * 32 * 64 + (dv & 63);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = half * 32 + i < len ? __bfloat162float(vs[i * 64]) : 0.f;
-      }
-      if (!wait(&x_done, ph)) break;
-      {
         uint32_t r[32];
-        tmem_ld32(lanes + kXCol + half * 32, r);
+        tmem_ld32(lanes + kXyCol + (c & 1) * 128 + half * 32, r);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 va = *reinterpret_cast<const float4*>(vec + i);
-          v[i] = fmaf(-va.x, __uint_as_float(r[i]), v[i]);
-          v[i + 1] = fmaf(-va.y, __uint_as_float(r[i + 1]), v[i + 1]);
-          v[i + 2] = fmaf(-va.z, __uint_as_float(r[i + 2]), v[i + 2]);
-          v[i + 3] = fmaf(-va.w, __uint_as_float(r[i + 3]), v[i + 3]);
+          v[i] = fmaf(-va.x, __uint_as_float(r[i]), __uint_as_float(vp[i / 2] << 16));
+          v[i + 1] = fmaf(-va.y, __uint_as_float(r[i + 1]), __uint_as_float(vp[i / 2] & 0xffff0000u));
+          v[i + 2] = fmaf(-va.z, __uint_as_float(r[i + 2]), __uint_as_float(vp[i / 2 + 1] << 16));
+          v[i + 3] = fmaf(-va.w, __uint_as_float(r[i + 3]), __uint_as_float(vp[i / 2 + 1] & 0xffff0000u));
         }
       }
-      store_parts<3, 16>(lanes + kWCol + half * 48, 16, v);
+      const uint32_t w0 = lanes + kVCol + half * 32, w2 = lanes + kVCol2 + half * 16;
+      store_parts3<16>(w0, w0 + 16, w2, v);
       hand_over(&v_ready, lane);
       // b Y
-      if (!wait(&y_done, ph)) break;
       {
-        const uint32_t ycol = lanes + kYuCol + (c & 1) * 64 + half * 32;
+        const uint32_t ycol = lanes + kXyCol + (c & 1) * 128 + 64 + half * 32;
         uint32_t r[32];
         tmem_ld32(ycol, r);
         tmem_wait_ld();
@@ -327,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         hand_over(&y_scaled, lane);
       }
       // ku U and U
-      if (!wait(&u_done, ph)) break;
+      wait(&u_done, ph);
       {
-        const uint32_t ucol = lanes + kYuCol + (1 - (c & 1)) * 64 + half * 32;
+        const uint32_t ucol = lanes + kXyCol + (c & 1) * 128 + half * 32;
         uint32_t r[32];
         tmem_ld32(ucol, r);
         tmem_wait_ld();
@@ -342,20 +368,27 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
           v[i + 3] = ku.w * __uint_as_float(r[i + 3]);
         }
         eG = vec[192 - half * 32];
-        store_parts<3, 16>(lanes + kWCol + half * 48, 16, v);
+        store_parts3<16>(w0, w0 + 16, w2, v);
         hand_over(&ku_ready, lane);
+        uint32_t p[2][16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        store_parts<2, 16>(ucol, 16, v);
+        for (int i = 0; i < 16; ++i) {
+          uint32_t w[2];
+          split2<2>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), w);
+          p[0][i] = w[0];
+          p[1][i] = w[1];
+        }
+        tmem_st16(ucol, p[0]);
+        tmem_st16(ucol + 16, p[1]);
         hand_over(&u_ready, lane);
       }
     }
-    if (ok && chunks > 0) {
-      if (wait(&d_done, (chunks - 1) & 1)) {
-        update(0);
-        update(L::kHalf / 2);
-      }
-      if (wait(&o_done, (chunks - 1) & 1)) write_o(chunks - 1);
+    if (chunks > 0) {
+      wait(&d_done, (chunks - 1) & 1);
+      update();
+      wait(&o_done, (chunks - 1) & 1);
+      write_o(chunks - 1);
+      if (quarter == 0) bulk_wait_all();
     }
     if (ok) {
 #pragma unroll
@@ -389,13 +422,14 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Tensor map of [T][H][d] bf16 rows, tokens ld elements apart: boxes of 64 channels of one head
-// by 64 tokens.
-bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld, bool swizzle) {
+// by `rows` tokens.
+bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld, int rows,
+            bool swizzle) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, 1, kC};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -411,9 +445,10 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   Chain t;
   t.a = a;
   t.ws = ws;
-  if (!encode(&t.tm_k, a.k, a.T_total, a.Hk, DK, a.ldk, true) ||
-      !encode(&t.tm_q, a.q, a.T_total, a.Hk, DK, a.ldq, true) ||
-      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, false))
+  if (!encode(&t.tm_k, a.k, a.T_total, a.Hk, DK, a.ldk, kC, true) ||
+      !encode(&t.tm_q, a.q, a.T_total, a.Hk, DK, a.ldq, kC, true) ||
+      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, kC, false) ||
+      !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, 32, false))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (int)kDv);
   gdr_chain_tc_kernel<DK><<<grid, kThreads, Layout<DK>::kSmem, s>>>(t);

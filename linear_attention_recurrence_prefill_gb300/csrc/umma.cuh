@@ -128,6 +128,45 @@ __device__ __forceinline__ void mma_commit(uint64_t* mbar) {
       :: "r"(smem_u32(mbar)) : "memory");
 }
 
+// The same for a whole warp in step, of which one lane (`leader` nonzero) issues: descriptors
+// that are the same in every lane need no move from a lane's registers.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t leader, uint64_t* mbar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      :: "r"(smem_u32(mbar)), "r"(leader) : "memory");
+}
+
 // ------------------------------------------------------------------ TMEM load/store
 // 32 lanes x 32 consecutive columns of 32-bit data; each thread of the warp
 // gets its lane's 32 words.  The warp may only touch its own 32-lane quarter.
@@ -306,6 +345,12 @@ __device__ __forceinline__ void tma_load_2d(void* dst_smem, const void* tmap, in
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];"
       :: "r"(smem_u32(dst_smem)), "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+// Tiled tensor copy shared -> global, 3-D box at coordinates (x, y, z) (bulk-group completion).
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src_smem, int x, int y,
+                                             int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+               :: "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src_smem)) : "memory");
 }
 // Fetch a tensor map's descriptor ahead of its first use.
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
