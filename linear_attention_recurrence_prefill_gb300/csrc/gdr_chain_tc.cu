@@ -1,22 +1,25 @@
 // gdr_chain_tc.cu -- the state's walk over the chunks of a sequence on tcgen05, for d_k of 64 or
 // 128 and 128 columns of the state (d_v) per CTA.  The algebra and the parts that operands are
 // split into are those of gdr_chunked.cu; everything is held transposed, lanes of TMEM = d_v:
-//     X^T = S^T K^T,  Y^T = S^T Q^T,  U^T = (V - a X)^T T^T,
+//     X^T = S^T K^T,  Y^T = S^T Q^T,  U^T = V^T T^T - (a X)^T T^T,
 //     O^T = b Y^T + U^T P^T,          S^T <- e^{g_C} S^T + (ku U)^T K.
 //
 // S^T stays in the registers of eight warps (thread = lane of TMEM = row of S^T, two warpgroups
-// for the two halves of d_k); the A operands of every product are written to TMEM, the B
-// operands lie in shared memory as prep and TMA put them there.  A chunk is a chain of
-// dependent steps, conversions by the eight warps and products by the tensor cores in turn:
-//     S -> parts | X and Y | V - a X -> parts | U | ku U -> parts | S's update
-// While the tensor cores work on X and Y the warps store the last chunk's o, while they work on
-// U the warps scale Y, and P U runs behind the update.  A product costs what its A operand takes to be fetched, N = 64 as much
-// as N = 128, so X and Y are one product against [K; Q].
+// for the two halves of d_k).  What they make of it is written to TMEM as A operands; V^T is an
+// A operand as it lies in shared memory, and so are the B operands, as prep and TMA put them
+// there.  A chunk is a chain of dependent steps, conversions by the eight warps and products by
+// the tensor cores in turn,
+//     S -> parts | X | -a X -> parts | U | ku U -> parts | S's update,
+// each handed over in pieces of 16 channels or tokens, so that the products of the first run
+// beside the conversion of the next.  The rest fills the gaps: Y runs beside the conversion of
+// X, V T of the next chunk beside that of U, P U beside that of S; the warps scale Y while the
+// tensor cores work on U and hand the last chunk's o to another warp, which stores it, while
+// they work on X.
 //
 // TMEM columns (d_k = 128): 0-191 the parts of S, the first two of which lie where the same
-// warpgroup's half of the update's product comes (0-127), the third (128-191) where V - a X and
-// ku U go with 192-223; from 224 two regions in turn: X, then U, then its parts; Y, then o.
-// A warpgroup writes and reads only its own columns, so that no barrier between the warps is
+// warpgroup's half of the update's product comes (0-127), the third (128-191) where -a X and
+// ku U go with 192-223; 224 and 288 in turn X and U, then U's parts; 352 and 416 in turn Y, then
+// o.  A warpgroup writes and reads only its own columns, so that no barrier between the warps is
 // needed.
 #include <cuda.h>
 
@@ -29,10 +32,10 @@ namespace {
 
 using namespace umma;
 
-constexpr int kStateWarps = 8, kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 320;
+constexpr int kStateWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpStore = 10;
+constexpr int kThreads = 352;
 constexpr uint32_t kDv = 128;
-constexpr uint32_t kVCol = 128, kVCol2 = 192, kXyCol = 224;
+constexpr uint32_t kVCol = 128, kVCol2 = 192, kXuCol = 224, kYCol = 352;
 
 template <int DK>
 struct Layout {
@@ -40,18 +43,19 @@ struct Layout {
   static constexpr uint32_t kPart = kHalf / 2;     // TMEM columns of one part of them
   static constexpr uint32_t kThird = 2 * DK / 2;   // where the third parts of S begin
   static constexpr uint32_t kRows = kC * 128;      // bytes of 64 rows of 64 channels
-  static constexpr uint32_t kKqAt = kBlock;        // 64 channels of K, then of Q; the next 64
-  static constexpr uint32_t kVAt = kKqAt + 2 * (DK / 64) * kRows;
+  static constexpr uint32_t kSteps = DK / 16, kSub = DK / 32;  // 16-channel steps, and of a half
+  static constexpr uint32_t kKAt = kBlock, kQAt = kKAt + DK / 64 * kRows;
+  static constexpr uint32_t kVAt = kQAt + DK / 64 * kRows;
   static constexpr uint32_t kStage = kVAt + 2 * kRows;
   static constexpr uint32_t kOAt = 2 * kStage;     // o [token][channel], bf16
   static constexpr uint32_t kSmem = kOAt + kC * kDv * 2 + 1024;
   // column of part k of the channels from 16 s on
   static constexpr uint32_t s_col(uint32_t s, uint32_t k) {
-    const uint32_t half = s / (DK / 32), at = s % (DK / 32) * 8;
+    const uint32_t half = s / kSub, at = s % kSub * 8;
     return (k < 2 ? half * 2 * kPart + k * kPart : kThird + half * kPart) + at;
   }
 };
-// column of part k of V - a X or ku U, tokens from 16 s on
+// column of part k of -a X or ku U, tokens from 16 s on
 __host__ __device__ constexpr uint32_t v_col(uint32_t s, uint32_t k) {
   return (k < 2 ? kVCol + (s >> 1) * 32 + k * 16 : kVCol2 + (s >> 1) * 16) + (s & 1) * 8;
 }
@@ -93,8 +97,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
   using L = Layout<DK>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[2], empty[2], sp[2], xy_done, v_ready, u_done, y_scaled, ku_ready, u_ready,
-      d_done, o_done, drained;
+  __shared__ uint64_t full[2], empty[2], s_ready[4], x_done, y_done, v_ready[2], u_done, y_scaled,
+      ku_ready[2], u_ready, d_done, o_done, o_ready, o_free, drained;
   __shared__ uint32_t tmem_base;
 
   const GdrArgs& a = t.a;
@@ -109,10 +113,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&sp[i], kStateWarps);
+      mbar_init(&v_ready[i], kStateWarps);
+      mbar_init(&ku_ready[i], kStateWarps);
     }
-    for (uint64_t* b : {&xy_done, &u_done, &d_done, &o_done, &drained}) mbar_init(b, 1);
-    for (uint64_t* b : {&v_ready, &y_scaled, &ku_ready, &u_ready}) mbar_init(b, kStateWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&s_ready[i], kStateWarps);
+    for (uint64_t* b : {&x_done, &y_done, &u_done, &d_done, &o_done, &o_free, &drained}) mbar_init(b, 1);
+    for (uint64_t* b : {&y_scaled, &u_ready, &o_ready}) mbar_init(b, kStateWarps);
     mbar_fence_init();
   }
   if (warp == kWarpMma) {
@@ -139,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       const int row = t0 + c * kC;
 #pragma unroll
       for (int i = 0; i < DK / 64; ++i) {
-        tma_load_3d(st + L::kKqAt + 2 * i * L::kRows, &t.tm_k, i * 64, hk, row, &full[b]);
-        tma_load_3d(st + L::kKqAt + (2 * i + 1) * L::kRows, &t.tm_q, i * 64, hk, row, &full[b]);
+        tma_load_3d(st + L::kKAt + i * L::kRows, &t.tm_k, i * 64, hk, row, &full[b]);
+        tma_load_3d(st + L::kQAt + i * L::kRows, &t.tm_q, i * 64, hk, row, &full[b]);
       }
       bulk_g2s(st, t.ws + ((size_t)(base + c) * a.Hv + h) * kBlock, kBlock, &full[b]);
 #pragma unroll
@@ -152,73 +158,129 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&full[j & 1], (j / 2) & 1, kGdrSpins);
   } else if (warp == kWarpMma) {
     const uint32_t lead = elect_leader();
-    constexpr uint32_t idesc_xy = idesc_f16(128, 128, true), idesc = idesc_f16(128, 64, true),
+    constexpr uint32_t idesc = idesc_f16(128, 64, true), idesc_v = idesc_f16(128, 64, true, true),
                        idesc_d = idesc_f16(128, DK, true, false, true);
-    constexpr uint32_t kSteps = DK / 16;
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
       fence_after_sync();
       return ok;
     };
-    for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1, ph = c & 1;
-      const uint32_t st = smem_u32(stages + b * L::kStage);
-      const uint32_t xcol = tmem + kXyCol + (c & 1) * 128, ycol = xcol + 64;
-      // descriptors: the address is their low 14 bits, in units of 16 bytes
-      const uint64_t kq = desc_k_sw128(st + L::kKqAt, 0), tt = desc_k_sw128(st + kT, 0),
-                     pp = desc_k_sw128(st + kP, 0), km = desc_mn_sw128(st + L::kKqAt, 0, 2 * L::kRows);
-      if (!wait(&full[b], (c / 2) & 1)) break;
-      // X and Y, half of each warpgroup's channels at a time
-#pragma unroll
-      for (uint32_t part_of = 0; part_of < 2; ++part_of) {
-        if (!wait(&sp[part_of], ph)) break;
-#pragma unroll
-        for (uint32_t half = 0; half < 2; ++half)
-#pragma unroll
-          for (uint32_t i = 0; i < kSteps / 4; ++i)
-#pragma unroll
-            for (uint32_t k = 0; k < 3; ++k) {
-              const uint32_t s = half * (kSteps / 2) + part_of * (kSteps / 4) + i;
-              mma_ts_if(lead, xcol, tmem + L::s_col(s, k), kq + (((s >> 2) * 2 * L::kRows + (s & 3) * 32) >> 4),
-                     idesc_xy, part_of + half + i + k > 0);
-            }
-      }
-      if (!ok) break;
-      mma_commit_if(lead, &xy_done);
-      // U: tokens 16 s .. of V - a X against T's columns
-      if (!wait(&v_ready, ph)) break;
+    auto len_of = [&](int c) { return min(kC, t1 - t0 - c * kC); };
+    // V T of chunk c: the beginning of its U
+    auto v_products = [&](int c) {
+      const uint32_t st = smem_u32(stages + (c & 1) * L::kStage);
+      const uint64_t vv = desc_mn_sw128(st + L::kVAt, 0, L::kRows), tt = desc_k_sw128(st + kT, 0);
 #pragma unroll
       for (uint32_t s = 0; s < 4; ++s)
 #pragma unroll
         for (uint32_t j = 0; j < 3; ++j)
+          mma_ss_if(lead, tmem + kXuCol + (c & 1) * 64, vv + (s * 2048 >> 4), tt + ((j * kTile + s * 32) >> 4),
+                    idesc_v, s + j > 0);
+    };
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c & 1, ph = c & 1;
+      const uint32_t st = smem_u32(stages + b * L::kStage);
+      const uint32_t ucol = tmem + kXuCol + (c & 1) * 64, xcol = tmem + kXuCol + (1 - (c & 1)) * 64,
+                     ycol = tmem + kYCol + (c & 1) * 64;
+      // descriptors: the address is their low 14 bits, in units of 16 bytes
+      const uint64_t kk = desc_k_sw128(st + L::kKAt, 0), qq = desc_k_sw128(st + L::kQAt, 0),
+                     tt = desc_k_sw128(st + kT, 0), pp = desc_k_sw128(st + kP, 0),
+                     km = desc_mn_sw128(st + L::kKAt, 0, L::kRows);
+      if (!wait(&full[b], (c / 2) & 1)) break;
+      if (c == 0 && len_of(0) == kC) v_products(0);
+      // X, 16 channels of each warpgroup at a time
 #pragma unroll
-          for (uint32_t k = 0; k < 3 - j; ++k)
-            mma_ts_if(lead, xcol, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4), idesc, s + j + k > 0);
+      for (uint32_t i = 0; i < L::kSub; ++i) {
+        if (!wait(&s_ready[i], ph)) break;
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half)
+#pragma unroll
+          for (uint32_t k = 0; k < 3; ++k) {
+            const uint32_t s = half * L::kSub + i;
+            mma_ts_if(lead, xcol, tmem + L::s_col(s, k), kk + (((s >> 2) * L::kRows + (s & 3) * 32) >> 4),
+                      idesc, i + half + k > 0);
+          }
+      }
+      if (!ok) break;
+      mma_commit_if(lead, &x_done);
+#pragma unroll
+      for (uint32_t s = 0; s < L::kSteps; ++s)
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k)
+          mma_ts_if(lead, ycol, tmem + L::s_col(s, k), qq + (((s >> 2) * L::kRows + (s & 3) * 32) >> 4),
+                    idesc, s + k > 0);
+      mma_commit_if(lead, &y_done);
+      // in a chunk that is not full V's last rows are cleared by the time S is handed over
+      if (len_of(c) < kC) v_products(c);
+      // U: tokens 16 s .. of -a X against T's columns
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) {
+        if (!wait(&v_ready[i], ph)) break;
+#pragma unroll
+        for (uint32_t s = i; s < 4; s += 2)
+#pragma unroll
+          for (uint32_t j = 0; j < 3; ++j)
+#pragma unroll
+            for (uint32_t k = 0; k < 3 - j; ++k)
+              mma_ts_if(lead, ucol, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4), idesc, 1);
+      }
+      if (!ok) break;
       mma_commit_if(lead, &u_done);
+      if (c + 1 < chunks && len_of(c + 1) == kC) {
+        if (!wait(&full[b ^ 1], ((c + 1) / 2) & 1)) break;
+        v_products(c + 1);
+      }
       // the update: ku U against K, tokens contracted
-      if (!wait(&ku_ready, ph)) break;
 #pragma unroll
-      for (uint32_t s = 0; s < 4; ++s)
+      for (uint32_t i = 0; i < 2; ++i) {
+        if (!wait(&ku_ready[i], ph)) break;
 #pragma unroll
-        for (uint32_t k = 0; k < 3; ++k)
-          mma_ts_if(lead, tmem, tmem + v_col(s, k), km + (s * 2048 >> 4), idesc_d, s + k > 0);
+        for (uint32_t s = i; s < 4; s += 2)
+#pragma unroll
+          for (uint32_t k = 0; k < 3; ++k)
+            mma_ts_if(lead, tmem, tmem + v_col(s, k), km + (s * 2048 >> 4), idesc_d, s + k > 0);
+      }
+      if (!ok) break;
       mma_commit_if(lead, &d_done);
-      // P U onto b Y
-      if (!wait(&y_scaled, ph) || !wait(&u_ready, ph)) break;
+      // P U onto b Y, behind the update: S waits for that
+      if (!wait(&y_scaled, ph) || !wait(&u_ready, ph) || !wait(&d_done, ph)) break;
 #pragma unroll
       for (uint32_t s = 0; s < 4; ++s)
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j)
 #pragma unroll
           for (uint32_t k = 0; k < 2 - j; ++k)
-            mma_ts_if(lead, ycol, xcol + (s >> 1) * 32 + k * 16 + (s & 1) * 8, pp + ((j * kTile + s * 32) >> 4),
-                   idesc, 1);
+            mma_ts_if(lead, ycol, ucol + (s >> 1) * 32 + k * 16 + (s & 1) * 8, pp + ((j * kTile + s * 32) >> 4),
+                      idesc, 1);
       mma_commit_if(lead, &o_done);
       mma_commit_if(lead, &empty[b]);
     }
     // products in flight end before shared memory and TMEM are released
     mma_commit_if(lead, &drained);
     mbar_wait(&drained, 0, kGdrSpins);
+  } else if (warp == kWarpStore) {
+    // o from shared memory: boxes of 64 channels, or row by row in a last chunk that is not full
+    // (what follows its rows is another sequence's)
+    const uint8_t* so = stages + L::kOAt;
+    for (int c = 0; c < chunks && ok; ++c) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_ready, c & 1, kGdrSpins));
+      if (!ok) break;
+      const int row = t0 + c * kC;
+      if (row + kC <= t1) {
+        if (lane < 2) tma_store_3d(&t.tm_o, so + lane * L::kRows, slice * (int)kDv + lane * 64, h, row);
+      } else {
+        for (int r = lane; row + r < t1; r += 32) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(row + r) * a.Hv + h) * a.dv + slice * kDv;
+          bulk_s2g(o, so + r * 128, 128);
+          bulk_s2g(o + 64, so + L::kRows + r * 128, 128);
+        }
+      }
+      bulk_commit();
+      bulk_wait_read();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free);
+    }
+    bulk_wait_all();
   } else if (warp < kStateWarps) {
     const int quarter = warp & 3, half = warp >> 2;
     const int dv = quarter * 32 + lane;  // this thread's row of S^T
@@ -229,11 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
 #pragma unroll
     for (uint32_t i = 0; i < L::kHalf; ++i) S[i] = a.S0 ? a.S0[mat + (size_t)i * a.dv] : 0.f;
     float eG = 1.f;
-    // A wait that gave up: the warp goes on without waiting, so that it meets the others at the
-    // named barriers, and stores nothing more to global memory.
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
       fence_after_sync();
+      return ok;
     };
     // S <- e^{g_C} S + the update's product
     auto update = [&] {
@@ -246,98 +307,74 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         for (uint32_t j = 0; j < 32; ++j) S[i + j] = fmaf(eG, S[i + j], __uint_as_float(r[j]));
       }
     };
-    // o of chunk c, this warpgroup's 32 tokens, through shared memory: two boxes of 64 channels,
-    // or row by row where the sequence ends among them (what follows is another's)
-    uint8_t* so = stages + L::kOAt + half * 2 * 4096;
+    // o of chunk c, this warpgroup's 32 tokens, into shared memory
     auto write_o = [&](int c) {
+      if (!wait(&o_done, c & 1) || (c > 0 && !wait(&o_free, (c - 1) & 1))) return;
       uint32_t r[32];
-      tmem_ld32(lanes + kXyCol + (c & 1) * 128 + 64 + half * 32, r);
-      if (quarter == 0) bulk_wait_read();  // the rows before have left
-      named_sync(1 + half, 128);
+      tmem_ld32(lanes + kYCol + (c & 1) * 64 + half * 32, r);
       tmem_wait_ld();
-      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(so + (dv >> 6) * 4096) + (dv & 63);
+      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(stages + L::kOAt + (dv >> 6) * L::kRows) +
+                          half * 32 * 64 + (dv & 63);
 #pragma unroll
       for (int i = 0; i < 32; ++i) to[i * 64] = __float2bfloat16_rn(__uint_as_float(r[i]));
       fence_proxy_async();
-      named_sync(1 + half, 128);
-      const int row = t0 + c * kC + half * 32;
-      if (quarter == 0 && ok) {
-        if (row + 32 <= t1) {
-          if (lane < 2) tma_store_3d(&t.tm_o, so + lane * 4096, slice * (int)kDv + lane * 64, h, row);
-        } else if (row + lane < t1) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(row + lane) * a.Hv + h) * a.dv + slice * kDv;
-          bulk_s2g(o, so + lane * 128, 128);
-          bulk_s2g(o + 64, so + 4096 + lane * 128, 128);
-        }
-        bulk_commit();
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_ready);
     };
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, ph = c & 1;
       uint8_t* st = stages + b * L::kStage;
       const float* vec = reinterpret_cast<const float*>(st + kVec) + half * 32;
       const int len = min(kC, t1 - t0 - c * kC);
-      // V, and zeros behind the last token: there the rows are the next sequence's (the products
-      // see them behind the hand-over below)
-      wait(&full[b], (c / 2) & 1);
-      uint32_t vp[16];
-      {
-        const uint16_t* vs = reinterpret_cast<const uint16_t*>(st + L::kVAt + (dv >> 6) * L::kRows) +
-                             half * 32 * 64 + (dv & 63);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const uint32_t lo = half * 32 + i < len ? vs[i * 64] : 0, hi = half * 32 + i + 1 < len ? vs[i * 64 + 64] : 0;
-          vp[i / 2] = lo | hi << 16;
-        }
-      }
       if (len < kC) {
-        for (int i = threadIdx.x; i < (kC - len) * 8 * (DK / 64) * 2; i += kStateWarps * 32) {
-          const int tile = i / ((kC - len) * 8), j = i % ((kC - len) * 8);
-          *reinterpret_cast<uint4*>(st + L::kKqAt + tile * L::kRows + (len + (j >> 3)) * 128 + (j & 7) * 16) =
+        // rows behind the last token are the next sequence's: zeros in their place, which the
+        // products see behind the hand-over below
+        if (!wait(&full[b], (c / 2) & 1)) break;
+        for (int i = threadIdx.x; i < (kC - len) * 8 * (2 * DK / 64 + 2); i += kStateWarps * 32) {
+          const int tile = i / ((kC - len) * 8), j = i % ((kC - len) * 8);  // of K, Q and V
+          *reinterpret_cast<uint4*>(st + L::kKAt + tile * L::kRows + (len + (j >> 3)) * 128 + (j & 7) * 16) =
               make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
       }
-      // S as parts, in two halves so that the products start on the first; the update's whole
-      // product is read before the parts take its place
+      // the update's whole product is read before the parts take its place
       if (c > 0) {
-        wait(&d_done, (c - 1) & 1);
+        if (!wait(&d_done, (c - 1) & 1)) break;
         update();
       }
 #pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        store_parts3<L::kHalf / 4>(lanes + half * 2 * L::kPart + i * (L::kPart / 2),
-                                   lanes + half * 2 * L::kPart + L::kPart + i * (L::kPart / 2),
-                                   lanes + L::kThird + half * L::kPart + i * (L::kPart / 2),
-                                   &S[i * L::kHalf / 2]);
-        hand_over(&sp[i], lane);
+      for (uint32_t i = 0; i < L::kSub; ++i) {
+        const uint32_t at = lanes + half * 2 * L::kPart + i * 8;
+        store_parts3<8>(at, at + L::kPart, lanes + L::kThird + half * L::kPart + i * 8, &S[i * 16]);
+        hand_over(&s_ready[i], lane);
       }
-      if (c > 0) {
-        wait(&o_done, (c - 1) & 1);
-        write_o(c - 1);
-      }
-      // V - a X
-      wait(&xy_done, ph);
-      float v[32];
+      if (c > 0) write_o(c - 1);
+      // -a X, 16 tokens at a time
+      const uint32_t w0 = lanes + kVCol + half * 32, w2 = lanes + kVCol2 + half * 16;
+      if (!wait(&full[b], (c / 2) & 1) || !wait(&x_done, ph)) break;
       {
         uint32_t r[32];
-        tmem_ld32(lanes + kXyCol + (c & 1) * 128 + half * 32, r);
+        tmem_ld32(lanes + kXuCol + (1 - (c & 1)) * 64 + half * 32, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 va = *reinterpret_cast<const float4*>(vec + i);
-          v[i] = fmaf(-va.x, __uint_as_float(r[i]), __uint_as_float(vp[i / 2] << 16));
-          v[i + 1] = fmaf(-va.y, __uint_as_float(r[i + 1]), __uint_as_float(vp[i / 2] & 0xffff0000u));
-          v[i + 2] = fmaf(-va.z, __uint_as_float(r[i + 2]), __uint_as_float(vp[i / 2 + 1] << 16));
-          v[i + 3] = fmaf(-va.w, __uint_as_float(r[i + 3]), __uint_as_float(vp[i / 2 + 1] & 0xffff0000u));
+        for (int j = 0; j < 2; ++j) {
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 va = *reinterpret_cast<const float4*>(vec + j * 16 + i);
+            v[i] = -va.x * __uint_as_float(r[j * 16 + i]);
+            v[i + 1] = -va.y * __uint_as_float(r[j * 16 + i + 1]);
+            v[i + 2] = -va.z * __uint_as_float(r[j * 16 + i + 2]);
+            v[i + 3] = -va.w * __uint_as_float(r[j * 16 + i + 3]);
+          }
+          store_parts3<8>(w0 + j * 8, w0 + 16 + j * 8, w2 + j * 8, v);
+          hand_over(&v_ready[j], lane);
         }
       }
-      const uint32_t w0 = lanes + kVCol + half * 32, w2 = lanes + kVCol2 + half * 16;
-      store_parts3<16>(w0, w0 + 16, w2, v);
-      hand_over(&v_ready, lane);
       // b Y
+      if (!wait(&y_done, ph)) break;
       {
-        const uint32_t ycol = lanes + kXyCol + (c & 1) * 128 + 64 + half * 32;
+        const uint32_t ycol = lanes + kYCol + (c & 1) * 64 + half * 32;
         uint32_t r[32];
         tmem_ld32(ycol, r);
         tmem_wait_ld();
@@ -352,24 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         tmem_st32(ycol, r);
         hand_over(&y_scaled, lane);
       }
-      // ku U and U
-      wait(&u_done, ph);
+      // ku U, then U
+      if (!wait(&u_done, ph)) break;
       {
-        const uint32_t ucol = lanes + kXyCol + (c & 1) * 128 + half * 32;
+        const uint32_t ucol = lanes + kXuCol + (c & 1) * 64 + half * 32;
         uint32_t r[32];
         tmem_ld32(ucol, r);
         tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 ku = *reinterpret_cast<const float4*>(vec + 128 + i);
-          v[i] = ku.x * __uint_as_float(r[i]);
-          v[i + 1] = ku.y * __uint_as_float(r[i + 1]);
-          v[i + 2] = ku.z * __uint_as_float(r[i + 2]);
-          v[i + 3] = ku.w * __uint_as_float(r[i + 3]);
-        }
         eG = vec[192 - half * 32];
-        store_parts3<16>(w0, w0 + 16, w2, v);
-        hand_over(&ku_ready, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 ku = *reinterpret_cast<const float4*>(vec + 128 + j * 16 + i);
+            v[i] = ku.x * __uint_as_float(r[j * 16 + i]);
+            v[i + 1] = ku.y * __uint_as_float(r[j * 16 + i + 1]);
+            v[i + 2] = ku.z * __uint_as_float(r[j * 16 + i + 2]);
+            v[i + 3] = ku.w * __uint_as_float(r[j * 16 + i + 3]);
+          }
+          store_parts3<8>(w0 + j * 8, w0 + 16 + j * 8, w2 + j * 8, v);
+          hand_over(&ku_ready[j], lane);
+        }
         uint32_t p[2][16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -383,12 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         hand_over(&u_ready, lane);
       }
     }
-    if (chunks > 0) {
-      wait(&d_done, (chunks - 1) & 1);
+    if (ok && chunks > 0 && wait(&d_done, (chunks - 1) & 1)) {
       update();
-      wait(&o_done, (chunks - 1) & 1);
       write_o(chunks - 1);
-      if (quarter == 0) bulk_wait_all();
     }
     if (ok) {
 #pragma unroll
@@ -447,8 +485,8 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   t.ws = ws;
   if (!encode(&t.tm_k, a.k, a.T_total, a.Hk, DK, a.ldk, kC, true) ||
       !encode(&t.tm_q, a.q, a.T_total, a.Hk, DK, a.ldq, kC, true) ||
-      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, kC, false) ||
-      !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, 32, false))
+      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, kC, true) ||
+      !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, kC, false))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (int)kDv);
   gdr_chain_tc_kernel<DK><<<grid, kThreads, Layout<DK>::kSmem, s>>>(t);

@@ -40,24 +40,24 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[kParts]) 
   p[kParts - 1] = umma::pack_bf162(x, y);
 }
 
-// The same for three parts, the middle one cut to 8 bits by r' = (c r) - (c r - r), c = 2^16 + 1
-// (Veltkamp), as packed fp32 operations: conversions and integer operations run at half the
-// rate of fp32 multiplications and additions.
+// The same for three parts, by cutting instead of rounding: 8 + 8 + 8 bits hold all of fp32's 24,
+// so the sum of the parts is exact.
 __device__ __forceinline__ unsigned long long f2(float x, float y) {
   return ((unsigned long long)__float_as_uint(y) << 32) | __float_as_uint(x);
 }
 __device__ __forceinline__ void split3(float x, float y, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-  const unsigned long long kMinus = f2(-1.f, -1.f), kC16 = f2(65537.f, 65537.f);
-  unsigned long long r = f2(x, y), t, h;
-  p0 = umma::pack_bf162(x, y);
-  h = f2(__uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u));
+  const unsigned long long kMinus = f2(-1.f, -1.f);
+  const uint32_t m = 0xffff0000u;
+  uint32_t xi = __float_as_uint(x), yi = __float_as_uint(y);
+  unsigned long long r = f2(x, y), h;
+  p0 = __byte_perm(xi, yi, 0x7632);
+  h = ((unsigned long long)(yi & m) << 32) | (xi & m);
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(h), "l"(kMinus));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(r), "l"(kC16));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(h) : "l"(r), "l"(kMinus), "l"(t));
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(h) : "l"(kMinus), "l"(t));
-  p1 = __byte_perm((uint32_t)h, (uint32_t)(h >> 32), 0x7632);
+  xi = (uint32_t)r; yi = (uint32_t)(r >> 32);
+  p1 = __byte_perm(xi, yi, 0x7632);
+  h = ((unsigned long long)(yi & m) << 32) | (xi & m);
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(h), "l"(kMinus));
-  p2 = umma::pack_bf162(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
+  p2 = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
 }
 
 // The walk over the chunks on tcgen05: d_k in {64, 128}, d_v a multiple of 128.
