@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     constexpr uint32_t idesc = idesc_f16(128, 64, true), idesc_v = idesc_f16(128, 64, true, true),
                        idesc_d = idesc_f16(128, DK, true, false, true);
     auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, kGdrSpins));
       fence_after_sync();
       return ok;
     };
@@ -171,12 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       const uint32_t st = smem_u32(stages + (c & 1) * L::kStage);
       const uint64_t vv = desc_mn_sw128(st + L::kVAt, 0, L::kRows), tt = desc_k_sw128(st + kT, 0);
 #pragma unroll
-      for (uint32_t s = 0; s < 4; ++s)
+      for (uint32_t j = 2; j < 3; --j)
 #pragma unroll
-        for (uint32_t j = 0; j < 3; ++j)
+        for (uint32_t s = 0; s < 4; ++s)
           mma_ss_if(lead, tmem + kXuCol + (c & 1) * 64, vv + (s * 2048 >> 4), tt + ((j * kTile + s * 32) >> 4),
-                    idesc_v, s + j > 0);
+                    idesc_v, s + 2 - j > 0);
     };
+    // Sums are cut, not rounded, as products are added: those of the smaller parts go first, while
+    // a sum is small.
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, ph = c & 1;
       const uint32_t st = smem_u32(stages + b * L::kStage);
@@ -193,22 +195,23 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (uint32_t i = 0; i < L::kSub; ++i) {
         if (!wait(&s_ready[i], ph)) break;
 #pragma unroll
-        for (uint32_t half = 0; half < 2; ++half)
+        for (uint32_t k = 2; k < 3; --k)
 #pragma unroll
-          for (uint32_t k = 0; k < 3; ++k) {
+          for (uint32_t half = 0; half < 2; ++half) {
             const uint32_t s = half * L::kSub + i;
             mma_ts_if(lead, xcol, tmem + L::s_col(s, k), kk + (((s >> 2) * L::kRows + (s & 3) * 32) >> 4),
-                      idesc, i + half + k > 0);
+                      idesc, i + half + 2 - k > 0);
           }
       }
       if (!ok) break;
       mma_commit_if(lead, &x_done);
+      if (!wait(&x_done, ph)) break;
 #pragma unroll
-      for (uint32_t s = 0; s < L::kSteps; ++s)
+      for (uint32_t k = 1; k < 2; --k)
 #pragma unroll
-        for (uint32_t k = 0; k < 2; ++k)
+        for (uint32_t s = 0; s < L::kSteps; ++s)
           mma_ts_if(lead, ycol, tmem + L::s_col(s, k), qq + (((s >> 2) * L::kRows + (s & 3) * 32) >> 4),
-                    idesc, s + k > 0);
+                    idesc, s + 1 - k > 0);
       mma_commit_if(lead, &y_done);
       // in a chunk that is not full V's last rows are cleared by the time S is handed over
       if (len_of(c) < kC) v_products(c);
@@ -217,11 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (uint32_t i = 0; i < 2; ++i) {
         if (!wait(&v_ready[i], ph)) break;
 #pragma unroll
-        for (uint32_t s = i; s < 4; s += 2)
+        for (uint32_t order = 2; order < 3; --order)
 #pragma unroll
-          for (uint32_t j = 0; j < 3; ++j)
+          for (uint32_t j = 0; j <= order; ++j)
 #pragma unroll
-            for (uint32_t k = 0; k < 3 - j; ++k)
+            for (uint32_t s = i, k = order - j; s < 4; s += 2)
               mma_ts_if(lead, ucol, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4), idesc, 1);
       }
       if (!ok) break;
@@ -235,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (uint32_t i = 0; i < 2; ++i) {
         if (!wait(&ku_ready[i], ph)) break;
 #pragma unroll
-        for (uint32_t s = i; s < 4; s += 2)
+        for (uint32_t k = 2; k < 3; --k)
 #pragma unroll
-          for (uint32_t k = 0; k < 3; ++k)
-            mma_ts_if(lead, tmem, tmem + v_col(s, k), km + (s * 2048 >> 4), idesc_d, s + k > 0);
+          for (uint32_t s = i; s < 4; s += 2)
+            mma_ts_if(lead, tmem, tmem + v_col(s, k), km + (s * 2048 >> 4), idesc_d, s + 2 - k > 0);
       }
       if (!ok) break;
       mma_commit_if(lead, &d_done);
@@ -259,20 +262,21 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     mma_commit_if(lead, &drained);
     mbar_wait(&drained, 0, kGdrSpins);
   } else if (warp == kWarpStore) {
-    // o from shared memory: boxes of 64 channels, or row by row in a last chunk that is not full
-    // (what follows its rows is another sequence's)
+    // o from shared memory: boxes of 64 channels, or by plain stores in a last chunk that is not
+    // full (what follows its rows is another sequence's)
     const uint8_t* so = stages + L::kOAt;
     for (int c = 0; c < chunks && ok; ++c) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_ready, c & 1, kGdrSpins));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&o_ready, c & 1, kGdrSpins));
       if (!ok) break;
       const int row = t0 + c * kC;
       if (row + kC <= t1) {
         if (lane < 2) tma_store_3d(&t.tm_o, so + lane * L::kRows, slice * (int)kDv + lane * 64, h, row);
       } else {
-        for (int r = lane; row + r < t1; r += 32) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(row + r) * a.Hv + h) * a.dv + slice * kDv;
-          bulk_s2g(o, so + r * 128, 128);
-          bulk_s2g(o + 64, so + L::kRows + r * 128, 128);
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((size_t)row * a.Hv + h) * a.dv + slice * kDv;
+        for (int i = lane; i < (t1 - row) * 16; i += 32) {  // 16-byte groups
+          const int r = i >> 4, g = i & 15;
+          *reinterpret_cast<uint4*>(o + (size_t)r * a.Hv * a.dv + g * 8) =
+              *reinterpret_cast<const uint4*>(so + (g >> 3) * L::kRows + r * 128 + (((g ^ r) & 7) << 4));
         }
       }
       bulk_commit();
@@ -292,31 +296,43 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     for (uint32_t i = 0; i < L::kHalf; ++i) S[i] = a.S0 ? a.S0[mat + (size_t)i * a.dv] : 0.f;
     float eG = 1.f;
     auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, kGdrSpins));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, kGdrSpins));
       fence_after_sync();
       return ok;
     };
     // S <- e^{g_C} S + the update's product
     auto update = [&] {
+      uint32_t r[L::kHalf / 32][32];
 #pragma unroll
-      for (uint32_t i = 0; i < L::kHalf; i += 32) {
-        uint32_t r[32];
-        tmem_ld32(lanes + half * L::kHalf + i, r);
-        tmem_wait_ld();
+      for (uint32_t i = 0; i < L::kHalf / 32; ++i) tmem_ld32(lanes + half * L::kHalf + i * 32, r[i]);
+      tmem_wait_ld();
 #pragma unroll
-        for (uint32_t j = 0; j < 32; ++j) S[i + j] = fmaf(eG, S[i + j], __uint_as_float(r[j]));
-      }
+      for (uint32_t i = 0; i < L::kHalf; ++i) S[i] = fmaf(eG, S[i], __uint_as_float(r[i / 32][i % 32]));
     };
-    // o of chunk c, this warpgroup's 32 tokens, into shared memory
+    // o of chunk c, this warpgroup's 32 tokens: 8 x 8 tiles transposed into rows of tokens
     auto write_o = [&](int c) {
       if (!wait(&o_done, c & 1) || (c > 0 && !wait(&o_free, (c - 1) & 1))) return;
-      uint32_t r[32];
-      tmem_ld32(lanes + kYCol + (c & 1) * 64 + half * 32, r);
-      tmem_wait_ld();
-      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(stages + L::kOAt + (dv >> 6) * L::kRows) +
-                          half * 32 * 64 + (dv & 63);
+      uint32_t r[2][16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) to[i * 64] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      for (int h16 = 0; h16 < 2; ++h16)
+        tmem_ld_frag4(taddr(lanes, h16 * 16, kYCol + (c & 1) * 64 + half * 32), r[h16]);
+      tmem_wait_ld();
+      const uint32_t row = half * 32 + (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+      for (int h16 = 0; h16 < 2; ++h16) {
+        const uint32_t group = quarter * 4 + h16 * 2 + ((lane >> 3) & 1);  // of 8 channels
+        const uint32_t at = smem_u32(stages + L::kOAt) + (group >> 3) * L::kRows + row * 128 +
+                            (((group ^ row) & 7) << 4);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t* x = &r[h16][p * 8];
+          const uint32_t m[4] = {pack_bf162(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                 pack_bf162(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                 pack_bf162(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                                 pack_bf162(__uint_as_float(x[6]), __uint_as_float(x[7]))};
+          stsm4t(at + p * 16 * 128, m);
+        }
+      }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_ready);
@@ -326,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       uint8_t* st = stages + b * L::kStage;
       const float* vec = reinterpret_cast<const float*>(st + kVec) + half * 32;
       const int len = min(kC, t1 - t0 - c * kC);
+      if (!wait(&full[b], (c / 2) & 1)) break;
       if (len < kC) {
         // rows behind the last token are the next sequence's: zeros in their place, which the
         // products see behind the hand-over below
-        if (!wait(&full[b], (c / 2) & 1)) break;
         for (int i = threadIdx.x; i < (kC - len) * 8 * (2 * DK / 64 + 2); i += kStateWarps * 32) {
           const int tile = i / ((kC - len) * 8), j = i % ((kC - len) * 8);  // of K, Q and V
           *reinterpret_cast<uint4*>(st + L::kKAt + tile * L::kRows + (len + (j >> 3)) * 128 + (j & 7) * 16) =
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       if (c > 0) write_o(c - 1);
       // -a X, 16 tokens at a time
       const uint32_t w0 = lanes + kVCol + half * 32, w2 = lanes + kVCol2 + half * 16;
-      if (!wait(&full[b], (c / 2) & 1) || !wait(&x_done, ph)) break;
+      if (!wait(&x_done, ph)) break;
       {
         uint32_t r[32];
         tmem_ld32(lanes + kXuCol + (1 - (c & 1)) * 64 + half * 32, r);
@@ -461,8 +477,7 @@ EncodeTiledFn encode_tiled() {
 
 // Tensor map of [T][H][d] bf16 rows, tokens ld elements apart: boxes of 64 channels of one head
 // by `rows` tokens.
-bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld, int rows,
-            bool swizzle) {
+bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld, int rows) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
@@ -471,7 +486,7 @@ bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld,
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -483,10 +498,10 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   Chain t;
   t.a = a;
   t.ws = ws;
-  if (!encode(&t.tm_k, a.k, a.T_total, a.Hk, DK, a.ldk, kC, true) ||
-      !encode(&t.tm_q, a.q, a.T_total, a.Hk, DK, a.ldq, kC, true) ||
-      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, kC, true) ||
-      !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, kC, false))
+  if (!encode(&t.tm_k, a.k, a.T_total, a.Hk, DK, a.ldk, kC) ||
+      !encode(&t.tm_q, a.q, a.T_total, a.Hk, DK, a.ldq, kC) ||
+      !encode(&t.tm_v, a.v, a.T_total, a.Hv, a.dv, a.ldv, kC) ||
+      !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, kC))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (int)kDv);
   gdr_chain_tc_kernel<DK><<<grid, kThreads, Layout<DK>::kSmem, s>>>(t);
