@@ -245,8 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       }
       if (!ok) break;
       mma_commit_if(lead, &d_done);
-      // P U onto b Y, behind the update: S waits for that
-      if (!wait(&y_scaled, ph) || !wait(&u_ready, ph) || !wait(&d_done, ph)) break;
+      // P U onto b Y, behind the update: S waits for that.  When it is done the place of o in
+      // shared memory is free too: the warps that write it wait for the one only.
+      if (!wait(&y_scaled, ph) || !wait(&u_ready, ph)) break;
+      if (c > 0 && !wait(&o_free, (c - 1) & 1)) break;
+      if (!wait(&d_done, ph)) break;
 #pragma unroll
       for (uint32_t s = 0; s < 4; ++s)
 #pragma unroll
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
     };
     // o of chunk c, this warpgroup's 32 tokens: 8 x 8 tiles transposed into rows of tokens
     auto write_o = [&](int c) {
-      if (!wait(&o_done, c & 1) || (c > 0 && !wait(&o_free, (c - 1) & 1))) return;
+      if (!wait(&o_done, c & 1)) return;
       uint32_t r[2][16];
 #pragma unroll
       for (int h16 = 0; h16 < 2; ++h16)
