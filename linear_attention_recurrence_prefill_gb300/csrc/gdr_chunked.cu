@@ -35,6 +35,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 // c += a b: a 16 x 16 (rows g = lane / 4 and g + 8), b 16 x 8, bf16, fp32 sums
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
@@ -51,23 +55,41 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
                                         uint32_t (&p)[kParts][4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t w[kParts];
-    split2<kParts>((i < 2 ? c0 : c1)[2 * (i & 1)], (i < 2 ? c0 : c1)[2 * (i & 1) + 1], w);
+    const float x = (i < 2 ? c0 : c1)[2 * (i & 1)], y = (i < 2 ? c0 : c1)[2 * (i & 1) + 1];
+    if constexpr (kParts == 3) {
+      split3(x, y, p[0][i], p[1][i], p[2][i]);
+    } else {
+      uint32_t w[kParts];
+      split2<kParts>(x, y, w);
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) p[k][i] = w[k];
+      for (int k = 0; k < kParts; ++k) p[k][i] = w[k];
+    }
   }
 }
 
 // ------------------------------------------------------------------ prep
-// One CTA per (chunk, query / key head): the two Grams once, then for each value head its
-// decays, A, P and the inverse of I + A:
-//   the four 16 x 16 diagonal blocks by forward substitution (a warp each, a lane per column),
-//   then twice [X00 0; X10 X11] with X10 = -X11 (A10 X00), from 16 to 32 and from 32 to 64,
-// all in fp32.  The operands are laid out in shared memory as the chain reads them and leave by
-// bulk copies.
+// One CTA per (chunk, query / key head).  All four warps form the two Grams, K K^T and Q K^T, in
+// fp32 in shared memory.  Then, value head by value head, two warps invert I + A and two write P
+// and the vectors; the pairs do not wait for each other.
+//
+// The inverse X, in 16 x 16 blocks: the diagonal ones by forward substitution (a lane per
+// column), then column by column X_ij = -X_ii sum_k A_ik X_kj on the tensor cores, transposed, so
+// that each result is the A operand of the next product as it lies:
+//     tmp^T = sum_k X_kj^T A_ik^T,   X_ij^T = -tmp^T X_ii^T,
+// every operand in three bf16 parts (fp32's 24 bits).  One warp takes column 0, the other 1 and 2.
+//
+// e^{g_i - g_j} off the diagonal blocks is e^{g_i - g_r} e^{g_r - g_j}, r the first row of i's
+// block: both exponents are <= 0, and the factors are vectors.
 constexpr int kPrepThreads = 128;
-constexpr int kPitchA = kC + 4;  // floats
-constexpr int kScan = 4;         // heads whose decays are summed up at once, one per warp
+constexpr int kPitchG = kC + 4;          // floats, Grams
+constexpr int kPitchD = 20, kDiag = 324;  // floats, diagonal blocks and from one to the next
+constexpr int kScan = 4;                 // heads whose decays are prepared at once, one per warp
+
+struct PrepHead {
+  float ghi[kC], glo[kC], beta[kC];
+  float e1[kC];      // e^{g_i - g_r}
+  float e2[3][kC];   // row block 1 + x: e^{g_r - g_j} ik_j, j < 16 (1 + x)
+};
 
 template <int DK>
 struct PrepSmem {
@@ -77,18 +99,122 @@ struct PrepSmem {
       __nv_bfloat16 k[kC * kPitch / 2], q[kC * kPitch / 2];
     };
     struct {
-      float A[kC][kPitchA], X[kC][kPitchA];  // behind the Grams
+      float kk[kC][kPitchG], qk[kC][kPitchG];
     };
   };
-  // staging: T's first two parts take A's place, the rest of the block lies here
-  alignas(16) uint8_t rest[kBlock - 2 * kTile];
+  float diag[4 * kDiag];           // A's diagonal blocks, then their inverses
+  alignas(16) uint8_t out[4][512];  // a 16 x 16 block of bf16 per warp
+  PrepHead head[kScan];
   float ik[kC], iq[kC];
-  float ghi[kScan][kC], glo[kScan][kC], beta[kScan][kC];
   int n, t0, t1;
 };
 
+// A 16 x 16 block of bf16 from 8 x 8 tiles w (kTrans: of its transpose) to the rows of a tile in
+// global memory, 32 bytes each: through shared memory, 16 bytes per lane.
+template <bool kTrans>
+__device__ __forceinline__ void store_block(uint8_t* tile, int row0, int col0, uint8_t* buf, int lane,
+                                            const uint32_t (&w)[4]) {
+  // lane l names row l & 7 of tile l >> 3; halves are swapped every four rows against conflicts
+  const uint32_t r = (lane & 7) + ((lane >> (kTrans ? 4 : 3)) & 1) * 8, h = (lane >> (kTrans ? 3 : 4)) & 1;
+  const uint32_t at = smem_u32(buf) + r * 32 + ((h ^ ((r >> 2) & 1)) << 4);
+  if constexpr (kTrans) stsm4t(at, w);
+  else stsm4(at, w);
+  __syncwarp();
+  const int row = lane >> 1, half = lane & 1;
+  const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
+  *reinterpret_cast<uint4*>(tile + tile_at(row0 + row, col0 + half * 8)) = v;
+  __syncwarp();
+}
+
+// One column of the inverse below its diagonal block, and T's blocks of that column.
+template <int J, int DK>
+__device__ __forceinline__ void invert_column(PrepSmem<DK>& s, const PrepHead& hd, int lane, uint8_t* buf,
+                                              uint8_t* out) {
+  const int g = lane >> 2, t = lane & 3;
+  const float b0 = hd.beta[J * 16 + g], b1 = hd.beta[J * 16 + g + 8];
+  // c: a block of X^T (rows: X's columns), as two 16 x 8 tiles; its parts as an A operand, and T's
+  auto finish = [&](const float (&c)[2][4], int i, uint32_t (&f)[3][4]) {
+    split_a<3>(c[0], c[1], f);
+    float z[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      z[x][0] = c[x][0] * b0; z[x][1] = c[x][1] * b0;
+      z[x][2] = c[x][2] * b1; z[x][3] = c[x][3] * b1;
+    }
+    uint32_t w[3][4];
+    split_a<3>(z[0], z[1], w);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) store_block<true>(out + kT + k * kTile, i * 16, J * 16, buf, lane, w[k]);
+  };
+  // six products of parts, smaller ones first
+  auto product = [&](float (&c)[2][4], const uint32_t (&f)[3][4], const uint32_t (&m)[3][4]) {
+#pragma unroll
+    for (int order = 2; order >= 0; --order)
+#pragma unroll
+      for (int j = 0; j <= order; ++j) {
+        mma(c[0], f[order - j], m[j][0], m[j][1]);
+        mma(c[1], f[order - j], m[j][2], m[j][3]);
+      }
+  };
+  uint32_t X[3][3][4];  // parts of X_kJ^T, k from J on
+  {
+    const float* d = s.diag + J * kDiag;
+    float c[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[x][e] = d[(x * 8 + t * 2 + (e & 1)) * kPitchD + g + (e >> 1) * 8];
+    finish(c, J, X[0]);
+  }
+#pragma unroll
+  for (int i = J + 1; i < 4; ++i) {
+    float c[2][4] = {};
+    // A_ik^T as B operands: rows 16 i + 8 x + g of A
+    float row[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = i * 16 + x * 8 + g;
+      row[x] = hd.beta[r] * s.ik[r] * hd.e1[r];
+    }
+#pragma unroll
+    for (int k = J; k < i; ++k) {
+      uint32_t m[3][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int col = k * 16 + y * 8 + t * 2;
+        const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[i - 1][col]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 kk = *reinterpret_cast<const float2*>(&s.kk[i * 16 + x * 8 + g][col]);
+          split3(row[x] * (e2.x * kk.x), row[x] * (e2.y * kk.y), m[0][x * 2 + y], m[1][x * 2 + y], m[2][x * 2 + y]);
+        }
+      }
+      product(c, X[k - J], m);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[x][e] = -c[x][e];
+    uint32_t f[3][4], m[3][4];
+    split_a<3>(c[0], c[1], f);
+    const float* d = s.diag + i * kDiag;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float2 v = *reinterpret_cast<const float2*>(&d[(x * 8 + g) * kPitchD + y * 8 + t * 2]);
+        split3(v.x, v.y, m[0][x * 2 + y], m[1][x * 2 + y], m[2][x * 2 + y]);
+      }
+    float z[2][4] = {};
+    product(z, f, m);
+    uint32_t last[3][4];
+    if (i < 3) finish(z, i, X[i - J]);
+    else finish(z, i, last);
+  }
+}
+
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, uint8_t* ws) {
+__global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, uint8_t* ws) {
   using Smem = PrepSmem<DK>;
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
@@ -145,6 +271,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, ui
   auto scan = [&](int h0) {
     if (h0 + warp >= G) return;
     const int h = hk * G + h0 + warp;
+    PrepHead& hd = s.head[warp];
     double g2[2];
     float be[2];
 #pragma unroll
@@ -166,15 +293,27 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, ui
     for (int i = 0; i < 2; ++i) {
       const int r = lane * 2 + i;
       const float hi = (float)g[i];
-      s.ghi[warp][r] = hi;
-      s.glo[warp][r] = (float)(g[i] - (double)hi);
-      s.beta[warp][r] = be[i];
+      hd.ghi[r] = hi;
+      hd.glo[r] = (float)(g[i] - (double)hi);
+      hd.beta[r] = be[i];
+    }
+  };
+  // the factors of e^{g_i - g_j}, when the norms are there
+  auto factors = [&](int h0) {
+    if (h0 + warp >= G) return;
+    PrepHead& hd = s.head[warp];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane + i * 32, r0 = r & ~15;
+      hd.e1[r] = expf(fminf((hd.ghi[r] - hd.ghi[r0]) + (hd.glo[r] - hd.glo[r0]), 0.f));
+#pragma unroll
+      for (int x = 1; x < 4; ++x)
+        if (r < 16 * x)
+          hd.e2[x - 1][r] = s.ik[r] * expf(fminf((hd.ghi[16 * x] - hd.ghi[r]) + (hd.glo[16 * x] - hd.glo[r]), 0.f));
     }
   };
   scan(0);
-  // the blocks of P above its diagonal stay zero
-  for (int i = tid; i < (int)sizeof(s.rest) / 16; i += kPrepThreads)
-    reinterpret_cast<uint4*>(s.rest)[i] = make_uint4(0, 0, 0, 0);
   cp_async_wait_all();
   __syncthreads();
 
@@ -207,8 +346,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, ui
   }
 
   // K K^T and Q K^T, 16 rows per warp, columns up to the diagonal block
-  float kk[8][4] = {}, qk[8][4] = {};
   {
+    float kk[8][4] = {}, qk[8][4] = {};
     const uint32_t row = warp * 16 + (lane & 15), col = (lane >> 4) * 16;
     const uint32_t ka = smem_u32(s.k) + row * Smem::kPitch + col;
     const uint32_t qa = smem_u32(s.q) + row * Smem::kPitch + col;
@@ -230,161 +369,139 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(GdrArgs a, ui
         mma(qk[2 * p + 1], fq, b[2], b[3]);
       }
     }
+    __syncthreads();  // K and Q are done with, the norms there
+    factors(0);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      if (nt > 2 * warp + 1) break;
+      const int r = warp * 16 + (lane >> 2), c = nt * 8 + (lane & 3) * 2;
+      *reinterpret_cast<float2*>(&s.kk[r][c]) = make_float2(kk[nt][0], kk[nt][1]);
+      *reinterpret_cast<float2*>(&s.kk[r + 8][c]) = make_float2(kk[nt][2], kk[nt][3]);
+      *reinterpret_cast<float2*>(&s.qk[r][c]) = make_float2(qk[nt][0], qk[nt][1]);
+      *reinterpret_cast<float2*>(&s.qk[r + 8][c]) = make_float2(qk[nt][2], qk[nt][3]);
+    }
   }
   __syncthreads();
 
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* buf = s.out[warp];
   for (int hg = 0; hg < G; ++hg) {
-    const int x = hg % kScan;
+    const PrepHead& hd = s.head[hg % kScan];
+    if (hg > 0 && hg % kScan == 0) {
+      __syncthreads();
+      scan(hg);
+      factors(hg);
+      __syncthreads();
+    }
     uint8_t* out = ws + ((size_t)blk * a.Hv + hk * G + hg) * kBlock;
-    if (hg > 0) {
-      if (tid == 0) bulk_wait_read();  // the last head's block has left shared memory
-      if (x == 0) scan(hg);
-      __syncthreads();
-    }
-    // A and P, from the Grams in registers; the vectors
+    // e^{g_i - g_j} on a diagonal block, j <= i
+    auto decay = [&](int i, int j) {
+      return expf(fminf((hd.ghi[i] - hd.ghi[j]) + (hd.glo[i] - hd.glo[j]), 0.f)) * s.ik[j];
+    };
+    if (warp < 2) {
+      named_sync(1, 64);  // both warps are done with the last head's diagonal blocks
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int i = warp * 16 + (lane >> 2) + half * 8;
-      const float gh = s.ghi[x][i], gl = s.glo[x][i], ak = s.beta[x][i] * s.ik[i], pq = s.iq[i];
+      for (int x = 0; x < 2; ++x) {
+        const int b0 = (warp * 2 + x) * 16;
+        float* d = s.diag + (warp * 2 + x) * kDiag;
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        if (nt > 2 * warp + 1) break;
-        float m[2], p[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = nt * 8 + (lane & 3) * 2 + e;
-          const float d = (gh - s.ghi[x][j]) + (gl - s.glo[x][j]);
-          const float w = j <= i ? expf(fminf(d, 0.f)) * s.ik[j] : 0.f;
-          m[e] = j < i ? ak * w * kk[nt][half * 2 + e] : 0.f;
-          p[e] = j <= i ? pq * w * qk[nt][half * 2 + e] : 0.f;
+        for (int e = 0; e < 8; ++e) {
+          const int r = g + (e >> 2) * 8, c = t * 2 + (e & 1) + ((e >> 1) & 1) * 8;
+          const int i = b0 + r, j = b0 + c;
+          d[r * kPitchD + c] = c < r ? hd.beta[i] * s.ik[i] * decay(i, j) * s.kk[i][j] : 0.f;
         }
-        const int j0 = nt * 8 + (lane & 3) * 2;
-        *reinterpret_cast<float2*>(&s.A[i][j0]) = make_float2(m[0], m[1]);
-        uint32_t w[2];
-        split2<2>(p[0], p[1], w);
-        uint8_t* dst = s.rest + (kP - 2 * kTile) + tile_at(i, j0);
-        *reinterpret_cast<uint32_t*>(dst) = w[0];
-        *reinterpret_cast<uint32_t*>(dst + kTile) = w[1];
       }
-    }
-    if (tid < kC) {
-      float* vec = reinterpret_cast<float*>(s.rest + (kVec - 2 * kTile));
-      const float gh = s.ghi[x][tid], gl = s.glo[x][tid], e = expf(gh);
-      const float Gh = s.ghi[x][kC - 1], Gl = s.glo[x][kC - 1];
-      vec[tid] = e * s.ik[tid];
-      vec[64 + tid] = e * s.iq[tid];
-      vec[128 + tid] = expf((Gh - gh) + (Gl - gl)) * s.ik[tid];
-      if (tid == 0) vec[192] = expf(Gh);
-    }
-    __syncthreads();
-
-    // diagonal blocks: column c of block `warp`, x_i = -sum_k A_ik x_k
-    if (lane < 16) {
-      const int b0 = warp * 16;
-      float v[16];
+      __syncwarp();
+      // x_i = -sum_k A_ik x_k: a half warp per block, a lane per column
+      {
+        float* d = s.diag + (warp * 2 + (lane >> 4)) * kDiag;
+        const int c = lane & 15;
+        float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float sum = i == lane ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i) v[i] = i == c ? 1.f : 0.f;
 #pragma unroll
-        for (int k = 0; k < i; ++k) sum = fmaf(-s.A[b0 + i][b0 + k], v[k], sum);
-        v[i] = sum;
-        s.X[b0 + i][b0 + lane] = sum;
+        for (int i = 1; i < 16; ++i) {
+          float A[16];
+#pragma unroll
+          for (int k = 0; k < i; k += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(&d[i * kPitchD + k]);
+            A[k] = y.x; A[k + 1] = y.y; A[k + 2] = y.z; A[k + 3] = y.w;
+          }
+          float even = 0.f, odd = 0.f;
+#pragma unroll
+          for (int k = 0; k < i; k += 2) {
+            even = fmaf(A[k], v[k], even);
+            if (k + 1 < i) odd = fmaf(A[k + 1], v[k + 1], odd);
+          }
+          v[i] -= even + odd;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i * kPitchD + c] = v[i];
       }
-    }
-    __syncthreads();
-    // 16 -> 32: blocks (1, 0) and (3, 2), 64 threads each, four columns of a row per thread;
-    // A10 X00 lies for the time being in the block above the diagonal
-    {
-      const int b0 = (tid >> 6) * 32, r = (tid >> 2) & 15, c = (tid & 3) * 4;
-      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float m = s.A[b0 + 16 + r][b0 + k];
-        const float4 y = *reinterpret_cast<const float4*>(&s.X[b0 + k][b0 + c]);
-        z.x = fmaf(m, y.x, z.x); z.y = fmaf(m, y.y, z.y);
-        z.z = fmaf(m, y.z, z.z); z.w = fmaf(m, y.w, z.w);
+      named_sync(1, 64);
+      if (warp == 0) {
+        invert_column<0, DK>(s, hd, lane, buf, out);
+        invert_column<3, DK>(s, hd, lane, buf, out);
+      } else {
+        invert_column<1, DK>(s, hd, lane, buf, out);
+        invert_column<2, DK>(s, hd, lane, buf, out);
       }
-      *reinterpret_cast<float4*>(&s.X[b0 + r][b0 + 16 + c]) = z;
-      __syncthreads();
-      z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float m = -s.X[b0 + 16 + r][b0 + 16 + k];
-        const float4 y = *reinterpret_cast<const float4*>(&s.X[b0 + k][b0 + 16 + c]);
-        z.x = fmaf(m, y.x, z.x); z.y = fmaf(m, y.y, z.y);
-        z.z = fmaf(m, y.z, z.z); z.w = fmaf(m, y.w, z.w);
-      }
-      *reinterpret_cast<float4*>(&s.X[b0 + 16 + r][b0 + c]) = z;
-    }
-    __syncthreads();
-    // 32 -> 64, eight columns of a row per thread; entries above the diagonals count as zero
-    {
-      const int r = tid >> 2, c = (tid & 3) * 8;
-      float z[8] = {};
-      auto step = [&](float m, const float* y) {
-        const float4 y0 = *reinterpret_cast<const float4*>(y);
-        const float4 y1 = *reinterpret_cast<const float4*>(y + 4);
-        z[0] = fmaf(m, y0.x, z[0]); z[1] = fmaf(m, y0.y, z[1]);
-        z[2] = fmaf(m, y0.z, z[2]); z[3] = fmaf(m, y0.w, z[3]);
-        z[4] = fmaf(m, y1.x, z[4]); z[5] = fmaf(m, y1.y, z[5]);
-        z[6] = fmaf(m, y1.z, z[6]); z[7] = fmaf(m, y1.w, z[7]);
-      };
-      if (c < 16)
-#pragma unroll 8
-        for (int k = 0; k < 16; ++k) step(s.A[32 + r][k], &s.X[k][c]);
-#pragma unroll 8
-      for (int k = 16; k < 32; ++k) step(s.A[32 + r][k], &s.X[k][c]);
-      *reinterpret_cast<float4*>(&s.X[r][32 + c]) = make_float4(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<float4*>(&s.X[r][36 + c]) = make_float4(z[4], z[5], z[6], z[7]);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < 16; ++k) step(-s.X[32 + r][32 + k], &s.X[k][32 + c]);
-      if (r >= 16)
-#pragma unroll 8
-        for (int k = 16; k < 32; ++k) step(-s.X[32 + r][32 + k], &s.X[k][32 + c]);
-      *reinterpret_cast<float4*>(&s.X[32 + r][c]) = make_float4(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<float4*>(&s.X[32 + r][c + 4]) = make_float4(z[4], z[5], z[6], z[7]);
-    }
-    __syncthreads();
-    // T = (I + A)^-1 Diag(beta) in three parts, eight columns at a time; A is done with
+    } else {
+      // P, row blocks 0 to 2 and 3; zeros above the diagonal blocks of T and P
 #pragma unroll 1
-    for (int i = tid; i < kC * 8; i += kPrepThreads) {
-      const int r = i >> 3, c = (i & 7) * 8;
-      uint4 w[3] = {};
-      if (c <= r) {
-        float v[8];
+      for (int ib = warp == 2 ? 0 : 3; ib < (warp == 2 ? 3 : 4); ++ib) {
+        float row[2];
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(&s.X[r][c + e]);
-          const float4 be = *reinterpret_cast<const float4*>(&s.beta[x][c + e]);
-          v[e] = y.x * be.x; v[e + 1] = y.y * be.y; v[e + 2] = y.z * be.z; v[e + 3] = y.w * be.w;
+        for (int x = 0; x < 2; ++x) {
+          const int r = ib * 16 + x * 8 + g;
+          row[x] = s.iq[r] * hd.e1[r];
         }
+#pragma unroll 1
+        for (int jb = 0; jb <= ib; ++jb) {
+          float c[2][4];  // tiles of columns
+          if (jb < ib) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e <= r ? v[e] : 0.f;
+            for (int y = 0; y < 2; ++y) {
+              const int col = jb * 16 + y * 8 + t * 2;
+              const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[ib - 1][col]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t p[3];
-          split2<3>(v[2 * e], v[2 * e + 1], p);
+              for (int x = 0; x < 2; ++x) {
+                const float2 qk = *reinterpret_cast<const float2*>(&s.qk[ib * 16 + x * 8 + g][col]);
+                c[y][2 * x] = row[x] * (e2.x * qk.x);
+                c[y][2 * x + 1] = row[x] * (e2.y * qk.y);
+              }
+            }
+          } else {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) (&w[k].x)[e] = p[k];
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = ib * 16 + g + (e >> 1) * 8, j = ib * 16 + y * 8 + t * 2 + (e & 1);
+                c[y][e] = j <= i ? s.iq[i] * decay(i, j) * s.qk[i][j] : 0.f;
+              }
+          }
+          uint32_t w[2][4];
+          split_a<2>(c[0], c[1], w);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) store_block<false>(out + kP + k * kTile, ib * 16, jb * 16, buf, lane, w[k]);
+        }
+        for (int i = lane; i < 16 * 5 * 2 * (3 - ib); i += 32) {
+          const int tile = i % 5, at = i / 5;
+          *reinterpret_cast<uint4*>(out + tile * kTile + tile_at(ib * 16 + (at & 15), (2 * ib + 2 + (at >> 4)) * 8)) =
+              make_uint4(0, 0, 0, 0);
         }
       }
-      uint8_t* t01 = reinterpret_cast<uint8_t*>(s.A) + tile_at(r, c);
-      *reinterpret_cast<uint4*>(t01) = w[0];
-      *reinterpret_cast<uint4*>(t01 + kTile) = w[1];
-      *reinterpret_cast<uint4*>(s.rest + tile_at(r, c)) = w[2];
-    }
-    fence_proxy_async();
-    __syncthreads();
-    if (tid == 0) {
-      bulk_s2g(out, s.A, 2 * kTile);
-      bulk_s2g(out + 2 * kTile, s.rest, kBlock - 2 * kTile);
-      bulk_commit();
+      const int r = tid - 64;
+      float* vec = reinterpret_cast<float*>(out + kVec);
+      const float gh = hd.ghi[r], gl = hd.glo[r], e = expf(gh);
+      const float Gh = hd.ghi[kC - 1], Gl = hd.glo[kC - 1];
+      vec[r] = e * s.ik[r];
+      vec[64 + r] = e * s.iq[r];
+      vec[128 + r] = expf((Gh - gh) + (Gl - gl)) * s.ik[r];
+      if (r == 0) vec[192] = expf(Gh);
     }
   }
-  if (tid == 0) bulk_wait_all();
 }
 
 // ------------------------------------------------------------------ chain
