@@ -69,22 +69,21 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
 
 // ------------------------------------------------------------------ prep
 // One CTA per (chunk, query / key head).  All four warps form the two Grams, K K^T and Q K^T, in
-// fp32 in shared memory.  Then, value head by value head, two warps invert I + A and two write P
-// and the vectors; the pairs do not wait for each other.
+// fp32 in shared memory.  Then each pair of warps takes every other value head, on its own: the
+// running sums of its decays, the inverse of I + A, T, P and the vectors.
 //
 // The inverse X, in 16 x 16 blocks: the diagonal ones by forward substitution (a lane per
 // column), then column by column X_ij = -X_ii sum_k A_ik X_kj on the tensor cores, transposed, so
 // that each result is the A operand of the next product as it lies:
 //     tmp^T = sum_k X_kj^T A_ik^T,   X_ij^T = -tmp^T X_ii^T,
-// every operand in three bf16 parts (fp32's 24 bits).  One warp takes column 0, the other 1 and 2.
+// every operand in three bf16 parts (fp32's 24 bits).  One warp takes column 0, the other 1 and 2
+// and the first rows of P.
 //
 // e^{g_i - g_j} off the diagonal blocks is e^{g_i - g_r} e^{g_r - g_j}, r the first row of i's
 // block: both exponents are <= 0, and the factors are vectors.
 constexpr int kPrepThreads = 128;
 constexpr int kPitchG = kC + 4;          // floats, Grams
 constexpr int kPitchD = 20, kDiag = 324;  // floats, diagonal blocks and from one to the next
-constexpr int kScan = 4;                 // heads whose decays are prepared at once, one per warp
-
 struct PrepHead {
   float ghi[kC], glo[kC], beta[kC];
   float e1[kC];      // e^{g_i - g_r}
@@ -102,34 +101,55 @@ struct PrepSmem {
       float kk[kC][kPitchG], qk[kC][kPitchG];
     };
   };
-  float diag[4 * kDiag];           // A's diagonal blocks, then their inverses
-  alignas(16) uint8_t out[4][512];  // a 16 x 16 block of bf16 per warp
-  PrepHead head[kScan];
+  float diag[2][4 * kDiag];          // A's diagonal blocks, then their inverses, per pair
+  alignas(16) uint8_t out[4][1536];  // three 16 x 16 blocks of bf16 per warp
+  PrepHead head[2];
   float ik[kC], iq[kC];
   int n, t0, t1;
 };
 
-// A 16 x 16 block of bf16 from 8 x 8 tiles w (kTrans: of its transpose) to the rows of a tile in
-// global memory, 32 bytes each: through shared memory, 16 bytes per lane.
-template <bool kTrans>
-__device__ __forceinline__ void store_block(uint8_t* tile, int row0, int col0, uint8_t* buf, int lane,
-                                            const uint32_t (&w)[4]) {
+// Differences of running sums are taken, so the sums are kept as hi + lo, exact to about 2^-48.
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b) {
+  const float s = __fadd_rn(a.hi, b.hi), v = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));
+  const float lo = __fadd_rn(e, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s))};
+}
+// e^{g_i - g_j}, j <= i
+__device__ __forceinline__ float decay_factor(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return expf(fminf((hi_i - hi_j) + (lo_i - lo_j), 0.f));
+}
+
+// kN 16 x 16 blocks of bf16, one per tile from `tile` on, from 8 x 8 tiles w (kTrans: of their
+// transposes) to 32-byte rows in global memory: through shared memory, 16 bytes per lane.
+template <bool kTrans, int kN>
+__device__ __forceinline__ void store_blocks(uint8_t* tile, int row0, int col0, uint8_t* buf, int lane,
+                                             const uint32_t (&w)[kN][4]) {
   // lane l names row l & 7 of tile l >> 3; halves are swapped every four rows against conflicts
   const uint32_t r = (lane & 7) + ((lane >> (kTrans ? 4 : 3)) & 1) * 8, h = (lane >> (kTrans ? 3 : 4)) & 1;
   const uint32_t at = smem_u32(buf) + r * 32 + ((h ^ ((r >> 2) & 1)) << 4);
-  if constexpr (kTrans) stsm4t(at, w);
-  else stsm4(at, w);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    if constexpr (kTrans) stsm4t(at + k * 512, w[k]);
+    else stsm4(at + k * 512, w[k]);
+  }
   __syncwarp();
   const int row = lane >> 1, half = lane & 1;
-  const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
-  *reinterpret_cast<uint4*>(tile + tile_at(row0 + row, col0 + half * 8)) = v;
+  const uint8_t* from = buf + row * 32 + ((half ^ ((row >> 2) & 1)) << 4);
+  uint8_t* to = tile + tile_at(row0 + row, col0 + half * 8);
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+    *reinterpret_cast<uint4*>(to + k * kTile) = *reinterpret_cast<const uint4*>(from + k * 512);
   __syncwarp();
 }
 
 // One column of the inverse below its diagonal block, and T's blocks of that column.
 template <int J, int DK>
-__device__ __forceinline__ void invert_column(PrepSmem<DK>& s, const PrepHead& hd, int lane, uint8_t* buf,
-                                              uint8_t* out) {
+__device__ __forceinline__ void invert_column(const PrepSmem<DK>& s, const PrepHead& hd, const float* diag,
+                                              int lane, uint8_t* buf, uint8_t* out) {
   const int g = lane >> 2, t = lane & 3;
   const float b0 = hd.beta[J * 16 + g], b1 = hd.beta[J * 16 + g + 8];
   // c: a block of X^T (rows: X's columns), as two 16 x 8 tiles; its parts as an A operand, and T's
@@ -143,8 +163,7 @@ __device__ __forceinline__ void invert_column(PrepSmem<DK>& s, const PrepHead& h
     }
     uint32_t w[3][4];
     split_a<3>(z[0], z[1], w);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) store_block<true>(out + kT + k * kTile, i * 16, J * 16, buf, lane, w[k]);
+    store_blocks<true>(out + kT, i * 16, J * 16, buf, lane, w);
   };
   // six products of parts, smaller ones first
   auto product = [&](float (&c)[2][4], const uint32_t (&f)[3][4], const uint32_t (&m)[3][4]) {
@@ -158,7 +177,7 @@ __device__ __forceinline__ void invert_column(PrepSmem<DK>& s, const PrepHead& h
   };
   uint32_t X[3][3][4];  // parts of X_kJ^T, k from J on
   {
-    const float* d = s.diag + J * kDiag;
+    const float* d = diag + J * kDiag;
     float c[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -197,7 +216,7 @@ __device__ __forceinline__ void invert_column(PrepSmem<DK>& s, const PrepHead& h
       for (int e = 0; e < 4; ++e) c[x][e] = -c[x][e];
     uint32_t f[3][4], m[3][4];
     split_a<3>(c[0], c[1], f);
-    const float* d = s.diag + i * kDiag;
+    const float* d = diag + i * kDiag;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -265,89 +284,60 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
     }
     cp_async_commit();
   }
-  // running sums of the log decays of heads h0 .., one per warp, in 64 bits: differences of
-  // them are taken
+  const int pair = warp >> 1, second = warp & 1;
+  PrepHead& hd = s.head[pair];
+  // running sums of the log decays of head hg, by one warp
   const __nv_bfloat16* beta = static_cast<const __nv_bfloat16*>(a.beta);
-  auto scan = [&](int h0) {
-    if (h0 + warp >= G) return;
-    const int h = hk * G + h0 + warp;
-    PrepHead& hd = s.head[warp];
-    double g2[2];
+  auto scan = [&](int hg) {
+    const int h = hk * G + hg;
+    Sum2 g[2];
     float be[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = lane * 2 + i;
       const size_t at = (size_t)(t0 + (r < len ? r : 0)) * a.Hv + h;
       const float la = a.log_alpha[at], b = to_f32(beta[at]);
-      g2[i] = r < len ? (double)gdr_log_decay(a, la, h) : 0.0;
+      g[i] = {r < len ? gdr_log_decay(a, la, h) : 0.f, 0.f};
       be[i] = r < len ? (a.beta_is_logit ? sigmoidf_(b) : b) : 0.f;
     }
-    double sum = g2[0] + g2[1];
+    g[1] = add2(g[0], g[1]);
+    Sum2 before = {0.f, 0.f}, sum = g[1];  // of the lanes before this one
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const double other = __shfl_up_sync(0xffffffffu, sum, m);
-      if (lane >= m) sum += other;
+      const Sum2 other = {__shfl_up_sync(0xffffffffu, sum.hi, m), __shfl_up_sync(0xffffffffu, sum.lo, m)};
+      if (lane >= m) {
+        sum = add2(other, sum);
+        before = add2(other, before);
+      }
     }
-    const double g[2] = {sum - g2[1], sum};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = lane * 2 + i;
-      const float hi = (float)g[i];
-      hd.ghi[r] = hi;
-      hd.glo[r] = (float)(g[i] - (double)hi);
-      hd.beta[r] = be[i];
+      const Sum2 x = add2(before, g[i]);
+      hd.ghi[lane * 2 + i] = x.hi;
+      hd.glo[lane * 2 + i] = x.lo;
+      hd.beta[lane * 2 + i] = be[i];
     }
   };
-  // the factors of e^{g_i - g_j}, when the norms are there
-  auto factors = [&](int h0) {
-    if (h0 + warp >= G) return;
-    PrepHead& hd = s.head[warp];
-    __syncwarp();
+  // the factors of e^{g_i - g_j}, when the sums and the norms are there
+  auto factors = [&] {
+    const int r = lane + second * 32, r0 = r & ~15;
+    const float hi = hd.ghi[r], lo = hd.glo[r], ik = s.ik[r];
+    const float e1 = decay_factor(hi, lo, hd.ghi[r0], hd.glo[r0]);
+    float e2[3];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = lane + i * 32, r0 = r & ~15;
-      hd.e1[r] = expf(fminf((hd.ghi[r] - hd.ghi[r0]) + (hd.glo[r] - hd.glo[r0]), 0.f));
+    for (int x = 1; x < 4; ++x) e2[x - 1] = ik * decay_factor(hd.ghi[16 * x], hd.glo[16 * x], hi, lo);
+    hd.e1[r] = e1;
 #pragma unroll
-      for (int x = 1; x < 4; ++x)
-        if (r < 16 * x)
-          hd.e2[x - 1][r] = s.ik[r] * expf(fminf((hd.ghi[16 * x] - hd.ghi[r]) + (hd.glo[16 * x] - hd.glo[r]), 0.f));
-    }
+    for (int x = 1; x < 4; ++x)
+      if (r < 16 * x) hd.e2[x - 1][r] = e2[x - 1];
   };
-  scan(0);
+  if (!second && pair < G) scan(pair);
   cp_async_wait_all();
   __syncthreads();
 
-  // norms: two threads per row
-  {
-    const int r = tid >> 1;
-    const uint4* kr = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(s.k) + r * Smem::kPitch) + (tid & 1);
-    const uint4* qr = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(s.q) + r * Smem::kPitch) + (tid & 1);
-    float kk = 0.f, qq = 0.f;
-    auto add = [](float& x, uint4 w) {
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(e[i] << 16), hi = __uint_as_float(e[i] & 0xffff0000u);
-        x = fmaf(lo, lo, x);
-        x = fmaf(hi, hi, x);
-      }
-    };
-#pragma unroll
-    for (int g = 0; g < DK / 16; ++g) {
-      add(kk, kr[g * 2]);
-      add(qq, qr[g * 2]);
-    }
-    kk += __shfl_xor_sync(0xffffffffu, kk, 1);
-    qq += __shfl_xor_sync(0xffffffffu, qq, 1);
-    if ((tid & 1) == 0) {
-      s.ik[r] = a.l2norm_qk ? gdr_inv_norm(kk, a.eps_l2) : 1.f;
-      s.iq[r] = a.q_scale * (a.l2norm_qk ? gdr_inv_norm(qq, a.eps_l2) : 1.f);
-    }
-  }
-
   // K K^T and Q K^T, 16 rows per warp, columns up to the diagonal block
   {
-    float kk[8][4] = {}, qk[8][4] = {};
+    float kk[8][4] = {}, qk[8][4] = {}, qq[2] = {};
     const uint32_t row = warp * 16 + (lane & 15), col = (lane >> 4) * 16;
     const uint32_t ka = smem_u32(s.k) + row * Smem::kPitch + col;
     const uint32_t qa = smem_u32(s.q) + row * Smem::kPitch + col;
@@ -359,6 +349,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
       ldsm4(fk, ka + x * 32);
       ldsm4(fq, qa + x * 32);
 #pragma unroll
+      for (int i = 0; i < 4; ++i) {  // |q|^2 of rows g and g + 8
+        const float lo = __uint_as_float(fq[i] << 16), hi = __uint_as_float(fq[i] & 0xffff0000u);
+        qq[i & 1] = fmaf(lo, lo, fmaf(hi, hi, qq[i & 1]));
+      }
+#pragma unroll
       for (int p = 0; p < 4; ++p) {
         if (p > warp) break;
         uint32_t b[4];
@@ -369,8 +364,23 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
         mma(qk[2 * p + 1], fq, b[2], b[3]);
       }
     }
-    __syncthreads();  // K and Q are done with, the norms there
-    factors(0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      qq[x] += __shfl_xor_sync(0xffffffffu, qq[x], 1);
+      qq[x] += __shfl_xor_sync(0xffffffffu, qq[x], 2);
+      if ((lane & 3) == 0)
+        s.iq[warp * 16 + (lane >> 2) + x * 8] = a.q_scale * (a.l2norm_qk ? gdr_inv_norm(qq[x], a.eps_l2) : 1.f);
+    }
+    // |k|^2: the diagonal, in the two column tiles of this warp's diagonal block
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = warp * 16 + (lane >> 2) + (e >> 1) * 8;
+        if (nt >> 1 == warp && r == nt * 8 + (lane & 3) * 2 + (e & 1))
+          s.ik[r] = a.l2norm_qk ? gdr_inv_norm(kk[nt][e], a.eps_l2) : 1.f;
+      }
+    __syncthreads();  // K and Q are done with
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
       if (nt > 2 * warp + 1) break;
@@ -380,127 +390,141 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
       *reinterpret_cast<float2*>(&s.qk[r][c]) = make_float2(qk[nt][0], qk[nt][1]);
       *reinterpret_cast<float2*>(&s.qk[r + 8][c]) = make_float2(qk[nt][2], qk[nt][3]);
     }
+    if (pair < G) factors();
   }
   __syncthreads();
 
   const int g = lane >> 2, t = lane & 3;
   uint8_t* buf = s.out[warp];
-  for (int hg = 0; hg < G; ++hg) {
-    const PrepHead& hd = s.head[hg % kScan];
-    if (hg > 0 && hg % kScan == 0) {
-      __syncthreads();
-      scan(hg);
-      factors(hg);
-      __syncthreads();
+  float* diag = s.diag[pair];
+  const uint32_t bar = 1 + pair;
+  for (int hg = pair; hg < G; hg += 2) {
+    if (hg >= 2) {
+      named_sync(bar, 64);  // both warps are done with the last head
+      if (!second) scan(hg);
+      named_sync(bar, 64);
+      factors();
+      named_sync(bar, 64);
     }
     uint8_t* out = ws + ((size_t)blk * a.Hv + hk * G + hg) * kBlock;
-    // e^{g_i - g_j} on a diagonal block, j <= i
-    auto decay = [&](int i, int j) {
-      return expf(fminf((hd.ghi[i] - hd.ghi[j]) + (hd.glo[i] - hd.glo[j]), 0.f)) * s.ik[j];
-    };
-    if (warp < 2) {
-      named_sync(1, 64);  // both warps are done with the last head's diagonal blocks
+    // A's diagonal blocks, two per warp, and P's: e[y][2 x + z] is row g + 8 x, column 8 y + 2 t + z
+#pragma unroll
+    for (int x2 = 0; x2 < 2; ++x2) {
+      const int ib = second * 2 + x2, b0 = ib * 16;
+      float* d = diag + ib * kDiag;
+      float e[2][4], p[2][4];
+      float rhi[2], rlo[2], rk[2], rq[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int b0 = (warp * 2 + x) * 16;
-        float* d = s.diag + (warp * 2 + x) * kDiag;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = g + (e >> 2) * 8, c = t * 2 + (e & 1) + ((e >> 1) & 1) * 8;
-          const int i = b0 + r, j = b0 + c;
-          d[r * kPitchD + c] = c < r ? hd.beta[i] * s.ik[i] * decay(i, j) * s.kk[i][j] : 0.f;
-        }
+        const int r = b0 + g + x * 8;
+        rhi[x] = hd.ghi[r]; rlo[x] = hd.glo[r]; rk[x] = hd.beta[r] * s.ik[r]; rq[x] = s.iq[r];
       }
-      __syncwarp();
-      // x_i = -sum_k A_ik x_k: a half warp per block, a lane per column
-      {
-        float* d = s.diag + (warp * 2 + (lane >> 4)) * kDiag;
-        const int c = lane & 15;
-        float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i == c ? 1.f : 0.f;
-#pragma unroll
-        for (int i = 1; i < 16; ++i) {
-          float A[16];
-#pragma unroll
-          for (int k = 0; k < i; k += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(&d[i * kPitchD + k]);
-            A[k] = y.x; A[k + 1] = y.y; A[k + 2] = y.z; A[k + 3] = y.w;
-          }
-          float even = 0.f, odd = 0.f;
-#pragma unroll
-          for (int k = 0; k < i; k += 2) {
-            even = fmaf(A[k], v[k], even);
-            if (k + 1 < i) odd = fmaf(A[k + 1], v[k + 1], odd);
-          }
-          v[i] -= even + odd;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[i * kPitchD + c] = v[i];
-      }
-      named_sync(1, 64);
-      if (warp == 0) {
-        invert_column<0, DK>(s, hd, lane, buf, out);
-        invert_column<3, DK>(s, hd, lane, buf, out);
-      } else {
-        invert_column<1, DK>(s, hd, lane, buf, out);
-        invert_column<2, DK>(s, hd, lane, buf, out);
-      }
-    } else {
-      // P, row blocks 0 to 2 and 3; zeros above the diagonal blocks of T and P
-#pragma unroll 1
-      for (int ib = warp == 2 ? 0 : 3; ib < (warp == 2 ? 3 : 4); ++ib) {
-        float row[2];
+      for (int y = 0; y < 2; ++y) {
+        const int c = y * 8 + t * 2;
+        const float2 chi = *reinterpret_cast<const float2*>(&hd.ghi[b0 + c]);
+        const float2 clo = *reinterpret_cast<const float2*>(&hd.glo[b0 + c]);
+        const float2 ck = *reinterpret_cast<const float2*>(&s.ik[b0 + c]);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int r = ib * 16 + x * 8 + g;
-          row[x] = s.iq[r] * hd.e1[r];
-        }
-#pragma unroll 1
-        for (int jb = 0; jb <= ib; ++jb) {
-          float c[2][4];  // tiles of columns
-          if (jb < ib) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int col = jb * 16 + y * 8 + t * 2;
-              const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[ib - 1][col]);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float2 qk = *reinterpret_cast<const float2*>(&s.qk[ib * 16 + x * 8 + g][col]);
-                c[y][2 * x] = row[x] * (e2.x * qk.x);
-                c[y][2 * x + 1] = row[x] * (e2.y * qk.y);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = ib * 16 + g + (e >> 1) * 8, j = ib * 16 + y * 8 + t * 2 + (e & 1);
-                c[y][e] = j <= i ? s.iq[i] * decay(i, j) * s.qk[i][j] : 0.f;
-              }
-          }
-          uint32_t w[2][4];
-          split_a<2>(c[0], c[1], w);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) store_block<false>(out + kP + k * kTile, ib * 16, jb * 16, buf, lane, w[k]);
-        }
-        for (int i = lane; i < 16 * 5 * 2 * (3 - ib); i += 32) {
-          const int tile = i % 5, at = i / 5;
-          *reinterpret_cast<uint4*>(out + tile * kTile + tile_at(ib * 16 + (at & 15), (2 * ib + 2 + (at >> 4)) * 8)) =
-              make_uint4(0, 0, 0, 0);
+          const int r = g + x * 8;
+          const float2 kk = *reinterpret_cast<const float2*>(&s.kk[b0 + r][b0 + c]);
+          const float2 qk = *reinterpret_cast<const float2*>(&s.qk[b0 + r][b0 + c]);
+          const float w0 = ck.x * decay_factor(rhi[x], rlo[x], chi.x, clo.x);
+          const float w1 = ck.y * decay_factor(rhi[x], rlo[x], chi.y, clo.y);
+          e[y][2 * x] = c < r ? rk[x] * w0 * kk.x : 0.f;
+          e[y][2 * x + 1] = c + 1 < r ? rk[x] * w1 * kk.y : 0.f;
+          p[y][2 * x] = c <= r ? rq[x] * w0 * qk.x : 0.f;
+          p[y][2 * x + 1] = c + 1 <= r ? rq[x] * w1 * qk.y : 0.f;
         }
       }
-      const int r = tid - 64;
-      float* vec = reinterpret_cast<float*>(out + kVec);
-      const float gh = hd.ghi[r], gl = hd.glo[r], e = expf(gh);
-      const float Gh = hd.ghi[kC - 1], Gl = hd.glo[kC - 1];
-      vec[r] = e * s.ik[r];
-      vec[64 + r] = e * s.iq[r];
-      vec[128 + r] = expf((Gh - gh) + (Gl - gl)) * s.ik[r];
-      if (r == 0) vec[192] = expf(Gh);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          *reinterpret_cast<float2*>(&d[(g + x * 8) * kPitchD + y * 8 + t * 2]) = make_float2(e[y][2 * x], e[y][2 * x + 1]);
+      uint32_t w[2][4];
+      split_a<2>(p[0], p[1], w);
+      store_blocks<false>(out + kP, b0, b0, buf, lane, w);
     }
+    // x_i = -sum_k A_ik x_k: a half warp per block, a lane per column
+    {
+      float* d = diag + (second * 2 + (lane >> 4)) * kDiag;
+      const int c = lane & 15;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = i == c ? 1.f : 0.f;
+#pragma unroll
+      for (int i = 1; i < 16; ++i) {
+        float A[16];
+#pragma unroll
+        for (int k = 0; k < i; k += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(&d[i * kPitchD + k]);
+          A[k] = y.x; A[k + 1] = y.y; A[k + 2] = y.z; A[k + 3] = y.w;
+        }
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int k = 0; k < i; k += 2) {
+          even = fmaf(A[k], v[k], even);
+          if (k + 1 < i) odd = fmaf(A[k + 1], v[k + 1], odd);
+        }
+        v[i] -= even + odd;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d[i * kPitchD + c] = v[i];
+    }
+    named_sync(bar, 64);
+    if (!second) {
+      invert_column<0, DK>(s, hd, diag, lane, buf, out);
+      invert_column<3, DK>(s, hd, diag, lane, buf, out);
+    } else {
+      invert_column<1, DK>(s, hd, diag, lane, buf, out);
+      invert_column<2, DK>(s, hd, diag, lane, buf, out);
+    }
+    // P below its diagonal blocks: row block 3, and 1 and 2; zeros above them in T and P
+#pragma unroll 1
+    for (int ib = second ? 1 : 3; ib < (second ? 3 : 4); ++ib) {
+      float row[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = ib * 16 + x * 8 + g;
+        row[x] = s.iq[r] * hd.e1[r];
+      }
+#pragma unroll 1
+      for (int jb = 0; jb < ib; ++jb) {
+        float c[2][4];  // tiles of columns
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int col = jb * 16 + y * 8 + t * 2;
+          const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[ib - 1][col]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 qk = *reinterpret_cast<const float2*>(&s.qk[ib * 16 + x * 8 + g][col]);
+            c[y][2 * x] = row[x] * (e2.x * qk.x);
+            c[y][2 * x + 1] = row[x] * (e2.y * qk.y);
+          }
+        }
+        uint32_t w[2][4];
+        split_a<2>(c[0], c[1], w);
+        store_blocks<false>(out + kP, ib * 16, jb * 16, buf, lane, w);
+      }
+    }
+#pragma unroll
+    for (int ib = 0; ib < 3; ++ib)
+      for (int i = lane + second * 32; i < 16 * 2 * (3 - ib); i += 64) {
+        uint8_t* to = out + tile_at(ib * 16 + (i & 15), (2 * ib + 2 + (i >> 4)) * 8);
+#pragma unroll
+        for (int k = 0; k < 5; ++k) *reinterpret_cast<uint4*>(to + k * kTile) = make_uint4(0, 0, 0, 0);
+      }
+    const int r = lane + second * 32;
+    float* vec = reinterpret_cast<float*>(out + kVec);
+    const float gh = hd.ghi[r], gl = hd.glo[r], e = expf(gh);
+    const float Gh = hd.ghi[kC - 1], Gl = hd.glo[kC - 1];
+    vec[r] = e * s.ik[r];
+    vec[64 + r] = e * s.iq[r];
+    vec[128 + r] = decay_factor(Gh, Gl, gh, gl) * s.ik[r];
+    if (r == 0) vec[192] = expf(Gh);
   }
 }
 
