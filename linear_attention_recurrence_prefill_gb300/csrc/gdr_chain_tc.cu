@@ -495,8 +495,7 @@ bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld,
 
 template <int DK>
 cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdr_chain_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<DK>::kSmem);
+  const cudaError_t e = allow_smem<gdr_chain_tc_kernel<DK>>(Layout<DK>::kSmem);
   if (e != cudaSuccess) return e;
   Chain t;
   t.a = a;

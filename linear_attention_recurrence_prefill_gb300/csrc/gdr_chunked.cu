@@ -772,15 +772,10 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
       a.S_T[mat + (size_t)(x * 8 + t * 2 + (e & 1)) * a.dv + col0 + g + (e >> 1) * 8] = S[x][e];
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <int DK, int W>
 cudaError_t launch_chain(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   const size_t bytes = sizeof(ChainSmem<DK, W>);
-  const cudaError_t e = allow_smem(gdr_chain_kernel<DK, W>, bytes);
+  const cudaError_t e = allow_smem<gdr_chain_kernel<DK, W>>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (16 * W));
   gdr_chain_kernel<DK, W><<<grid, W * 32 + 32, bytes, s>>>(a, ws);
@@ -790,7 +785,7 @@ cudaError_t launch_chain(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
 template <int DK>
 cudaError_t launch_dk(const GdrArgs& a, uint8_t* ws, cudaStream_t s) {
   const size_t bytes = sizeof(PrepSmem<DK>);
-  cudaError_t e = allow_smem(gdr_prep_kernel<DK>, bytes);
+  cudaError_t e = allow_smem<gdr_prep_kernel<DK>>(bytes);
   if (e != cudaSuccess) return e;
   gdr_prep_kernel<DK><<<dim3(a.T_total / kC + a.N, a.Hk), kPrepThreads, bytes, s>>>(a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

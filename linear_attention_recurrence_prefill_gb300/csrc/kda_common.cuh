@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kda.h"
 
 namespace kda {
@@ -157,6 +159,20 @@ cudaError_t launch_decode(const DecodeArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_gated_rmsnorm(const void* o, const void* gate, const float* w, void* y,
                                  long long rows_heads, int d, float eps, int dtype,
                                  cudaStream_t s);
+
+// Dynamic shared memory of a kernel beyond the default limit, asked for once per device.
+template <auto kKernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 // Device address of the library's status word on the current device.
 int* status_word();

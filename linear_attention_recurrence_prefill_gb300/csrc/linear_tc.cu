@@ -11,14 +11,16 @@
 // TMA loads of a ring of stages (64 columns of w and x each, 128-byte swizzle),
 // 5 issues the MMAs.
 //
-// Two forms.
-//  * kSplit = false: a persistent grid, one CTA per SM walking the tiles, two
-//    accumulators in TMEM so that a tile's epilogue runs beside the next tile's
-//    products.
-//  * kSplit = true, where there are too few tiles to fill the GPU (few tokens,
-//    or a small product): the CTAs of a cluster share one tile, each takes a part
-//    of K, and the partial sums meet in distributed shared memory, added in the
-//    order of the ranks, so that results repeat to the bit.
+// Two kernels.
+//  * linear_pair_kernel: pairs of CTAs (cta_group::2) share tiles of 256 rows of w by BN tokens, a
+//    persistent pair per two SMs walking the tiles, two accumulators in TMEM so that a tile's
+//    epilogue runs beside the next tile's products.  Alone, a CTA would fetch 128 + 256 rows for
+//    each 128 x 256 products, 96 bytes per clock from L2 at the tensor cores' full rate, more than
+//    an SM gets; a pair fetches 64.
+//  * linear_split_kernel, where there are too few tiles to fill the GPU (few tokens, or a small
+//    product): the CTAs of a cluster share one tile, each takes a part of K, and the partial sums
+//    meet in distributed shared memory, added in the order of the ranks, so that results repeat
+//    to the bit.
 #include <cuda.h>
 
 #include <mutex>
@@ -82,34 +84,160 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r
     if (j < cols) y[j * a.ldy] = __float2bfloat16_rn(z[j] + __bfloat162float(add[j]));
 }
 
-template <int BN, int kStages>
-constexpr uint32_t smem_bytes() {
-  return 1024 + kStages * (kRowsA + BN) * kBlockK * 2;
-}
+constexpr uint32_t kAlign = 1024;  // the swizzled tiles' alignment
 
-template <int BN, int kStages, bool kSplit>
-__global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_constant__ Tc t) {
-  constexpr uint32_t kStage = (kRowsA + BN) * kBlockK * 2;
-  constexpr int kAcc = kSplit ? 1 : 2;  // accumulators in TMEM
-  constexpr uint32_t kCols = kAcc * BN <= 32 ? 32 : kAcc * BN <= 64 ? 64 : kAcc * BN <= 128 ? 128
-                             : kAcc * BN <= 256 ? 256 : 512;
+template <int BN>
+struct Pair {
+  static constexpr uint32_t kStage = (kRowsA + BN / 2) * kBlockK * 2;
+  static constexpr int kStages = BN > 192 ? 6 : 7;
+  static constexpr uint32_t kSmem = kStages * kStage + kAlign;
+  static constexpr uint32_t kAcc = 256;  // columns from one accumulator to the next
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
+    linear_pair_kernel(const __grid_constant__ Tc t) {
+  using P = Pair<BN>;
+  constexpr int kStages = P::kStages;
   extern __shared__ uint8_t raw[];
-  uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc], drained;
+  uint8_t* ring = raw + ((kAlign - (smem_u32(raw) & (kAlign - 1))) & (kAlign - 1));
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kSplit ? cluster_ctarank() : 0, ranks = kSplit ? gridDim.z : 1;
+  const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kAcc; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);  // four warps of each CTA
     }
     mbar_init(&drained, 1);
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) {
+    pair_tmem_alloc(&tmem_base, 512);
+    pair_tmem_relinquish();
+  }
+  fence_before_sync();
+  cluster_sync();
+  fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  const int tiles = t.n_tiles * t.m_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  bool ok = true;
+  if (warp == kWarpLoad && lane == 0) {
+    // each CTA its rows of w and half of the tokens; all arrive on the even CTA's barrier
+    int it = 0;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const int n0 = tile % t.n_tiles * 256 + (int)rank * 128, m0 = tile / t.n_tiles * BN + (int)rank * (BN / 2);
+      for (int kb = 0; kb < t.k_blocks; ++kb, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages && !mbar_wait_soon(&empty[s], (it / kStages - 1) & 1, kSpins)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = ring + s * P::kStage;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kStage);
+        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+        pair_tma_load_2d(dst, &t.tm_w, kb * (int)kBlockK, n0, bar);
+        pair_tma_load_2d(dst + kRowsA * kBlockK * 2, &t.tm_x, kb * (int)kBlockK, m0, bar);
+      }
+    }
+    // a wait that gave up: the loads in flight land before shared memory is released
+    if (!ok && rank == 0)
+      for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+        mbar_wait(&full[j % kStages], (j / kStages) & 1, kSpins);
+  } else if (warp == kWarpMma && rank == 0) {
+    const uint32_t lead = elect_leader();
+    constexpr uint32_t idesc = idesc_f16(256, BN, true);
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, kSpins));
+      fence_after_sync();
+      return ok;
+    };
+    int it = 0, n = 0;
+    for (int tile = first; tile < tiles; tile += step, ++n) {
+      const int acc = n & 1;
+      if (n >= 2 && !wait(&acc_empty[acc], (n / 2 - 1) & 1)) break;
+      const uint32_t d = tmem + acc * P::kAcc;
+      for (int kb = 0; kb < t.k_blocks; ++kb, ++it) {
+        const int s = it % kStages;
+        if (!wait(&full[s], (it / kStages) & 1)) break;
+        const uint32_t at = smem_u32(ring + s * P::kStage);
+        const uint64_t wd = desc_k_sw128(at, 0), xd = desc_k_sw128(at + kRowsA * kBlockK * 2, 0);
+#pragma unroll
+        for (uint32_t k = 0; k < kBlockK / 16; ++k)
+          pair_mma_ss_if(lead, d, wd + (k * 32 >> 4), xd + (k * 32 >> 4), idesc, kb > 0 || k > 0);
+        pair_commit_if(lead, &empty[s]);
+      }
+      if (!ok) break;
+      pair_commit_if(lead, &acc_full[acc]);
+    }
+    // products in flight end before shared memory and TMEM are released
+    pair_commit_if(lead, &drained);
+    mbar_wait(&drained, 0, kSpins);
+  } else if (warp < 4) {
+    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
+    int i = 0;
+    for (int tile = first; tile < tiles; tile += step, ++i) {
+      const int acc = i & 1;
+      const int n = tile % t.n_tiles * 256 + (int)rank * 128 + warp * 32 + lane;
+      const long long m0 = (long long)(tile / t.n_tiles) * BN;
+      const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_full[acc], (i / 2) & 1, kSpins));
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t d = taddr(tmem, warp * 32, acc * P::kAcc);
+      const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(d + c, r);
+        tmem_wait_ld();
+        if (c + 32 >= cols) {  // the accumulator is in registers: its place is free
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+        }
+        if (n < t.a.N) finish32(t.a, r, b, m0 + c, n, cols - c);
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicExch(t.status, KDA_ERR_TIMEOUT);
+  __syncwarp();
+  fence_before_sync();
+  cluster_sync();  // no CTA leaves while the other reads its shared memory or signals to it
+  fence_after_sync();
+  if (warp == kWarpMma) pair_tmem_dealloc(tmem, 512);
+}
+
+template <int BN, int kStages>
+constexpr uint32_t split_smem() {
+  return kAlign + kStages * (kRowsA + BN) * kBlockK * 2;
+}
+
+template <int BN, int kStages>
+__global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_constant__ Tc t) {
+  constexpr uint32_t kStage = (kRowsA + BN) * kBlockK * 2;
+  constexpr uint32_t kCols = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;
+  static_assert(kStages * kStage >= BN * kRowsA * 4, "the partial sums fit in the ring");
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = raw + ((kAlign - (smem_u32(raw) & (kAlign - 1))) & (kAlign - 1));
+  __shared__ uint64_t full[kStages], empty[kStages], done;
+  __shared__ uint32_t tmem_base;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
     mbar_fence_init();
   }
   if (warp == kWarpMma) {
@@ -120,132 +248,93 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = tmem_base;
-
-  // tiles of this CTA, and its part of K
-  const int tiles = t.n_tiles * t.m_tiles;
-  const int first = kSplit ? blockIdx.x + t.n_tiles * blockIdx.y : blockIdx.x;
-  const int step = kSplit ? tiles : gridDim.x;
+  // this CTA's part of K: one block at least
   const int kb0 = (int)((long long)t.k_blocks * rank / ranks);
-  const int kb1 = (int)((long long)t.k_blocks * (rank + 1) / ranks);
+  const int blocks = (int)((long long)t.k_blocks * (rank + 1) / ranks) - kb0;
 
   bool ok = true;
   if (warp == kWarpLoad && lane == 0) {
+    const int n0 = blockIdx.x * (int)kRowsA, m0 = blockIdx.y * BN;
     int it = 0;
-    for (int tile = first; tile < tiles && ok; tile += step) {
-      const int n0 = tile % t.n_tiles * (int)kRowsA, m0 = tile / t.n_tiles * BN;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !mbar_wait(&empty[s], (it / kStages - 1) & 1, kSpins)) {
-          ok = false;
-          break;
-        }
-        uint8_t* dst = ring + s * kStage;
-        mbar_arrive_expect_tx(&full[s], kStage);
-        tma_load_2d(dst, &t.tm_w, kb * (int)kBlockK, n0, &full[s]);
-        tma_load_2d(dst + kRowsA * kBlockK * 2, &t.tm_x, kb * (int)kBlockK, m0, &full[s]);
+    for (; it < blocks; ++it) {
+      const int s = it % kStages, x = (kb0 + it) * (int)kBlockK;
+      if (it >= kStages && !mbar_wait_soon(&empty[s], (it / kStages - 1) & 1, kSpins)) {
+        ok = false;
+        break;
       }
+      uint8_t* dst = ring + s * kStage;
+      mbar_arrive_expect_tx(&full[s], kStage);
+      tma_load_2d(dst, &t.tm_w, x, n0, &full[s]);
+      tma_load_2d(dst + kRowsA * kBlockK * 2, &t.tm_x, x, m0, &full[s]);
     }
     // a wait that gave up: the loads in flight land before shared memory is released
     if (!ok)
       for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
         mbar_wait(&full[j % kStages], (j / kStages) & 1, kSpins);
-  } else if (warp == kWarpMma && lane == 0) {
+  } else if (warp == kWarpMma) {
+    const uint32_t lead = elect_leader();
     constexpr uint32_t idesc = idesc_f16(kRowsA, BN, true);
-    int it = 0, n = 0;
-    for (int tile = first; tile < tiles && ok; tile += step, ++n) {
-      const int acc = n % kAcc;
-      if (n >= kAcc && !mbar_wait(&acc_empty[acc], (n / kAcc - 1) & 1, kSpins)) {
-        ok = false;
-        break;
-      }
-      fence_after_sync();
-      const uint32_t d = tmem + acc * BN;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kStages;
-        if (!mbar_wait(&full[s], (it / kStages) & 1, kSpins)) {
-          ok = false;
-          break;
-        }
-        fence_after_sync();
-        const uint32_t wa = smem_u32(ring + s * kStage), xa = wa + kRowsA * kBlockK * 2;
-#pragma unroll
-        for (uint32_t k = 0; k < kBlockK / 16; ++k)
-          mma_ss(d, desc_k_sw128(wa, k * 32), desc_k_sw128(xa, k * 32), idesc,
-                 kb > kb0 || k > 0);
-        mma_commit(&empty[s]);
-      }
+    for (int it = 0; it < blocks; ++it) {
+      const int s = it % kStages;
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&full[s], (it / kStages) & 1, kSpins));
       if (!ok) break;
-      mma_commit(&acc_full[acc]);
+      fence_after_sync();
+      const uint32_t at = smem_u32(ring + s * kStage);
+      const uint64_t wd = desc_k_sw128(at, 0), xd = desc_k_sw128(at + kRowsA * kBlockK * 2, 0);
+#pragma unroll
+      for (uint32_t k = 0; k < kBlockK / 16; ++k)
+        mma_ss_if(lead, tmem, wd + (k * 32 >> 4), xd + (k * 32 >> 4), idesc, it > 0 || k > 0);
+      mma_commit_if(lead, &empty[s]);
     }
-    if (!ok) {  // products in flight end before shared memory and TMEM are released
-      mma_commit(&drained);
-      mbar_wait(&drained, 0, kSpins);
-    }
+    // everything issued is complete before the ring or TMEM is used again, or released
+    mma_commit_if(lead, &done);
+    mbar_wait(&done, 0, kSpins);
   } else if (warp < 4) {
-    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
-    int i = 0;
-    for (int tile = first; tile < tiles; tile += step, ++i) {
-      const int acc = i % kAcc;
-      const int n = tile % t.n_tiles * (int)kRowsA + warp * 32 + lane;
-      const long long m0 = (long long)(tile / t.n_tiles) * BN;
-      const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
-      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], (i / kAcc) & 1, kSpins));
-      if (!ok) break;
-      fence_after_sync();
-      const uint32_t d = taddr(tmem, warp * 32, acc * BN);
-      if constexpr (kSplit) {
-        // partial sums [column][channel] over the ring, whose loads and products are done
-        float* part = reinterpret_cast<float*>(ring) + warp * 32 + lane;
+    ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, kSpins));
+    fence_after_sync();
+    if (ok) {
+      // partial sums [column][channel] over the ring, whose loads and products are done
+      const uint32_t d = taddr(tmem, warp * 32, 0);
+      float* part = reinterpret_cast<float*>(ring) + warp * 32 + lane;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(d + c, r);
-          tmem_wait_ld();
+      for (int c = 0; c < BN; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(d + c, r);
+        tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(c + j) * (int)kRowsA] = __uint_as_float(r[j]);
-        }
-      } else {
-        const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(d + c, r);
-          tmem_wait_ld();
-          if (c + 32 >= cols) {  // the accumulator is in registers: its place is free
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
-          }
-          if (n < t.a.N) finish32(t.a, r, b, m0 + c, n, cols - c);
-        }
+        for (int j = 0; j < 16; ++j) part[(c + j) * (int)kRowsA] = __uint_as_float(r[j]);
       }
     }
   }
   if (!ok && lane == 0) atomicExch(t.status, KDA_ERR_TIMEOUT);
 
-  if constexpr (kSplit) {
-    // every rank adds up its share of the tile's elements over all ranks; a CTA that gave up
-    // takes part in the barriers all the same
-    __syncwarp();
-    cluster_sync();
-    if (warp < 4) {
-      const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
-      const int n = blockIdx.x * (int)kRowsA + warp * 32 + lane;
-      const long long m0 = (long long)blockIdx.y * BN;
-      const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
-      const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
-      const uint32_t part = smem_u32(ring) + (warp * 32 + lane) * 4;
-      for (int c = rank; c < cols; c += ranks) {
-        float z = 0.f;
-        for (uint32_t r = 0; r < ranks; ++r)
-          z += ld_cluster_f32(map_to_rank(part + c * kRowsA * 4, r));
-        if (n < t.a.N) finish<__nv_bfloat16>(t.a, z, b, m0 + c, n);
-      }
+  // every rank adds up its share of the tile's columns over all ranks; a CTA that gave up takes
+  // part in the barriers all the same
+  __syncwarp();
+  cluster_sync();
+  if (warp < 4) {
+    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
+    const int n = blockIdx.x * (int)kRowsA + warp * 32 + lane;
+    const long long m0 = (long long)blockIdx.y * BN;
+    const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
+    const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
+    const uint32_t part = smem_u32(ring) + (warp * 32 + lane) * 4;
+    uint32_t from[8];
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) from[r] = map_to_rank(part, r < ranks ? r : 0);
+#pragma unroll 4
+    for (int c = rank; c < cols; c += ranks) {
+      float v[8];
+#pragma unroll
+      for (uint32_t r = 0; r < 8; ++r) v[r] = r < ranks ? ld_cluster_f32(from[r] + c * kRowsA * 4) : 0.f;
+      float z = v[0];
+#pragma unroll
+      for (uint32_t r = 1; r < 8; ++r) z += v[r];
+      if (n < t.a.N) finish<__nv_bfloat16>(t.a, z, b, m0 + c, n);
     }
-    cluster_sync();  // no CTA leaves while its sums are read
   }
   fence_before_sync();
-  __syncthreads();
+  cluster_sync();  // no CTA leaves while its sums are read
   fence_after_sync();
   if (warp == kWarpMma) tmem_dealloc(tmem, kCols);
 }
@@ -292,47 +381,46 @@ int sm_count() {
   return count[dev] > 0 ? count[dev] : 152;
 }
 
-template <int BN, int kStages, bool kSplit>
-cudaError_t launch(const LinearArgs& a, int* status, int split, cudaStream_t s) {
-  constexpr auto kern = linear_tc_kernel<BN, kStages, kSplit>;
-  static_assert(!kSplit || kStages * (kRowsA + BN) * kBlockK * 2 >= BN * kRowsA * 4,
-                "the partial sums fit in the ring");
-  static bool ready[64] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<BN, kStages>());
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev] = true;
-  }
-  Tc t;
+bool fill(Tc& t, const LinearArgs& a, int* status, int rows_w, int box_w, int rows_x, int box_x) {
   t.a = a;
   t.status = status;
-  t.n_tiles = (a.N + (int)kRowsA - 1) / (int)kRowsA;
-  t.m_tiles = (a.M + BN - 1) / BN;
+  t.n_tiles = (a.N + rows_w - 1) / rows_w;
+  t.m_tiles = (int)(((long long)a.M + rows_x - 1) / rows_x);
   t.k_blocks = (a.K + (int)kBlockK - 1) / (int)kBlockK;
-  if (!encode(&t.tm_w, a.w, a.N, a.K, a.ldw, kRowsA) || !encode(&t.tm_x, a.x, a.M, a.K, a.ldx, BN))
-    return cudaErrorInvalidValue;
+  return encode(&t.tm_w, a.w, a.N, a.K, a.ldw, box_w) && encode(&t.tm_x, a.x, a.M, a.K, a.ldx, box_x);
+}
+
+template <int BN>
+cudaError_t launch_pair(const LinearArgs& a, int* status, cudaStream_t s) {
+  const cudaError_t e = allow_smem<linear_pair_kernel<BN>>(Pair<BN>::kSmem);
+  if (e != cudaSuccess) return e;
+  Tc t;
+  if (!fill(t, a, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
+  const long long tiles = (long long)t.n_tiles * t.m_tiles;
+  const int pairs = sm_count() / 2;
+  linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kThreads, Pair<BN>::kSmem, s>>>(t);
+  return cudaGetLastError();
+}
+
+template <int BN, int kStages>
+cudaError_t launch_split(const LinearArgs& a, int* status, int split, cudaStream_t s) {
+  constexpr auto kern = linear_split_kernel<BN, kStages>;
+  const cudaError_t e = allow_smem<kern>(split_smem<BN, kStages>());
+  if (e != cudaSuccess) return e;
+  Tc t;
+  if (!fill(t, a, status, kRowsA, kRowsA, BN, BN)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<BN, kStages>();
+  cfg.dynamicSmemBytes = split_smem<BN, kStages>();
   cfg.stream = s;
+  cfg.gridDim = dim3(t.n_tiles, t.m_tiles, split);
   cudaLaunchAttribute attr[1];
-  if (kSplit) {
-    cfg.gridDim = dim3(t.n_tiles, t.m_tiles, split);
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = split;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  } else {
-    const long long tiles = (long long)t.n_tiles * t.m_tiles;
-    const int sms = sm_count();
-    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
-  }
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = split;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, t);
 }
 
@@ -346,20 +434,38 @@ bool linear_tc_takes(const LinearArgs& a, int dtype) {
 }
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int* status, cudaStream_t s) {
-  const long long n_tiles = (a.N + 127LL) / 128;
   const int k_blocks = (a.K + 63) / 64, sms = sm_count();
-  // Tiles of 256 tokens where they fill the SMs; else smaller ones, K split over the CTAs of a
-  // cluster until there are two CTAs per SM.
-  if (n_tiles * ((a.M + 255LL) / 256) >= sms) return launch<256, 4, false>(a, status, 1, s);
+  // Pairs of CTAs where their tiles fill the SMs, with the width of tile whose waves cost least.
+  const long long rows = (a.N + 255LL) / 256, pairs = sms / 2;
+  if (rows * ((a.M + 127LL) / 128) >= pairs) {
+    long long best = 0;
+    int width = 0;
+    for (int bn : {256, 224, 192, 160, 128}) {
+      const long long tiles = rows * ((a.M + bn - 1LL) / bn);
+      const long long cost = (tiles + pairs - 1) / pairs * bn;
+      if (!width || cost < best) {
+        best = cost;
+        width = bn;
+      }
+    }
+    switch (width) {
+      case 256: return launch_pair<256>(a, status, s);
+      case 224: return launch_pair<224>(a, status, s);
+      case 192: return launch_pair<192>(a, status, s);
+      case 160: return launch_pair<160>(a, status, s);
+      default: return launch_pair<128>(a, status, s);
+    }
+  }
+  // Else K split over the CTAs of a cluster until there are two CTAs per SM.
   const int bn = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-  const long long tiles = n_tiles * ((a.M + bn - 1) / bn);
+  const long long tiles = (a.N + 127LL) / 128 * ((a.M + bn - 1LL) / bn);
   int split = 1;
   while (split < 8 && split * 2 <= k_blocks && tiles * split * 2 <= 2LL * sms) split *= 2;
   switch (bn) {
-    case 16: return launch<16, 6, true>(a, status, split, s);
-    case 32: return launch<32, 5, true>(a, status, split, s);
-    case 64: return launch<64, 4, true>(a, status, split, s);
-    default: return launch<128, 3, true>(a, status, split, s);
+    case 16: return launch_split<16, 6>(a, status, split, s);
+    case 32: return launch_split<32, 5>(a, status, split, s);
+    case 64: return launch_split<64, 4>(a, status, split, s);
+    default: return launch_split<128, 3>(a, status, split, s);
   }
 }
 

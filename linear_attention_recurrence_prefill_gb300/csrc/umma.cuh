@@ -167,6 +167,53 @@ __device__ __forceinline__ void mma_commit_if(uint32_t leader, uint64_t* mbar) {
       :: "r"(smem_u32(mbar)), "r"(leader) : "memory");
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// The forms for two CTAs of a cluster that share one product (cta_group::2): the MMA of 256 rows,
+// 128 in each CTA's TMEM, is issued by the CTA of even rank; A's rows lie half in each CTA's shared
+// memory, and so do B's, at the same addresses.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :: "r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+               :: "r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma_ss_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc,
+                                               uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// The barrier at this address in both CTAs arrives once every MMA issued so far has completed.
+__device__ __forceinline__ void pair_commit_if(uint32_t leader, uint64_t* mbar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %2;\n\t}"
+      :: "r"(smem_u32(mbar)), "r"(leader), "h"((uint16_t)3) : "memory");
+}
+// 2-D box into this CTA's shared memory, completing on a barrier of either CTA (a cluster address).
+__device__ __forceinline__ void pair_tma_load_2d(void* dst_smem, const void* tmap, int x, int y,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(smem_u32(dst_smem)), "l"(tmap), "r"(x), "r"(y), "r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar)
+               : "memory");
+}
+
 // ------------------------------------------------------------------ TMEM load/store
 // 32 lanes x 32 consecutive columns of 32-bit data; each thread of the warp
 // gets its lane's 32 words.  The warp may only touch its own 32-lane quarter.
