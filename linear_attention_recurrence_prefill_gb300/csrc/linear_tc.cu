@@ -45,22 +45,17 @@ struct Tc {
   int n_tiles, m_tiles, k_blocks;
 };
 
-// The epilogue of output channel n for the 32 tokens from m on, of which `cols` exist.
-// All of the residual is fetched before the first store: y may be the residual, so the
-// compiler would not move a load over a store by itself.
-__device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r)[32], float bias,
-                                         long long m, int n, int cols) {
+// The epilogue of output channel n for the 32 tokens from m on, of which `cols` exist: the
+// residual, fetched ahead of the sums, then the rest.
+__device__ __forceinline__ void load_residual(const LinearArgs& a, __nv_bfloat16 (&add)[32], long long m,
+                                              int n, int cols) {
   const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.residual) + m * a.ldr + n;
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + m * a.ldy + n;
-  __nv_bfloat16 add[32];
-  if (a.residual) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < cols) add[j] = res[j * a.ldr];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) add[j] = __ushort_as_bfloat16(0);
-  }
+  for (int j = 0; j < 32; ++j) add[j] = a.residual && j < cols ? res[j * a.ldr] : __ushort_as_bfloat16(0);
+}
+
+__device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r)[32], float bias,
+                                         const __nv_bfloat16 (&add)[32], long long m, int n, int cols) {
   float z[32];
 #pragma unroll
   for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]) + bias;
@@ -79,6 +74,7 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r
     case KDA_ACT_SIGMOID: all([](float x) { return activate<true>(x, KDA_ACT_SIGMOID); }); break;
     default: break;
   }
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + m * a.ldy + n;
 #pragma unroll
   for (int j = 0; j < 32; ++j)
     if (j < cols) y[j * a.ldy] = __float2bfloat16_rn(z[j] + __bfloat162float(add[j]));
@@ -94,8 +90,19 @@ struct Pair {
   static constexpr uint32_t kAcc = 256;  // columns from one accumulator to the next
 };
 
+constexpr int kPairThreads = 320, kPairOut = 8, kPairLoad = 8, kPairMma = 9;
+
+// Tile i as its rows of w and its tokens: eight rows of tiles at a time, so that the tiles in work
+// at once share both and what they read stays in L2.
+__device__ __forceinline__ void tile_of(const Tc& t, int i, int& n, int& m) {
+  const int full = 8 * t.m_tiles, group = i / full, in = i - group * full;
+  const int rows = min(8, t.n_tiles - group * 8);
+  m = in / rows;
+  n = group * 8 + in - m * rows;
+}
+
 template <int BN>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ Tc t) {
   using P = Pair<BN>;
   constexpr int kStages = P::kStages;
@@ -113,12 +120,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);  // four warps of each CTA
+      mbar_init(&acc_empty[i], 2 * kPairOut);
     }
     mbar_init(&drained, 1);
     mbar_fence_init();
   }
-  if (warp == kWarpMma) {
+  if (warp == kPairMma) {
     pair_tmem_alloc(&tmem_base, 512);
     pair_tmem_relinquish();
   }
@@ -129,11 +136,13 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
   const int tiles = t.n_tiles * t.m_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
 
   bool ok = true;
-  if (warp == kWarpLoad && lane == 0) {
+  if (warp == kPairLoad && lane == 0) {
     // each CTA its rows of w and half of the tokens; all arrive on the even CTA's barrier
     int it = 0;
     for (int tile = first; tile < tiles && ok; tile += step) {
-      const int n0 = tile % t.n_tiles * 256 + (int)rank * 128, m0 = tile / t.n_tiles * BN + (int)rank * (BN / 2);
+      int tn, tm;
+      tile_of(t, tile, tn, tm);
+      const int n0 = tn * 256 + (int)rank * 128, m0 = tm * BN + (int)rank * (BN / 2);
       for (int kb = 0; kb < t.k_blocks; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !mbar_wait_soon(&empty[s], (it / kStages - 1) & 1, kSpins)) {
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
     if (!ok && rank == 0)
       for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
         mbar_wait(&full[j % kStages], (j / kStages) & 1, kSpins);
-  } else if (warp == kWarpMma && rank == 0) {
+  } else if (warp == kPairMma && rank == 0) {
     const uint32_t lead = elect_leader();
     constexpr uint32_t idesc = idesc_f16(256, BN, true);
     auto wait = [&](uint64_t* bar, int parity) {
@@ -180,31 +189,39 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
     // products in flight end before shared memory and TMEM are released
     pair_commit_if(lead, &drained);
     mbar_wait(&drained, 0, kSpins);
-  } else if (warp < 4) {
+  } else if (warp < kPairOut) {
+    // two warps per quarter of the lanes, every other 32 tokens each
     const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
+    const int quarter = warp & 3, half = warp >> 2;
     int i = 0;
     for (int tile = first; tile < tiles; tile += step, ++i) {
       const int acc = i & 1;
-      const int n = tile % t.n_tiles * 256 + (int)rank * 128 + warp * 32 + lane;
-      const long long m0 = (long long)(tile / t.n_tiles) * BN;
+      int tn, tm;
+      tile_of(t, tile, tn, tm);
+      const int n = tn * 256 + (int)rank * 128 + quarter * 32 + lane;
+      const long long m0 = (long long)tm * BN;
       const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
+      const bool in = n < t.a.N;
+      const float b = bias && in ? to_f32(bias[n]) : 0.f;
+      __nv_bfloat16 add[32], next[32];
+      if (in) load_residual(t.a, add, m0 + half * 32, n, cols - half * 32);
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_full[acc], (i / 2) & 1, kSpins));
       if (!ok) break;
       fence_after_sync();
-      const uint32_t d = taddr(tmem, warp * 32, acc * P::kAcc);
-      const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
+      const uint32_t d = taddr(tmem, quarter * 32, acc * P::kAcc);
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
+      for (int c = half * 32; c < cols; c += 64) {
         uint32_t r[32];
         tmem_ld32(d + c, r);
+        if (in && c + 64 < cols) load_residual(t.a, next, m0 + c + 64, n, cols - c - 64);
         tmem_wait_ld();
-        if (c + 32 >= cols) {  // the accumulator is in registers: its place is free
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
-        }
-        if (n < t.a.N) finish32(t.a, r, b, m0 + c, n, cols - c);
+        if (in) finish32(t.a, r, b, add, m0 + c, n, cols - c);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) add[j] = next[j];
       }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
     }
   }
   if (!ok && lane == 0) atomicExch(t.status, KDA_ERR_TIMEOUT);
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(2, 1, 1)
   fence_before_sync();
   cluster_sync();  // no CTA leaves while the other reads its shared memory or signals to it
   fence_after_sync();
-  if (warp == kWarpMma) pair_tmem_dealloc(tmem, 512);
+  if (warp == kPairMma) pair_tmem_dealloc(tmem, 512);
 }
 
 template <int BN, int kStages>
@@ -398,7 +415,7 @@ cudaError_t launch_pair(const LinearArgs& a, int* status, cudaStream_t s) {
   if (!fill(t, a, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
   const long long tiles = (long long)t.n_tiles * t.m_tiles;
   const int pairs = sm_count() / 2;
-  linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kThreads, Pair<BN>::kSmem, s>>>(t);
+  linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads, Pair<BN>::kSmem, s>>>(t);
   return cudaGetLastError();
 }
 
