@@ -10,6 +10,17 @@ using namespace kda;
 
 namespace {
 
+int sm_count() {  // of the current device
+  static std::atomic<int> count[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool gdr_dk(int d) { return d == 32 || d == 64 || d == 128; }
 bool gdr_dv(int d) { return gdr_dk(d) || d == 256; }
@@ -183,13 +194,16 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
   a.ldx = ldx; a.ldw = ldw; a.ldr = ldr; a.ldy = ldy;
   a.M = M; a.N = N; a.K = K; a.act = act;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = sm_count();
   cudaError_t e;
-  if (linear_tc_takes(a, dtype)) {
+  if (linear_few_takes(a, dtype)) {
+    e = launch_linear_few(a, dtype, sms, s);
+  } else if (linear_tc_takes(a, dtype)) {
     int* status = status_word();
     if (!status) return KDA_ERR_CUDA;
-    e = launch_linear_tc(a, status, s);
+    e = launch_linear_tc(a, sms, status, s);
   } else {
-    e = launch_linear_simt(a, dtype, s);
+    e = launch_linear_simt(a, dtype, sms, s);
   }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -53,9 +53,13 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float z, float bias,
   static_cast<T*>(a.y)[m * a.ldy + n] = from_f32<T>(z);
 }
 
-cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, cudaStream_t s);
-// bf16 with x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
+// Launchers, for a device of `sms` SMs; each returns the launch's cudaError_t.
+cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
+// Up to four rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
+bool linear_few_takes(const LinearArgs& a, int dtype);
+cudaError_t launch_linear_few(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
+// bf16, x and w as above, any number of rows.
 bool linear_tc_takes(const LinearArgs& a, int dtype);
-cudaError_t launch_linear_tc(const LinearArgs& a, int* status, cudaStream_t s);
+cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s);
 
 }  // namespace kda

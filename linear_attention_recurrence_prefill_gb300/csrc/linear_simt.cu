@@ -1,63 +1,129 @@
-// linear_simt.cu -- y = act(x w^T + bias) + residual on the CUDA cores: fp32
-// data, and bf16 data whose rows the tensor-core path cannot fetch (addresses
-// or strides that are not multiples of 16 bytes).
+// linear_simt.cu -- y = act(x w^T + bias) + residual on the CUDA cores: fp32 data, and bf16 data
+// whose rows the tensor-core path cannot fetch (addresses or strides that are not multiples of 16
+// bytes).
 //
-// One CTA of 256 threads per 64 x 64 tile of y, 4 x 4 sums per thread, x and w
-// taken through shared memory 16 columns at a time.  Every sum runs over k in
-// ascending order in fp32.
+// A CTA of 128 threads per 64 x 64 tile of y, 8 x 4 sums per thread as pairs (fma.rn.f32x2): three
+// 16-byte reads of shared memory for 32 products.  x and w pass through shared memory 16 columns at
+// a time, the next ones fetched into registers meanwhile.  Where there are too few tiles to give
+// every SM two CTAs, the CTAs of a cluster share a tile, each takes a part of K, and the sums meet
+// in distributed shared memory, added in the order of the ranks.
 #include "linear.cuh"
+#include "umma.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+using umma::cluster_ctarank;
+using umma::cluster_sync;
+using umma::ld_cluster_f32;
+using umma::map_to_rank;
+using umma::smem_u32;
 
-template <typename T>
-__global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a) {
-  __shared__ float sx[kStep][kTile + 4], sw[kStep][kTile + 4];
-  const T* x = static_cast<const T*>(a.x);
-  const T* w = static_cast<const T*>(a.w);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int n0 = blockIdx.x * kTile;
-  const long long m0 = (long long)blockIdx.y * kTile;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kStep) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (tid >> 4) + 16 * i, c = tid & 15;
-      const bool kin = k0 + c < a.K;
-      sx[c][r] = kin && m0 + r < a.M ? to_f32(x[(m0 + r) * a.ldx + k0 + c]) : 0.f;
-      sw[c][r] = kin && n0 + r < a.N ? to_f32(w[(long long)(n0 + r) * a.ldw + k0 + c]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kStep; ++c) {
-      const float4 xa = *reinterpret_cast<const float4*>(&sx[c][ty * 4]);
-      const float4 wb = *reinterpret_cast<const float4*>(&sw[c][tx * 4]);
-      const float xs[4] = {xa.x, xa.y, xa.z, xa.w}, ws[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ws[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-  const T* bias = static_cast<const T*>(a.bias);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long m = m0 + ty * 4 + i;
-    if (m >= a.M) break;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (n >= a.N) break;
-      finish<T>(a, acc[i][j], bias ? to_f32(bias[n]) : 0.f, m, n);
-    }
-  }
+constexpr int kTile = 64, kStep = 16, kThreads = 128, kPitch = kTile + 4;
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 both(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return ((f32x2)b << 32) | b;
 }
 
 template <typename T>
-cudaError_t launch_t(const LinearArgs& a, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads) linear_simt_kernel(LinearArgs a) {
+  // the tiles, [column][row]; then the partial sums [row of y][column]
+  __shared__ __align__(16) union {
+    struct {
+      float x[2][kStep][kPitch], w[2][kStep][kPitch];
+    };
+    float part[kTile][kTile];
+  } s;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
+  const long long n0 = (long long)blockIdx.x * kTile, m0 = (long long)blockIdx.y * kTile;
+  const T* x = static_cast<const T*>(a.x);
+  const T* w = static_cast<const T*>(a.w);
+  const int steps = (a.K + kStep - 1) / kStep;
+  const int s0 = (int)((long long)steps * rank / ranks), s1 = (int)((long long)steps * (rank + 1) / ranks);
+
+  // a thread fetches column c of rows r, r + 8, ...
+  const int c = tid & 15, r = tid >> 4;
+  float fx[8], fw[8];
+  auto fetch = [&](int step) {
+    const int k = step * kStep + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long m = m0 + r + i * 8, n = n0 + r + i * 8;
+      fx[i] = k < a.K && m < a.M ? to_f32(x[m * a.ldx + k]) : 0.f;
+      fw[i] = k < a.K && n < a.N ? to_f32(w[n * a.ldw + k]) : 0.f;
+    }
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s.x[b][c][r + i * 8] = fx[i];
+      s.w[b][c][r + i * 8] = fw[i];
+    }
+  };
+  f32x2 acc[8][2] = {};  // rows ty * 8 + i, columns tx * 4 + 2 j, + 1
+  if (s0 < s1) {
+    fetch(s0);
+    put(0);
+  }
+  __syncthreads();
+  for (int step = s0; step < s1; ++step) {
+    const int b = (step - s0) & 1;
+    if (step + 1 < s1) fetch(step + 1);
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      const float4 x0 = *reinterpret_cast<const float4*>(&s.x[b][k][ty * 8]);
+      const float4 x1 = *reinterpret_cast<const float4*>(&s.x[b][k][ty * 8 + 4]);
+      const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(&s.w[b][k][tx * 4]);
+      const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f32x2 xx = both(xs[i]);
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][0]) : "l"(xx), "l"(ww.x));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][1]) : "l"(xx), "l"(ww.y));
+      }
+    }
+    if (step + 1 < s1) put(b ^ 1);
+    __syncthreads();
+  }
+  const T* bias = static_cast<const T*>(a.bias);
+  auto out = [&](float z, int row, int col) {
+    const long long m = m0 + row, n = n0 + col;
+    if (m < a.M && n < a.N) finish<T>(a, z, bias ? to_f32(bias[n]) : 0.f, m, (int)n);
+  };
+  if (ranks == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        out(__uint_as_float((uint32_t)(acc[i][j >> 1] >> (32 * (j & 1)))), ty * 8 + i, tx * 4 + j);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<ulonglong2*>(&s.part[ty * 8 + i][tx * 4]) = make_ulonglong2(acc[i][0], acc[i][1]);
+  cluster_sync();
+  uint32_t from[8];
+#pragma unroll
+  for (uint32_t q = 0; q < 8; ++q) from[q] = map_to_rank(smem_u32(&s.part[0][0]), q < ranks ? q : 0);
+  // rank q finishes rows q, q + ranks, ..
+  for (int i = tid; i < kTile / (int)ranks * kTile; i += kThreads) {
+    const int row = i / kTile * (int)ranks + (int)rank, col = i % kTile;
+    float v[8];
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q) v[q] = q < ranks ? ld_cluster_f32(from[q] + (row * kTile + col) * 4) : 0.f;
+    float z = v[0];
+#pragma unroll
+    for (uint32_t q = 1; q < 8; ++q) z += v[q];
+    out(z, row, col);
+  }
+  cluster_sync();  // no CTA leaves while its sums are read
+}
+
+template <typename T>
+cudaError_t launch_t(const LinearArgs& a, int sms, cudaStream_t s) {
   // gridDim.y holds 65,535 tiles of rows: more rows go in several launches
   constexpr int kRows = 65535 * kTile;
   for (long long m = 0; m < a.M; m += kRows) {
@@ -66,9 +132,22 @@ cudaError_t launch_t(const LinearArgs& a, cudaStream_t s) {
     if (a.residual) b.residual = static_cast<const T*>(a.residual) + m * a.ldr;
     b.y = static_cast<T*>(a.y) + m * a.ldy;
     b.M = a.M - m < kRows ? (int)(a.M - m) : kRows;
-    const dim3 grid((a.N + kTile - 1) / kTile, (b.M + kTile - 1) / kTile);
-    linear_simt_kernel<T><<<grid, 256, 0, s>>>(b);
-    const cudaError_t e = cudaGetLastError();
+    const long long nt = (b.N + kTile - 1LL) / kTile, mt = (b.M + kTile - 1LL) / kTile;
+    const int steps = (b.K + kStep - 1) / kStep;
+    int split = 1;
+    while (split < 8 && split * 8 <= steps && nt * mt * split * 2 <= 4LL * sms) split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nt, (unsigned)mt, split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = split;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_simt_kernel<T>, b);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -76,8 +155,8 @@ cudaError_t launch_t(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, cudaStream_t s) {
-  return dtype == KDA_BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
+cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, int sms, cudaStream_t s) {
+  return dtype == KDA_BF16 ? launch_t<__nv_bfloat16>(a, sms, s) : launch_t<float>(a, sms, s);
 }
 
 }  // namespace kda

@@ -390,14 +390,6 @@ bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  static int count[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (count[dev] == 0) cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev);
-  return count[dev] > 0 ? count[dev] : 152;
-}
-
 bool fill(Tc& t, const LinearArgs& a, int* status, int rows_w, int box_w, int rows_x, int box_x) {
   t.a = a;
   t.status = status;
@@ -408,13 +400,12 @@ bool fill(Tc& t, const LinearArgs& a, int* status, int rows_w, int box_w, int ro
 }
 
 template <int BN>
-cudaError_t launch_pair(const LinearArgs& a, int* status, cudaStream_t s) {
+cudaError_t launch_pair(const LinearArgs& a, int pairs, int* status, cudaStream_t s) {
   const cudaError_t e = allow_smem<linear_pair_kernel<BN>>(Pair<BN>::kSmem);
   if (e != cudaSuccess) return e;
   Tc t;
   if (!fill(t, a, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
   const long long tiles = (long long)t.n_tiles * t.m_tiles;
-  const int pairs = sm_count() / 2;
   linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads, Pair<BN>::kSmem, s>>>(t);
   return cudaGetLastError();
 }
@@ -450,27 +441,30 @@ bool linear_tc_takes(const LinearArgs& a, int dtype) {
          a.ldw < (1LL << 38);
 }
 
-cudaError_t launch_linear_tc(const LinearArgs& a, int* status, cudaStream_t s) {
-  const int k_blocks = (a.K + 63) / 64, sms = sm_count();
-  // Pairs of CTAs where their tiles fill the SMs, with the width of tile whose waves cost least.
-  const long long rows = (a.N + 255LL) / 256, pairs = sms / 2;
+cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
+  const int k_blocks = (a.K + 63) / 64;
+  // Pairs of CTAs where their tiles fill the SMs, with the width of tile whose waves cost least.  A
+  // tile's time hardly falls with its width, since the rows of w have to come all the same: at
+  // 8192 x 8192 x 8192 a wave took 41.5, 38.5, 36.6, 35.8, 35.2 us for 256, 224, 192, 160, 128.
+  const long long rows = (a.N + 255LL) / 256;
+  const int pairs = sms / 2;
   if (rows * ((a.M + 127LL) / 128) >= pairs) {
     long long best = 0;
     int width = 0;
     for (int bn : {256, 224, 192, 160, 128}) {
       const long long tiles = rows * ((a.M + bn - 1LL) / bn);
-      const long long cost = (tiles + pairs - 1) / pairs * bn;
+      const long long cost = (tiles + pairs - 1) / pairs * (448 + bn);
       if (!width || cost < best) {
         best = cost;
         width = bn;
       }
     }
     switch (width) {
-      case 256: return launch_pair<256>(a, status, s);
-      case 224: return launch_pair<224>(a, status, s);
-      case 192: return launch_pair<192>(a, status, s);
-      case 160: return launch_pair<160>(a, status, s);
-      default: return launch_pair<128>(a, status, s);
+      case 256: return launch_pair<256>(a, pairs, status, s);
+      case 224: return launch_pair<224>(a, pairs, status, s);
+      case 192: return launch_pair<192>(a, pairs, status, s);
+      case 160: return launch_pair<160>(a, pairs, status, s);
+      default: return launch_pair<128>(a, pairs, status, s);
     }
   }
   // Else K split over the CTAs of a cluster until there are two CTAs per SM.
