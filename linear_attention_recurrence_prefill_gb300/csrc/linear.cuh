@@ -53,6 +53,47 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float z, float bias,
   static_cast<T*>(a.y)[m * a.ldy + n] = from_f32<T>(z);
 }
 
+// Four neighbouring channels n .. of token m, those below N: as one access where y (and the
+// residual) allow it, which `wide` says (rows and addresses a multiple of four elements).
+__device__ __forceinline__ bool wide4(const LinearArgs& a, size_t elem) {
+  auto ok = [&](const void* p, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & (4 * elem - 1)) == 0 && (ld & 3) == 0;
+  };
+  return ok(a.y, a.ldy) && (!a.residual || ok(a.residual, a.ldr));
+}
+template <typename T>
+__device__ __forceinline__ void finish4(const LinearArgs& a, bool wide, float4 z, float4 bias,
+                                        long long m, int n) {
+  if (wide && n + 3 < a.N) {
+    struct alignas(4 * sizeof(T)) V {
+      T e[4];
+    };
+    float v[4] = {z.x + bias.x, z.y + bias.y, z.z + bias.z, z.w + bias.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = activate<sizeof(T) == 2>(v[i], a.act);
+    if (a.residual) {
+      const V r = *reinterpret_cast<const V*>(static_cast<const T*>(a.residual) + m * a.ldr + n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += to_f32(r.e[i]);
+    }
+    V y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.e[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<V*>(static_cast<T*>(a.y) + m * a.ldy + n) = y;
+    return;
+  }
+  if (n < a.N) finish<T>(a, z.x, bias.x, m, n);
+  if (n + 1 < a.N) finish<T>(a, z.y, bias.y, m, n + 1);
+  if (n + 2 < a.N) finish<T>(a, z.z, bias.z, m, n + 2);
+  if (n + 3 < a.N) finish<T>(a, z.w, bias.w, m, n + 3);
+}
+template <typename T>
+__device__ __forceinline__ float4 bias4(const LinearArgs& a, int n) {
+  const T* b = static_cast<const T*>(a.bias);
+  auto at = [&](int i) { return b && n + i < a.N ? to_f32(b[n + i]) : 0.f; };
+  return make_float4(at(0), at(1), at(2), at(3));
+}
+
 // Launchers, for a device of `sms` SMs; each returns the launch's cudaError_t.
 cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
 // Up to four rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.

@@ -265,16 +265,16 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = tmem_base;
-  // this CTA's part of K: one block at least
-  const int kb0 = (int)((long long)t.k_blocks * rank / ranks);
-  const int blocks = (int)((long long)t.k_blocks * (rank + 1) / ranks) - kb0;
+  // this CTA's part of K: every ranks-th block (one at least), so that the cluster reads rows of w
+  // in pieces of ranks * 128 bytes
+  const int blocks = (t.k_blocks - (int)rank + (int)ranks - 1) / (int)ranks;
 
   bool ok = true;
   if (warp == kWarpLoad && lane == 0) {
     const int n0 = blockIdx.x * (int)kRowsA, m0 = blockIdx.y * BN;
     int it = 0;
     for (; it < blocks; ++it) {
-      const int s = it % kStages, x = (kb0 + it) * (int)kBlockK;
+      const int s = it % kStages, x = (it * (int)ranks + (int)rank) * (int)kBlockK;
       if (it >= kStages && !mbar_wait_soon(&empty[s], (it / kStages - 1) & 1, kSpins)) {
         ok = false;
         break;
@@ -330,24 +330,28 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
   __syncwarp();
   cluster_sync();
   if (warp < 4) {
-    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
-    const int n = blockIdx.x * (int)kRowsA + warp * 32 + lane;
+    // four neighbouring channels per thread, a column per warp
+    const int n = blockIdx.x * (int)kRowsA + lane * 4;
     const long long m0 = (long long)blockIdx.y * BN;
     const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
-    const float b = bias && n < t.a.N ? to_f32(bias[n]) : 0.f;
-    const uint32_t part = smem_u32(ring) + (warp * 32 + lane) * 4;
+    const bool wide = wide4(t.a, 2);
+    const float4 b = bias4<__nv_bfloat16>(t.a, n);
+    const uint32_t part = smem_u32(ring) + lane * 16;
     uint32_t from[8];
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r) from[r] = map_to_rank(part, r < ranks ? r : 0);
-#pragma unroll 4
-    for (int c = rank; c < cols; c += ranks) {
-      float v[8];
+#pragma unroll 2
+    for (int c = rank + warp * ranks; c < cols; c += 4 * ranks) {
+      float4 v[8];
 #pragma unroll
-      for (uint32_t r = 0; r < 8; ++r) v[r] = r < ranks ? ld_cluster_f32(from[r] + c * kRowsA * 4) : 0.f;
-      float z = v[0];
+      for (uint32_t r = 0; r < 8; ++r)
+        v[r] = r < ranks ? ld_cluster_f32x4(from[r] + c * kRowsA * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 z = v[0];
 #pragma unroll
-      for (uint32_t r = 1; r < 8; ++r) z += v[r];
-      if (n < t.a.N) finish<__nv_bfloat16>(t.a, z, b, m0 + c, n);
+      for (uint32_t r = 1; r < 8; ++r) {
+        z.x += v[r].x; z.y += v[r].y; z.z += v[r].z; z.w += v[r].w;
+      }
+      finish4<__nv_bfloat16>(t.a, wide, z, b, m0 + c, n);
     }
   }
   fence_before_sync();
@@ -443,12 +447,13 @@ bool linear_tc_takes(const LinearArgs& a, int dtype) {
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
   const int k_blocks = (a.K + 63) / 64;
-  // Pairs of CTAs where their tiles fill the SMs, with the width of tile whose waves cost least.  A
+  // Pairs of CTAs where their tiles fill half of the SMs at least (4096 x 4096 weights: 25 against
+  // 34 us with 512 tokens, 25 against 21 us with 256), with the width of tile whose waves cost least.  A
   // tile's time hardly falls with its width, since the rows of w have to come all the same: at
   // 8192 x 8192 x 8192 a wave took 41.5, 38.5, 36.6, 35.8, 35.2 us for 256, 224, 192, 160, 128.
   const long long rows = (a.N + 255LL) / 256;
   const int pairs = sms / 2;
-  if (rows * ((a.M + 127LL) / 128) >= pairs) {
+  if (rows * ((a.M + 127LL) / 128) >= pairs / 2) {
     long long best = 0;
     int width = 0;
     for (int bn : {256, 224, 192, 160, 128}) {
