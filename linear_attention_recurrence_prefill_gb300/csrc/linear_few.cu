@@ -1,6 +1,6 @@
 // linear_few.cu -- y = act(x w^T + bias) + residual for up to two rows of x in bf16, four in fp32
-// (the next token of a few sequences), where w is read once and that is all the time there is: fp32 sums on the CUDA
-// cores, w streamed in 16-byte loads.
+// (the next token of a few sequences), where reading w is all the time there is: fp32 sums on the
+// CUDA cores, w streamed in 16-byte loads.
 //
 // A warp takes kRows neighbouring rows of w; a lane its vectors of 16 bytes, kUnroll of them per
 // row in flight (4 KB per warp).  Where w has too few rows to give every SM 16 warps, the warps of

@@ -2,8 +2,8 @@
 // whose rows the tensor-core path cannot fetch (addresses or strides that are not multiples of 16
 // bytes).
 //
-// A CTA of 128 threads per 64 x 64 tile of y, 8 x 4 sums per thread as pairs (fma.rn.f32x2): three
-// 16-byte reads of shared memory for 32 products.  x and w pass through shared memory 16 columns at
+// A CTA of 128 threads per 64 x 64 tile of y, 8 x 4 sums per thread as pairs of rows
+// (fma.rn.f32x2): three 16-byte reads of shared memory for 32 products.  x and w pass through shared memory 16 columns at
 // a time, the next ones fetched into registers meanwhile.  Where there are too few tiles to give
 // every SM two CTAs, the CTAs of a cluster share a tile, each takes a part of K, and the sums meet
 // in distributed shared memory, added in the order of the ranks.
@@ -27,7 +27,8 @@ __device__ __forceinline__ f32x2 both(float x) {
   return ((f32x2)b << 32) | b;
 }
 
-template <typename T>
+// kVec: fp32 rows of x and w that 16-byte loads can fetch (K, too, a multiple of four).
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) linear_simt_kernel(LinearArgs a) {
   // the tiles, [column][row]; then the partial sums [row of y][column]
   __shared__ __align__(16) union {
@@ -44,26 +45,36 @@ __global__ void __launch_bounds__(kThreads) linear_simt_kernel(LinearArgs a) {
   const int steps = (a.K + kStep - 1) / kStep;
   const int s0 = (int)((long long)steps * rank / ranks), s1 = (int)((long long)steps * (rank + 1) / ranks);
 
-  // a thread fetches column c of rows r, r + 8, ...
-  const int c = tid & 15, r = tid >> 4;
-  float fx[8], fw[8];
+  // a thread fetches column c of rows r, r + 8, ..., or columns c .. c + 3 of rows r and r + 32
+  constexpr int kFetch = 8, kApart = kVec ? 32 : 8, kWide = kVec ? 4 : 1;
+  const int c = kVec ? (tid & 3) * 4 : tid & 15, r = kVec ? tid >> 2 : tid >> 4;
+  float fx[kFetch], fw[kFetch];
   auto fetch = [&](int step) {
     const int k = step * kStep + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long m = m0 + r + i * 8, n = n0 + r + i * 8;
-      fx[i] = k < a.K && m < a.M ? to_f32(x[m * a.ldx + k]) : 0.f;
-      fw[i] = k < a.K && n < a.N ? to_f32(w[n * a.ldw + k]) : 0.f;
+    for (int i = 0; i < kFetch / kWide; ++i) {
+      const long long m = m0 + r + i * kApart, n = n0 + r + i * kApart;
+      const bool mi = k < a.K && m < a.M, ni = k < a.K && n < a.N;
+      if constexpr (kVec) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(&fx[4 * i]) = mi ? *reinterpret_cast<const float4*>(&x[m * a.ldx + k]) : zero;
+        *reinterpret_cast<float4*>(&fw[4 * i]) = ni ? *reinterpret_cast<const float4*>(&w[n * a.ldw + k]) : zero;
+      } else {
+        fx[i] = mi ? to_f32(x[m * a.ldx + k]) : 0.f;
+        fw[i] = ni ? to_f32(w[n * a.ldw + k]) : 0.f;
+      }
     }
   };
   auto put = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s.x[b][c][r + i * 8] = fx[i];
-      s.w[b][c][r + i * 8] = fw[i];
-    }
+    for (int i = 0; i < kFetch / kWide; ++i)
+#pragma unroll
+      for (int j = 0; j < kWide; ++j) {
+        s.x[b][c + j][r + i * kApart] = fx[i * kWide + j];
+        s.w[b][c + j][r + i * kApart] = fw[i * kWide + j];
+      }
   };
-  f32x2 acc[8][2] = {};  // rows ty * 8 + i, columns tx * 4 + 2 j, + 1
+  f32x2 acc[4][4] = {};  // rows ty * 8 + 2 i, + 1, column tx * 4 + j
   if (s0 < s1) {
     fetch(s0);
     put(0);
@@ -74,20 +85,19 @@ __global__ void __launch_bounds__(kThreads) linear_simt_kernel(LinearArgs a) {
     if (step + 1 < s1) fetch(step + 1);
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
-      const float4 x0 = *reinterpret_cast<const float4*>(&s.x[b][k][ty * 8]);
-      const float4 x1 = *reinterpret_cast<const float4*>(&s.x[b][k][ty * 8 + 4]);
-      const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(&s.w[b][k][tx * 4]);
-      const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      const ulonglong2 x0 = *reinterpret_cast<const ulonglong2*>(&s.x[b][k][ty * 8]);
+      const ulonglong2 x1 = *reinterpret_cast<const ulonglong2*>(&s.x[b][k][ty * 8 + 4]);
+      const float4 w4 = *reinterpret_cast<const float4*>(&s.w[b][k][tx * 4]);
+      const f32x2 xs[4] = {x0.x, x0.y, x1.x, x1.y}, ws[4] = {both(w4.x), both(w4.y), both(w4.z), both(w4.w)};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const f32x2 xx = both(xs[i]);
-        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][0]) : "l"(xx), "l"(ww.x));
-        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][1]) : "l"(xx), "l"(ww.y));
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][j]) : "l"(xs[i]), "l"(ws[j]));
     }
     if (step + 1 < s1) put(b ^ 1);
     __syncthreads();
   }
+  auto sum = [&](int i, int j) { return __uint_as_float((uint32_t)(acc[i >> 1][j] >> (32 * (i & 1)))); };
   const T* bias = static_cast<const T*>(a.bias);
   auto out = [&](float z, int row, int col) {
     const long long m = m0 + row, n = n0 + col;
@@ -98,12 +108,12 @@ __global__ void __launch_bounds__(kThreads) linear_simt_kernel(LinearArgs a) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        out(__uint_as_float((uint32_t)(acc[i][j >> 1] >> (32 * (j & 1)))), ty * 8 + i, tx * 4 + j);
+        out(sum(i, j), ty * 8 + i, tx * 4 + j);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<ulonglong2*>(&s.part[ty * 8 + i][tx * 4]) = make_ulonglong2(acc[i][0], acc[i][1]);
+    *reinterpret_cast<float4*>(&s.part[ty * 8 + i][tx * 4]) = make_float4(sum(i, 0), sum(i, 1), sum(i, 2), sum(i, 3));
   cluster_sync();
   uint32_t from[8];
 #pragma unroll
@@ -147,7 +157,14 @@ cudaError_t launch_t(const LinearArgs& a, int sms, cudaStream_t s) {
     attr[0].val.clusterDim.z = split;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_simt_kernel<T>, b);
+    cudaError_t e;
+    if constexpr (sizeof(T) == 4) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(b.x) | reinterpret_cast<uintptr_t>(b.w);
+      const bool vec = (at & 15) == 0 && b.ldx % 4 == 0 && b.ldw % 4 == 0 && b.K % 4 == 0;
+      e = cudaLaunchKernelEx(&cfg, vec ? linear_simt_kernel<T, true> : linear_simt_kernel<T, false>, b);
+    } else {
+      e = cudaLaunchKernelEx(&cfg, linear_simt_kernel<T, false>, b);
+    }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
