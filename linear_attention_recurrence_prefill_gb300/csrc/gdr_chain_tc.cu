@@ -148,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         tma_load_3d(st + L::kKAt + i * L::kRows, &t.tm_k, i * 64, hk, row, &full[b]);
         tma_load_3d(st + L::kQAt + i * L::kRows, &t.tm_q, i * 64, hk, row, &full[b]);
       }
-      bulk_g2s(st, t.ws + ((size_t)(base + c) * a.Hv + h) * kBlock, kBlock, &full[b]);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         tma_load_3d(st + L::kVAt + i * L::kRows, &t.tm_v, slice * (int)kDv + i * 64, h, row, &full[b]);
+      if (c == 0) grid_wait_prerequisites();  // prep's blocks
+      bulk_g2s(st, t.ws + ((size_t)(base + c) * a.Hv + h) * kBlock, kBlock, &full[b]);
     }
     // loads in flight land before shared memory is released
     if (!ok)
@@ -506,8 +507,7 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
       !encode(&t.tm_o, a.o, a.T_total, a.Hv, a.dv, (long long)a.Hv * a.dv, kC))
     return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (int)kDv);
-  gdr_chain_tc_kernel<DK><<<grid, kThreads, Layout<DK>::kSmem, s>>>(t);
-  return cudaGetLastError();
+  return launch_behind_prep(gdr_chain_tc_kernel<DK>, grid, kThreads, Layout<DK>::kSmem, s, t);
 }
 
 }  // namespace

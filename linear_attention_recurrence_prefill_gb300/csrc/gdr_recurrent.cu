@@ -20,34 +20,47 @@ namespace {
 
 constexpr int kRecWarps = 4;
 
-// R consecutive elements (R * sizeof(T) a multiple of 8 bytes, at least 8-byte aligned)
+// R consecutive elements as they lie (R * sizeof(T) a multiple of 8 bytes, so aligned at least)
 template <int R, typename T>
-__device__ __forceinline__ void load_row(float (&x)[R], const T* p) {
-  constexpr int kBytes = R * (int)sizeof(T);
-  if constexpr (kBytes % 16 == 0) {
-    uint4 raw[kBytes / 16];
+struct Row {
+  uint2 raw[R * (int)sizeof(T) / 8];
+  __device__ __forceinline__ void load(const T* p) {
+    constexpr int n = R * (int)sizeof(T) / 16;
+    if constexpr (n > 0) {
 #pragma unroll
-    for (int i = 0; i < kBytes / 16; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* e = reinterpret_cast<const T*>(raw);
-#pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = to_f32(e[i]);
-  } else {
-    uint2 raw[kBytes / 8];
-#pragma unroll
-    for (int i = 0; i < kBytes / 8; ++i) raw[i] = reinterpret_cast<const uint2*>(p)[i];
-    const T* e = reinterpret_cast<const T*>(raw);
-#pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = to_f32(e[i]);
+      for (int i = 0; i < n; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        raw[2 * i] = make_uint2(v.x, v.y);
+        raw[2 * i + 1] = make_uint2(v.z, v.w);
+      }
+    } else {
+      raw[0] = *reinterpret_cast<const uint2*>(p);
+    }
   }
-}
-
-template <int R>
-struct Token {
-  float k[R], q[R], v[4], la, b;
+  __device__ __forceinline__ void widen(float (&x)[R]) const {
+#pragma unroll
+    for (int i = 0; i < R * (int)sizeof(T) / 4; ++i) {
+      const uint32_t w = i & 1 ? raw[i / 2].y : raw[i / 2].x;
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(w);
+      } else {
+        x[2 * i] = __uint_as_float(w << 16);
+        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+  }
 };
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(kRecWarps * 32) gdr_recurrent_kernel(GdrArgs a) {
+template <int R, typename T>
+struct Token {
+  Row<R, T> k, q;
+  Row<4, T> v;
+  float la, b;
+};
+
+// kMany: any number of tokens per sequence, the next one's rows fetched ahead; else one.
+template <int DK, typename T, bool kMany>
+__global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_kernel(GdrArgs a) {
   constexpr int R = DK / 8;  // rows of the state per lane
   const int lane = threadIdx.x & 31, rg = lane >> 2, c4 = lane & 3;
   const int slices = a.dv / 16;
@@ -72,19 +85,26 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdr_recurrent_kernel(GdrArgs a
   const T* v = static_cast<const T*>(a.v) + (size_t)h * a.dv + col;
   const T* beta = static_cast<const T*>(a.beta) + h;
   T* o = static_cast<T*>(a.o) + (size_t)h * a.dv + col;
-  auto load = [&](Token<R>& x, int t) {
-    load_row<R>(x.k, k + (size_t)t * a.ldk);
-    load_row<R>(x.q, q + (size_t)t * a.ldq);
-    load_row<4>(x.v, v + (size_t)t * a.ldv);
+  auto load = [&](Token<R, T>& x, int t) {
+    x.k.load(k + (size_t)t * a.ldk);
+    x.q.load(q + (size_t)t * a.ldq);
+    x.v.load(v + (size_t)t * a.ldv);
     x.la = a.log_alpha[(size_t)t * a.Hv + h];
     x.b = to_f32(beta[(size_t)t * a.Hv]);
   };
 
-  Token<R> next;
+  Token<R, T> next;
   if (t0 < t1) load(next, t0);
-  for (int t = t0; t < t1; ++t) {
-    const Token<R> x = next;
-    if (t + 1 < t1) load(next, t + 1);
+  for (int t = t0; t < (kMany ? t1 : t0 + 1); ++t) {
+    struct {
+      float k[R], q[R], v[4], la, b;
+    } x;
+    next.k.widen(x.k);
+    next.q.widen(x.q);
+    next.v.widen(x.v);
+    x.la = next.la;
+    x.b = next.b;
+    if (kMany && t + 1 < t1) load(next, t + 1);
     // |k|^2, |q|^2, k.q over all rows
     float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll
@@ -150,15 +170,22 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdr_recurrent_kernel(GdrArgs a
     *reinterpret_cast<float4*>(a.S_T + mat + (size_t)i * a.dv) = s[i];
 }
 
+template <int DK, typename T>
+void launch_dk(const GdrArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
+  // one token per sequence: equal lengths of one
+  if (!a.cu_seqlens && a.T_total == a.N) gdr_recurrent_kernel<DK, T, false><<<grid, block, 0, s>>>(a);
+  else gdr_recurrent_kernel<DK, T, true><<<grid, block, 0, s>>>(a);
+}
+
 template <typename T>
 cudaError_t launch_t(const GdrArgs& a, cudaStream_t s) {
   const long long warps = (long long)a.N * a.Hv * (a.dv / 16);
   const long long blocks = (warps + kRecWarps - 1) / kRecWarps;
   const dim3 grid((unsigned)blocks), block(kRecWarps * 32);
   switch (a.dk) {
-    case 32: gdr_recurrent_kernel<32, T><<<grid, block, 0, s>>>(a); break;
-    case 64: gdr_recurrent_kernel<64, T><<<grid, block, 0, s>>>(a); break;
-    case 128: gdr_recurrent_kernel<128, T><<<grid, block, 0, s>>>(a); break;
+    case 32: launch_dk<32, T>(a, grid, block, s); break;
+    case 64: launch_dk<64, T>(a, grid, block, s); break;
+    case 128: launch_dk<128, T>(a, grid, block, s); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

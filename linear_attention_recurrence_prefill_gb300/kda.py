@@ -516,36 +516,39 @@ def _expect(x, name, shape, dtype):
 def _gdr_call(host, q, k, v, log_alpha, beta, S0, S_T, slots, o, decay_scale, decay_bias, N,
               l2norm_qk, beta_is_logit, decay_from_logit, q_scale, eps_l2):
     """Checks what the two entry points share; returns (o, options, sizes)."""
-    shape, dtype = q.shape, q.dtype
-    if k.shape != shape or v.shape[:-2] != shape[:-2]:
+    shape, values, dtype = q.shape, v.shape, q.dtype
+    if k.shape != shape or values[:-2] != shape[:-2]:
         raise ValueError("q and k [..., H_k, d_k] and v [..., H_v, d_v] of the same tokens")
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v of one dtype")
     Hk, dk = shape[-2:]
-    Hv, dv = v.shape[-2:]
-    rows = tuple(shape[:-2])
-    _expect(log_alpha, "log_alpha", (*rows, Hv), host.f32)
-    _expect(beta, "beta", (*rows, Hv), dtype)
+    Hv, dv = values[-2:]
+    per_head = values[:-1]
+    _expect(log_alpha, "log_alpha", per_head, host.f32)
+    _expect(beta, "beta", per_head, dtype)
     if o is None:
-        o = host.empty((*rows, Hv, dv), dtype=dtype, device=q.device)
+        o = host.empty(values, dtype=dtype, device=q.device)
     else:
-        _expect(o, "o", (*rows, Hv, dv), dtype)
-    n_slots = N
+        _expect(o, "o", values, dtype)
+    n_slots, at = N, None
     if slots is not None:
         _expect(slots, "slots", (N,), host.i32)
-        n_slots = S_T.shape[0]
+        n_slots, at = S_T.shape[0], slots.data_ptr()
     states = (n_slots, Hv, dk, dv)
     _expect(S_T, "state", states, host.f32)
     if S0 is not None and S0 is not S_T:
         _expect(S0, "S0", states, host.f32)
+    A = b = None
     if decay_scale is not None:
         _expect(decay_scale, "decay_scale", (Hv,), host.f32)
+        A = decay_scale.data_ptr()
     if decay_bias is not None:
         _expect(decay_bias, "decay_bias", (Hv,), host.f32)
+        b = decay_bias.data_ptr()
     opt = kda_gdr_options(
-        1 if l2norm_qk else 0, 1 if beta_is_logit else 0, 1 if decay_from_logit else 0,
-        _ptr(decay_scale), _ptr(decay_bias), q_scale, eps_l2, _token_stride(q, "q"),
-        _token_stride(k, "k"), _token_stride(v, "v"), _ptr(slots), n_slots)
+        1 if l2norm_qk else 0, 1 if beta_is_logit else 0, 1 if decay_from_logit else 0, A, b,
+        q_scale, eps_l2, _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"), at,
+        n_slots)
     return o, opt, (Hk, Hv, dk, dv)
 
 
