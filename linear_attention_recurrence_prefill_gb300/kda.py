@@ -439,7 +439,7 @@ class _Host:
                                                 lib.kda_gdr_prefill)
         self.codes = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
         self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
-        self.empty = torch.empty
+        self.empty, self.empty_like = torch.empty, torch.empty_like
         self.current_device = torch._C._cuda_getDevice
         # (device) -> address of the current stream
         self.current_stream = torch._C._cuda_getCurrentRawStream
@@ -527,7 +527,8 @@ def _gdr_call(host, q, k, v, log_alpha, beta, S0, S_T, slots, o, decay_scale, de
     _expect(log_alpha, "log_alpha", per_head, host.f32)
     _expect(beta, "beta", per_head, dtype)
     if o is None:
-        o = host.empty(values, dtype=dtype, device=q.device)
+        o = (host.empty_like(v) if v.is_contiguous()
+             else host.empty(values, dtype=dtype, device=q.device))
     else:
         _expect(o, "o", values, dtype)
     n_slots, at = N, None
