@@ -381,9 +381,9 @@ enum {
  *
  * Sums, bias, activation and residual are in fp32, rounded once to dtype.
  * Pointers need the alignment of their elements; bf16 products run on the
- * tensor cores where x and w are 16-byte aligned with rows a multiple of 16
- * bytes apart, on the CUDA cores otherwise, and so do fp32 products.  M, N or
- * K may be 0 (K = 0: y = act(bias) + residual).
+ * tensor cores, fastest where x and w are 16-byte aligned with rows a multiple
+ * of 16 bytes apart, fp32 products on the CUDA cores.  M, N or K may be 0
+ * (K = 0: y = act(bias) + residual).
  */
 int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
                const void* residual, long long ldr, void* y, long long ldy, int M, int N, int K,

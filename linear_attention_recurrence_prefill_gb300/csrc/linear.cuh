@@ -99,7 +99,7 @@ cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, int sms, cudaStre
 // Up to four rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
 bool linear_few_takes(const LinearArgs& a, int dtype);
 cudaError_t launch_linear_few(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
-// bf16, x and w as above, any number of rows.
+// bf16, any alignment, any number of rows, K > 0.
 bool linear_tc_takes(const LinearArgs& a, int dtype);
 cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s);
 

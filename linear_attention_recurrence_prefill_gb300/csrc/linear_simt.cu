@@ -1,6 +1,5 @@
 // linear_simt.cu -- y = act(x w^T + bias) + residual on the CUDA cores: fp32 data, and bf16 data
-// whose rows the tensor-core path cannot fetch (addresses or strides that are not multiples of 16
-// bytes).
+// without columns (K = 0).
 //
 // A CTA of 128 threads per 64 x 64 tile of y, 8 x 4 sums per thread as pairs of rows
 // (fma.rn.f32x2): three 16-byte reads of shared memory for 32 products.  x and w pass through shared memory 16 columns at

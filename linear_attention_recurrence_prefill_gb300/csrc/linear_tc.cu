@@ -20,7 +20,9 @@
 //  * linear_split_kernel, where there are too few tiles to fill the GPU (few tokens, or a small
 //    product): the CTAs of a cluster share one tile, each takes a part of K, and the partial sums
 //    meet in distributed shared memory, added in the order of the ranks, so that results repeat
-//    to the bit.
+//    to the bit.  It also takes arrays that TMA cannot (rows that are no multiple of 16 bytes
+//    apart): eight warps then fill the ring, from aligned 16-byte loads that they shift into
+//    place.
 #include <cuda.h>
 
 #include <mutex>
@@ -33,7 +35,7 @@ namespace {
 
 using namespace umma;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192, kFillThreads = 320;
 constexpr int kWarpLoad = 4, kWarpMma = 5;
 constexpr uint32_t kRowsA = 128, kBlockK = 64;
 constexpr long long kSpins = 4000000000LL;  // ~2 s of clock cycles
@@ -237,8 +239,70 @@ constexpr uint32_t split_smem() {
   return kAlign + kStages * (kRowsA + BN) * kBlockK * 2;
 }
 
-template <int BN, int kStages>
-__global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_constant__ Tc t) {
+// The aligned 16 bytes at `at`, as far as they lie in the array [lo, hi).
+__device__ __forceinline__ uint4 part_of_array(uintptr_t at, uintptr_t lo, uintptr_t hi) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int i = 0; i < 8; ++i) {
+    const uintptr_t e = at + 2 * i;
+    if (e >= lo && e < hi) w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(e) << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 16 bytes from byte `off` (even) of a and b on.
+__device__ __forceinline__ uint4 shift_pieces(const uint4& a, const uint4& b, uint32_t off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = off & 2 ? __byte_perm(w[i], w[i + 1], 0x5432) : w[i];
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// kRows rows of 64 columns, from row r0 and column k0 on, into a tile of the ring, by 256 threads:
+// eight per row, 16 bytes each, from two aligned loads; zeros outside the array.
+template <int kRows>
+__device__ __forceinline__ void fill_tile(uint8_t* tile, const void* base, long long ld, int rows, int K,
+                                          long long r0, int k0, int tid) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(base), hi = lo + ((rows - 1) * ld + K) * 2;
+  const int g = tid & 7, k = k0 + g * 8;
+  // everything that the loads below touch lies in the array, except at its very ends
+  const long long last = r0 + kRows < rows ? r0 + kRows - 1 : rows - 1;
+  const bool inside = ((lo + (r0 * ld + k0) * 2) & ~(uintptr_t)15) >= lo && lo + (last * ld + k0 + 64) * 2 + 32 <= hi;
+  constexpr int kPasses = kRows < 32 ? 1 : kRows / 32, kBatch = kPasses < 4 ? kPasses : 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+    uint4 v[kBatch][2];
+    uint32_t off[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long r = r0 + (tid >> 3) + (i0 + i) * 32;
+      const uintptr_t at = lo + ((r < rows ? r : last) * ld + k) * 2;
+      off[i] = (uint32_t)at & 15;
+      const uintptr_t from = at - off[i];
+      if (inside) {
+        v[i][0] = *reinterpret_cast<const uint4*>(from);
+        v[i][1] = *reinterpret_cast<const uint4*>(from + 16);
+      } else {
+        v[i][0] = part_of_array(from, lo, hi);
+        v[i][1] = part_of_array(from + 16, lo, hi);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = (tid >> 3) + (i0 + i) * 32;
+      uint4 z = shift_pieces(v[i][0], v[i][1], off[i]);
+      uint32_t* w = &z.x;
+      const int left = r0 + row < rows ? K - k : 0;  // columns from here on that exist
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = left > 2 * e + 1 ? w[e] : left > 2 * e ? w[e] & 0xffffu : 0;
+      if (kRows >= 32 || row < kRows) *reinterpret_cast<uint4*>(tile + sw128_chunk(row, g, kRows)) = z;
+    }
+  }
+}
+
+template <int BN, int kStages, bool kTma>
+__global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_kernel(const __grid_constant__ Tc t) {
   constexpr uint32_t kStage = (kRowsA + BN) * kBlockK * 2;
   constexpr uint32_t kCols = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;
   static_assert(kStages * kStage >= BN * kRowsA * 4, "the partial sums fit in the ring");
@@ -251,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
   const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], kTma ? 1 : 8);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
@@ -269,9 +333,10 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
   // in pieces of ranks * 128 bytes
   const int blocks = (t.k_blocks - (int)rank + (int)ranks - 1) / (int)ranks;
 
+  const int n0 = blockIdx.x % t.n_tiles * (int)kRowsA, m0 = blockIdx.x / t.n_tiles * BN;
+
   bool ok = true;
-  if (warp == kWarpLoad && lane == 0) {
-    const int n0 = blockIdx.x * (int)kRowsA, m0 = blockIdx.y * BN;
+  if (kTma && warp == kWarpLoad && lane == 0) {
     int it = 0;
     for (; it < blocks; ++it) {
       const int s = it % kStages, x = (it * (int)ranks + (int)rank) * (int)kBlockK;
@@ -306,10 +371,25 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
     // everything issued is complete before the ring or TMEM is used again, or released
     mma_commit_if(lead, &done);
     mbar_wait(&done, 0, kSpins);
-  } else if (warp < 4) {
-    ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, kSpins));
+  } else if (warp < 4 || warp > kWarpMma) {
+    if constexpr (!kTma) {
+      const int tid = threadIdx.x - (warp < 4 ? 0 : 64);
+      for (int it = 0; it < blocks && ok; ++it) {
+        const int s = it % kStages, x = (it * (int)ranks + (int)rank) * (int)kBlockK;
+        if (it >= kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&empty[s], (it / kStages - 1) & 1, kSpins));
+        if (!ok) break;
+        uint8_t* dst = ring + s * kStage;
+        fill_tile<kRowsA>(dst, t.a.w, t.a.ldw, t.a.N, t.a.K, n0, x, tid);
+        fill_tile<BN>(dst + kRowsA * kBlockK * 2, t.a.x, t.a.ldx, t.a.M, t.a.K, m0, x, tid);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+    }
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&done, 0, kSpins));
     fence_after_sync();
-    if (ok) {
+    if (ok && warp < 4) {
       // partial sums [column][channel] over the ring, whose loads and products are done
       const uint32_t d = taddr(tmem, warp * 32, 0);
       float* part = reinterpret_cast<float*>(ring) + warp * 32 + lane;
@@ -331,9 +411,8 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
   cluster_sync();
   if (warp < 4) {
     // four neighbouring channels per thread, a column per warp
-    const int n = blockIdx.x * (int)kRowsA + lane * 4;
-    const long long m0 = (long long)blockIdx.y * BN;
-    const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
+    const int n = n0 + lane * 4;
+    const int cols = t.a.M - m0 < BN ? t.a.M - m0 : BN;
     const bool wide = wide4(t.a, 2);
     const float4 b = bias4<__nv_bfloat16>(t.a, n);
     const uint32_t part = smem_u32(ring) + lane * 16;
@@ -394,13 +473,14 @@ bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool fill(Tc& t, const LinearArgs& a, int* status, int rows_w, int box_w, int rows_x, int box_x) {
+bool fill(Tc& t, const LinearArgs& a, bool tma, int* status, int rows_w, int box_w, int rows_x, int box_x) {
   t.a = a;
   t.status = status;
   t.n_tiles = (a.N + rows_w - 1) / rows_w;
   t.m_tiles = (int)(((long long)a.M + rows_x - 1) / rows_x);
   t.k_blocks = (a.K + (int)kBlockK - 1) / (int)kBlockK;
-  return encode(&t.tm_w, a.w, a.N, a.K, a.ldw, box_w) && encode(&t.tm_x, a.x, a.M, a.K, a.ldx, box_x);
+  return !tma || (encode(&t.tm_w, a.w, a.N, a.K, a.ldw, box_w) &&
+                  encode(&t.tm_x, a.x, a.M, a.K, a.ldx, box_x));
 }
 
 template <int BN>
@@ -408,24 +488,24 @@ cudaError_t launch_pair(const LinearArgs& a, int pairs, int* status, cudaStream_
   const cudaError_t e = allow_smem<linear_pair_kernel<BN>>(Pair<BN>::kSmem);
   if (e != cudaSuccess) return e;
   Tc t;
-  if (!fill(t, a, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
+  if (!fill(t, a, true, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
   const long long tiles = (long long)t.n_tiles * t.m_tiles;
   linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads, Pair<BN>::kSmem, s>>>(t);
   return cudaGetLastError();
 }
 
-template <int BN, int kStages>
-cudaError_t launch_split(const LinearArgs& a, int* status, int split, cudaStream_t s) {
-  constexpr auto kern = linear_split_kernel<BN, kStages>;
+template <int BN, int kStages, bool kTma>
+cudaError_t launch_split_of(const LinearArgs& a, int* status, int split, cudaStream_t s) {
+  constexpr auto kern = linear_split_kernel<BN, kStages, kTma>;
   const cudaError_t e = allow_smem<kern>(split_smem<BN, kStages>());
   if (e != cudaSuccess) return e;
   Tc t;
-  if (!fill(t, a, status, kRowsA, kRowsA, BN, BN)) return cudaErrorInvalidValue;
+  if (!fill(t, a, kTma, status, kRowsA, kRowsA, BN, BN)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kTma ? kThreads : kFillThreads);
   cfg.dynamicSmemBytes = split_smem<BN, kStages>();
   cfg.stream = s;
-  cfg.gridDim = dim3(t.n_tiles, t.m_tiles, split);
+  cfg.gridDim = dim3((unsigned)((long long)t.n_tiles * t.m_tiles), 1, split);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
@@ -436,14 +516,25 @@ cudaError_t launch_split(const LinearArgs& a, int* status, int split, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, t);
 }
 
-}  // namespace
-
-bool linear_tc_takes(const LinearArgs& a, int dtype) {
-  if (dtype != KDA_BF16 || a.K < 1) return false;
+bool tma_takes(const LinearArgs& a) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w);
   return (at & 15) == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0 && a.ldx < (1LL << 38) &&
          a.ldw < (1LL << 38);
 }
+
+template <int BN, int kStages>
+cudaError_t launch_split(const LinearArgs& a, bool tma, int* status, int split, cudaStream_t s) {
+  return tma ? launch_split_of<BN, kStages, true>(a, status, split, s)
+             : launch_split_of<BN, kStages, false>(a, status, split, s);
+}
+
+}  // namespace
+
+bool linear_tc_takes(const LinearArgs& a, int dtype) {
+  return dtype == KDA_BF16 && a.K > 0 &&
+         (a.N + 127LL) / 128 * ((a.M + 15LL) / 16) <= 0x7fffffffLL;  // tiles in a grid
+}
+
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
   const int k_blocks = (a.K + 63) / 64;
@@ -453,7 +544,8 @@ cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStre
   // 8192 x 8192 x 8192 a wave took 41.5, 38.5, 36.6, 35.8, 35.2 us for 256, 224, 192, 160, 128.
   const long long rows = (a.N + 255LL) / 256;
   const int pairs = sms / 2;
-  if (rows * ((a.M + 127LL) / 128) >= pairs / 2) {
+  const bool tma = tma_takes(a);
+  if (tma && rows * ((a.M + 127LL) / 128) >= pairs / 2) {
     long long best = 0;
     int width = 0;
     for (int bn : {256, 224, 192, 160, 128}) {
@@ -478,10 +570,10 @@ cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStre
   int split = 1;
   while (split < 8 && split * 2 <= k_blocks && tiles * split * 2 <= 2LL * sms) split *= 2;
   switch (bn) {
-    case 16: return launch_split<16, 6>(a, status, split, s);
-    case 32: return launch_split<32, 5>(a, status, split, s);
-    case 64: return launch_split<64, 4>(a, status, split, s);
-    default: return launch_split<128, 3>(a, status, split, s);
+    case 16: return launch_split<16, 6>(a, tma, status, split, s);
+    case 32: return launch_split<32, 5>(a, tma, status, split, s);
+    case 64: return launch_split<64, 4>(a, tma, status, split, s);
+    default: return launch_split<128, 3>(a, tma, status, split, s);
   }
 }
 
