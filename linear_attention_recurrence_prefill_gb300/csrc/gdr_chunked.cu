@@ -287,19 +287,25 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
   }
   const int pair = warp >> 1, second = warp & 1;
   PrepHead& hd = s.head[pair];
-  // running sums of the log decays of head hg, by one warp
+  // running sums of the log decays of head hg, by one warp: two tokens per lane
   const __nv_bfloat16* beta = static_cast<const __nv_bfloat16*>(a.beta);
-  auto scan = [&](int hg) {
-    const int h = hk * G + hg;
-    Sum2 g[2];
-    float be[2];
+  float la[2], be[2];
+  auto fetch_decays = [&](int hg) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = lane * 2 + i;
-      const size_t at = (size_t)(t0 + (r < len ? r : 0)) * a.Hv + h;
-      const float la = a.log_alpha[at], b = to_f32(beta[at]);
-      g[i] = {r < len ? gdr_log_decay(a, la, h) : 0.f, 0.f};
-      be[i] = r < len ? (a.beta_is_logit ? sigmoidf_(b) : b) : 0.f;
+      const size_t at = (size_t)(t0 + (r < len ? r : 0)) * a.Hv + hk * G + hg;
+      la[i] = a.log_alpha[at];
+      be[i] = to_f32(beta[at]);
+    }
+  };
+  auto scan = [&](int hg, PrepHead& to) {
+    Sum2 g[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = lane * 2 + i < len;
+      g[i] = {in ? gdr_log_decay(a, la[i], hk * G + hg) : 0.f, 0.f};
+      to.beta[lane * 2 + i] = in ? (a.beta_is_logit ? sigmoidf_(be[i]) : be[i]) : 0.f;
     }
     g[1] = add2(g[0], g[1]);
     Sum2 before = {0.f, 0.f}, sum = g[1];  // of the lanes before this one
@@ -314,9 +320,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const Sum2 x = add2(before, g[i]);
-      hd.ghi[lane * 2 + i] = x.hi;
-      hd.glo[lane * 2 + i] = x.lo;
-      hd.beta[lane * 2 + i] = be[i];
+      to.ghi[lane * 2 + i] = x.hi;
+      to.glo[lane * 2 + i] = x.lo;
     }
   };
   // the factors of e^{g_i - g_j}, when the sums and the norms are there
@@ -332,9 +337,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
     for (int x = 1; x < 4; ++x)
       if (r < 16 * x) hd.e2[x - 1][r] = e2[x - 1];
   };
-  if (!second && pair < G) scan(pair);
+  // the first two heads: warps 0 and 1, which have the fewest tiles of the Grams
+  const bool scans = warp < 2 && warp < G;
+  if (scans) fetch_decays(warp);
   cp_async_wait_all();
   __syncthreads();
+  if (scans) scan(warp, s.head[warp]);
 
   // K K^T and Q K^T, 16 rows per warp, columns up to the diagonal block
   {
@@ -402,7 +410,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
   for (int hg = pair; hg < G; hg += 2) {
     if (hg >= 2) {
       named_sync(bar, 64);  // both warps are done with the last head
-      if (!second) scan(hg);
+      if (!second) {
+        fetch_decays(hg);
+        scan(hg, hd);
+      }
       named_sync(bar, 64);
       factors();
       named_sync(bar, 64);
