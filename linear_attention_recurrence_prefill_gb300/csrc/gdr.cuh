@@ -54,22 +54,33 @@ __device__ __forceinline__ int gdr_offset(const GdrArgs& a, int i) {
 // (every lane gets the answer).  False: the sequence is left out, because its
 // slot is negative, or (status word set) because its slot is out of range or
 // taken by an earlier sequence, its tokens are out of range, or the offsets
-// decrease at it or before it.
+// decrease at it or before it.  Up to 32 sequences take one round of loads, a
+// sequence per lane.
 __device__ __forceinline__ bool gdr_sequence(const GdrArgs& a, int n, int& t0, int& t1,
                                              int& slot) {
   const int lane = threadIdx.x & 31;
-  seq_range(a.cu_seqlens, a.N, a.T_total, n, t0, t1);
-  slot = n;
-  bool bad = t0 < 0 || t1 < t0 || t1 > a.T_total, found = false;
-  if (a.cu_seqlens)
-    for (int i = lane; i < n; i += 32) found |= a.cu_seqlens[i] > a.cu_seqlens[i + 1];
-  if (a.slots) {
-    slot = a.slots[n];
+  bool bad;
+  if (a.N <= 32) {
+    const int i = lane < a.N ? lane : a.N - 1;
+    const int off = gdr_offset(a, i), end = gdr_offset(a, i + 1), sl = a.slots ? a.slots[i] : i;
+    t0 = __shfl_sync(0xffffffffu, off, n);
+    t1 = __shfl_sync(0xffffffffu, end, n);
+    slot = __shfl_sync(0xffffffffu, sl, n);
     if (slot < 0) return false;
-    bad |= slot >= a.n_slots;
-    for (int i = lane; i < n; i += 32) found |= a.slots[i] == slot;
+    bad = t0 < 0 || t1 > a.T_total || (a.slots && slot >= a.n_slots) ||
+          __any_sync(0xffffffffu, (lane <= n && off > end) || (lane < n && sl == slot));
+  } else {
+    seq_range(a.cu_seqlens, a.N, a.T_total, n, t0, t1);
+    slot = a.slots ? a.slots[n] : n;
+    if (slot < 0) return false;
+    bad = t0 < 0 || t1 < t0 || t1 > a.T_total || (a.slots && slot >= a.n_slots);
+    bool found = false;
+    if (a.cu_seqlens)
+      for (int i = lane; i < n; i += 32) found |= a.cu_seqlens[i] > a.cu_seqlens[i + 1];
+    if (a.slots)
+      for (int i = lane; i < n; i += 32) found |= a.slots[i] == slot;
+    bad |= __any_sync(0xffffffffu, found);
   }
-  bad |= __any_sync(0xffffffffu, found);
   if (bad && lane == 0) atomicExch(a.status, KDA_ERR_SHAPE);
   return !bad;
 }

@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
   if (warp == 0) {
     // the sequence of this block: the last one whose base is not behind it, as far as the
     // offsets do not decrease (later sequences are left out)
-    int n = -1;
-    for (int i0 = 0; i0 < a.N; i0 += 32) {
+    int n = a.N == 1 ? 0 : -1;
+    for (int i0 = 0; i0 < a.N && a.N > 1; i0 += 32) {
       const int i = i0 + lane;
       const int off = i < a.N ? gdr_offset(a, i) : 0;
       const bool down = i < a.N && off > gdr_offset(a, i + 1);
