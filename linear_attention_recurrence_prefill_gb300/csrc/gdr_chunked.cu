@@ -82,13 +82,15 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
 // e^{g_i - g_j} off the diagonal blocks is e^{g_i - g_r} e^{g_r - g_j}, r the first row of i's
 // block: both exponents are <= 0, and the factors are vectors.
 constexpr int kPrepThreads = 128;
-constexpr int kPitchG = kC + 4;          // floats, Grams
+constexpr int kPitchG = kC + 8;          // floats, Grams: pairs of four rows meet no bank twice
 constexpr int kPitchD = 20, kDiag = 324;  // floats, diagonal blocks and from one to the next
 struct PrepHead {
   float ghi[kC], glo[kC], beta[kC];
   float e1[kC];      // e^{g_i - g_r}
-  float e2[3][kC];   // row block 1 + x: e^{g_r - g_j} ik_j, j < 16 (1 + x)
+  float e2[96];      // e^{g_r - g_j} ik_j, j < 16 x, of row blocks x = 1, 2, 3: from 0, 16, 48 on
 };
+
+__host__ __device__ constexpr int e2_at(int x) { return 8 * x * (x - 1); }
 
 template <int DK>
 struct PrepSmem {
@@ -201,7 +203,7 @@ __device__ __forceinline__ void invert_column(const PrepSmem<DK>& s, const PrepH
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int col = k * 16 + y * 8 + t * 2;
-        const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[i - 1][col]);
+        const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[e2_at(i) + col]);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float2 kk = *reinterpret_cast<const float2*>(&s.kk[i * 16 + x * 8 + g][col]);
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
     hd.e1[r] = e1;
 #pragma unroll
     for (int x = 1; x < 4; ++x)
-      if (r < 16 * x) hd.e2[x - 1][r] = e2[x - 1];
+      if (r < 16 * x) hd.e2[e2_at(x) + r] = e2[x - 1];
   };
   // the first two heads: warps 0 and 1, which have the fewest tiles of the Grams
   const bool scans = warp < 2 && warp < G;
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int col = jb * 16 + y * 8 + t * 2;
-          const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[ib - 1][col]);
+          const float2 e2 = *reinterpret_cast<const float2*>(&hd.e2[e2_at(ib) + col]);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float2 qk = *reinterpret_cast<const float2*>(&s.qk[ib * 16 + x * 8 + g][col]);
