@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&full[j & 1], (j / 2) & 1, kGdrSpins);
   } else if (warp == kWarpMma) {
     const uint32_t lead = elect_leader();
-    constexpr uint32_t idesc = idesc_f16(128, 64, true), idesc_v = idesc_f16(128, 64, true, true),
-                       idesc_d = idesc_f16(128, DK, true, false, true);
+    // products with the columns of T or P from 16 s on meet their rows from 16 s on only
+    constexpr uint32_t kBelow = 16 * 128 >> 4;  // 16 rows, in a descriptor's units
+    constexpr uint32_t idesc = idesc_f16(128, 64, true), idesc_d = idesc_f16(128, DK, true, false, true);
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, kGdrSpins));
       fence_after_sync();
@@ -175,8 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       for (uint32_t j = 2; j < 3; --j)
 #pragma unroll
         for (uint32_t s = 0; s < 4; ++s)
-          mma_ss_if(lead, tmem + kXuCol + (c & 1) * 64, vv + (s * 2048 >> 4), tt + ((j * kTile + s * 32) >> 4),
-                    idesc_v, s + 2 - j > 0);
+          mma_ss_if(lead, tmem + kXuCol + (c & 1) * 64 + 16 * s, vv + (s * 2048 >> 4),
+                    tt + ((j * kTile + s * 32) >> 4) + s * kBelow, idesc_f16(128, 64 - 16 * s, true, true),
+                    s + 2 - j > 0);
     };
     // Sums are cut, not rounded, as products are added: those of the smaller parts go first, while
     // a sum is small.
@@ -226,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
           for (uint32_t j = 0; j <= order; ++j)
 #pragma unroll
             for (uint32_t s = i, k = order - j; s < 4; s += 2)
-              mma_ts_if(lead, ucol, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4), idesc, 1);
+              mma_ts_if(lead, ucol + 16 * s, tmem + v_col(s, k), tt + ((j * kTile + s * 32) >> 4) + s * kBelow,
+                        idesc_f16(128, 64 - 16 * s, true), 1);
       }
       if (!ok) break;
       mma_commit_if(lead, &u_done);
@@ -257,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
         for (uint32_t j = 0; j < 2; ++j)
 #pragma unroll
           for (uint32_t k = 0; k < 2 - j; ++k)
-            mma_ts_if(lead, ycol, ucol + (s >> 1) * 32 + k * 16 + (s & 1) * 8, pp + ((j * kTile + s * 32) >> 4),
-                      idesc, 1);
+            mma_ts_if(lead, ycol + 16 * s, ucol + (s >> 1) * 32 + k * 16 + (s & 1) * 8,
+                      pp + ((j * kTile + s * 32) >> 4) + s * kBelow, idesc_f16(128, 64 - 16 * s, true), 1);
       mma_commit_if(lead, &o_done);
       mma_commit_if(lead, &empty[b]);
     }

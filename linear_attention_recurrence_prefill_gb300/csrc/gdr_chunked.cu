@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
       invert_column<1, DK>(s, hd, diag, lane, buf, out);
       invert_column<2, DK>(s, hd, diag, lane, buf, out);
     }
-    // P below its diagonal blocks: row block 3, and 1 and 2; zeros above them in T and P
+    // P below its diagonal blocks: row block 3, and 1 and 2 (what is above them is never read)
 #pragma unroll 1
     for (int ib = second ? 1 : 3; ib < (second ? 3 : 4); ++ib) {
       float row[2];
@@ -524,13 +524,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
         store_blocks<false>(out + kP, ib * 16, jb * 16, buf, lane, w);
       }
     }
-#pragma unroll
-    for (int ib = 0; ib < 3; ++ib)
-      for (int i = lane + second * 32; i < 16 * 2 * (3 - ib); i += 64) {
-        uint8_t* to = out + tile_at(ib * 16 + (i & 15), (2 * ib + 2 + (i >> 4)) * 8);
-#pragma unroll
-        for (int k = 0; k < 5; ++k) *reinterpret_cast<uint4*>(to + k * kTile) = make_uint4(0, 0, 0, 0);
-      }
     const int r = lane + second * 32;
     float* vec = reinterpret_cast<float*>(out + kVec);
     const float gh = hd.ghi[r], gl = hd.glo[r], e = expf(gh);

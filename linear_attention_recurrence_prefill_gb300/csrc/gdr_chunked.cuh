@@ -11,7 +11,8 @@ constexpr int kC = 64;                 // tokens per chunk
 constexpr long long kGdrSpins = 4000000000LL;  // ~2 s of clock cycles
 
 // One (chunk, value head) of the workspace: the bf16 parts of T and P as tiles [row][64] of
-// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.
+// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.  The
+// 16 x 16 blocks above the diagonal ones are neither written nor read.
 constexpr uint32_t kTile = kC * kC * 2;
 constexpr uint32_t kT = 0, kP = 3 * kTile;  // T: three parts, P: two
 constexpr uint32_t kVec = 5 * kTile;        // floats: a[64], b[64], ku[64], e^{g_C}
