@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
   const GdrArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = a.dv / (int)kDv;
-  const int slice = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv, n = blockIdx.x / slices / a.Hv;
+  const int slice = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
+  const int n = longest_first(a, blockIdx.x / slices / a.Hv);
   int t0, t1, slot;
   if (!gdr_sequence(a, n, t0, t1, slot)) return;  // every warp finds the same
   const int chunks = (t1 - t0 + kC - 1) / kC, base = block_base(t0, n);

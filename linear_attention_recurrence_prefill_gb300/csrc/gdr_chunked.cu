@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = a.dv / Smem::kDv;
   const int unit = blockIdx.x;
-  const int slice = unit % slices, h = unit / slices % a.Hv, n = unit / slices / a.Hv;
+  const int slice = unit % slices, h = unit / slices % a.Hv, n = longest_first(a, unit / slices / a.Hv);
   const int hk = h / (a.Hv / a.Hk);
   int t0, t1, slot;
   if (!gdr_sequence(a, n, t0, t1, slot)) return;  // every warp finds the same

@@ -61,6 +61,20 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& p0, uint32_t&
   p2 = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
 }
 
+// The sequence that the walk takes as its `place`-th: the longest first (ties by index), so that the
+// grid's last CTAs have little to do; up to 32 sequences, in their own order beyond.  By a whole warp.
+__device__ __forceinline__ int longest_first(const GdrArgs& a, int place) {
+  if (!a.cu_seqlens || a.N == 1 || a.N > 32) return place;
+  const int lane = threadIdx.x & 31;
+  const int len = lane < a.N ? a.cu_seqlens[lane + 1] - a.cu_seqlens[lane] : 0;
+  int before = 0;
+  for (int i = 0; i < a.N; ++i) {
+    const int other = __shfl_sync(0xffffffffu, len, i);
+    before += other > len || (other == len && i < lane);
+  }
+  return __ffs(__ballot_sync(0xffffffffu, lane < a.N && before == place)) - 1;
+}
+
 // Launches a walk behind prep by programmatic dependent launch: its CTAs start while prep's last
 // ones run, load what prep does not write, and wait for prep before they read its blocks.
 template <typename K, typename... Args>
