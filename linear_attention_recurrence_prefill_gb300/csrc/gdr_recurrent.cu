@@ -13,55 +13,53 @@
 // seven shuffles: at each level a lane hands half of its sums to its partner and
 // keeps the other half, so that of the eight sums (u and r of four columns) each
 // row group ends up with one.
+//
+// One token per sequence (decode): bound by reading and writing the state.  More
+// tokens: bound by the latency of a token's chain of reductions.  So whatever does
+// not hang on the state is taken off it: the rows of the next tokens are fetched
+// into a ring in shared memory, the warp's own; decays and betas are taken 32 tokens
+// at a time, a token per lane; norms and k.q four at a time, a token for each of the
+// four lanes that hold the same rows.
 #include "gdr.cuh"
+#include "umma.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kRecWarps = 4;
+constexpr int kRecWarps = 4, kRing = 8;
 
-// R consecutive elements as they lie (R * sizeof(T) a multiple of 8 bytes, so aligned at least)
-template <int R, typename T>
-struct Row {
-  uint2 raw[R * (int)sizeof(T) / 8];
-  __device__ __forceinline__ void load(const T* p) {
-    constexpr int n = R * (int)sizeof(T) / 16;
-    if constexpr (n > 0) {
+// V consecutive elements (8 or 16 bytes) widened to fp32.
+template <int V, typename T>
+__device__ __forceinline__ void load_vec(float* x, const T* p) {
+  uint32_t w[V * sizeof(T) / 4];
+  if constexpr (V * sizeof(T) == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  }
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-        raw[2 * i] = make_uint2(v.x, v.y);
-        raw[2 * i + 1] = make_uint2(v.z, v.w);
-      }
+  for (int i = 0; i < V * (int)sizeof(T) / 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
     } else {
-      raw[0] = *reinterpret_cast<const uint2*>(p);
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ __forceinline__ void widen(float (&x)[R]) const {
-#pragma unroll
-    for (int i = 0; i < R * (int)sizeof(T) / 4; ++i) {
-      const uint32_t w = i & 1 ? raw[i / 2].y : raw[i / 2].x;
-      if constexpr (sizeof(T) == 4) {
-        x[i] = __uint_as_float(w);
-      } else {
-        x[2 * i] = __uint_as_float(w << 16);
-        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-      }
-    }
-  }
-};
+}
 
-template <int R, typename T>
-struct Token {
-  Row<R, T> k, q;
-  Row<4, T> v;
-  float la, b;
-};
-
-// kMany: any number of tokens per sequence, the next one's rows fetched ahead; else one.
+// kMany: any number of tokens per sequence; else one.
 template <int DK, typename T, bool kMany>
 __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_kernel(GdrArgs a) {
-  constexpr int R = DK / 8;  // rows of the state per lane
+  constexpr int R = DK / 8;  // rows of the state per lane, in vectors of V: row group rg has
+  constexpr int V = R < 16 / (int)sizeof(T) ? R : 16 / (int)sizeof(T);  // every eighth vector
+  // a token in the ring: k, q, this warp's 16 values
+  constexpr int kTokenBytes = (2 * DK + 16) * (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t ring_all[];
+  uint8_t* ring = ring_all + (threadIdx.x >> 5) * kRing * kTokenBytes;
+
   const int lane = threadIdx.x & 31, rg = lane >> 2, c4 = lane & 3;
   const int slices = a.dv / 16;
   const long long unit = (long long)blockIdx.x * kRecWarps + (threadIdx.x >> 5);
@@ -71,47 +69,53 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
   const int h = (int)(nh % a.Hv), n = (int)(nh / a.Hv);
   int t0, t1, slot;
   if (!gdr_sequence(a, n, t0, t1, slot)) return;
-  const int hk = h / (a.Hv / a.Hk), col = slice * 16 + c4 * 4, row = rg * R;
+  const int hk = h / (a.Hv / a.Hk), col = slice * 16 + c4 * 4;
+  // row i of this lane, behind its first one
+  auto row_at = [](int i) { return i / V * 8 * V + i % V; };
 
-  const size_t mat = ((size_t)slot * a.Hv + h) * DK * a.dv + (size_t)row * a.dv + col;
+  const size_t mat = ((size_t)slot * a.Hv + h) * DK * a.dv + (size_t)(rg * V) * a.dv + col;
   float4 s[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    s[i] = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + mat + (size_t)i * a.dv)
+    s[i] = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + mat + (size_t)row_at(i) * a.dv)
                 : make_float4(0.f, 0.f, 0.f, 0.f);
 
-  const T* q = static_cast<const T*>(a.q) + (size_t)hk * DK + row;
-  const T* k = static_cast<const T*>(a.k) + (size_t)hk * DK + row;
-  const T* v = static_cast<const T*>(a.v) + (size_t)h * a.dv + col;
+  const T* q = static_cast<const T*>(a.q) + (size_t)hk * DK;
+  const T* k = static_cast<const T*>(a.k) + (size_t)hk * DK;
+  const T* v = static_cast<const T*>(a.v) + (size_t)h * a.dv + slice * 16;
   const T* beta = static_cast<const T*>(a.beta) + h;
   T* o = static_cast<T*>(a.o) + (size_t)h * a.dv + col;
-  auto load = [&](Token<R, T>& x, int t) {
-    x.k.load(k + (size_t)t * a.ldk);
-    x.q.load(q + (size_t)t * a.ldq);
-    x.v.load(v + (size_t)t * a.ldv);
-    x.la = a.log_alpha[(size_t)t * a.Hv + h];
-    x.b = to_f32(beta[(size_t)t * a.Hv]);
-  };
 
-  Token<R, T> next;
-  if (t0 < t1) load(next, t0);
-  for (int t = t0; t < (kMany ? t1 : t0 + 1); ++t) {
-    struct {
-      float k[R], q[R], v[4], la, b;
-    } x;
-    next.k.widen(x.k);
-    next.q.widen(x.q);
-    next.v.widen(x.v);
-    x.la = next.la;
-    x.b = next.b;
-    if (kMany && t + 1 < t1) load(next, t + 1);
-    // |k|^2, |q|^2, k.q over all rows
-    float kk = 0.f, qq = 0.f, kq = 0.f;
+  // the rows of token t on their way to the ring (one group of copies each, empty behind the end)
+  auto fetch = [&](int t) {
+    if (t < t1) {
+      constexpr int kPieces = DK * (int)sizeof(T) / 16;  // of 16 bytes
+      const uint32_t to = umma::smem_u32(ring) + (t - t0) % kRing * kTokenBytes;
+      const T* kt = k + (size_t)t * a.ldk;
+      const T* qt = q + (size_t)t * a.ldq;
+#pragma unroll
+      for (int i = 0; i < (2 * kPieces + 31) / 32; ++i) {
+        const int p = lane + i * 32;
+        if (p < 2 * kPieces)
+          umma::cp_async16(to + p * 16, p < kPieces ? kt + p * (16 / sizeof(T)) : qt + (p - kPieces) * (16 / sizeof(T)), 16);
+      }
+      if (lane < (int)sizeof(T))
+        umma::cp_async16(to + 2 * DK * (int)sizeof(T) + lane * 16, v + (size_t)t * a.ldv + lane * (16 / sizeof(T)), 16);
+    }
+    umma::cp_async_commit();
+  };
+  if (kMany)
+    for (int i = 0; i < kRing - 1; ++i) fetch(t0 + i);
+
+  // 1 / |k|, q_scale / |q| and k.q of a token, summed over the row groups
+  auto norms = [&](const float (&kx)[R], const float (&qx)[R], float& ik, float& iq, float& kq) {
+    float kk = 0.f, qq = 0.f;
+    kq = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      kk = fmaf(x.k[i], x.k[i], kk);
-      qq = fmaf(x.q[i], x.q[i], qq);
-      kq = fmaf(x.k[i], x.q[i], kq);
+      kk = fmaf(kx[i], kx[i], kk);
+      qq = fmaf(qx[i], qx[i], qq);
+      kq = fmaf(kx[i], qx[i], kq);
     }
 #pragma unroll
     for (int m = 4; m < 32; m <<= 1) {
@@ -119,10 +123,60 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
       qq += __shfl_xor_sync(0xffffffffu, qq, m);
       kq += __shfl_xor_sync(0xffffffffu, kq, m);
     }
-    const float ik = a.l2norm_qk ? gdr_inv_norm(kk, a.eps_l2) : 1.f;
-    const float iq = a.q_scale * (a.l2norm_qk ? gdr_inv_norm(qq, a.eps_l2) : 1.f);
-    const float al = expf(gdr_log_decay(a, x.la, h));
-    const float b = a.beta_is_logit ? sigmoidf_(x.b) : x.b;
+    ik = a.l2norm_qk ? gdr_inv_norm(kk, a.eps_l2) : 1.f;
+    iq = a.q_scale * (a.l2norm_qk ? gdr_inv_norm(qq, a.eps_l2) : 1.f);
+  };
+  auto from_ring = [&](float (&kx)[R], float (&qx)[R], const T* at) {
+#pragma unroll
+    for (int i = 0; i < R; i += V) {
+      load_vec<V>(&kx[i], at + rg * V + row_at(i));
+      load_vec<V>(&qx[i], at + DK + rg * V + row_at(i));
+    }
+  };
+  auto decay_and_beta = [&](float la, float be, float& al, float& b) {
+    al = expf(gdr_log_decay(a, la, h));
+    b = a.beta_is_logit ? sigmoidf_(be) : be;
+  };
+
+  float al32 = 0.f, b32 = 0.f;              // of the lane's token among 32
+  float ik4 = 0.f, iq4 = 0.f, kq4 = 0.f;    // of token c4 among four
+  for (int t = t0; t < (kMany ? t1 : t0 + 1); ++t) {
+    struct {
+      float k[R], q[R], v[4];
+    } x;
+    float al, b, ik, iq, kq;
+    if (kMany) {
+      const int i = t - t0;
+      if (i % 32 == 0) {
+        const size_t at = (size_t)min(t + lane, t1 - 1) * a.Hv;
+        decay_and_beta(a.log_alpha[at + h], to_f32(beta[at]), al32, b32);
+      }
+      if (i % 4 == 0) {
+        umma::cp_async_wait_group<kRing - 5>();  // tokens t to t + 3 are there
+        __syncwarp();
+        from_ring(x.k, x.q, reinterpret_cast<const T*>(ring + (i + c4) % kRing * kTokenBytes));
+        norms(x.k, x.q, ik4, iq4, kq4);
+      }
+      al = __shfl_sync(0xffffffffu, al32, i % 32);
+      b = __shfl_sync(0xffffffffu, b32, i % 32);
+      ik = __shfl_sync(0xffffffffu, ik4, i % 4);
+      iq = __shfl_sync(0xffffffffu, iq4, i % 4);
+      kq = __shfl_sync(0xffffffffu, kq4, i % 4);
+      const T* at = reinterpret_cast<const T*>(ring + i % kRing * kTokenBytes);
+      from_ring(x.k, x.q, at);
+      load_vec<4>(x.v, at + 2 * DK + c4 * 4);
+      fetch(t + kRing - 1);  // where token t - 1 was: every lane has read that
+    } else {
+      const float la = a.log_alpha[(size_t)t * a.Hv + h], be = to_f32(beta[(size_t)t * a.Hv]);
+#pragma unroll
+      for (int i = 0; i < R; i += V) {
+        load_vec<V>(&x.k[i], k + (size_t)t * a.ldk + rg * V + row_at(i));
+        load_vec<V>(&x.q[i], q + (size_t)t * a.ldq + rg * V + row_at(i));
+      }
+      load_vec<4>(x.v, v + (size_t)t * a.ldv + c4 * 4);
+      decay_and_beta(la, be, al, b);
+      norms(x.k, x.q, ik, iq, kq);
+    }
 
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f), r = u;
 #pragma unroll
@@ -160,21 +214,23 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
       s[i].z = fmaf(x.k[i], w2, al * s[i].z); s[i].w = fmaf(x.k[i], w3, al * s[i].w);
     }
     if (a.snapshots) {  // [n][token of the sequence][h]: here sequences have equal lengths
-      float* sp = a.snapshots + ((size_t)t * a.Hv + h) * DK * a.dv + (size_t)row * a.dv + col;
+      float* sp = a.snapshots + ((size_t)t * a.Hv + h) * DK * a.dv + (size_t)(rg * V) * a.dv + col;
 #pragma unroll
-      for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(sp + (size_t)i * a.dv) = s[i];
+      for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(sp + (size_t)row_at(i) * a.dv) = s[i];
     }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    *reinterpret_cast<float4*>(a.S_T + mat + (size_t)i * a.dv) = s[i];
+    *reinterpret_cast<float4*>(a.S_T + mat + (size_t)row_at(i) * a.dv) = s[i];
 }
 
 template <int DK, typename T>
 void launch_dk(const GdrArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
   // one token per sequence: equal lengths of one
+  constexpr int ring = kRecWarps * kRing * (2 * DK + 16) * (int)sizeof(T);
+  static_assert(ring <= 48 * 1024, "shared memory without asking");
   if (!a.cu_seqlens && a.T_total == a.N) gdr_recurrent_kernel<DK, T, false><<<grid, block, 0, s>>>(a);
-  else gdr_recurrent_kernel<DK, T, true><<<grid, block, 0, s>>>(a);
+  else gdr_recurrent_kernel<DK, T, true><<<grid, block, ring, s>>>(a);
 }
 
 template <typename T>
