@@ -86,26 +86,40 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
   const T* beta = static_cast<const T*>(a.beta) + h;
   T* o = static_cast<T*>(a.o) + (size_t)h * a.dv + col;
 
-  // the rows of token t on their way to the ring (one group of copies each, empty behind the end)
-  auto fetch = [&](int t) {
-    if (t < t1) {
-      constexpr int kPieces = DK * (int)sizeof(T) / 16;  // of 16 bytes
-      const uint32_t to = umma::smem_u32(ring) + (t - t0) % kRing * kTokenBytes;
-      const T* kt = k + (size_t)t * a.ldk;
-      const T* qt = q + (size_t)t * a.ldq;
+  // The rows of the next token on their way to the ring (one group of copies each, empty behind the
+  // end).  A lane copies the same pieces of 16 bytes of every token.
+  constexpr int kPieces = DK * (int)sizeof(T) / 16, kCopies = (2 * kPieces + 31) / 32;
+  constexpr int kPiece = 16 / (int)sizeof(T);
+  const T* from[kCopies];
+  long long ahead[kCopies];
 #pragma unroll
-      for (int i = 0; i < (2 * kPieces + 31) / 32; ++i) {
+  for (int i = 0; i < kCopies; ++i) {
+    const int p = lane + i * 32;
+    from[i] = p < kPieces ? k + (size_t)t0 * a.ldk + p * kPiece : q + (size_t)t0 * a.ldq + (p - kPieces) * kPiece;
+    ahead[i] = p < kPieces ? a.ldk : a.ldq;
+  }
+  const T* from_v = v + (size_t)t0 * a.ldv + lane * kPiece;
+  int left = t1 - t0;
+  uint32_t to = 0;
+  auto fetch = [&] {
+    if (left > 0) {
+      const uint32_t at = umma::smem_u32(ring) + to;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
         const int p = lane + i * 32;
-        if (p < 2 * kPieces)
-          umma::cp_async16(to + p * 16, p < kPieces ? kt + p * (16 / sizeof(T)) : qt + (p - kPieces) * (16 / sizeof(T)), 16);
+        if (p < 2 * kPieces) umma::cp_async16(at + p * 16, from[i], 16);
+        from[i] += ahead[i];
       }
-      if (lane < (int)sizeof(T))
-        umma::cp_async16(to + 2 * DK * (int)sizeof(T) + lane * 16, v + (size_t)t * a.ldv + lane * (16 / sizeof(T)), 16);
+      if (lane < (int)sizeof(T)) umma::cp_async16(at + (2 * kPieces + lane) * 16, from_v, 16);
+      from_v += a.ldv;
+      to = to == (kRing - 1) * kTokenBytes ? 0 : to + kTokenBytes;
+      --left;
     }
     umma::cp_async_commit();
   };
   if (kMany)
-    for (int i = 0; i < kRing - 1; ++i) fetch(t0 + i);
+    for (int i = 0; i < kRing - 1; ++i) fetch();
+  o += (size_t)t0 * a.Hv * a.dv;
 
   // 1 / |k|, q_scale / |q| and k.q of a token, summed over the row groups
   auto norms = [&](const float (&kx)[R], const float (&qx)[R], float& ik, float& iq, float& kq) {
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
       const T* at = reinterpret_cast<const T*>(ring + i % kRing * kTokenBytes);
       from_ring(x.k, x.q, at);
       load_vec<4>(x.v, at + 2 * DK + c4 * 4);
-      fetch(t + kRing - 1);  // where token t - 1 was: every lane has read that
+      fetch();  // token t + kRing - 1, where t - 1 was: every lane has read that
     } else {
       const float la = a.log_alpha[(size_t)t * a.Hv + h], be = to_f32(beta[(size_t)t * a.Hv]);
 #pragma unroll
@@ -205,7 +219,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, kMany ? 3 : 4) gdr_recurrent_k
     float wj = b * (vj - al * ik * sum);  // for rg < 4
     wj = __shfl_sync(0xffffffffu, wj, (j << 2) | c4);
     if (rg >= 4)
-      o[(size_t)t * a.Hv * a.dv + j] = from_f32<T>(iq * (al * sum + kq * ik * wj));
+      o[j] = from_f32<T>(iq * (al * sum + kq * ik * wj));
+    o += (size_t)a.Hv * a.dv;
     const float w0 = ik * __shfl_sync(0xffffffffu, wj, c4), w1 = ik * __shfl_sync(0xffffffffu, wj, 4 | c4),
                 w2 = ik * __shfl_sync(0xffffffffu, wj, 8 | c4), w3 = ik * __shfl_sync(0xffffffffu, wj, 12 | c4);
 #pragma unroll
