@@ -273,7 +273,9 @@ int kda_prefill_noalloc(const void* q, const void* k, const void* v, const float
  *
  * Head sizes: d_k in {32, 64, 128}, d_v in {32, 64, 128, 256}; H_v a multiple
  * of H_k.  Log decays below -200 (minus infinity among them) act as -200: their
- * factor is 0 in fp32.
+ * factor is 0 in fp32.  A token that is not finite spoils its sequence from
+ * there on, in chunks also up to 15 tokens before it; other sequences, heads and
+ * (for v) columns are not touched.
  */
 typedef struct kda_gdr_options {
   int l2norm_qk;         /* 1 (default): L2-normalise q and k per head per token */
@@ -299,7 +301,9 @@ typedef struct kda_gdr_options {
                             [N][L][H_v][d_k][d_v] that receives the state after
                             each token (of proposed tokens, some of which are
                             taken), rows of sequences left out untouched       */
-  int max_seqlen;        /* host-side bound on the longest sequence, 0 = T_total */
+  int max_seqlen;        /* kda_gdr_prefill: the longest sequence, 0 = T_total;
+                            short ones are taken token by token (it decides the
+                            speed only)                                        */
   int impl;              /* kda_gdr_prefill: KDA_IMPL_AUTO, KDA_IMPL_SIMT (token
                             by token on the CUDA cores) or KDA_IMPL_TC (chunks
                             of 64 on the tensor cores, bf16 data only)         */

@@ -36,7 +36,7 @@ __device__ __forceinline__ float gdr_log_decay(const GdrArgs& a, float x, int h)
     const float z = x + (a.decay_bias ? a.decay_bias[h] : 0.f);
     x = -A * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
   }
-  return fmaxf(fminf(x, 0.f), -200.f);
+  return x > 0.f ? 0.f : x < -200.f ? -200.f : x;  // NaN stays
 }
 
 // 1 / sqrt(|x|^2 + eps) (0 for a zero row with eps = 0).

@@ -107,7 +107,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
   const int slice = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
   const int n = longest_first(a, blockIdx.x / slices / a.Hv);
   int t0, t1, slot;
-  if (!gdr_sequence(a, n, t0, t1, slot)) return;  // every warp finds the same
+  if (!gdr_sequence(a, n, t0, t1, slot)) {  // every warp finds the same
+    grid_wait_prerequisites();  // no CTA of this grid is done before prep is
+    return;
+  }
   const int chunks = (t1 - t0 + kC - 1) / kC, base = block_base(t0, n);
 
   if (threadIdx.x == 0) {
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       if (c == 0) grid_wait_prerequisites();  // prep's blocks
       bulk_g2s(st, t.ws + ((size_t)(base + c) * a.Hv + h) * kBlock, kBlock, &full[b]);
     }
+    if (c == 0) grid_wait_prerequisites();
     // loads in flight land before shared memory is released
     if (!ok)
       for (int j = max(0, c - 2); j < c; ++j) mbar_wait(&full[j & 1], (j / 2) & 1, kGdrSpins);

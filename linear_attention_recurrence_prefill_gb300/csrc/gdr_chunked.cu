@@ -122,7 +122,8 @@ __device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b) {
 }
 // e^{g_i - g_j}, j <= i
 __device__ __forceinline__ float decay_factor(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return expf(fminf((hi_i - hi_j) + (lo_i - lo_j), 0.f));
+  const float d = (hi_i - hi_j) + (lo_i - lo_j);
+  return expf(d > 0.f ? 0.f : d);  // rounding apart, d <= 0; NaN stays
 }
 
 // kN 16 x 16 blocks of bf16, one per tile from `tile` on, from 8 x 8 tiles w (kTrans: of their
@@ -564,7 +565,10 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
   const int slice = unit % slices, h = unit / slices % a.Hv, n = longest_first(a, unit / slices / a.Hv);
   const int hk = h / (a.Hv / a.Hk);
   int t0, t1, slot;
-  if (!gdr_sequence(a, n, t0, t1, slot)) return;  // every warp finds the same
+  if (!gdr_sequence(a, n, t0, t1, slot)) {  // every warp finds the same
+    grid_wait_prerequisites();  // no CTA of this grid is done before prep is
+    return;
+  }
   const int chunks = (t1 - t0 + kC - 1) / kC, base = block_base(t0, n);
 
   // rows behind the last token are not loaded: what lies there must be finite

@@ -125,6 +125,7 @@ SHARED = [
     (dict(S=None), {}, kda.KDA_ERR_ARG),
     (dict(N=0), {}, kda.KDA_ERR_SHAPE), (dict(Hk=0), {}, kda.KDA_ERR_SHAPE),
     (dict(Hk=3), {}, kda.KDA_ERR_SHAPE), (dict(Hv=0), {}, kda.KDA_ERR_SHAPE),
+    (dict(Hk=65536, Hv=65536), {}, kda.KDA_ERR_SHAPE),
     (dict(dk=256), {}, kda.KDA_ERR_UNSUPPORTED), (dict(dk=48), {}, kda.KDA_ERR_UNSUPPORTED),
     (dict(dv=96), {}, kda.KDA_ERR_UNSUPPORTED), (dict(dtype=7), {}, kda.KDA_ERR_DTYPE),
     (dict(q=A + 8), {}, kda.KDA_ERR_ALIGN), (dict(v=A + 2), {}, kda.KDA_ERR_ALIGN),
@@ -161,6 +162,23 @@ def test_refusals_of_one():
     assert _step(L=0) == kda.KDA_ERR_SHAPE
     assert _step(N=1 << 20, L=1 << 12) == kda.KDA_ERR_SHAPE
     assert _step(kda.kda_gdr_options_init(snapshots=A + 8)) == kda.KDA_ERR_ALIGN
+
+
+def test_path():
+    """Chunks on the tensor cores for bf16 from 17 tokens on (49 with small heads)."""
+    path = kda.kda_gdr_prefill_path
+    o = kda.kda_gdr_options_init
+    assert path(17, 1, 2, 4, 128, 128) == "tc" and path(16, 1, 2, 4, 128, 128) == "simt"
+    assert path(49, 1, 2, 4, 64, 64) == "tc" and path(48, 1, 2, 4, 64, 64) == "simt"
+    assert path(4096, 256, 2, 4, 128, 128, kda.KDA_BF16, o(max_seqlen=16)) == "simt"
+    assert path(4096, 256, 2, 4, 128, 128, kda.KDA_F32) == "simt"
+    assert path(4096, 1, 2, 4, 128, 128, kda.KDA_BF16, o(impl="simt")) == "simt"
+    assert path(1, 1, 2, 4, 128, 128, kda.KDA_BF16, o(impl="tc")) == "tc"
+    size = kda.kda_gdr_prefill_workspace_size
+    assert size(16, 1, 2, 4, 128, 128) == 0
+    # a block of 41 KB per value head and chunk, 4096 / 64 + 3 chunks at most
+    assert size(4096, 3, 2, 4, 128, 128) == 67 * 4 * 41 * 1024
+    assert size(4096, 3, 2, 4, 128, 128, kda.KDA_F32) == 0
 
 
 def test_binding_refuses():
@@ -325,6 +343,73 @@ def test_prefill_leaves_out_what_is_out_of_range(impl, dtype):
         for n in good:
             _, S_ref = expect_prefill([x[cu[n]:cu[n + 1]] for x in args], [cu[n + 1] - cu[n]], S0[n:n + 1])
             check(S[n], S_ref[0], TOL[impl], f"state {n}")
+
+
+@gpu
+@pytest.mark.parametrize("impl, dtype", IMPL)
+def test_prefill_keeps_what_is_not_finite_to_itself(impl, dtype):
+    """NaN and infinity in one sequence, and in the rows behind the last one: the neighbours on
+    either side, whose chunks end inside the same 64 rows, do not see them; nor do other columns
+    see one of v."""
+    lens = [70, 40, 90]
+    q, k, v, la, beta = draw((230,), 1, 2, 128, 128, dtype, seed=40)  # 30 rows of no sequence
+    S0 = pool(3, 2, 128, 128)
+    clean = [x[:200].clone() for x in (q, k, v, la, beta)]
+    for x in (q, k, v, la, beta):
+        x[200:] = float("nan")
+    q[70] = float("inf")
+    k[75] = float("nan")
+    la[80] = float("nan")
+    args = [x[:200] for x in (q, k, v, la, beta)]
+    o, S = kda.kda_gdr_prefill(*args, S0, cu_of(lens), impl=impl)
+    o_ref, S_ref = expect_prefill(clean, lens, S0)
+    keep = torch.ones(200, dtype=torch.bool)
+    keep[70:110] = False
+    check(o[keep], o_ref[keep], TOL[impl], "o")
+    check(S[[0, 2]], S_ref[[0, 2]], TOL[impl], "states")
+    assert S[1].isnan().any()
+    args = [x.clone() for x in clean]
+    args[2][20, 1, 5] = float("inf")
+    o, S = kda.kda_gdr_prefill(*args, S0, cu_of(lens), impl=impl)
+    cols = [i for i in range(128) if i != 5]
+    check(o[:, 1][:, cols], o_ref[:, 1][:, cols], TOL[impl], "o")
+    check(S[..., cols], S_ref[..., cols], TOL[impl], "states")
+    check(o[:, 0], o_ref[:, 0], TOL[impl], "o of the other head")
+    assert not torch.isfinite(S[0, 1, :, 5]).all()
+
+
+@gpu
+@pytest.mark.parametrize("impl, dtype", IMPL)
+def test_prefill_of_many_sequences(impl, dtype):
+    """More sequences than a warp has lanes, some empty, some left out, states in a pool."""
+    g = torch.Generator().manual_seed(41)
+    lens = torch.randint(0, 40, (70,), generator=g).tolist()
+    lens[3] = 0
+    lens[50] = 130
+    args = draw((sum(lens),), 1, 2, 64, 64, dtype, seed=42)
+    slots = torch.randperm(80, generator=g)[:70].to(torch.int32)
+    slots[7] = -1
+    slots[60] = slots[2]
+    slots[61] = 80
+    P = pool(80, 2, 64, 64)
+    before = P.clone()
+    o = torch.full_like(args[2], 9.0)
+    kda.kda_gdr_prefill(*args, P, cu_of(lens), o=o, S_T=P, slots=slots.cuda(), impl=impl)
+    assert kda.kda_get_last_error() == kda.KDA_ERR_SHAPE
+    out = (7, 60, 61)
+    o_ref, S_ref = expect_prefill(args, lens, before[[s % 80 if s >= 0 else 0 for s in slots.tolist()]])
+    used, at = [], 0
+    for n, L in enumerate(lens):
+        if n in out:
+            assert (o[at:at + L] == 9).all()
+        else:
+            if L:
+                check(o[at:at + L], o_ref[at:at + L], TOL[impl], f"o {n}")
+            check(P[slots[n]], S_ref[n], TOL[impl], f"state {n}")
+            used.append(int(slots[n]))
+        at += L
+    rest = [i for i in range(80) if i not in used]
+    assert torch.equal(P[rest], before[rest])
 
 
 @gpu

@@ -137,6 +137,26 @@ def test_strides(dtype, M, K, N, ldx, ldw, ldr, ldy, off):
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M, K, N, off, pad", [
+    (1, 77, 50, 1, 3), (2, 333, 130, 3, 0), (40, 1003, 515, 1, 0), (300, 65, 130, 5, 2), (17, 9, 300, 7, 7),
+    (600, 1023, 1030, 1, 0)])
+def test_unaligned_rows_between_nan(dtype, M, K, N, off, pad):
+    """Rows at odd addresses and distances with NaN before, between and behind them."""
+    g = torch.Generator().manual_seed(12)
+
+    def part(rows, width, scale):
+        flat = torch.full((off + rows * (width + pad) + 16,), float("nan"))
+        view = flat[off:off + rows * (width + pad)].view(rows, width + pad)[:, :width]
+        view.copy_(torch.randn(rows, width, generator=g) * scale)
+        return flat.to(dtype).cuda()[off:off + rows * (width + pad)].view(rows, width + pad)[:, :width]
+
+    x, w, r = part(M, K, 1.0), part(N, K, K ** -0.5), part(M, N, 1.0)
+    y = kda.kda_linear(x, w, None, r, act="gelu")
+    check(y, *plain64.linear(x, w, None, r, "gelu"))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("M, K, N", [(1, 64, 96), (70, 200, 136), (300, 64, 384)])
 def test_residual_in_place(dtype, M, K, N):
     x, w, b, r = make(M, K, N, dtype, seed=4)
