@@ -239,6 +239,36 @@ constexpr uint32_t split_smem() {
   return kAlign + kStages * (kRowsA + BN) * kBlockK * 2;
 }
 
+// This rank's columns of the tile, added up over R ranks, and their epilogue: a column per warp and
+// four neighbouring channels per lane, several columns in flight.
+template <int R>
+__device__ __forceinline__ void join(const LinearArgs& a, uint32_t part, uint32_t rank, int warp, int cols,
+                                     bool wide, float4 bias, long long m0, int n) {
+  constexpr int kFlight = R == 8 ? 2 : 4;
+  uint32_t from[R];
+#pragma unroll
+  for (uint32_t r = 0; r < R; ++r) from[r] = map_to_rank(part, r);
+  for (int c0 = rank + warp * R; c0 < cols; c0 += 4 * R * kFlight) {
+    float4 v[kFlight][R];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int c = c0 + 4 * R * i < cols ? c0 + 4 * R * i : c0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[i][r] = ld_cluster_f32x4(from[r] + c * kRowsA * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      float4 z = v[i][0];
+#pragma unroll
+      for (int r = 1; r < R; ++r) {
+        z.x += v[i][r].x; z.y += v[i][r].y; z.z += v[i][r].z; z.w += v[i][r].w;
+      }
+      const int c = c0 + 4 * R * i;
+      if (c < cols) finish4<__nv_bfloat16>(a, wide, z, bias, m0 + c, n);
+    }
+  }
+}
+
 // The aligned 16 bytes at `at`, as far as they lie in the array [lo, hi).
 __device__ __forceinline__ uint4 part_of_array(uintptr_t at, uintptr_t lo, uintptr_t hi) {
   uint32_t w[4] = {0, 0, 0, 0};
@@ -416,21 +446,11 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
     const bool wide = wide4(t.a, 2);
     const float4 b = bias4<__nv_bfloat16>(t.a, n);
     const uint32_t part = smem_u32(ring) + lane * 16;
-    uint32_t from[8];
-#pragma unroll
-    for (uint32_t r = 0; r < 8; ++r) from[r] = map_to_rank(part, r < ranks ? r : 0);
-#pragma unroll 2
-    for (int c = rank + warp * ranks; c < cols; c += 4 * ranks) {
-      float4 v[8];
-#pragma unroll
-      for (uint32_t r = 0; r < 8; ++r)
-        v[r] = r < ranks ? ld_cluster_f32x4(from[r] + c * kRowsA * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      float4 z = v[0];
-#pragma unroll
-      for (uint32_t r = 1; r < 8; ++r) {
-        z.x += v[r].x; z.y += v[r].y; z.z += v[r].z; z.w += v[r].w;
-      }
-      finish4<__nv_bfloat16>(t.a, wide, z, b, m0 + c, n);
+    switch (ranks) {
+      case 1: join<1>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
+      case 2: join<2>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
+      case 4: join<4>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
+      default: join<8>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
     }
   }
   fence_before_sync();
