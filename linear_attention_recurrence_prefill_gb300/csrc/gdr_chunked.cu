@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
   Smem& s = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int blk = blockIdx.x, hk = blockIdx.y, G = a.Hv / a.Hk;
-  grid_launch_dependents();  // the walk's CTAs start as soon as there is room for them
 
   if (warp == 0) {
     // the sequence of this block: the last one whose base is not behind it, as far as the
@@ -565,10 +564,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
   const int slice = unit % slices, h = unit / slices % a.Hv, n = longest_first(a, unit / slices / a.Hv);
   const int hk = h / (a.Hv / a.Hk);
   int t0, t1, slot;
-  if (!gdr_sequence(a, n, t0, t1, slot)) {  // every warp finds the same
-    grid_wait_prerequisites();  // no CTA of this grid is done before prep is
-    return;
-  }
+  if (!gdr_sequence(a, n, t0, t1, slot)) return;  // every warp finds the same
   const int chunks = (t1 - t0 + kC - 1) / kC, base = block_base(t0, n);
 
   // rows behind the last token are not loaded: what lies there must be finite
@@ -585,7 +581,6 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
   __syncthreads();
 
   if (warp == W) {  // loads
-    grid_wait_prerequisites();  // prep's blocks
     const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + (size_t)hk * DK;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (size_t)hk * DK;
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (size_t)h * a.dv + slice * Smem::kDv;
@@ -790,7 +785,8 @@ cudaError_t launch_chain(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   const cudaError_t e = allow_smem<gdr_chain_kernel<DK, W>>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)a.N * a.Hv * (a.dv / (16 * W));
-  return launch_behind_prep(gdr_chain_kernel<DK, W>, grid, W * 32 + 32, bytes, s, a, ws);
+  gdr_chain_kernel<DK, W><<<grid, W * 32 + 32, bytes, s>>>(a, ws);
+  return cudaGetLastError();
 }
 
 template <int DK>

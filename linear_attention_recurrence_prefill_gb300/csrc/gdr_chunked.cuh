@@ -75,24 +75,6 @@ __device__ __forceinline__ int longest_first(const GdrArgs& a, int place) {
   return __ffs(__ballot_sync(0xffffffffu, lane < a.N && before == place)) - 1;
 }
 
-// Launches a walk behind prep by programmatic dependent launch: its CTAs start while prep's last
-// ones run, load what prep does not write, and wait for prep before they read its blocks.
-template <typename K, typename... Args>
-cudaError_t launch_behind_prep(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
-                               const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // The walk over the chunks on tcgen05: d_k in {64, 128}, d_v a multiple of 128.
 bool gdr_chain_tc_takes(const GdrArgs& a);
 cudaError_t launch_gdr_chain_tc(const GdrArgs& a, const uint8_t* ws, cudaStream_t s);
