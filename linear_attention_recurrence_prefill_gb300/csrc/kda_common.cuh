@@ -174,6 +174,30 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
+// Launches a kernel that may start while the one before it in the stream ends
+// (programmatic dependent launch): every thread of it waits for that one
+// (griddepcontrol.wait) before it touches global memory, so only its set-up
+// runs early.  `clusters` CTAs along z share a cluster.
+template <typename K, typename... Args>
+cudaError_t launch_early(K kern, dim3 grid, unsigned threads, size_t smem, unsigned clusters,
+                         cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = clusters;
+  cfg.attrs = attr;
+  cfg.numAttrs = clusters > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Device address of the library's status word on the current device.
 int* status_word();
 

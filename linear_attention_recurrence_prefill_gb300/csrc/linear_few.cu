@@ -7,6 +7,7 @@
 // a CTA share rows, each takes a part of K, and their sums meet in shared memory, added in the
 // order of the warps.  x comes from L1.
 #include "linear.cuh"
+#include "umma.cuh"
 
 namespace kda {
 namespace {
@@ -40,6 +41,8 @@ __global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(LinearArgs a, i
   __shared__ float sums[kWarps][kRows * M];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % parts;
+  umma::grid_launch_dependents();
+  umma::grid_wait_prerequisites();  // what ran before is complete
   const long long n0 = ((long long)blockIdx.x * (kWarps / parts) + warp / parts) * kRows;
   const T* x = static_cast<const T*>(a.x);
   const T* w = static_cast<const T*>(a.w);
@@ -113,8 +116,7 @@ cudaError_t launch_m(const LinearArgs& a, int sms, cudaStream_t s) {
   int parts = 1;
   while (parts < kWarps && groups * parts < 16LL * sms) parts *= 2;
   const long long blocks = (groups + kWarps / parts - 1) / (kWarps / parts);
-  linear_few_kernel<M, T><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a, parts);
-  return cudaGetLastError();
+  return launch_early(linear_few_kernel<M, T>, dim3((unsigned)blocks), kWarps * 32, 0, 1, s, a, parts);
 }
 
 template <typename T>

@@ -145,6 +145,7 @@ cudaError_t launch_t(const LinearArgs& a, int sms, cudaStream_t s) {
     const int steps = (b.K + kStep - 1) / kStep;
     int split = 1;
     while (split < 8 && split * 8 <= steps && nt * mt * split * 2 <= 4LL * sms) split *= 2;
+    // an ordinary launch: behind each other, started early, 200 x 512 x 640 took 13.1 us, not 9.7
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)nt, (unsigned)mt, split);
     cfg.blockDim = dim3(kThreads);

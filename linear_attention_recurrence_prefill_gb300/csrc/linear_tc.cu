@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
   cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_base;
+  grid_launch_dependents();
+  grid_wait_prerequisites();  // what ran before is complete
   const int tiles = t.n_tiles * t.m_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
 
   bool ok = true;
@@ -359,6 +361,8 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = tmem_base;
+  grid_launch_dependents();
+  grid_wait_prerequisites();  // what ran before is complete
   // this CTA's part of K: every ranks-th block (one at least), so that the cluster reads rows of w
   // in pieces of ranks * 128 bytes
   const int blocks = (t.k_blocks - (int)rank + (int)ranks - 1) / (int)ranks;
@@ -510,8 +514,8 @@ cudaError_t launch_pair(const LinearArgs& a, int pairs, int* status, cudaStream_
   Tc t;
   if (!fill(t, a, true, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
   const long long tiles = (long long)t.n_tiles * t.m_tiles;
-  linear_pair_kernel<BN><<<2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads, Pair<BN>::kSmem, s>>>(t);
-  return cudaGetLastError();
+  return launch_early(linear_pair_kernel<BN>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), kPairThreads,
+                      Pair<BN>::kSmem, 1, s, t);
 }
 
 template <int BN, int kStages, bool kTma>
@@ -521,19 +525,8 @@ cudaError_t launch_split_of(const LinearArgs& a, int* status, int split, cudaStr
   if (e != cudaSuccess) return e;
   Tc t;
   if (!fill(t, a, kTma, status, kRowsA, kRowsA, BN, BN)) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kTma ? kThreads : kFillThreads);
-  cfg.dynamicSmemBytes = split_smem<BN, kStages>();
-  cfg.stream = s;
-  cfg.gridDim = dim3((unsigned)((long long)t.n_tiles * t.m_tiles), 1, split);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = split;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, t);
+  return launch_early(kern, dim3((unsigned)((long long)t.n_tiles * t.m_tiles), 1, split),
+                      kTma ? kThreads : kFillThreads, split_smem<BN, kStages>(), split, s, t);
 }
 
 bool tma_takes(const LinearArgs& a) {
