@@ -82,7 +82,7 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
 // and the first rows of P.
 //
 // No one thing bounds it: 16 warps per SM issue in 40 % of the cycles, shared memory is busy in
-// half of them, 104 MB are read and 165 MB written in 95 us (most of which stay in L2), and taking
+// half of them, 104 MB are read and 160 MB written in 95 us (126 MB to DRAM by its end), and taking
 // any one step out saves 4 to 30 us.
 //
 // e^{g_i - g_j} off the diagonal blocks is e^{g_i - g_r} e^{g_r - g_j}, r the first row of i's

@@ -15,7 +15,7 @@
 // row group ends up with one.
 //
 // One token per sequence (decode): bound by reading and writing the state: 64
-// sequences x 96 heads of 128 x 128, 810 MB, take 119 us, 1.02 of the measured copy
+// sequences x 96 heads of 128 x 128, 810 MB, take 120 us, 1.01 of the measured copy
 // bandwidth (some of it stays in L2).  More tokens: four for 24 sequences x 32
 // heads with the state after each, 304 MB, take 51.6 us (0.88); long sequences are
 // bound by the latency of a token's chain of reductions, 0.49 us (fp32, 64 x 128).  So whatever does

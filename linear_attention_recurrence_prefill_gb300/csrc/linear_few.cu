@@ -5,7 +5,7 @@
 // A warp takes kRows neighbouring rows of w; a lane its vectors of 16 bytes, kUnroll of them per
 // row in flight (4 KB per warp).  Where w has too few rows to give every SM 16 warps, the warps of
 // a CTA share rows, each takes a part of K, and their sums meet in shared memory, added in the
-// order of the warps.  x comes from L1.  One row with 4096 x 4096 weights takes 8.4 us (4.0 TB/s, of
+// order of the warps.  x comes from L1.  One row with 4096 x 4096 weights takes 8.3 us (4.0 TB/s, of
 // which some 3 us are the launch and the first loads' latency), with 4096 x 12288 19.6 us (5.1 TB/s).
 #include "linear.cuh"
 #include "umma.cuh"

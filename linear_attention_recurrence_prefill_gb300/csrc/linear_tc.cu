@@ -16,8 +16,9 @@
 //    persistent pair per two SMs walking the tiles, two accumulators in TMEM so that a tile's
 //    epilogue runs beside the next tile's products.  Alone, a CTA would fetch 128 + 256 rows for
 //    each 128 x 256 products, 96 bytes per clock from L2 at the tensor cores' full rate, more than
-//    an SM gets; a pair fetches 64.  4096 x 4096 x 12288: 242 us, 1.70 PFLOP/s, 0.88
-//    of the measured bf16 rate (with bias, GELU and residual 256 us); 8192^3: 581 us, 0.98.  The
+//    an SM gets; a pair fetches 64.  4096 x 4096 x 12288: 234 to 242 us, 1.70 to 1.76
+//    PFLOP/s, 0.89 to 0.92 of the measured bf16 rate (with bias, GELU and residual 251 to 262 us;
+//    the library's plain product 208 us); 8192^3: 571 us (the library's 542).  The
 //    tensor pipe is active in 79 % of the cycles of the former; the rest is 768 tiles in waves of 76,
 //    the last one of eight tiles.
 //  * linear_split_kernel, where there are too few tiles to fill the GPU (few tokens, or a small
@@ -25,7 +26,7 @@
 //    meet in distributed shared memory, added in the order of the ranks, so that results repeat
 //    to the bit.  It also takes arrays that TMA cannot (rows that are no multiple of 16 bytes
 //    apart): eight warps then fill the ring, from aligned 16-byte loads that they shift into
-//    place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.4 us, 4.8 TB/s with its 5 us of set-up
+//    place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.4 us, 4.8 TB/s with its set-up
 //    and joining; 4096 x 4095 x 4097, shifted, 584 us.
 #include <cuda.h>
 
