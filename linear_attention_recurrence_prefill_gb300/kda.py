@@ -609,6 +609,8 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
     dt = _code(host, q.dtype)
     opt.max_seqlen = max_seqlen
     opt.impl = IMPLS[impl] if isinstance(impl, str) else int(impl)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: libkda takes contiguous tensors")
     need = load().kda_gdr_prefill_workspace_size(T, N, *sizes, dt, opt)
     if need > 0:
         if workspace is None:

@@ -579,3 +579,12 @@ def test_step_captured():
         o_ref, states = plain64.rule(*tokens, start[n])
         check(S[n], states[-1], TOL["simt"], "state")
         check(o[n], o_ref[-1], TOL["simt"], "o")
+
+
+@gpu
+def test_refuses_a_broadcast_workspace():
+    """One byte repeated has the size that is asked for, and not the memory."""
+    args = draw((200,), 2, 4, 128, 128, BF16)
+    need = kda.kda_gdr_prefill_workspace_size(200, 1, 2, 4, 128, 128)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_prefill(*args, workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(need))
