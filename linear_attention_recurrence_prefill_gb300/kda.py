@@ -10,6 +10,7 @@ missing or unloadable library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import build as _build
@@ -477,10 +478,22 @@ def _one_device(host, first, *ts) -> int:
     return dev
 
 
-def _stream_of(host, stream, dev: int) -> int:
-    if stream is None:
-        return host.current_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _on_stream(call):
+    """`call` with ``stream`` (a torch stream or its address, None = the current one) as the
+    current stream: what it allocates then belongs to the stream that the kernels run on,
+    so that the allocator hands none of it out before they are done."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        if stream.device.index != torch.cuda.current_device():
+            raise ValueError("the stream is not one of the current CUDA device")
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on_stream
 
 
 def _token_stride(x, name: str) -> int:
@@ -571,11 +584,12 @@ def kda_gdr_prefill_path(T_total: int, N: int, H_k: int, H_v: int, d_k: int, d_v
     return PATH_NAMES[rc]
 
 
+@_on_stream
 def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int | None = None,
                     o=None, S_T=None, *, slots=None, l2norm_qk: bool = True,
                     beta_is_logit: bool = False, decay_from_logit: bool = False, decay_scale=None,
                     decay_bias=None, q_scale: float = 1.0, eps_l2: float = 1e-6,
-                    max_seqlen: int = 0, impl="auto", workspace=None, stream=None):
+                    max_seqlen: int = 0, impl="auto", workspace=None):
     """The gated delta rule over packed sequences (C ``kda_gdr_prefill``).
 
     q, k [T, H_k, d_k]; v [T, H_v, d_v]; each token's heads contiguous, tokens any
@@ -586,7 +600,8 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
     [n_slots, H_v, d_k, d_v] and sequence n's state is matrix slots[n]; S_T has
     to be given (it may be S0).  ``decay_from_logit``: log_alpha holds logits z,
     the log decay is -A softplus(z + b) with decay_scale A [H_v] and decay_bias
-    b [H_v] (fp32, None = ones / zeros)."""
+    b [H_v] (fp32, None = ones / zeros).  ``stream``: the stream to run on, None =
+    the current one."""
     host = _host()
     dev = _one_device(host, q, k, v, log_alpha, beta, S0, cu_seqlens, o, S_T, slots, decay_scale,
                       decay_bias, workspace)
@@ -619,16 +634,17 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
         opt.workspace_bytes = workspace.numel() * workspace.element_size()
     rc = host.prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
                       beta.data_ptr(), _ptr(S0), _ptr(cu_seqlens), N, o.data_ptr(),
-                      S_T.data_ptr(), T, *sizes, dt, opt, _stream_of(host, stream, dev))
+                      S_T.data_ptr(), T, *sizes, dt, opt, host.current_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_gdr_prefill")
     return o, S_T
 
 
+@_on_stream
 def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snapshots=None,
                         l2norm_qk: bool = True, beta_is_logit: bool = False,
                         decay_from_logit: bool = False, decay_scale=None, decay_bias=None,
-                        q_scale: float = 1.0, eps_l2: float = 1e-6, stream=None):
+                        q_scale: float = 1.0, eps_l2: float = 1e-6):
     """L recurrent tokens for each of N sequences (C ``kda_gdr_decode_step``).
 
     q, k [N, L, H_k, d_k]; v [N, L, H_v, d_v]; log_alpha, beta [N, L, H_v]; or all
@@ -636,7 +652,7 @@ def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snap
     [n_slots, H_v, d_k, d_v] with ``slots`` [N] int32) is updated in place.
     Returns o [N, (L,) H_v, d_v].  ``snapshots``: True or a tensor
     [N, L, H_v, d_k, d_v] fp32 for the state after each token; then returns
-    (o, snapshots)."""
+    (o, snapshots).  ``stream`` as in kda_gdr_prefill."""
     host = _host()
     dev = _one_device(host, q, k, v, log_alpha, beta, S, o, slots, decay_scale, decay_bias)
     if q.dim() not in (3, 4) or v.dim() != q.dim():
@@ -657,7 +673,7 @@ def kda_gdr_decode_step(q, k, v, log_alpha, beta, S, o=None, *, slots=None, snap
         opt.snapshots = snapshots.data_ptr()
     rc = host.step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
                    beta.data_ptr(), S.data_ptr(), o.data_ptr(), N, L, *sizes,
-                   _code(host, q.dtype), opt, _stream_of(host, stream, dev))
+                   _code(host, q.dtype), opt, host.current_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_gdr_decode_step")
     return o if snapshots is None else (o, snapshots)
@@ -683,12 +699,13 @@ def _rows(x, name: str, rows: int, width: int) -> int:
     return x.stride(0)
 
 
-def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none", stream=None):
+@_on_stream
+def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none"):
     """y = act(x w^T + bias) + residual (C ``kda_linear``).
 
     x [M, K], w [N, K], bias [N] or None, residual [M, N] or None, all of one
     dtype; rows contiguous, any distance apart.  ``act``: a key of ``ACTS``.
-    y [M, N] may be the residual itself."""
+    y [M, N] may be the residual itself.  ``stream`` as in kda_gdr_prefill."""
     host = _host()
     dev = _one_device(host, x, w, bias, residual, y)
     if x.dim() != 2 or w.dim() != 2:
@@ -712,7 +729,7 @@ def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none", stream=Non
         if y.dtype != dtype:
             raise TypeError("x, w, bias, residual and y of one dtype")
     rc = host.linear(x.data_ptr(), ldx, w.data_ptr(), ldw, b, r, ldr, y.data_ptr(), ldy, M, N, K,
-                     ACTS[act], code, _stream_of(host, stream, dev))
+                     ACTS[act], code, host.current_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_linear")
     return y

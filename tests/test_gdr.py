@@ -588,3 +588,45 @@ def test_refuses_a_broadcast_workspace():
     need = kda.kda_gdr_prefill_workspace_size(200, 1, 2, 4, 128, 128)
     with pytest.raises(ValueError):
         kda.kda_gdr_prefill(*args, workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(need))
+
+
+@gpu
+def test_a_stream_owns_what_its_calls_allocate(monkeypatch):
+    """With ``stream``, workspace and results come from that stream's memory: the workspace is
+    given back on return, while the kernels still use it."""
+    args = draw((200,), 2, 4, 128, 128, BF16)
+    want, S_want = kda.kda_gdr_prefill(*args, impl="tc")
+    host, st, seen = kda._host(), torch.cuda.Stream(), []
+
+    def empty(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return torch.empty(*a, **kw)
+
+    def empty_like(x):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return torch.empty_like(x)
+
+    monkeypatch.setattr(host, "empty", empty)
+    monkeypatch.setattr(host, "empty_like", empty_like)
+    torch.cuda.synchronize()
+    before = torch.cuda.current_stream().cuda_stream
+    for stream in (st, st.cuda_stream):
+        o, S_T = kda.kda_gdr_prefill(*args, impl="tc", stream=stream)
+        st.synchronize()
+        assert torch.equal(o, want) and torch.equal(S_T, S_want)
+    x = torch.randn(8, 64, device="cuda").to(BF16)
+    torch.cuda.synchronize()
+    y = kda.kda_linear(x, x, stream=st)
+    st.synchronize()
+    assert torch.equal(y, kda.kda_linear(x, x))
+    assert len(seen) == 8 and seen[:7] == [st.cuda_stream] * 7 and seen[7] == before
+    assert torch.cuda.current_stream().cuda_stream == before
+
+
+@gpu
+def test_refuses_a_stream_of_another_device():
+    class Other:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+    args = draw((8,), 2, 4, 32, 32, BF16)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_prefill(*args, stream=Other())
