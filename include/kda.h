@@ -326,8 +326,9 @@ void kda_gdr_options_init(kda_gdr_options* opt);
  *   o           [T_total][H_v][d_v] dtype out
  *   S_T         as S0, final states out (may be S0)
  *
- * opt NULL: the defaults.  q, k, v, S0, S_T, o 16-byte aligned.  o must not
- * overlap an input.  KDA_ERR_WORKSPACE where the workspace is too small; the
+ * opt NULL: the defaults.  q, k, v, S0, S_T, o 16-byte aligned.  o and S_T must
+ * not overlap an input or each other, S_T at S0 apart (KDA_ERR_ARG where two start
+ * at one address).  KDA_ERR_WORKSPACE where the workspace is too small; the
  * workspace holds nothing between calls, but calls that can overlap on the GPU
  * need one each.
  */
@@ -382,6 +383,7 @@ enum {
  *   residual  [M][N] dtype, rows ldr elements apart (0 = N), or NULL
  *   y         [M][N] dtype out, rows ldy elements apart (0 = N); may be the
  *             residual itself (same address and stride), else overlaps no input
+ *             (KDA_ERR_ARG where it starts at one)
  *
  * Sums, bias, activation and residual are in fp32, rounded once to dtype.
  * Pointers need the alignment of their elements; bf16 products run on the

@@ -3,6 +3,8 @@
 // runs on the host before anything is enqueued; a rejected call launches nothing.
 #include <string.h>
 
+#include <initializer_list>
+
 #include "gdr.cuh"
 #include "linear.cuh"
 
@@ -63,6 +65,13 @@ int check_gdr_arrays(const void* q, const void* k, const void* v, const float* l
     if (!aligned(p, 16)) return KDA_ERR_ALIGN;
   if (!aligned(log_alpha, 4) || !aligned(beta, elem(dtype))) return KDA_ERR_ALIGN;
   return KDA_OK;
+}
+
+// An output at the address of an input: other warps still read what one has written.
+bool same(const void* out, std::initializer_list<const void*> in) {
+  for (const void* p : in)
+    if (out && out == p) return true;
+  return false;
 }
 
 GdrArgs gdr_args(const void* q, const void* k, const void* v, const float* log_alpha,
@@ -145,6 +154,8 @@ int kda_gdr_prefill(const void* q, const void* k, const void* v, const float* lo
       return KDA_ERR_WORKSPACE;
     if (!aligned(op->workspace, 16)) return KDA_ERR_ALIGN;
   }
+  if (same(o, {q, k, v, log_alpha, beta, S0, S_T, op->workspace})) return KDA_ERR_ARG;
+  if (same(S_T, {q, k, v, log_alpha, beta, op->workspace})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GdrArgs a = gdr_args(q, k, v, log_alpha, beta, S0, S_T, o, N, T_total, H_k, H_v, d_k, d_v, op,
@@ -170,6 +181,9 @@ int kda_gdr_decode_step(const void* q, const void* k, const void* v, const float
   rc = check_gdr_sizes(N, T, H_k, H_v, d_k, d_v, dtype, op);
   if (rc != KDA_OK) return rc;
   if (!aligned(op->snapshots, 16)) return KDA_ERR_ALIGN;
+  if (same(o, {q, k, v, log_alpha, beta, S, op->snapshots})) return KDA_ERR_ARG;
+  if (same(S, {q, k, v, log_alpha, beta})) return KDA_ERR_ARG;
+  if (same(op->snapshots, {q, k, v, log_alpha, beta, S})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GdrArgs a = gdr_args(q, k, v, log_alpha, beta, S, S, o, N, T, H_k, H_v, d_k, d_v, op, status);
@@ -196,6 +210,7 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
     if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
   // in place only where every element is read and written by the same thread
   if (residual == y && ldr != ldy) return KDA_ERR_ARG;
+  if (same(y, {bias}) || (K > 0 && same(y, {x, w}))) return KDA_ERR_ARG;
   LinearArgs a;
   a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
   a.ldx = ldx; a.ldw = ldw; a.ldr = ldr; a.ldy = ldy;

@@ -630,3 +630,28 @@ def test_refuses_a_stream_of_another_device():
     args = draw((8,), 2, 4, 32, 32, BF16)
     with pytest.raises(ValueError):
         kda.kda_gdr_prefill(*args, stream=Other())
+
+
+def apart():
+    return {x: A * (i + 1) for i, x in enumerate(("q", "k", "v", "la", "beta", "o", "S"))}
+
+
+@no_gpu
+@pytest.mark.parametrize("out, other", [(a, b) for a in "oS" for b in ("q", "k", "v", "la", "beta")]
+                         + [("o", "S")])
+def test_refuses_an_output_on_an_input(out, other):
+    at = apart()
+    at[out] = at[other]
+    assert _step(**at) == kda.KDA_ERR_ARG
+    assert _prefill(kda.kda_gdr_options_init(impl="simt"), **at) == kda.KDA_ERR_ARG
+
+
+@no_gpu
+def test_refuses_shared_states_and_scratch():
+    at = apart()
+    for x in ("S", "q", "o"):
+        assert _step(kda.kda_gdr_options_init(snapshots=at[x]), **at) == kda.KDA_ERR_ARG
+    assert _prefill(kda.kda_gdr_options_init(impl="simt"), **at | {"S0": at["o"]}) == kda.KDA_ERR_ARG
+    for x in ("S", "o"):
+        opt = kda.kda_gdr_options_init(impl="tc", workspace=at[x], workspace_bytes=1 << 30)
+        assert _prefill(opt, **at) == kda.KDA_ERR_ARG

@@ -359,3 +359,10 @@ def test_layer_prefill_then_decode():
         assert plain64.rel(out, ref) <= 2.0 ** -7
         assert plain64.rel(P[slots.long()], states) <= 2.0 ** -7
     assert kda.kda_get_last_error() == kda.KDA_OK
+
+
+@no_gpu
+def test_refuses_an_output_on_an_input():
+    at = dict(x=A, w=2 * A, b=3 * A, r=4 * A, y=5 * A)
+    for name in ("x", "w", "b"):
+        assert _linear(**at | {"y": at[name]}) == kda.KDA_ERR_ARG
