@@ -117,7 +117,9 @@ int kda_gdr_prefill_path(int T_total, int N, int H_k, int H_v, int d_k, int d_v,
   const bool tc = gdr_chunked_supported(d_k, d_v, dtype);
   switch (op->impl) {
     case KDA_IMPL_SIMT: return KDA_IMPL_SIMT;
-    case KDA_IMPL_TC: return tc ? KDA_IMPL_TC : KDA_ERR_UNSUPPORTED;
+    case KDA_IMPL_TC:  // without a token there is no chunk, only states to hand on
+      if (!tc) return KDA_ERR_UNSUPPORTED;
+      return T_total > 0 ? KDA_IMPL_TC : KDA_IMPL_SIMT;
     case KDA_IMPL_AUTO: {
       // Token by token where no sequence is longer than this.  One sequence of 16 tokens took 13 us
       // that way and 18 us in chunks, 16 sequences 52 and 47 us (32 heads of 128 x 128); heads of

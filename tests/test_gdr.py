@@ -655,3 +655,19 @@ def test_refuses_shared_states_and_scratch():
     for x in ("S", "o"):
         opt = kda.kda_gdr_options_init(impl="tc", workspace=at[x], workspace_bytes=1 << 30)
         assert _prefill(opt, **at) == kda.KDA_ERR_ARG
+
+
+def test_path_without_tokens():
+    opt = kda.kda_gdr_options_init(impl="tc")
+    assert kda.kda_gdr_prefill_path(0, 2, 2, 4, 128, 128, kda.KDA_BF16, opt) == "simt"
+    assert kda.kda_gdr_prefill_workspace_size(0, 2, 2, 4, 128, 128, kda.KDA_BF16, opt) == 0
+
+
+@gpu
+@pytest.mark.parametrize("impl", ["auto", "simt", "tc"])
+def test_no_tokens_hand_the_states_on(impl):
+    args = draw((0,), 2, 4, 128, 128, BF16)
+    S0 = pool(2, 4, 128, 128)
+    o, S_T = kda.kda_gdr_prefill(*args, S0, cu_of([0, 0]), impl=impl)
+    assert o.shape == (0, 4, 128) and torch.equal(S_T, S0)
+    assert kda.kda_get_last_error() == kda.KDA_OK
