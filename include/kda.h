@@ -388,7 +388,8 @@ enum {
  * Sums, bias, activation and residual are in fp32, rounded once to dtype.
  * Pointers need the alignment of their elements; bf16 products run on the
  * tensor cores, fastest where x and w are 16-byte aligned with rows a multiple
- * of 16 bytes apart, fp32 products on the CUDA cores.  M, N or K may be 0
+ * of 16 bytes apart, fp32 products on the CUDA cores.  M, N and K are
+ * from 0 to 2^31 - 257
  * (K = 0: y = act(bias) + residual).
  */
 int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,

@@ -12,6 +12,9 @@ using namespace kda;
 
 namespace {
 
+// Sizes leave a tile's room below 2^31, so that the kernels round up in 32 bits.
+constexpr int kMaxSize = 0x7fffffff - 256;
+
 int sm_count() {  // of the current device
   static std::atomic<int> count[64];
   int dev = 0, n = 0;
@@ -31,7 +34,7 @@ size_t elem(int dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 // Checks that kda_gdr_prefill and kda_gdr_decode_step share.
 int check_gdr_sizes(int N, int T_total, int H_k, int H_v, int d_k, int d_v, int dtype,
                     const kda_gdr_options* o) {
-  if (N < 1 || T_total < 0 || H_k < 1 || H_k > 65535 || H_v < 1 || H_v % H_k != 0)
+  if (N < 1 || T_total < 0 || T_total > kMaxSize || H_k < 1 || H_k > 65535 || H_v < 1 || H_v % H_k != 0)
     return KDA_ERR_SHAPE;
   if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
   if (!gdr_dk(d_k) || !gdr_dv(d_v)) return KDA_ERR_UNSUPPORTED;
@@ -197,7 +200,7 @@ int kda_gdr_decode_step(const void* q, const void* k, const void* v, const float
 int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
                const void* residual, long long ldr, void* y, long long ldy, int M, int N, int K,
                int act, int dtype, kda_stream_t stream) {
-  if (M < 0 || N < 0 || K < 0) return KDA_ERR_SHAPE;
+  if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return KDA_ERR_SHAPE;
   if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
   if (act < KDA_ACT_NONE || act > KDA_ACT_SIGMOID) return KDA_ERR_ARG;
   if (ldx == 0) ldx = K;

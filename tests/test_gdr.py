@@ -671,3 +671,9 @@ def test_no_tokens_hand_the_states_on(impl):
     o, S_T = kda.kda_gdr_prefill(*args, S0, cu_of([0, 0]), impl=impl)
     assert o.shape == (0, 4, 128) and torch.equal(S_T, S0)
     assert kda.kda_get_last_error() == kda.KDA_OK
+
+
+@no_gpu
+def test_refuses_tokens_near_two_to_the_31():
+    assert _prefill(T=2 ** 31 - 256) == kda.KDA_ERR_SHAPE
+    assert _step(N=2 ** 31 - 256, Hk=1, Hv=1, dk=32, dv=32) == kda.KDA_ERR_SHAPE

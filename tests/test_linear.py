@@ -366,3 +366,10 @@ def test_refuses_an_output_on_an_input():
     at = dict(x=A, w=2 * A, b=3 * A, r=4 * A, y=5 * A)
     for name in ("x", "w", "b"):
         assert _linear(**at | {"y": at[name]}) == kda.KDA_ERR_ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("size", ["M", "N", "K"])
+def test_refuses_sizes_near_two_to_the_31(size):
+    at = dict(x=A, w=2 * A, y=5 * A)
+    assert _linear(**at | {size: 2 ** 31 - 256}) == kda.KDA_ERR_SHAPE
