@@ -327,7 +327,7 @@ void kda_gdr_options_init(kda_gdr_options* opt);
  *   S_T         as S0, final states out (may be S0)
  *
  * opt NULL: the defaults.  q, k, v, S0, S_T, o 16-byte aligned.  o and S_T must
- * not overlap an input or each other, S_T at S0 apart (KDA_ERR_ARG where two start
+ * not overlap an input or each other, but S_T may be S0 (KDA_ERR_ARG where two start
  * at one address).  KDA_ERR_WORKSPACE where the workspace is too small; the
  * workspace holds nothing between calls, but calls that can overlap on the GPU
  * need one each.
