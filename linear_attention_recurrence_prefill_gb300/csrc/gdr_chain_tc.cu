@@ -17,13 +17,13 @@
 // they work on X.
 //
 // A chunk of 128 x 128 heads takes 5,400 cycles (4096 tokens x 96 heads: 180 us on 96 SMs), of which
-// the products need 4,700: 88 MMAs of N = 64, 45 cycles each whatever N is below 128, and 12 of
+// the products need 5,300: 101 MMAs of N = 64, 45 cycles each whatever N is below 128, and 12 of
 // N = 128, 64 each.  (X and Y as one product against [K; Q] need fewer cycles, but X comes 460 later.)
 //
 // TMEM columns (d_k = 128): 0-191 the parts of S, the first two of which lie where the same
 // warpgroup's half of the update's product comes (0-127), the third (128-191) where -a X and
-// ku U go with 192-223; 224 and 288 in turn X and U, then U's parts; 352 and 416 in turn Y, then
-// o.  A warpgroup writes and reads only its own columns, so that no barrier between the warps is
+// ku U go with 192-223; 224 and 288 in turn X and U, then U's first two parts; 352 and 416 in turn
+// Y, then o; 480-511 U's third part.  A warpgroup writes and reads only its own columns, so that no barrier between the warps is
 // needed.
 #include <cuda.h>
 
@@ -39,7 +39,7 @@ using namespace umma;
 constexpr int kStateWarps = 8, kWarpLoad = 8, kWarpMma = 9, kWarpStore = 10;
 constexpr int kThreads = 352;
 constexpr uint32_t kDv = 128;
-constexpr uint32_t kVCol = 128, kVCol2 = 192, kXuCol = 224, kYCol = 352;
+constexpr uint32_t kVCol = 128, kVCol2 = 192, kXuCol = 224, kYCol = 352, kUCol2 = 480;
 
 template <int DK>
 struct Layout {
@@ -62,6 +62,11 @@ struct Layout {
 // column of part k of -a X or ku U, tokens from 16 s on
 __host__ __device__ constexpr uint32_t v_col(uint32_t s, uint32_t k) {
   return (k < 2 ? kVCol + (s >> 1) * 32 + k * 16 : kVCol2 + (s >> 1) * 16) + (s & 1) * 8;
+}
+
+// column of part k of U, tokens from 16 s on: the first two in place of U itself
+__device__ __forceinline__ uint32_t u_col(uint32_t ucol, uint32_t tmem, uint32_t s, uint32_t k) {
+  return (k < 2 ? ucol + (s >> 1) * 32 + k * 16 : tmem + kUCol2 + (s >> 1) * 16) + (s & 1) * 8;
 }
 
 struct Chain {
@@ -259,12 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
       if (c > 0 && !wait(&o_free, (c - 1) & 1)) break;
       if (!wait(&d_done, ph)) break;
 #pragma unroll
-      for (uint32_t s = 0; s < 4; ++s)
+      for (int i = 4; i >= 0; --i) {  // P's third part: column i (0: rows 16 on), then the first block
+        const uint32_t s = i < 4 ? i : 0, row = i == 0 ? 1 : s;
+        const PlaceOfP at = third_of_p(row, s);
+        mma_ts_if(lead, ycol + 16 * row, u_col(ucol, tmem, s, 0), pp + ((at.tile * kTile + at.col * 32) >> 4),
+                  idesc_f16(128, i < 4 ? 64 - 16 * row : 16, true), 1);
+      }
 #pragma unroll
-        for (uint32_t j = 0; j < 2; ++j)
+      for (uint32_t order = 2; order < 3; --order)
 #pragma unroll
-          for (uint32_t k = 0; k < 2 - j; ++k)
-            mma_ts_if(lead, ycol + 16 * s, ucol + (s >> 1) * 32 + k * 16 + (s & 1) * 8,
+        for (uint32_t j = 0; j <= (order < 1 ? order : 1); ++j)
+#pragma unroll
+          for (uint32_t s = 0, k = order - j; s < 4; ++s)
+            mma_ts_if(lead, ycol + 16 * s, u_col(ucol, tmem, s, k),
                       pp + ((j * kTile + s * 32) >> 4) + s * kBelow, idesc_f16(128, 64 - 16 * s, true), 1);
       mma_commit_if(lead, &o_done);
       mma_commit_if(lead, &empty[b]);
@@ -438,16 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
           store_parts3<8>(w0 + j * 8, w0 + 16 + j * 8, w2 + j * 8, v);
           hand_over(&ku_ready[j], lane);
         }
-        uint32_t p[2][16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t w[2];
-          split2<2>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), w);
-          p[0][i] = w[0];
-          p[1][i] = w[1];
+        for (int j = 0; j < 2; ++j) {
+          float u[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = __uint_as_float(r[j * 16 + i]);
+          store_parts3<8>(ucol + j * 8, ucol + 16 + j * 8, lanes + kUCol2 + half * 16 + j * 8, u);
         }
-        tmem_st16(ucol, p[0]);
-        tmem_st16(ucol + 16, p[1]);
         hand_over(&u_ready, lane);
       }
     }

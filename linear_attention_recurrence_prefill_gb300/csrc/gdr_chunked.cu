@@ -18,9 +18,11 @@
 // Precision: the final states are fp32 results, so no operand on the state's way may be
 // rounded to bf16.  K, Q and V are bf16 as they come and enter the products unscaled (norms
 // and decays multiply rows of results or fp32 operands).  Everything else enters as a sum of
-// bf16 parts: the state, V - e^g K S, U and T as three (24 bits, an fp32 value), of whose
-// products those of order 2^-24 are left out; what only o sees (Q S and P U, rounded to bf16
-// in the end) as two.
+// three bf16 parts (24 bits, an fp32 value), of whose products those of order 2^-24 are left
+// out.  Only Q S, which o alone sees, takes the first two of the state's parts: 2^-17 at most,
+// and in the walk on tcgen05 the third part has to make room for what X becomes meanwhile.
+// With P and U in two parts too, o was off by 4.4e-6 of its size before it was rounded, not by
+// 1e-6, and 4096 tokens x 96 heads took 22 us less.
 #include "gdr_chunked.cuh"
 
 namespace kda {
@@ -52,20 +54,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 // The accumulators of two neighbouring 16 x 8 tiles as the parts of a 16 x 16 A operand: the
 // layouts agree element by element.
-template <int kParts>
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4],
-                                        uint32_t (&p)[kParts][4]) {
+                                        uint32_t (&p)[3][4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = (i < 2 ? c0 : c1)[2 * (i & 1)], y = (i < 2 ? c0 : c1)[2 * (i & 1) + 1];
-    if constexpr (kParts == 3) {
-      split3(x, y, p[0][i], p[1][i], p[2][i]);
-    } else {
-      uint32_t w[kParts];
-      split2<kParts>(x, y, w);
-#pragma unroll
-      for (int k = 0; k < kParts; ++k) p[k][i] = w[k];
-    }
+    split3(x, y, p[0][i], p[1][i], p[2][i]);
   }
 }
 
@@ -78,7 +72,7 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
 // column), then column by column X_ij = -X_ii sum_k A_ik X_kj on the tensor cores, transposed, so
 // that each result is the A operand of the next product as it lies:
 //     tmp^T = sum_k X_kj^T A_ik^T,   X_ij^T = -tmp^T X_ii^T,
-// every operand in three bf16 parts (fp32's 24 bits).  One warp takes column 0, the other 1 and 2
+// every operand in three bf16 parts.  One warp takes column 0, the other 1 and 2
 // and the first rows of P.
 //
 // No one thing bounds it: 16 warps per SM issue in 40 % of the cycles, shared memory is busy in
@@ -132,11 +126,12 @@ __device__ __forceinline__ float decay_factor(float hi_i, float lo_i, float hi_j
   return expf(d > 0.f ? 0.f : d);  // rounding apart, d <= 0; NaN stays
 }
 
-// kN 16 x 16 blocks of bf16, one per tile from `tile` on, from 8 x 8 tiles w (kTrans: of their
-// transposes) to 32-byte rows in global memory: through shared memory, 16 bytes per lane.
-template <bool kTrans, int kN>
+// Three 16 x 16 blocks of bf16, parts of T (kTrans: from their transposes) or of P, from 8 x 8 tiles w
+// to 32-byte rows of the tiles from `tile` on: through shared memory, 16 bytes per lane.
+template <bool kTrans>
 __device__ __forceinline__ void store_blocks(uint8_t* tile, int row0, int col0, uint8_t* buf, int lane,
-                                             const uint32_t (&w)[kN][4]) {
+                                             const uint32_t (&w)[3][4]) {
+  constexpr int kN = 3;
   // lane l names row l & 7 of tile l >> 3; halves are swapped every four rows against conflicts
   const uint32_t r = (lane & 7) + ((lane >> (kTrans ? 4 : 3)) & 1) * 8, h = (lane >> (kTrans ? 3 : 4)) & 1;
   const uint32_t at = smem_u32(buf) + r * 32 + ((h ^ ((r >> 2) & 1)) << 4);
@@ -150,8 +145,14 @@ __device__ __forceinline__ void store_blocks(uint8_t* tile, int row0, int col0, 
   const uint8_t* from = buf + row * 32 + ((half ^ ((row >> 2) & 1)) << 4);
   uint8_t* to = tile + tile_at(row0 + row, col0 + half * 8);
 #pragma unroll
-  for (int k = 0; k < kN; ++k)
-    *reinterpret_cast<uint4*>(to + k * kTile) = *reinterpret_cast<const uint4*>(from + k * 512);
+  for (int k = 0; k < kN; ++k) {
+    uint8_t* at = to + k * kTile;
+    if (!kTrans && k == 2) {
+      const PlaceOfP p = third_of_p(row0 / 16, col0 / 16);
+      at = tile + p.tile * kTile + tile_at(p.row * 16 + row, p.col * 16 + half * 8);
+    }
+    *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(from + k * 512);
+  }
   __syncwarp();
 }
 
@@ -163,7 +164,7 @@ __device__ __forceinline__ void invert_column(const PrepSmem<DK>& s, const PrepH
   const float b0 = hd.beta[J * 16 + g], b1 = hd.beta[J * 16 + g + 8];
   // c: a block of X^T (rows: X's columns), as two 16 x 8 tiles; its parts as an A operand, and T's
   auto finish = [&](const float (&c)[2][4], int i, uint32_t (&f)[3][4]) {
-    split_a<3>(c[0], c[1], f);
+    split_a(c[0], c[1], f);
     float z[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -171,7 +172,7 @@ __device__ __forceinline__ void invert_column(const PrepSmem<DK>& s, const PrepH
       z[x][2] = c[x][2] * b1; z[x][3] = c[x][3] * b1;
     }
     uint32_t w[3][4];
-    split_a<3>(z[0], z[1], w);
+    split_a(z[0], z[1], w);
     store_blocks<true>(out + kT, i * 16, J * 16, buf, lane, w);
   };
   // six products of parts, smaller ones first
@@ -224,7 +225,7 @@ __device__ __forceinline__ void invert_column(const PrepSmem<DK>& s, const PrepH
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[x][e] = -c[x][e];
     uint32_t f[3][4], m[3][4];
-    split_a<3>(c[0], c[1], f);
+    split_a(c[0], c[1], f);
     const float* d = diag + i * kDiag;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -463,8 +464,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           *reinterpret_cast<float2*>(&d[(g + x * 8) * kPitchD + y * 8 + t * 2]) = make_float2(e[y][2 * x], e[y][2 * x + 1]);
-      uint32_t w[2][4];
-      split_a<2>(p[0], p[1], w);
+      uint32_t w[3][4];
+      split_a(p[0], p[1], w);
       store_blocks<false>(out + kP, b0, b0, buf, lane, w);
     }
     // x_i = -sum_k A_ik x_k: a half warp per block, a lane per column
@@ -525,8 +526,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(GdrArgs a, ui
             c[y][2 * x + 1] = row[x] * (e2.y * qk.y);
           }
         }
-        uint32_t w[2][4];
-        split_a<2>(c[0], c[1], w);
+        uint32_t w[3][4];
+        split_a(c[0], c[1], w);
         store_blocks<false>(out + kP, ib * 16, jb * 16, buf, lane, w);
       }
     }
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
 #pragma unroll
     for (int x = 0; x < DK / 16; ++x) {
       uint32_t f[3][4];
-      split_a<3>(S[2 * x], S[2 * x + 1], f);
+      split_a(S[2 * x], S[2 * x + 1], f);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t fk[4], fq[4];
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       uint32_t f[3][4];
-      split_a<3>(X[2 * x], X[2 * x + 1], f);
+      split_a(X[2 * x], X[2 * x + 1], f);
 #pragma unroll
       for (int p = x; p < 4; ++p) {
         const uint32_t at = sb + kT + tile_at(p * 16 + nb, x * 16 + kb * 8);
@@ -708,17 +709,19 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
     // O^T = e^g Y^T + U^T P^T
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      uint32_t f[2][4];
-      split_a<2>(U[2 * x], U[2 * x + 1], f);
+      uint32_t f[3][4];
+      split_a(U[2 * x], U[2 * x + 1], f);
 #pragma unroll
       for (int p = x; p < 4; ++p) {
         const uint32_t at = sb + kP + tile_at(p * 16 + nb, x * 16 + kb * 8);
+        const PlaceOfP third = third_of_p(p, x);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 3; ++j) {
           uint32_t m[4];
-          ldsm4(m, at + j * kTile);
+          ldsm4(m, j < 2 ? at + j * kTile : sb + kP + third.tile * kTile +
+                                                tile_at(third.row * 16 + nb, third.col * 16 + kb * 8));
 #pragma unroll
-          for (int i = 0; i < 2 - j; ++i) {
+          for (int i = 0; i < 3 - j; ++i) {
             mma(Y[2 * p], f[i], m[0], m[1]);
             mma(Y[2 * p + 1], f[i], m[2], m[3]);
           }
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const
           uu[0] *= ku.x; uu[1] *= ku.y; uu[2] *= ku.x; uu[3] *= ku.y;
         }
         uint32_t f[3][4];
-        split_a<3>(U[2 * x], U[2 * x + 1], f);
+        split_a(U[2 * x], U[2 * x + 1], f);
 #pragma unroll
         for (int p = 0; p < DK / 16; ++p) {
           uint32_t m[4];  // tokens 16 x + (0-7, 8-15) x channels 16 p + (0-7, 8-15)

@@ -11,10 +11,11 @@ constexpr int kC = 64;                 // tokens per chunk
 constexpr long long kGdrSpins = 4000000000LL;  // ~2 s of clock cycles
 
 // One (chunk, value head) of the workspace: the bf16 parts of T and P as tiles [row][64] of
-// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.  The
-// 16 x 16 blocks above the diagonal ones are neither written nor read.
+// 128-byte rows whose 16-byte groups are XORed with the row's low three bits, then vectors.  T has
+// three tiles, P two: the 16 x 16 blocks above the diagonal ones are zeros that no product reads, and
+// P's third part lies there in its two tiles (third_of_p).
 constexpr uint32_t kTile = kC * kC * 2;
-constexpr uint32_t kT = 0, kP = 3 * kTile;  // T: three parts, P: two
+constexpr uint32_t kT = 0, kP = 3 * kTile;
 constexpr uint32_t kVec = 5 * kTile;        // floats: a[64], b[64], ku[64], e^{g_C}
 constexpr uint32_t kBlock = kVec + 1024;
 
@@ -22,42 +23,41 @@ __host__ __device__ constexpr uint32_t tile_at(uint32_t row, uint32_t col) {
   return row * 128u + ((((col >> 3) ^ row) & 7u) << 4) + (col & 7u) * 2u;
 }
 
+// Where the 16 x 16 block (i, j), j <= i, of P's third part lies: the tile of P, and the block in it.
+// The blocks of a column stay below each other, so that one product takes them, but for (0, 0): no
+// tile has four above its diagonal.
+struct PlaceOfP {
+  int tile, row, col;
+};
+__host__ __device__ constexpr PlaceOfP third_of_p(int i, int j) {
+  return j == 0 ? (i == 0 ? PlaceOfP{1, 0, 1} : PlaceOfP{0, i - 1, 3})
+                : PlaceOfP{j == 1 ? 1 : 0, i - j, 4 - j};
+}
+
 // Chunk c of sequence n has block (t0 / 64 + n) + c: floor((t0 + len) / 64) + 1 is at
 // least floor(t0 / 64) + ceil(len / 64), so that sequences never share a block, and no
 // prefix sum over the sequences is needed.
 __host__ __device__ constexpr int block_base(int t0, int n) { return t0 / kC + n; }
 
-// x, y as sums of bf16 parts, packed
-__device__ __forceinline__ uint32_t part(float& x, float& y) {  // takes the next part off
-  const uint32_t p = umma::pack_bf162(x, y);
-  x -= __uint_as_float(p << 16);
-  y -= __uint_as_float(p & 0xffff0000u);
-  return p;
-}
-template <int kParts>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[kParts]) {
-#pragma unroll
-  for (int i = 0; i < kParts - 1; ++i) p[i] = part(x, y);
-  p[kParts - 1] = umma::pack_bf162(x, y);
-}
-
-// The same for three parts, by cutting instead of rounding: 8 + 8 + 8 bits hold all of fp32's 24,
-// so the sum of the parts is exact.
+// x and y as sums of three bf16 parts, packed.  Each part is rounded to nearest: what the first two
+// leave is at most 2^-17 of the value, of either sign, and has at most 8 bits, so that the sum of
+// the three is exact.  (Parts cut off instead would leave up to 2^-15, always toward zero, in the
+// products that take two of them: by emulation o off by 1e-5 of its size, not 3e-6, with states of
+// 30 times v's.)
 __device__ __forceinline__ unsigned long long f2(float x, float y) {
   return ((unsigned long long)__float_as_uint(y) << 32) | __float_as_uint(x);
 }
 __device__ __forceinline__ void split3(float x, float y, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
   const unsigned long long kMinus = f2(-1.f, -1.f);
-  const uint32_t m = 0xffff0000u;
-  uint32_t xi = __float_as_uint(x), yi = __float_as_uint(y);
-  unsigned long long r = f2(x, y), h;
-  p0 = __byte_perm(xi, yi, 0x7632);
-  h = ((unsigned long long)(yi & m) << 32) | (xi & m);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(h), "l"(kMinus));
-  xi = (uint32_t)r; yi = (uint32_t)(r >> 32);
-  p1 = __byte_perm(xi, yi, 0x7632);
-  h = ((unsigned long long)(yi & m) << 32) | (xi & m);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(h), "l"(kMinus));
+  unsigned long long r = f2(x, y);
+  auto take = [&](float lo, float hi) {
+    const uint32_t p = umma::pack_bf162(lo, hi);
+    const unsigned long long h = ((unsigned long long)(p & 0xffff0000u) << 32) | (p << 16);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(h), "l"(kMinus));
+    return p;
+  };
+  p0 = take(x, y);
+  p1 = take(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
   p2 = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
 }
 
