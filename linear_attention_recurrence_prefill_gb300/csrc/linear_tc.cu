@@ -234,7 +234,6 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
     }
   }
   if (!ok && lane == 0) atomicExch(t.status, KDA_ERR_TIMEOUT);
-  __syncwarp();
   fence_before_sync();
   cluster_sync();  // no CTA leaves while the other reads its shared memory or signals to it
   fence_after_sync();
@@ -446,7 +445,6 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
 
   // every rank adds up its share of the tile's columns over all ranks; a CTA that gave up takes
   // part in the barriers all the same
-  __syncwarp();
   cluster_sync();
   if (warp < 4) {
     // four neighbouring channels per thread, a column per warp

@@ -446,8 +446,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 // Barrier of every thread of the cluster; shared-memory writes before it are
-// visible to the whole cluster behind it.
+// visible to the whole cluster behind it.  The aligned forms want the warp in step, which
+// branches of single lanes before them need not leave it.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
