@@ -165,10 +165,13 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
         pair_tma_load_2d(dst + kRowsA * kBlockK * 2, &t.tm_x, kb * (int)kBlockK, m0, bar);
       }
     }
-    // a wait that gave up: the loads in flight land before shared memory is released
-    if (!ok && rank == 0)
-      for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
-        mbar_wait(&full[j % kStages], (j / kStages) & 1, kSpins);
+    // The last signals to either CTA arrive before it leaves: those of the products that read the
+    // stages, or, after a wait that gave up, of the loads in flight.
+    for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+      if (ok) ok = mbar_wait(&empty[j % kStages], (j / kStages) & 1, kSpins);
+      else if (rank == 0) mbar_wait(&full[j % kStages], (j / kStages) & 1, kSpins);
+    // (the odd CTA issues no products, but is signalled to all the same)
+    if (rank == 1 && !mbar_wait(&drained, 0, 2 * kSpins)) ok = false;
   } else if (warp == kPairMma && rank == 0) {
     const uint32_t lead = elect_leader();
     constexpr uint32_t idesc = idesc_f16(256, BN, true);

@@ -45,3 +45,72 @@ def run_all(M, K, N, dtype, act, seed):
 def test_split_with_lanes_outside(M, K, N, dtype):
     """The last tile's lanes fall outside y one by one: they meet the cluster's barrier in step."""
     run_all(M, K, N, dtype, "silu", seed=M + N)
+
+
+# ------------------------------------------------------------------ pairs of CTAs
+def pair_width(M, N):
+    """The width of tile that pairs of CTAs take for aligned bf16 rows: the one whose waves cost
+    least; None where too few tiles send the product to the split form."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    rows = -(-N // 256)
+    if rows * -(-M // 128) < pairs // 2:
+        return None
+    return min((256, 224, 192, 160, 128),  # the first of equal ones
+               key=lambda bn: -(-rows * -(-M // bn) // pairs) * (448 + bn))
+
+
+PAIRS = [(1300, 1000, 128), (2900, 1000, 160), (3500, 1000, 192), (4100, 1000, 224), (4700, 1000, 256)]
+
+
+@gpu
+@pytest.mark.parametrize("M, N, width", PAIRS)
+@pytest.mark.parametrize("K, act", [(136, "gelu_tanh"), (520, "silu"), (1000, "none")])
+def test_pairs(M, N, width, K, act):
+    """Every width, tiles that M, N and K leave part-filled, every form of the epilogue."""
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert pair_width(M, N) == width
+    run_all(M, K, N, BF16, act, seed=M + K)
+
+
+@gpu
+@pytest.mark.parametrize("act", sorted(kda.ACTS))
+def test_pairs_activations(act):
+    """Odd rows of y: no two channels share an aligned word."""
+    assert pair_width(1301, 1001) is not None
+    run_all(1301, 264, 1001, BF16, act, seed=7)
+
+
+@gpu
+def test_pairs_several_tiles_each():
+    """More tiles than pairs, so that accumulators and stages come round; wide rows of x and w."""
+    M, K, N = 2700, 72, 5000
+    assert pair_width(M, N) is not None
+    x, w, b, r = make(M, K, N, BF16, seed=8)
+    x, w = wider(x, 8), wider(w, 16)
+    for _ in range(3):
+        check(kda.kda_linear(x, w, b, r, act="gelu"), *plain64.linear(x, w, b, r, "gelu"))
+
+
+@gpu
+def test_pairs_what_is_not_finite():
+    """NaN and infinities stay in their rows of x and w (and with them in y's)."""
+    M, K, N = 1300, 136, 1000
+    x, w, b, r = make(M, K, N, BF16, seed=9)
+    x[17, 3], x[1299, 135], w[999, 0], w[4, 77] = float("nan"), float("inf"), float("-inf"), float("nan")
+    y = kda.kda_linear(x, w, b, r, act="relu")
+    rows, cols = torch.ones(M, dtype=torch.bool), torch.ones(N, dtype=torch.bool)
+    rows[[17, 1299]] = False
+    cols[[999, 4]] = False
+    y_ref, off = plain64.linear(x[rows.cuda()], w[cols.cuda()], b[cols.cuda()], r[rows.cuda()][:, cols.cuda()], "relu")
+    check(y[rows.cuda()][:, cols.cuda()], y_ref, off)
+    assert y[17].isnan().all() and y[:, 4].isnan().all()
+
+
+@gpu
+def test_pairs_columns_behind_k_are_not_read():
+    """Rows of x and w in wider arrays that hold NaN behind them."""
+    M, K, N = 1300, 136, 1000
+    x, w, b, r = make(M, K, N, BF16, seed=10)
+    xs, ws = (torch.full((t.shape[0], K + 24), float("nan"), dtype=BF16, device="cuda") for t in (x, w))
+    xs[:, :K], ws[:, :K] = x, w
+    check(kda.kda_linear(xs[:, :K], ws[:, :K], b, r), *plain64.linear(x, w, b, r))
