@@ -428,7 +428,9 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
         if (lane == 0) mbar_arrive(&full[s]);
       }
     }
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(&done, 0, kSpins));
+    // Done behind all of this CTA's blocks, each of which has a wait of its own that gives up (the
+    // MMA warp then signals all the same): a block takes some 300 to 5,000 cycles.
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&done, 0, 3 * kSpins + (long long)blocks * 65536));
     fence_after_sync();
     if (ok && warp < 4) {
       // partial sums [column][channel] over the ring, whose loads and products are done

@@ -114,3 +114,17 @@ def test_pairs_columns_behind_k_are_not_read():
     xs, ws = (torch.full((t.shape[0], K + 24), float("nan"), dtype=BF16, device="cuda") for t in (x, w))
     xs[:, :K], ws[:, :K] = x, w
     check(kda.kda_linear(xs[:, :K], ws[:, :K], b, r), *plain64.linear(x, w, b, r))
+
+
+# ------------------------------------------------------------------ very long rows
+@gpu
+def test_a_product_of_seconds():
+    """One row whose shifted parts of K take seconds: no wait of the call covers all of them."""
+    K = 1_200_000_001
+    x, w = (torch.zeros(K + 1, dtype=BF16, device="cuda")[1:].unsqueeze(0) for _ in range(2))
+    at = torch.arange(0, K, 9_999_991, device="cuda")  # 121 places, the sum exact in fp32 and bf16
+    x[0, at], w[0, at] = 1.0, 1.0
+    w[0, K - 1], x[0, K - 1] = 2.0, 3.0
+    y = kda.kda_linear(x, w)
+    assert kda.kda_get_last_error() == kda.KDA_OK
+    assert float(y) == len(at) + 6
