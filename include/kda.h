@@ -302,9 +302,10 @@ typedef struct kda_gdr_options {
                             [N][L][H_v][d_k][d_v] that receives the state after
                             each token (of proposed tokens, some of which are
                             taken), rows of sequences left out untouched       */
-  int max_seqlen;        /* kda_gdr_prefill: the longest sequence, 0 = T_total;
-                            short ones are taken token by token (it decides the
-                            speed only)                                        */
+  int max_seqlen;        /* kda_gdr_prefill: the longest sequence, 0 = T_total
+                            (without cu_seqlens too: there T_total / N is the
+                            one to give); short ones are taken token by token
+                            (it decides the speed and the workspace only)      */
   int impl;              /* kda_gdr_prefill: KDA_IMPL_AUTO, KDA_IMPL_SIMT (token
                             by token on the CUDA cores) or KDA_IMPL_TC (chunks
                             of 64 on the tensor cores, bf16 data only)         */

@@ -124,9 +124,10 @@ int kda_gdr_prefill_path(int T_total, int N, int H_k, int H_v, int d_k, int d_v,
       if (!tc) return KDA_ERR_UNSUPPORTED;
       return T_total > 0 ? KDA_IMPL_TC : KDA_IMPL_SIMT;
     case KDA_IMPL_AUTO: {
-      // Token by token where no sequence is longer than this.  One sequence of 16 tokens took 13 us
-      // that way and 18 us in chunks, 16 sequences 52 and 47 us (32 heads of 128 x 128); heads of
-      // 64 x 64, 48 tokens, 16 sequences: 45 and 48 us.
+      // Token by token where no sequence is longer than this.  32 heads of 128 x 128, 1, 16 and 256
+      // sequences: 16 tokens took 14, 53 and 641 us that way and 21, 53 and 688 us in chunks, 24
+      // tokens 19, 74 and 914 against 21, 56 and 697 us.  Heads of 64 x 64, 16 sequences: 48 tokens
+      // 46 and 52 us, 64 tokens 59 and 60 us.
       const int longest = op->max_seqlen > 0 ? op->max_seqlen : T_total;
       return tc && longest > (d_k * d_v <= 64 * 64 ? 48 : 16) ? KDA_IMPL_TC : KDA_IMPL_SIMT;
     }

@@ -595,8 +595,9 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
     q, k [T, H_k, d_k]; v [T, H_v, d_v]; each token's heads contiguous, tokens any
     even distance apart (slices of one projection).  log_alpha [T, H_v] fp32;
     beta [T, H_v]; S0 [N, H_v, d_k, d_v] fp32 or None (zeros); cu_seqlens [N+1]
-    int32 on the device, or None for N sequences of T / N tokens.  Returns
-    (o, S_T).  With ``slots`` [N] int32, S0 and S_T are pools
+    int32 on the device, or None for N sequences of T / N tokens.  ``max_seqlen``:
+    the longest sequence, 0 = T (T / N without cu_seqlens); short ones are taken
+    token by token, without a workspace.  Returns (o, S_T).  With ``slots`` [N] int32, S0 and S_T are pools
     [n_slots, H_v, d_k, d_v] and sequence n's state is matrix slots[n]; S_T has
     to be given (it may be S0).  ``decay_from_logit``: log_alpha holds logits z,
     the log decay is -A softplus(z + b) with decay_scale A [H_v] and decay_bias
@@ -622,6 +623,8 @@ def kda_gdr_prefill(q, k, v, log_alpha, beta, S0=None, cu_seqlens=None, N: int |
                               decay_bias, N, l2norm_qk, beta_is_logit, decay_from_logit, q_scale,
                               eps_l2)
     dt = _code(host, q.dtype)
+    if max_seqlen == 0 and cu_seqlens is None and N > 0:
+        max_seqlen = T // N  # every length is known
     opt.max_seqlen = max_seqlen
     opt.impl = IMPLS[impl] if isinstance(impl, str) else int(impl)
     if workspace is not None and not workspace.is_contiguous():
