@@ -25,11 +25,8 @@
 // ku U go with 192-223; 224 and 288 in turn X and U, then U's first two parts; 352 and 416 in turn
 // Y, then o; 480-511 U's third part.  A warpgroup writes and reads only its own columns, so that no barrier between the warps is
 // needed.
-#include <cuda.h>
-
-#include <mutex>
-
 #include "gdr_chunked.cuh"
+#include "tensor_map.cuh"
 
 namespace kda {
 namespace {
@@ -476,25 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdr_chain_tc_kernel(const __grid_
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-// cuTensorMapEncodeTiled, reached through the runtime (no link against the driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
 // Tensor map of [T][H][d] bf16 rows, tokens ld elements apart: boxes of 64 channels of one head
 // by `rows` tokens.
 bool encode(CUtensorMap* m, const void* base, int T, int H, int d, long long ld, int rows) {
@@ -530,10 +508,6 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
 }
 
 }  // namespace
-
-bool gdr_chain_tc_takes(const GdrArgs& a) {
-  return (a.dk == 64 || a.dk == 128) && a.dv % (int)kDv == 0;
-}
 
 cudaError_t launch_gdr_chain_tc(const GdrArgs& a, const uint8_t* ws, cudaStream_t s) {
   return a.dk == 128 ? launch<128>(a, ws, s) : launch<64>(a, ws, s);

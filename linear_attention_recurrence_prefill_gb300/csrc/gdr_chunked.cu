@@ -807,8 +807,10 @@ cudaError_t launch_dk(const GdrArgs& a, uint8_t* ws, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   gdr_prep_kernel<DK><<<dim3(a.T_total / kC + a.N, a.Hk), kPrepThreads, bytes, s>>>(a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (gdr_chain_tc_takes(a)) return launch_gdr_chain_tc(a, ws, s);
-  if (a.dv % 128 == 0) return launch_chain<DK, 8>(a, ws, s);
+  if (a.dv % 128 == 0) {
+    if constexpr (DK == 32) return launch_chain<DK, 8>(a, ws, s);
+    else return launch_gdr_chain_tc(a, ws, s);
+  }
   if (a.dv == 64) return launch_chain<DK, 4>(a, ws, s);
   return launch_chain<DK, 2>(a, ws, s);
 }

@@ -76,7 +76,6 @@ __device__ __forceinline__ int longest_first(const GdrArgs& a, int place) {
 }
 
 // The walk over the chunks on tcgen05: d_k in {64, 128}, d_v a multiple of 128.
-bool gdr_chain_tc_takes(const GdrArgs& a);
 cudaError_t launch_gdr_chain_tc(const GdrArgs& a, const uint8_t* ws, cudaStream_t s);
 
 }  // namespace kda

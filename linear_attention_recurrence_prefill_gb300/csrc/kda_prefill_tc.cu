@@ -54,12 +54,10 @@
 // every other product uses fp16 operands (11 significant bits; all values there
 // are within fp16 range or negligibly small) with fp32 accumulation; the state
 // itself stays fp32.
-#include <cuda.h>
 #include <stdio.h>
 
-#include <mutex>
-
 #include "kda_tc.cuh"
+#include "tensor_map.cuh"
 #include "umma.cuh"
 
 namespace kda {
@@ -1612,26 +1610,6 @@ __global__ void __launch_bounds__(kChThreads, 1) chain_kernel(TcArgs t) {
   __syncthreads();
   fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, 512);
-}
-
-// cuTensorMapEncodeTiled, reached through the runtime (no link against the
-// driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
 }
 
 // Tensor map of a [T][H][128] token array of 2-byte (bf16) or 4-byte (fp32)

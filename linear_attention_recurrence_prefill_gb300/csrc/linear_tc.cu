@@ -28,11 +28,8 @@
 //    apart): eight warps then fill the ring, from aligned 16-byte loads that they shift into
 //    place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.4 us, 4.8 TB/s with its set-up
 //    and joining; 4096 x 4095 x 4097, shifted, 584 us.
-#include <cuda.h>
-
-#include <mutex>
-
 #include "linear.cuh"
+#include "tensor_map.cuh"
 #include "umma.cuh"
 
 namespace kda {
@@ -469,26 +466,6 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
   cluster_sync();  // no CTA leaves while its sums are read
   fence_after_sync();
   if (warp == kWarpMma) tmem_dealloc(tmem, kCols);
-}
-
-// cuTensorMapEncodeTiled, reached through the runtime (no link against the
-// driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
 }
 
 // Tensor map of a [rows][K] bf16 array, rows ld elements apart: boxes of 64
