@@ -90,9 +90,11 @@ GdrArgs gdr_args(const void* q, const void* k, const void* v, const float* log_a
   a.l2norm_qk = op->l2norm_qk; a.beta_is_logit = op->beta_is_logit;
   a.decay_from_logit = op->decay_from_logit;
   a.q_scale = op->q_scale; a.eps_l2 = op->eps_l2;
-  a.ldq = op->ldq ? op->ldq : (long long)H_k * d_k;
-  a.ldk = op->ldk ? op->ldk : (long long)H_k * d_k;
-  a.ldv = op->ldv ? op->ldv : (long long)H_v * d_v;
+  // a single token's stride says nothing, and a tensor map takes none of 2^40 bytes
+  const bool dense = T_total < 2;
+  a.ldq = op->ldq && !dense ? op->ldq : (long long)H_k * d_k;
+  a.ldk = op->ldk && !dense ? op->ldk : (long long)H_k * d_k;
+  a.ldv = op->ldv && !dense ? op->ldv : (long long)H_v * d_v;
   return a;
 }
 

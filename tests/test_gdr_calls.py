@@ -114,3 +114,22 @@ def test_chunks_of_narrow_heads(Hk, Hv, dk, dv):
     o_ref, S_ref = expect_prefill(args, lens, S0)
     check(o, o_ref, TOL["tc"], "o")
     check(S, S_ref, TOL["tc"], "S_T")
+
+
+@gpu
+@pytest.mark.parametrize("impl", ["simt", "tc"])
+def test_one_token_whatever_its_stride(impl):
+    Hk, Hv, d = 1, 2, 128
+    q, k, v, la, beta = draw((1,), Hk, Hv, d, d, BF16, seed=36)
+    o, S = torch.empty_like(v), torch.empty(1, Hv, d, d, device="cuda")
+    opt = kda.kda_gdr_options_init(impl=impl, ldq=1 << 40, ldk=1 << 41, ldv=1 << 42)
+    ws = torch.empty(kda.kda_gdr_prefill_workspace_size(1, 1, Hk, Hv, d, d, kda.KDA_BF16, opt) or 16,
+                     dtype=torch.uint8, device="cuda")
+    opt.workspace, opt.workspace_bytes = ws.data_ptr(), ws.numel()
+    rc = kda.load().kda_gdr_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), la.data_ptr(), beta.data_ptr(),
+                                    None, None, 1, o.data_ptr(), S.data_ptr(), 1, Hk, Hv, d, d,
+                                    kda.KDA_BF16, opt, torch.cuda.current_stream().cuda_stream)
+    assert rc == kda.KDA_OK and kda.kda_get_last_error() == kda.KDA_OK
+    o_ref, S_ref = expect_prefill((q, k, v, la, beta), [1], None)
+    check(o, o_ref, TOL[impl], "o")
+    check(S, S_ref, TOL[impl], "S_T")
