@@ -16,7 +16,7 @@
 // tensor cores work on U and hand the last chunk's o to another warp, which stores it, while
 // they work on X.
 //
-// A chunk of 128 x 128 heads takes 5,400 cycles (4096 tokens x 96 heads: 180 us on 96 SMs), of which
+// A chunk of 128 x 128 heads takes 6,000 cycles (4096 tokens x 96 heads: 202 us on 96 SMs), of which
 // the products need 5,300: 101 MMAs of N = 64, 45 cycles each whatever N is below 128, and 12 of
 // N = 128, 64 each.  (X and Y as one product against [K; Q] need fewer cycles, but X comes 460 later.)
 //

@@ -12,8 +12,8 @@
 //
 // Two kernels.  prep: T, P and the vectors of every chunk, all chunks in
 // parallel.  chain: the state's walk over the chunks of a sequence (gdr_chain_tc.cu; here
-// the one for d_v of 32 and 64 and d_k of 32).  4096 tokens x 96 heads of 128 x 128: 95 and
-// 180 us.
+// the one for d_v of 32 and 64 and d_k of 32).  4096 tokens x 96 heads of 128 x 128: 100 and
+// 202 us.
 //
 // Precision: the final states are fp32 results, so no operand on the state's way may be
 // rounded to bf16.  K, Q and V are bf16 as they come and enter the products unscaled (norms
@@ -76,7 +76,7 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
 // and the first rows of P.
 //
 // No one thing bounds it: 16 warps per SM issue in 40 % of the cycles, shared memory is busy in
-// half of them, 104 MB are read and 160 MB written in 95 us (126 MB to DRAM by its end), and taking
+// half of them, 104 MB are read and 193 MB written in 100 us (151 MB to DRAM by its end), and taking
 // any one step out saves 4 to 30 us.
 //
 // e^{g_i - g_j} off the diagonal blocks is e^{g_i - g_r} e^{g_r - g_j}, r the first row of i's
@@ -561,7 +561,8 @@ struct ChainSmem {
 // operand of the next product as they lie.  No warp waits for another, only for the loads,
 // which an extra warp issues two chunks ahead.  Bound by mma.sync, a quarter of tcgen05's rate:
 // 4096 tokens x 96 heads of 128 x 128 took 519 us so; it is kept for the heads that tcgen05's 128
-// rows do not fit.
+// rows do not fit (per-chunk kernel included, 4096 tokens x 32 heads of 64 x 64: 436 us; 2000
+// tokens in five sequences x 16 heads of 32 x 256: 104 us).
 template <int DK, int W>
 __global__ void __launch_bounds__(W * 32 + 32) gdr_chain_kernel(GdrArgs a, const uint8_t* ws) {
   using Smem = ChainSmem<DK, W>;

@@ -16,8 +16,9 @@ struct LinearArgs {
 };
 
 // kFast, for results that are rounded to bf16: the exponential and the division
-// by their approximate instructions, off by a few 2^-23, not by half a step of bf16
-// (2^-9 and more).
+// by their approximate instructions.  __expf(y) is off by up to 2 + floor(|1.173 y|) units of
+// 2^-23, about 100 where y is near 88, which is 2^-16: 128 times less than half a step of
+// bf16 (2^-9 and more).
 template <bool kFast>
 __device__ __forceinline__ float over_1_plus_exp(float x, float y) {  // x / (1 + e^y)
   if constexpr (kFast) {
@@ -96,7 +97,7 @@ __device__ __forceinline__ float4 bias4(const LinearArgs& a, int n) {
 
 // Launchers, for a device of `sms` SMs; each returns the launch's cudaError_t.
 cudaError_t launch_linear_simt(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
-// Up to four rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
+// Up to two rows of x in bf16, four in fp32; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
 bool linear_few_takes(const LinearArgs& a, int dtype);
 cudaError_t launch_linear_few(const LinearArgs& a, int dtype, int sms, cudaStream_t s);
 // bf16, any alignment, any number of rows, K > 0.

@@ -5,9 +5,10 @@
 // (fma.rn.f32x2): three 16-byte reads of shared memory for 32 products.  x and w pass through shared memory 16 columns at
 // a time, the next ones fetched into registers meanwhile.  Where there are too few tiles to give
 // every SM two CTAs, the CTAs of a cluster share a tile, each takes a part of K, and the sums meet
-// in distributed shared memory, added in the order of the ranks.  Bound by the issue of the
-// multiply-adds where there is work enough (1024^3: 70 us, 31 TFLOP/s), by latency where not
-// (200 x 512 x 640: 10.4 us).
+// in distributed shared memory, added in the order of the ranks.  1024^3 takes 70 us
+// (31 TFLOP/s, under half of the CUDA cores' rate: 256 tiles are 1.7 waves of 152 SMs, with two warps
+// per scheduler and one step fetched ahead); small products are bound by latency (200 x 512 x 640:
+// 10.5 us).
 #include "linear.cuh"
 #include "umma.cuh"
 

@@ -2,21 +2,18 @@
 // (bf16 data).
 //
 // The product is taken transposed: D[n][m] = sum_k w[n][k] x[m][k], 128 rows of
-// w (the M of the MMA, the lanes of TMEM) by BN rows of x (its N, the columns).
-// A lane of the epilogue then owns one output channel n: its bias is one
-// register, and for every token the 32 lanes of a warp write 32 neighbouring
-// elements of y, and read those of the residual, whatever their alignment.
-//
-// Six warps: 0-3 the epilogue (each its quarter of the TMEM lanes), 4 issues the
-// TMA loads of a ring of stages (64 columns of w and x each, 128-byte swizzle),
-// 5 issues the MMAs.
+// w (the M of the MMA, the lanes of TMEM) by BN rows of x (its N, the columns),
+// from a ring of stages of 64 columns of w and x each, with a 128-byte swizzle.
 //
 // Two kernels; each starts its set-up while the kernel before it in the stream ends.
 //  * linear_pair_kernel: pairs of CTAs (cta_group::2) share tiles of 256 rows of w by BN tokens, a
 //    persistent pair per two SMs walking the tiles, two accumulators in TMEM so that a tile's
 //    epilogue runs beside the next tile's products.  Alone, a CTA would fetch 128 + 256 rows for
 //    each 128 x 256 products, 96 bytes per clock from L2 at the tensor cores' full rate, more than
-//    an SM gets; a pair fetches 64.  4096 x 4096 x 12288: 234 to 242 us, 1.70 to 1.76
+//    an SM gets; a pair fetches 64.  Ten warps: 0-7 the epilogue, a lane per output channel (its
+//    bias is one register, and for every token a warp writes 32 neighbouring elements of y and reads
+//    those of the residual, whatever their alignment), 8 loads, 9 issues the MMAs.
+//    4096 x 4096 x 12288: 234 to 242 us, 1.70 to 1.76
 //    PFLOP/s, 0.89 to 0.92 of the measured bf16 rate (with bias, GELU and residual 251 to 262 us;
 //    the library's plain product 208 us); 8192^3: 571 us (the library's 542).  The
 //    tensor pipe is active in 79 % of the cycles of the former; the rest is 768 tiles in waves of 76,
@@ -24,10 +21,12 @@
 //  * linear_split_kernel, where there are too few tiles to fill the GPU (few tokens, or a small
 //    product): the CTAs of a cluster share one tile, each takes a part of K, and the partial sums
 //    meet in distributed shared memory, added in the order of the ranks, so that results repeat
-//    to the bit.  It also takes arrays that TMA cannot (rows that are no multiple of 16 bytes
-//    apart): eight warps then fill the ring, from aligned 16-byte loads that they shift into
-//    place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.4 us, 4.8 TB/s with its set-up
-//    and joining; 4096 x 4095 x 4097, shifted, 584 us.
+//    to the bit; four neighbouring channels per lane, a token per warp, which is one access where y's
+//    and the residual's rows are multiples of four elements and four where not.  Six warps: 0-3 read
+//    the sums, 4 loads, 5 issues the MMAs.  It also takes arrays that TMA cannot (rows that are no
+//    multiple of 16 bytes apart): 0-3 and four more warps then fill the ring, from aligned 16-byte
+//    loads that they shift into place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.5 us, 4.8 TB/s with its set-up
+//    and joining; 4096 x 4095 x 4097, shifted by every CTA that uses a tile, 584 us.
 #include "linear.cuh"
 #include "tensor_map.cuh"
 #include "umma.cuh"
