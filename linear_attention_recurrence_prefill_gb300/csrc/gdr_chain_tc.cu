@@ -23,8 +23,8 @@
 // TMEM columns (d_k = 128): 0-191 the parts of S, the first two of which lie where the same
 // warpgroup's half of the update's product comes (0-127), the third (128-191) where -a X and
 // ku U go with 192-223; 224 and 288 in turn X and U, then U's first two parts; 352 and 416 in turn
-// Y, then o; 480-511 U's third part.  A warpgroup writes and reads only its own columns, so that no barrier between the warps is
-// needed.
+// Y, then o; 480-511 U's third part.  A warpgroup writes and reads only its own columns, so that no
+// barrier between the warps is needed.
 #include "gdr_chunked.cuh"
 #include "tensor_map.cuh"
 

@@ -21,8 +21,8 @@
 // three bf16 parts (24 bits, an fp32 value), of whose products those of order 2^-24 are left
 // out.  Only Q S, which o alone sees, takes the first two of the state's parts: 2^-17 at most,
 // and in the walk on tcgen05 the third part has to make room for what X becomes meanwhile.
-// With P and U in two parts too, o was off by 4.4e-6 of its size before it was rounded, not by
-// 1e-6, and 4096 tokens x 96 heads took 22 us less.
+// With P and U in two parts too, o would be off by 4.4e-6 of its size before it is rounded, not by
+// 7e-7 (by emulation, sums exact); 4096 tokens x 96 heads took 22 us less so.
 #include "gdr_chunked.cuh"
 
 namespace kda {
