@@ -399,6 +399,168 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
                int act, int dtype, kda_stream_t stream);
 
 /*
+ * kda_rmsnorm -- the norm before a layer's projections, with the residual's
+ * addition: per token m
+ *
+ *     s = x_m + residual_m                       (32 bits, not rounded in between)
+ *     n = s / sqrt(mean_d s_d^2 + eps) * w
+ *     sum_m = s,  y_m = n  (dtype),  scale_m = max_d |n_d| / 127,  q_m = n / scale_m
+ *
+ *   x         [M][D] dtype, rows ldx elements apart (0 = D)
+ *   residual  [M][D] dtype, rows ldr elements apart (0 = D), or NULL
+ *   w         [D] fp32, or NULL (= ones)
+ *   sum       [M][D] dtype out, rows lds elements apart (0 = D), or NULL; may be x or
+ *             the residual itself (same address and stride)
+ *   y         [M][D] dtype out, rows ldy elements apart (0 = D), or NULL
+ *   q, scale  [M][D] int8 out, rows ldq elements apart (0 = D), and [M] fp32 out, or
+ *             both NULL: what kda_linear_i8 takes
+ *
+ * At least one of y and q is given; outputs overlap no input (but sum) and not
+ * each other (KDA_ERR_ARG where two start at one address).  q is the integer nearest
+ * to 127 n / max |n| as it is without rounding errors, ties to the even one.  A row of
+ * zeros has scale 0 and q = 0; one with an infinity or a NaN in n a scale that is not
+ * finite and q = 0.  Squares are summed in fp32: their sum must stay below 3.4e38.
+ * Pointers need the alignment of their elements.  M and D are below 2^31 - 256, D is
+ * positive.
+ */
+int kda_rmsnorm(const void* x, long long ldx, const void* residual, long long ldr, const float* w,
+                void* sum, long long lds, void* y, long long ldy, int8_t* q, long long ldq,
+                float* scale, int M, int D, float eps, int dtype, kda_stream_t stream);
+
+/* The same without a norm, a residual and weights: scale_m = max |x_m| / 127, q_m =
+ * x_m / scale_m, for a product whose input comes from elsewhere. */
+int kda_quantize_i8(const void* x, long long ldx, int8_t* q, long long ldq, float* scale, int M,
+                    int D, int dtype, kda_stream_t stream);
+
+/*
+ * kda_linear_i8 -- kda_linear in 8-bit integers with a scale per token and per
+ * channel: y = act(x_scale_m w_scale_n sum_k x_mk w_nk + bias_n) + residual.
+ *
+ *   x, x_scale  [M][K] int8, rows ldx bytes apart (0 = K); [M] fp32
+ *   w, w_scale  [N][K] int8, rows ldw bytes apart (0 = K); [N] fp32
+ *   bias        [N] dtype or NULL
+ *   residual    [M][N] dtype, rows ldr elements apart (0 = N), or NULL
+ *   y           [M][N] dtype out, as in kda_linear
+ *
+ * All integers from -128 to 127 are taken.  The sum is exact while no partial sum
+ * exceeds 2^24 (any K up to 1024; beyond, what an addition cuts off is at most 2^-23 of the
+ * sum); (sum x_scale) w_scale, bias, activation and residual are in fp32, rounded once to
+ * dtype.  M, N and K are from 0 to 2^31 - 257 (K = 0: y = act(bias) + residual).  The
+ * workspace (kda_linear_i8_workspace_size bytes, none where that is 0; 16-byte aligned)
+ * holds nothing between calls, but calls that can overlap on the GPU need one each.
+ */
+int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w,
+                  long long ldw, const float* w_scale, const void* bias, const void* residual,
+                  long long ldr, void* y, long long ldy, int M, int N, int K, int act, int dtype,
+                  void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of device workspace kda_linear_i8 needs on the current device. */
+size_t kda_linear_i8_workspace_size(int M, int N, int K);
+
+/*
+ * The gated linear recurrence: a state per channel instead of a matrix per head, one
+ * decay per channel and token.  Per sequence, per channel, per token t:
+ *
+ *     g   =  min(la, 0)  or  -A softplus(la + b)  or  -A sigmoid(la + b);   a = e^g
+ *     u   =  c sigmoid(i) x,    c = 1  or  1 - a  or  sqrt(1 - a^2)
+ *     h_t =  a_t h_{t-1} + u_t,   y_t = h_t
+ *
+ * (A and b per channel, A >= 0; without input gate i: u = c x.)  States are fp32; a decay near
+ * one is held as a - 1, so that a state that remembers thousands of tokens is as exact
+ * as one that remembers ten.  A token that is not finite spoils its channel of its sequence
+ * from there on (in the gradient: up to there); no other channel or sequence is touched.
+ */
+enum { /* decay_from */
+  KDA_GLR_LOG = 0,     /* log_alpha holds log decays, above 0 taken as 0 */
+  KDA_GLR_SOFTPLUS = 1, /* it holds logits: g = -A softplus(la + b)       */
+  KDA_GLR_SIGMOID = 2  /* it holds logits: g = -A sigmoid(la + b)        */
+};
+enum { /* input_scale */
+  KDA_GLR_INPUT_NONE = 0,       /* c = 1            */
+  KDA_GLR_INPUT_COMPLEMENT = 1, /* c = 1 - a        */
+  KDA_GLR_INPUT_NORMALIZED = 2  /* c = sqrt(1 - a^2) */
+};
+#define KDA_GLR_TILE 64
+typedef struct kda_glr_options {
+  int decay_from;        /* KDA_GLR_*, default KDA_GLR_LOG                         */
+  const float* decay_scale; /* A [D] fp32, NULL = ones (unused with KDA_GLR_LOG)   */
+  const float* decay_bias;  /* b [D] fp32, NULL = zeros (unused with KDA_GLR_LOG)  */
+  int input_scale;       /* KDA_GLR_INPUT_*, default KDA_GLR_INPUT_NONE            */
+  const void* input_gate; /* i, logits, as x in shape and dtype; NULL: none        */
+  long long ldx, ldla, ldg; /* elements between the rows of successive tokens in
+                            x, log_alpha, input_gate; 0 = D                       */
+  const int32_t* slots;  /* as in kda_gdr_options (not in the backward pass)       */
+  int n_slots;
+  float* checkpoints;    /* kda_glr_scan: NULL, or fp32 [T_total / 64 + N][D] that
+                            receives the states before every KDA_GLR_TILE-th token
+                            of each sequence (rows between them are not written);
+                            kda_glr_scan_backward reads them                      */
+  int max_seqlen;        /* the longest sequence, 0 = T_total (it decides the speed
+                            and, in the backward pass, the workspace only)         */
+  void* workspace;       /* kda_glr_scan_backward: device scratch, >=
+                            kda_glr_backward_workspace_size(), 16-byte aligned     */
+  size_t workspace_bytes;
+} kda_glr_options;
+
+/* Fill *opt with the defaults listed above. */
+void kda_glr_options_init(kda_glr_options* opt);
+
+/*
+ * kda_glr_scan -- the recurrence over packed sequences.
+ *
+ *   x, log_alpha  [T_total][D] dtype (token strides in opt)
+ *   h0            [N or n_slots][D] fp32 initial states, NULL = zeros
+ *   cu_seqlens    as in kda_prefill; rows of y behind the last sequence are left
+ *                 as they are
+ *   y             [T_total][D] dtype out
+ *   h_T           as h0, final states out (may be h0)
+ *
+ * opt NULL: the defaults.  Pointers need the alignment of their elements (bf16 arrays
+ * are read fastest with an even D, even strides and 4-byte alignment).  y, h_T and the
+ * checkpoints overlap no input and not each other, but h_T may be h0 (KDA_ERR_ARG
+ * where two start at one address).
+ */
+int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const int32_t* cu_seqlens,
+                 int N, void* y, float* h_T, int T_total, int D, int dtype,
+                 const kda_glr_options* opt, kda_stream_t stream);
+
+/*
+ * kda_glr_step -- L tokens for each of N sequences, states updated in place.
+ *
+ *   x, log_alpha  [N][L][D] dtype (token strides in opt)
+ *   h             [N or n_slots][D] fp32, read and overwritten
+ *   y             [N][L][D] dtype out
+ */
+int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N, int L, int D,
+                 int dtype, const kda_glr_options* opt, kda_stream_t stream);
+
+/*
+ * kda_glr_scan_backward -- the gradient of kda_glr_scan, with the options of that call
+ * and the checkpoints that it wrote.
+ *
+ *   dy            [T_total][D] dtype, the gradient of y, NULL = zeros
+ *   dh_T          [N][D] fp32, the gradient of h_T, NULL = zeros
+ *   dx, dlog_alpha [T_total][D] dtype out
+ *   dinput_gate   [T_total][D] dtype out, or NULL (not with opt->input_gate NULL)
+ *   dh0           [N][D] fp32 out, or NULL
+ *   ddecay_scale, ddecay_bias  [D] fp32 out, or NULL (not with KDA_GLR_LOG): summed over
+ *                 all tokens, in an order of its own that does not change
+ *
+ * Rows of outputs behind the last sequence are left as they are.  Where the decay is 1
+ * to the last bit, the slope of sqrt(1 - a^2), which is infinite there, is taken as 0.
+ */
+int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, const void* log_alpha,
+                          const int32_t* cu_seqlens, int N, void* dx, void* dlog_alpha,
+                          void* dinput_gate, float* dh0, float* ddecay_scale, float* ddecay_bias,
+                          int T_total, int D, int dtype, const kda_glr_options* opt,
+                          kda_stream_t stream);
+
+/* Bytes of device workspace kda_glr_scan_backward needs on the current device where
+ * ddecay_scale or ddecay_bias is wanted (none where neither is). */
+size_t kda_glr_backward_workspace_size(int T_total, int N, int D, int dtype,
+                                       const kda_glr_options* opt);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: KDA_OK, KDA_ERR_TIMEOUT (a bounded device wait gave up),
  * KDA_ERR_SHAPE (a kernel found cu_seqlens or a state slot out of range, or a

@@ -45,8 +45,10 @@ __device__ __forceinline__ float gdr_inv_norm(float sum_sq, float eps) {
   return s > 0.f ? 1.0f / sqrtf(s) : 0.f;
 }
 
-// Offset i of the packed sequences (cu_seqlens, or equal lengths).
-__device__ __forceinline__ int gdr_offset(const GdrArgs& a, int i) {
+// Offset i of the packed sequences (cu_seqlens, or equal lengths).  Args: a struct with the
+// fields cu_seqlens, slots, status, N, T_total and n_slots, here and below.
+template <typename Args>
+__device__ __forceinline__ int gdr_offset(const Args& a, int i) {
   return a.cu_seqlens ? a.cu_seqlens[i] : i * (a.T_total / a.N);
 }
 
@@ -56,8 +58,8 @@ __device__ __forceinline__ int gdr_offset(const GdrArgs& a, int i) {
 // taken by an earlier sequence, its tokens are out of range, or the offsets
 // decrease at it or before it.  Up to 32 sequences take one round of loads, a
 // sequence per lane.
-__device__ __forceinline__ bool gdr_sequence(const GdrArgs& a, int n, int& t0, int& t1,
-                                             int& slot) {
+template <typename Args>
+__device__ __forceinline__ bool gdr_sequence(const Args& a, int n, int& t0, int& t1, int& slot) {
   const int lane = threadIdx.x & 31;
   bool bad;
   if (a.N <= 32) {

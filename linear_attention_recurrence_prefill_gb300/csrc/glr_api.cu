@@ -1,0 +1,183 @@
+// glr_api.cu -- the C ABI of the gated linear recurrence: argument checks and
+// path selection, on the host before anything is enqueued.
+#include <string.h>
+
+#include "checks.cuh"
+#include "glr.cuh"
+
+using namespace kda;
+
+namespace {
+
+// Tiles of tokens are counted in 32 bits, up to 16 CTAs of them beyond the end.
+constexpr int kMaxTokens = 0x7fffffff - 2048;
+
+int check_glr(int N, int T_total, int D, int dtype, const kda_glr_options* o) {
+  if (N < 1 || T_total < 0 || T_total > kMaxTokens || D < 1 || D > kMaxSize) return KDA_ERR_SHAPE;
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  if (o->decay_from < KDA_GLR_LOG || o->decay_from > KDA_GLR_SIGMOID) return KDA_ERR_ARG;
+  if (o->input_scale < KDA_GLR_INPUT_NONE || o->input_scale > KDA_GLR_INPUT_NORMALIZED) return KDA_ERR_ARG;
+  if (o->max_seqlen < 0 || o->max_seqlen > T_total) return KDA_ERR_SHAPE;
+  for (long long ld : {o->ldx, o->ldla, o->ldg})
+    if (ld != 0 && ld < D) return KDA_ERR_SHAPE;
+  if (o->slots && o->n_slots < 1) return KDA_ERR_SHAPE;
+  if (!aligned(o->slots, 4)) return KDA_ERR_ALIGN;
+  for (const void* p : {(const void*)o->decay_scale, (const void*)o->decay_bias, (const void*)o->checkpoints})
+    if (!aligned(p, 4)) return KDA_ERR_ALIGN;
+  if (!aligned(o->input_gate, elem(dtype))) return KDA_ERR_ALIGN;
+  if ((D + 31LL) / 32 * N > 0x7fffffffLL) return KDA_ERR_SHAPE;  // the grid
+  return KDA_OK;
+}
+
+GlrArgs glr_args(const void* x, const void* la, const int32_t* cu, int N, int T_total, int D,
+                 const kda_glr_options* o, int* status) {
+  GlrArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.la = la; a.gate = o->input_gate;
+  a.cu_seqlens = cu; a.slots = o->slots; a.n_slots = o->n_slots;
+  const bool log = o->decay_from == KDA_GLR_LOG;
+  a.decay_scale = log ? nullptr : o->decay_scale;
+  a.decay_bias = log ? nullptr : o->decay_bias;
+  a.checkpoints = o->checkpoints; a.status = status;
+  a.N = N; a.T_total = T_total; a.D = D;
+  a.decay_from = o->decay_from; a.input_scale = o->input_scale;
+  a.ldx = o->ldx ? o->ldx : D; a.ldla = o->ldla ? o->ldla : D; a.ldg = o->ldg ? o->ldg : D;
+  return a;
+}
+
+// Whether two bf16 channels can be moved as one (see GlrLane).
+bool pairs(const GlrArgs& a) {
+  if (a.D % 2 || a.ldx % 2 || a.ldla % 2 || (a.gate && a.ldg % 2)) return false;
+  for (const void* p : {a.x, a.la, a.gate, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dla,
+                        (const void*)a.dgate})
+    if (!aligned(p, 4)) return false;
+  return true;
+}
+
+// CTAs that share a sequence's tokens, a power of two: as many as give every SM two, and no more
+// than the longest sequence has tiles.
+int glr_ranks(int T_total, int N, int D, int dtype, int max_seqlen) {
+  const long long longest = max_seqlen > 0 ? max_seqlen : T_total;
+  const long long tiles = (longest + kGlrTile - 1) / kGlrTile;
+  const long long units = (D + (dtype == KDA_BF16 ? 63LL : 31LL)) / (dtype == KDA_BF16 ? 64 : 32) * N;
+  int ranks = 1;
+  while (ranks < 8 && units * ranks * 2 <= 2LL * sm_count() && ranks * 2 <= tiles) ranks *= 2;
+  return ranks;
+}
+
+}  // namespace
+
+extern "C" {
+
+void kda_glr_options_init(kda_glr_options* opt) {
+  if (!opt) return;
+  memset(opt, 0, sizeof(*opt));
+  opt->decay_from = KDA_GLR_LOG;
+  opt->input_scale = KDA_GLR_INPUT_NONE;
+}
+
+int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const int32_t* cu_seqlens,
+                 int N, void* y, float* h_T, int T_total, int D, int dtype,
+                 const kda_glr_options* opt, kda_stream_t stream) {
+  kda_glr_options def;
+  if (!opt) kda_glr_options_init(&def);
+  const kda_glr_options* o = opt ? opt : &def;
+  const int rc = check_glr(N, T_total, D, dtype, o);
+  if (rc != KDA_OK) return rc;
+  if (!h_T || (T_total > 0 && (!x || !log_alpha || !y))) return KDA_ERR_ARG;
+  for (const void* p : {x, log_alpha, (const void*)y})
+    if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
+  if (!aligned(h0, 4) || !aligned(h_T, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_ALIGN;
+  if (!cu_seqlens && T_total % N != 0) return KDA_ERR_SHAPE;
+  if (same(y, {x, log_alpha, o->input_gate, h0, h_T, o->checkpoints})) return KDA_ERR_ARG;
+  if (same(h_T, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias})) return KDA_ERR_ARG;
+  if (same(o->checkpoints, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias, h0, h_T})) return KDA_ERR_ARG;
+  int* status = status_word();
+  if (!status) return KDA_ERR_CUDA;
+  GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
+  a.h0 = h0; a.h_T = h_T; a.y = y;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int longest = o->max_seqlen > 0 ? o->max_seqlen : T_total;
+  const cudaError_t e =
+      longest <= 16 ? launch_glr_few(a, dtype, pairs(a), s)
+                    : launch_glr_scan(a, dtype, pairs(a), glr_ranks(T_total, N, D, dtype, o->max_seqlen), s);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N, int L, int D,
+                 int dtype, const kda_glr_options* opt, kda_stream_t stream) {
+  kda_glr_options def;
+  if (!opt) kda_glr_options_init(&def);
+  const kda_glr_options* o = opt ? opt : &def;
+  if (N < 1 || L < 1 || (long long)N * L > kMaxTokens) return KDA_ERR_SHAPE;
+  const int T = N * L;
+  const int rc = check_glr(N, T, D, dtype, o);
+  if (rc != KDA_OK) return rc;
+  if (o->checkpoints) return KDA_ERR_UNSUPPORTED;
+  if (!x || !log_alpha || !h || !y) return KDA_ERR_ARG;
+  for (const void* p : {x, log_alpha, (const void*)y})
+    if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
+  if (!aligned(h, 4)) return KDA_ERR_ALIGN;
+  if (same(y, {x, log_alpha, o->input_gate, h})) return KDA_ERR_ARG;
+  if (same(h, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias})) return KDA_ERR_ARG;
+  int* status = status_word();
+  if (!status) return KDA_ERR_CUDA;
+  GlrArgs a = glr_args(x, log_alpha, nullptr, N, T, D, o, status);
+  a.h0 = h; a.h_T = h; a.y = y;
+  const cudaError_t e = launch_glr_few(a, dtype, pairs(a), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_glr_backward_workspace_size(int T_total, int N, int D, int dtype,
+                                       const kda_glr_options* opt) {
+  kda_glr_options def;
+  if (!opt) kda_glr_options_init(&def);
+  const kda_glr_options* o = opt ? opt : &def;
+  if (check_glr(N, T_total, D, dtype, o) != KDA_OK) return 0;
+  return (size_t)N * glr_ranks(T_total, N, D, dtype, o->max_seqlen) * D * sizeof(double2);
+}
+
+int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, const void* log_alpha,
+                          const int32_t* cu_seqlens, int N, void* dx, void* dlog_alpha,
+                          void* dinput_gate, float* dh0, float* ddecay_scale, float* ddecay_bias,
+                          int T_total, int D, int dtype, const kda_glr_options* opt,
+                          kda_stream_t stream) {
+  kda_glr_options def;
+  if (!opt) kda_glr_options_init(&def);
+  const kda_glr_options* o = opt ? opt : &def;
+  const int rc = check_glr(N, T_total, D, dtype, o);
+  if (rc != KDA_OK) return rc;
+  if (o->slots) return KDA_ERR_UNSUPPORTED;
+  if (T_total > 0 && (!x || !log_alpha || !dx || !dlog_alpha || !o->checkpoints)) return KDA_ERR_ARG;
+  if (dinput_gate && !o->input_gate) return KDA_ERR_ARG;
+  const bool sums = ddecay_scale || ddecay_bias;
+  if (sums && o->decay_from == KDA_GLR_LOG) return KDA_ERR_ARG;
+  for (const void* p : {dy, x, log_alpha, (const void*)dx, (const void*)dlog_alpha, (const void*)dinput_gate})
+    if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
+  for (const void* p : {(const void*)dh_T, (const void*)dh0, (const void*)ddecay_scale, (const void*)ddecay_bias,
+                        (const void*)cu_seqlens})
+    if (!aligned(p, 4)) return KDA_ERR_ALIGN;
+  if (!cu_seqlens && T_total % N != 0) return KDA_ERR_SHAPE;
+  void* const ws = sums ? o->workspace : nullptr;
+  if (sums) {
+    if (!ws || o->workspace_bytes < kda_glr_backward_workspace_size(T_total, N, D, dtype, o)) return KDA_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return KDA_ERR_ALIGN;
+  }
+  const void* out[] = {dx, dlog_alpha, dinput_gate, dh0, ddecay_scale, ddecay_bias, ws};
+  for (int i = 0; i < 7; ++i) {
+    if (same(out[i], {dy, dh_T, x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias, o->checkpoints, cu_seqlens}))
+      return KDA_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (same(out[i], {out[j]})) return KDA_ERR_ARG;
+  }
+  int* status = status_word();
+  if (!status) return KDA_ERR_CUDA;
+  GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
+  a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dla = dlog_alpha; a.dgate = dinput_gate; a.dh0 = dh0;
+  a.partial = static_cast<double2*>(ws);
+  const cudaError_t e = launch_glr_backward(a, dtype, pairs(a), glr_ranks(T_total, N, D, dtype, o->max_seqlen),
+                                            ddecay_scale, ddecay_bias, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,35 +1,19 @@
-// layer_api.cu -- the C ABI of the gated delta rule and of the projections
-// around it: argument checks and path selection.  As in kda_api.cu, every check
+// layer_api.cu -- the C ABI of the gated delta rule and of the projections and the
+// norm around it: argument checks and path selection.  As in kda_api.cu, every check
 // runs on the host before anything is enqueued; a rejected call launches nothing.
 #include <string.h>
 
-#include <initializer_list>
-
+#include "checks.cuh"
 #include "gdr.cuh"
-#include "linear.cuh"
+#include "linear_i8.cuh"
+#include "norm.cuh"
 
 using namespace kda;
 
 namespace {
 
-// Sizes leave a tile's room below 2^31, so that the kernels round up in 32 bits.
-constexpr int kMaxSize = 0x7fffffff - 256;
-
-int sm_count() {  // of the current device
-  static std::atomic<int> count[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  n = count[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    count[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool gdr_dk(int d) { return d == 32 || d == 64 || d == 128; }
 bool gdr_dv(int d) { return gdr_dk(d) || d == 256; }
-size_t elem(int dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 
 // Checks that kda_gdr_prefill and kda_gdr_decode_step share.
 int check_gdr_sizes(int N, int T_total, int H_k, int H_v, int d_k, int d_v, int dtype,
@@ -68,13 +52,6 @@ int check_gdr_arrays(const void* q, const void* k, const void* v, const float* l
     if (!aligned(p, 16)) return KDA_ERR_ALIGN;
   if (!aligned(log_alpha, 4) || !aligned(beta, elem(dtype))) return KDA_ERR_ALIGN;
   return KDA_OK;
-}
-
-// An output at the address of an input: other warps still read what one has written.
-bool same(const void* out, std::initializer_list<const void*> in) {
-  for (const void* p : in)
-    if (out && out == p) return true;
-  return false;
 }
 
 GdrArgs gdr_args(const void* q, const void* k, const void* v, const float* log_alpha,
@@ -235,6 +212,94 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
   } else {
     e = launch_linear_simt(a, dtype, sms, s);
   }
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_linear_i8_workspace_size(int M, int N, int K) {
+  (void)M; (void)N; (void)K;
+  return 0;
+}
+
+int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w,
+                  long long ldw, const float* w_scale, const void* bias, const void* residual,
+                  long long ldr, void* y, long long ldy, int M, int N, int K, int act, int dtype,
+                  void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return KDA_ERR_SHAPE;
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  if (act < KDA_ACT_NONE || act > KDA_ACT_SIGMOID) return KDA_ERR_ARG;
+  if (ldx == 0) ldx = K;
+  if (ldw == 0) ldw = K;
+  if (ldr == 0) ldr = N;
+  if (ldy == 0) ldy = N;
+  if (ldx < K || ldw < K || ldr < N || ldy < N) return KDA_ERR_SHAPE;
+  if (M == 0 || N == 0) return KDA_OK;
+  if (!y || !x_scale || !w_scale || (K > 0 && (!x || !w))) return KDA_ERR_ARG;
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return KDA_ERR_ALIGN;
+  for (const void* p : {bias, residual, (const void*)y})
+    if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
+  const size_t need = kda_linear_i8_workspace_size(M, N, K);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;
+  }
+  // in place only where every element is read and written by the same thread
+  if (residual == y && ldr != ldy) return KDA_ERR_ARG;
+  void* const ws = need > 0 ? workspace : nullptr;
+  if (same(y, {bias, x_scale, w_scale, ws}) || (K > 0 && same(y, {x, w}))) return KDA_ERR_ARG;
+  if (same(ws, {x, w, x_scale, w_scale, bias, residual})) return KDA_ERR_ARG;
+  LinearI8Args a;
+  a.l.x = x; a.l.w = w; a.l.bias = bias; a.l.residual = residual; a.l.y = y;
+  a.l.ldx = ldx; a.l.ldw = ldw; a.l.ldr = ldr; a.l.ldy = ldy;
+  a.l.M = M; a.l.N = N; a.l.K = K; a.l.act = act;
+  a.x_scale = x_scale; a.w_scale = w_scale;
+  const cudaError_t e = launch_linear_i8_simt(a, dtype, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_rmsnorm(const void* x, long long ldx, const void* residual, long long ldr, const float* w,
+                void* sum, long long lds, void* y, long long ldy, int8_t* q, long long ldq,
+                float* scale, int M, int D, float eps, int dtype, kda_stream_t stream) {
+  if (M < 0 || D < 1 || M > kMaxSize || D > kMaxSize) return KDA_ERR_SHAPE;
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  if (!(eps >= 0.f)) return KDA_ERR_ARG;
+  long long* const lds_of[] = {&ldx, &ldr, &lds, &ldy, &ldq};
+  for (long long* ld : lds_of) {
+    if (*ld == 0) *ld = D;
+    if (*ld < D) return KDA_ERR_SHAPE;
+  }
+  if (M == 0) return KDA_OK;  // (arrays without an element have no address)
+  if (!x || (q == nullptr) != (scale == nullptr) || (!y && !q)) return KDA_ERR_ARG;
+  for (const void* p : {x, residual, (const void*)sum, (const void*)y})
+    if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
+  if (!aligned(w, 4) || !aligned(scale, 4)) return KDA_ERR_ALIGN;
+  if (same(y, {x, residual, w, sum, q, scale}) || same(q, {x, residual, w, sum, scale})) return KDA_ERR_ARG;
+  if (same(scale, {x, residual, w, sum}) || same(sum, {w})) return KDA_ERR_ARG;
+  if ((sum == x && lds != ldx) || (sum && sum == residual && lds != ldr)) return KDA_ERR_ARG;
+  NormArgs a;
+  a.x = x; a.residual = residual; a.w = w; a.sum = sum; a.y = y; a.q = q; a.scale = scale;
+  a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldy = ldy; a.ldq = ldq;
+  a.M = M; a.D = D; a.eps = eps; a.norm = true;
+  const cudaError_t e = launch_norm(a, dtype, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_quantize_i8(const void* x, long long ldx, int8_t* q, long long ldq, float* scale, int M,
+                    int D, int dtype, kda_stream_t stream) {
+  if (M < 0 || D < 1 || M > kMaxSize || D > kMaxSize) return KDA_ERR_SHAPE;
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  if (ldx == 0) ldx = D;
+  if (ldq == 0) ldq = D;
+  if (ldx < D || ldq < D) return KDA_ERR_SHAPE;
+  if (M == 0) return KDA_OK;
+  if (!x || !q || !scale) return KDA_ERR_ARG;
+  if (!aligned(x, elem(dtype)) || !aligned(scale, 4)) return KDA_ERR_ALIGN;
+  if (same(q, {x, scale}) || same(scale, {x})) return KDA_ERR_ARG;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.q = q; a.scale = scale;
+  a.ldx = ldx; a.ldq = ldq;
+  a.M = M; a.D = D; a.norm = false;
+  const cudaError_t e = launch_norm(a, dtype, sm_count(), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

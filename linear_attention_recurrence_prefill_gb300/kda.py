@@ -87,6 +87,26 @@ class kda_gdr_options(ctypes.Structure):
     ]
 
 
+class kda_glr_options(ctypes.Structure):
+    """Mirror of ``struct kda_glr_options`` (field order and types as in kda.h)."""
+    _fields_ = [
+        ("decay_from", ctypes.c_int),
+        ("decay_scale", ctypes.c_void_p),
+        ("decay_bias", ctypes.c_void_p),
+        ("input_scale", ctypes.c_int),
+        ("input_gate", ctypes.c_void_p),
+        ("ldx", ctypes.c_longlong),
+        ("ldla", ctypes.c_longlong),
+        ("ldg", ctypes.c_longlong),
+        ("slots", ctypes.c_void_p),
+        ("n_slots", ctypes.c_int),
+        ("checkpoints", ctypes.c_void_p),
+        ("max_seqlen", ctypes.c_int),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -99,7 +119,9 @@ EXPORTS = ("kda_options_init", "kda_prefill", "kda_prefill_noalloc",
            "kda_decode_step", "kda_gated_rmsnorm", "kda_get_last_error", "kda_status_string",
            "kda_abi_version", "kda_gdr_options_init", "kda_gdr_prefill",
            "kda_gdr_prefill_workspace_size", "kda_gdr_prefill_path", "kda_gdr_decode_step",
-           "kda_linear")
+           "kda_linear", "kda_rmsnorm", "kda_quantize_i8", "kda_linear_i8",
+           "kda_linear_i8_workspace_size", "kda_glr_options_init", "kda_glr_scan", "kda_glr_step",
+           "kda_glr_scan_backward", "kda_glr_backward_workspace_size")
 PATH_NAMES = {1: "simt", 2: "tc"}
 
 
@@ -152,6 +174,28 @@ def load(path: str | None = None):
     lib.kda_gdr_decode_step.restype = ci
     lib.kda_linear.argtypes = [vp, cl, vp, cl, vp, vp, cl, vp, cl, ci, ci, ci, ci, ci, vp]
     lib.kda_linear.restype = ci
+    lib.kda_rmsnorm.argtypes = [vp, cl, vp, cl, vp, vp, cl, vp, cl, vp, cl, vp, ci, ci, cf, ci, vp]
+    lib.kda_rmsnorm.restype = ci
+    lib.kda_quantize_i8.argtypes = [vp, cl, vp, cl, vp, ci, ci, ci, vp]
+    lib.kda_quantize_i8.restype = ci
+    cz = ctypes.c_size_t
+    lib.kda_linear_i8.argtypes = [vp, cl, vp, vp, cl, vp, vp, vp, cl, vp, cl, ci, ci, ci, ci, ci,
+                                  vp, cz, vp]
+    lib.kda_linear_i8.restype = ci
+    lib.kda_linear_i8_workspace_size.argtypes = [ci, ci, ci]
+    lib.kda_linear_i8_workspace_size.restype = cz
+    pl = ctypes.POINTER(kda_glr_options)
+    lib.kda_glr_options_init.argtypes = [pl]
+    lib.kda_glr_options_init.restype = None
+    lib.kda_glr_scan.argtypes = [vp, vp, vp, vp, ci, vp, vp, ci, ci, ci, pl, vp]
+    lib.kda_glr_scan.restype = ci
+    lib.kda_glr_step.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, pl, vp]
+    lib.kda_glr_step.restype = ci
+    lib.kda_glr_scan_backward.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, vp, vp, vp, vp, ci, ci,
+                                          ci, pl, vp]
+    lib.kda_glr_scan_backward.restype = ci
+    lib.kda_glr_backward_workspace_size.argtypes = [ci, ci, ci, ci, pl]
+    lib.kda_glr_backward_workspace_size.restype = cz
     if path == _build.LIB or _LIB is None:
         _LIB = lib
     return lib
@@ -438,8 +482,15 @@ class _Host:
         lib = load()
         self.linear, self.step, self.prefill = (lib.kda_linear, lib.kda_gdr_decode_step,
                                                 lib.kda_gdr_prefill)
+        self.rmsnorm, self.quantize_i8 = lib.kda_rmsnorm, lib.kda_quantize_i8
+        self.linear_i8, self.linear_i8_size = lib.kda_linear_i8, lib.kda_linear_i8_workspace_size
+        self.glr_scan, self.glr_step = lib.kda_glr_scan, lib.kda_glr_step
+        self.glr_backward, self.glr_backward_size = (lib.kda_glr_scan_backward,
+                                                     lib.kda_glr_backward_workspace_size)
         self.codes = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
-        self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
+        self.f32, self.i32, self.u8, self.i8 = (torch.float32, torch.int32, torch.uint8,
+                                                torch.int8)
+        self.bf16 = torch.bfloat16
         self.empty, self.empty_like = torch.empty, torch.empty_like
         self.current_device = torch._C._cuda_getDevice
         # (device) -> address of the current stream
@@ -736,3 +787,327 @@ def kda_linear(x, w, bias=None, residual=None, y=None, *, act="none"):
     if rc != KDA_OK:
         raise KdaError(rc, "kda_linear")
     return y
+
+
+def _workspace(host, workspace, need, device):
+    """(address, bytes, the tensor that holds them) of a workspace of `need` bytes at least, allocated if not given."""
+    if need == 0:
+        return None, 0, None
+    if workspace is None:
+        workspace = host.empty(need, dtype=host.u8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: libkda takes contiguous tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+@_on_stream
+def kda_linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, y=None, *, act="none",
+                  dtype=None, workspace=None):
+    """y = act(x_scale_m w_scale_n (x w^T) + bias) + residual (C ``kda_linear_i8``).
+
+    x [M, K], w [N, K] int8, rows contiguous, any distance apart; x_scale [M], w_scale
+    [N] fp32; bias [N], residual [M, N] of ``dtype`` (None: y's, the residual's or the
+    bias's, else bfloat16) or None.  ``act``: a key of ``ACTS``.  y [M, N] may be the residual
+    itself.  ``stream`` as in kda_gdr_prefill."""
+    host = _host()
+    dev = _one_device(host, x, x_scale, w, w_scale, bias, residual, y, workspace)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x [M, K] and w [N, K]")
+    if x.dtype != host.i8 or w.dtype != host.i8:
+        raise TypeError("x and w: int8")
+    M, (N, K) = x.shape[0], w.shape
+    if dtype is None:
+        dtype = next((t.dtype for t in (y, residual, bias) if t is not None), host.bf16)
+    code = _code(host, dtype)
+    ldx, ldw, ldr, ldy, b, r = _rows(x, "x", M, K), _rows(w, "w", N, K), 0, 0, None, None
+    _expect(x_scale, "x_scale", (M,), host.f32)
+    _expect(w_scale, "w_scale", (N,), host.f32)
+    if bias is not None:
+        _expect(bias, "bias", (N,), dtype)
+        b = bias.data_ptr()
+    if residual is not None:
+        ldr, r = _rows(residual, "residual", M, N), residual.data_ptr()
+        if residual.dtype != dtype:
+            raise TypeError("bias, residual and y of one dtype")
+    if y is None:
+        y = host.empty((M, N), dtype=dtype, device=x.device)
+    else:
+        ldy = _rows(y, "y", M, N)
+        if y.dtype != dtype:
+            raise TypeError("bias, residual and y of one dtype")
+    at, size, workspace = _workspace(host, workspace, host.linear_i8_size(M, N, K), x.device)
+    rc = host.linear_i8(x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
+                        w_scale.data_ptr(), b, r, ldr, y.data_ptr(), ldy, M, N, K, ACTS[act], code,
+                        at, size, host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_linear_i8")
+    return y
+
+
+# ------------------------------------------------- the norm before a layer
+def _norm(x, w, residual, total, y, q, scale, eps, i8):
+    host = _host()
+    dev = _one_device(host, x, w, residual, total, y, q, scale)
+    if x.dim() != 2:
+        raise ValueError("x [M, D]")
+    (M, D), dtype = x.shape, x.dtype
+    code = _code(host, dtype)
+    ldx, ldr, lds, ldy, ldq = _rows(x, "x", M, D), 0, 0, 0, 0
+    at = dict.fromkeys(("w", "residual", "sum", "y", "q", "scale"))
+    if w is not None:
+        _expect(w, "w", (D,), host.f32)
+        at["w"] = w.data_ptr()
+    if residual is None:
+        if total is not None:
+            raise ValueError("total: the sum with a residual, and there is none")
+    else:
+        ldr, at["residual"] = _rows(residual, "residual", M, D), residual.data_ptr()
+        if total is None:
+            total = host.empty((M, D), dtype=dtype, device=x.device)
+        lds, at["sum"] = _rows(total, "total", M, D), total.data_ptr()
+        if residual.dtype != dtype or total.dtype != dtype:
+            raise TypeError("x, residual, total and y of one dtype")
+    if y is None and not i8:
+        y = host.empty((M, D), dtype=dtype, device=x.device)
+    if y is not None:
+        ldy, at["y"] = _rows(y, "y", M, D), y.data_ptr()
+        if y.dtype != dtype:
+            raise TypeError("x, residual, total and y of one dtype")
+    if i8:
+        if q is None:
+            q = host.empty((M, D), dtype=host.i8, device=x.device)
+        if scale is None:
+            scale = host.empty((M,), dtype=host.f32, device=x.device)
+        _expect(scale, "scale", (M,), host.f32)
+        ldq, at["q"], at["scale"] = _rows(q, "q", M, D), q.data_ptr(), scale.data_ptr()
+        if q.dtype != host.i8:
+            raise TypeError("q: int8")
+    rc = host.rmsnorm(x.data_ptr(), ldx, at["residual"], ldr, at["w"], at["sum"], lds, at["y"],
+                      ldy, at["q"], ldq, at["scale"], M, D, eps, code, host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_rmsnorm")
+    return y, q, scale, total
+
+
+@_on_stream
+def kda_rmsnorm(x, w=None, residual=None, y=None, *, total=None, eps: float = 1e-6):
+    """s = x + residual; y = s / sqrt(mean(s^2) + eps) * w per row (C ``kda_rmsnorm``).
+
+    x, residual [M, D] of one dtype, rows contiguous, any distance apart; w [D] fp32 or None
+    (ones).  Returns y, or with a residual (y, s); ``total``: where s goes, which may be x or the
+    residual itself.  ``stream`` as in kda_gdr_prefill."""
+    y, _, _, total = _norm(x, w, residual, total, y, None, None, eps, False)
+    return y if residual is None else (y, total)
+
+
+@_on_stream
+def kda_rmsnorm_i8(x, w=None, residual=None, q=None, scale=None, *, total=None, y=None,
+                   eps: float = 1e-6):
+    """kda_rmsnorm with its output in 8-bit integers: q [M, D] int8 and scale [M] fp32, the
+    values scale * q (C ``kda_rmsnorm``).  Returns (q, scale), or with a residual
+    (q, scale, s); ``y``: where the output goes in the data type too."""
+    _, q, scale, total = _norm(x, w, residual, total, y, q, scale, eps, True)
+    return (q, scale) if residual is None else (q, scale, total)
+
+
+@_on_stream
+def kda_quantize_i8(x, q=None, scale=None):
+    """x [M, D] in 8-bit integers with a scale per row (C ``kda_quantize_i8``): (q, scale)."""
+    host = _host()
+    dev = _one_device(host, x, q, scale)
+    if x.dim() != 2:
+        raise ValueError("x [M, D]")
+    M, D = x.shape
+    code = _code(host, x.dtype)
+    if q is None:
+        q = host.empty((M, D), dtype=host.i8, device=x.device)
+    if scale is None:
+        scale = host.empty((M,), dtype=host.f32, device=x.device)
+    _expect(scale, "scale", (M,), host.f32)
+    if q.dtype != host.i8:
+        raise TypeError("q: int8")
+    rc = host.quantize_i8(x.data_ptr(), _rows(x, "x", M, D), q.data_ptr(), _rows(q, "q", M, D),
+                          scale.data_ptr(), M, D, code, host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_quantize_i8")
+    return q, scale
+
+
+# ------------------------------------------------- the gated linear recurrence
+DECAY_FROM = {"log": 0, "softplus": 1, "sigmoid": 2}                # KDA_GLR_*
+INPUT_SCALES = {"none": 0, "complement": 1, "normalized": 2}        # KDA_GLR_INPUT_*
+GLR_TILE = 64
+
+
+def kda_glr_options_init(**overrides) -> kda_glr_options:
+    """Default options (C kda_glr_options_init), then keyword overrides."""
+    opt = kda_glr_options()
+    load().kda_glr_options_init(ctypes.byref(opt))
+    for key, val in overrides.items():
+        setattr(opt, key, val)
+    return opt
+
+
+def _tokens(x, name: str, shape, dtype) -> int:
+    """Elements between the rows of successive tokens of x [..., D], channels dense, tokens
+    evenly spaced; 0 for dense rows."""
+    if x.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name}: {x.dtype}, expected {dtype}")
+    return 0 if x.is_contiguous() else _token_stride(x.unsqueeze(-2), name)
+
+
+def _glr_options(host, x, log_alpha, decay_from, decay_scale, decay_bias, input_scale, input_gate,
+                 slots, pool, N):
+    """Options of a call on tokens x [..., D] (log_alpha and the gate alike); checks them."""
+    shape, dtype, D = x.shape, x.dtype, x.shape[-1]
+    ldx, ldla = _tokens(x, "x", shape, dtype), _tokens(log_alpha, "log_alpha", shape, dtype)
+    ldg, gate, A, b, at, n_slots = 0, None, None, None, None, N
+    if input_gate is not None:
+        ldg, gate = _tokens(input_gate, "input_gate", shape, dtype), input_gate.data_ptr()
+    if decay_scale is not None:
+        _expect(decay_scale, "decay_scale", (D,), host.f32)
+        A = decay_scale.data_ptr()
+    if decay_bias is not None:
+        _expect(decay_bias, "decay_bias", (D,), host.f32)
+        b = decay_bias.data_ptr()
+    if slots is not None:
+        _expect(slots, "slots", (N,), host.i32)
+        at, n_slots = slots.data_ptr(), pool.shape[0]
+    return n_slots, kda_glr_options(DECAY_FROM[decay_from], A, b, INPUT_SCALES[input_scale], gate,
+                                    ldx, ldla, ldg, at, n_slots)
+
+
+def _sequences(host, T, cu_seqlens, N, max_seqlen):
+    """(N, the longest sequence as far as it is known)"""
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        _expect(cu_seqlens, "cu_seqlens", (N + 1,), host.i32)
+    elif N is None:
+        N = 1
+    if max_seqlen == 0 and cu_seqlens is None and N > 0:
+        max_seqlen = T // N
+    return N, max_seqlen
+
+
+@_on_stream
+def kda_glr_scan(x, log_alpha, h0=None, cu_seqlens=None, N: int | None = None, y=None, h_T=None, *,
+                 slots=None, decay_from="log", decay_scale=None, decay_bias=None,
+                 input_scale="none", input_gate=None, checkpoints=None, max_seqlen: int = 0):
+    """The gated linear recurrence over packed sequences (C ``kda_glr_scan``).
+
+    h_t = a_t h_{t-1} + c_t sigmoid(i_t) x_t per channel, a = e^g; x, log_alpha and input_gate
+    (i, or None) [T, D] of one dtype, channels contiguous, tokens any even distance apart.
+    ``decay_from``: "log" (g = min(log_alpha, 0)), "softplus" or "sigmoid" (g = -A f(log_alpha + b)
+    with decay_scale A >= 0 and decay_bias b [D] fp32, None = ones / zeros).  ``input_scale``: "none"
+    (c = 1), "complement" (1 - a) or "normalized" (sqrt(1 - a^2)).  h0 [N, D] fp32 or None
+    (zeros); cu_seqlens, N, max_seqlen, slots (h0 and h_T are pools [n_slots, D] then) and
+    stream as in kda_gdr_prefill.  Returns (y, h_T); with ``checkpoints`` (True, or a tensor
+    [T // 64 + N, D] fp32) (y, h_T, checkpoints), which kda_glr_scan_backward takes."""
+    host = _host()
+    if checkpoints is False:
+        checkpoints = None
+    dev = _one_device(host, x, log_alpha, h0, cu_seqlens, y, h_T, slots, decay_scale, decay_bias,
+                      input_gate, None if checkpoints is True else checkpoints)
+    if x.dim() != 2:
+        raise ValueError("x [T, D]")
+    (T, D), dtype = x.shape, x.dtype
+    code = _code(host, dtype)
+    N, max_seqlen = _sequences(host, T, cu_seqlens, N, max_seqlen)
+    if h_T is None:
+        if slots is not None:
+            raise ValueError("with slots, h_T is the pool that the states are written to")
+        h_T = host.empty((max(N, 0), D), dtype=host.f32, device=x.device)
+    n_slots, opt = _glr_options(host, x, log_alpha, decay_from, decay_scale, decay_bias,
+                                input_scale, input_gate, slots, h_T, N)
+    _expect(h_T, "h_T", (n_slots, D), host.f32)
+    if h0 is not None and h0 is not h_T:
+        _expect(h0, "h0", (n_slots, D), host.f32)
+    if y is None:
+        y = host.empty((T, D), dtype=dtype, device=x.device)
+    else:
+        _expect(y, "y", (T, D), dtype)
+    if checkpoints is not None:
+        rows = (T // GLR_TILE + N, D)
+        if checkpoints is True:
+            checkpoints = host.empty(rows, dtype=host.f32, device=x.device)
+        else:
+            _expect(checkpoints, "checkpoints", rows, host.f32)
+        opt.checkpoints = checkpoints.data_ptr()
+    opt.max_seqlen = max_seqlen
+    rc = host.glr_scan(x.data_ptr(), log_alpha.data_ptr(), _ptr(h0), _ptr(cu_seqlens), N,
+                       y.data_ptr(), h_T.data_ptr(), T, D, code, opt, host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_glr_scan")
+    return (y, h_T) if checkpoints is None else (y, h_T, checkpoints)
+
+
+@_on_stream
+def kda_glr_step(x, log_alpha, h, y=None, *, slots=None, decay_from="log", decay_scale=None,
+                 decay_bias=None, input_scale="none", input_gate=None):
+    """L tokens for each of N sequences, states in place (C ``kda_glr_step``): x, log_alpha and
+    input_gate [N, L, D], or without L for one token; h [N, D] fp32 (a pool [n_slots, D] with
+    ``slots`` [N] int32).  The rest as in kda_glr_scan.  Returns y."""
+    host = _host()
+    dev = _one_device(host, x, log_alpha, h, y, slots, decay_scale, decay_bias, input_gate)
+    if x.dim() not in (2, 3):
+        raise ValueError("x [N, D] or [N, L, D]")
+    N, D = x.shape[0], x.shape[-1]
+    L = x.shape[1] if x.dim() == 3 else 1
+    n_slots, opt = _glr_options(host, x, log_alpha, decay_from, decay_scale, decay_bias,
+                                input_scale, input_gate, slots, h, N)
+    _expect(h, "h", (n_slots, D), host.f32)
+    if y is None:
+        y = host.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _expect(y, "y", x.shape, x.dtype)
+    rc = host.glr_step(x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), y.data_ptr(), N, L, D,
+                       _code(host, x.dtype), opt, host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_glr_step")
+    return y
+
+
+@_on_stream
+def kda_glr_scan_backward(dy, dh_T, x, log_alpha, checkpoints, cu_seqlens=None,
+                          N: int | None = None, *, decay_from="log", decay_scale=None,
+                          decay_bias=None, input_scale="none", input_gate=None,
+                          max_seqlen: int = 0, workspace=None):
+    """The gradient of kda_glr_scan (C ``kda_glr_scan_backward``): dy [T, D] and dh_T [N, D] fp32
+    are those of its outputs (either may be None: zeros), the rest is what it was given and the
+    checkpoints that it returned.  Returns (dx, dlog_alpha, dinput_gate, dh0, ddecay_scale,
+    ddecay_bias), None for what the call had not (the last two come with logits, whether or not
+    the parameters were given); rows behind the last sequence are not written."""
+    host = _host()
+    dev = _one_device(host, x, dy, dh_T, log_alpha, checkpoints, cu_seqlens, decay_scale,
+                      decay_bias, input_gate, workspace)
+    if x.dim() != 2:
+        raise ValueError("x [T, D]")
+    (T, D), dtype, device = x.shape, x.dtype, x.device
+    code = _code(host, dtype)
+    N, max_seqlen = _sequences(host, T, cu_seqlens, N, max_seqlen)
+    _, opt = _glr_options(host, x, log_alpha, decay_from, decay_scale, decay_bias, input_scale,
+                          input_gate, None, None, N)
+    if dy is not None:
+        _expect(dy, "dy", (T, D), dtype)
+    if dh_T is not None:
+        _expect(dh_T, "dh_T", (N, D), host.f32)
+    _expect(checkpoints, "checkpoints", (T // GLR_TILE + N, D), host.f32)
+    opt.checkpoints = checkpoints.data_ptr()
+    opt.max_seqlen = max_seqlen
+    dx, dla = (host.empty((T, D), dtype=dtype, device=device) for _ in range(2))
+    dgate = host.empty((T, D), dtype=dtype, device=device) if input_gate is not None else None
+    dh0 = host.empty((N, D), dtype=host.f32, device=device)
+    dA = db = None
+    if decay_from != "log":
+        dA, db = (host.empty(D, dtype=host.f32, device=device) for _ in range(2))
+        opt.workspace, opt.workspace_bytes, workspace = _workspace(
+            host, workspace, host.glr_backward_size(T, N, D, code, opt), device)
+    rc = host.glr_backward(_ptr(dy), _ptr(dh_T), x.data_ptr(), log_alpha.data_ptr(),
+                           _ptr(cu_seqlens), N, dx.data_ptr(), dla.data_ptr(), _ptr(dgate),
+                           dh0.data_ptr(), _ptr(dA), _ptr(db), T, D, code, opt,
+                           host.current_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_glr_scan_backward")
+    return dx, dla, dgate, dh0, dA, db
