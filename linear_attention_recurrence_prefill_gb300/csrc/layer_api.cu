@@ -216,8 +216,8 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
 }
 
 size_t kda_linear_i8_workspace_size(int M, int N, int K) {
-  (void)M; (void)N; (void)K;
-  return 0;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return 0;
+  return linear_i8_workspace_bytes(M, N, K, sm_count());
 }
 
 int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w,
@@ -233,6 +233,7 @@ int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const in
   if (ldy == 0) ldy = N;
   if (ldx < K || ldw < K || ldr < N || ldy < N) return KDA_ERR_SHAPE;
   if (M == 0 || N == 0) return KDA_OK;
+  if (!linear_i8_tc_takes(M, N)) return KDA_ERR_SHAPE;  // tiles in a grid
   if (!y || !x_scale || !w_scale || (K > 0 && (!x || !w))) return KDA_ERR_ARG;
   if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return KDA_ERR_ALIGN;
   for (const void* p : {bias, residual, (const void*)y})
@@ -252,7 +253,15 @@ int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const in
   a.l.ldx = ldx; a.l.ldw = ldw; a.l.ldr = ldr; a.l.ldy = ldy;
   a.l.M = M; a.l.N = N; a.l.K = K; a.l.act = act;
   a.x_scale = x_scale; a.w_scale = w_scale;
-  const cudaError_t e = launch_linear_i8_simt(a, dtype, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (K == 0) {
+    e = launch_linear_i8_none(a, dtype, s);
+  } else {
+    int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    e = launch_linear_i8_tc(a, dtype, ws, sm_count(), status, s);
+  }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -13,6 +13,14 @@ struct LinearI8Args {
   const float* w_scale;
 };
 
-cudaError_t launch_linear_i8_simt(const LinearI8Args& a, int dtype, int sms, cudaStream_t s);
+// K = 0 only: y = act(bias) + residual.
+cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s);
+// Any alignment and number of rows, K > 0.
+bool linear_i8_tc_takes(int M, int N);
+size_t linear_i8_workspace_bytes(int M, int N, int K, int sms);
+cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspace, int sms, int* status,
+                                cudaStream_t s);
+// linear_tc.cu: l.x and l.w are fp16 arrays that hold the integers, rows 16-byte aligned.
+cudaError_t launch_linear_i8_pair(const LinearI8Args& a, int dtype, int sms, int* status, cudaStream_t s);
 
 }  // namespace kda

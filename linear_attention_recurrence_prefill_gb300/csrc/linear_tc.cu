@@ -27,7 +27,10 @@
 //    multiple of 16 bytes apart): 0-3 and four more warps then fill the ring, from aligned 16-byte
 //    loads that they shift into place.  Bound by reading w: 64 x 12288 -> 4096 takes 21.5 us, 4.8 TB/s with its set-up
 //    and joining; 4096 x 4095 x 4097, shifted by every CTA that uses a tile, 584 us.
-#include "linear.cuh"
+#include <initializer_list>
+
+#include "linear_i8.cuh"
+#include "linear_join.cuh"
 #include "tensor_map.cuh"
 #include "umma.cuh"
 
@@ -44,43 +47,46 @@ constexpr long long kSpins = 4000000000LL;  // ~2 s of clock cycles
 struct Tc {
   CUtensorMap tm_w, tm_x;
   LinearArgs a;
+  const float* x_scale;  // of an 8-bit product, whose integers are the operands
+  const float* w_scale;
   int* status;
   int n_tiles, m_tiles, k_blocks;
 };
 
 // The epilogue of output channel n for the 32 tokens from m on, of which `cols` exist: the
-// residual, fetched ahead of the sums, then the rest.
-__device__ __forceinline__ void load_residual(const LinearArgs& a, __nv_bfloat16 (&add)[32], long long m,
-                                              int n, int cols) {
-  const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.residual) + m * a.ldr + n;
+// residual, fetched ahead of the sums, then the rest.  T: the type of residual and y.
+template <typename T>
+__device__ __forceinline__ void load_residual(const LinearArgs& a, T (&add)[32], long long m, int n, int cols) {
+  const T* res = static_cast<const T*>(a.residual) + m * a.ldr + n;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) add[j] = a.residual && j < cols ? res[j * a.ldr] : __ushort_as_bfloat16(0);
+  for (int j = 0; j < 32; ++j) add[j] = a.residual && j < cols ? res[j * a.ldr] : from_f32<T>(0.f);
 }
 
-__device__ __forceinline__ void finish32(const LinearArgs& a, const uint32_t (&r)[32], float bias,
-                                         const __nv_bfloat16 (&add)[32], long long m, int n, int cols) {
-  float z[32];
+template <typename T>
+__device__ __forceinline__ void finish32(const LinearArgs& a, float (&z)[32], float bias, const T (&add)[32],
+                                         long long m, int n, int cols) {
+  constexpr bool kFast = sizeof(T) == 2;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]) + bias;
+  for (int j = 0; j < 32; ++j) z[j] += bias;
   // the activation chosen once for all
   auto all = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) z[j] = f(z[j]);
   };
   switch (a.act) {
-    case KDA_ACT_RELU: all([](float x) { return activate<true>(x, KDA_ACT_RELU); }); break;
-    case KDA_ACT_SILU: all([](float x) { return activate<true>(x, KDA_ACT_SILU); }); break;
-    case KDA_ACT_GELU: all([](float x) { return activate<true>(x, KDA_ACT_GELU); }); break;
+    case KDA_ACT_RELU: all([](float x) { return activate<kFast>(x, KDA_ACT_RELU); }); break;
+    case KDA_ACT_SILU: all([](float x) { return activate<kFast>(x, KDA_ACT_SILU); }); break;
+    case KDA_ACT_GELU: all([](float x) { return activate<kFast>(x, KDA_ACT_GELU); }); break;
     case KDA_ACT_GELU_TANH:
-      all([](float x) { return activate<true>(x, KDA_ACT_GELU_TANH); });
+      all([](float x) { return activate<kFast>(x, KDA_ACT_GELU_TANH); });
       break;
-    case KDA_ACT_SIGMOID: all([](float x) { return activate<true>(x, KDA_ACT_SIGMOID); }); break;
+    case KDA_ACT_SIGMOID: all([](float x) { return activate<kFast>(x, KDA_ACT_SIGMOID); }); break;
     default: break;
   }
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + m * a.ldy + n;
+  T* y = static_cast<T*>(a.y) + m * a.ldy + n;
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (j < cols) y[j * a.ldy] = __float2bfloat16_rn(z[j] + __bfloat162float(add[j]));
+    if (j < cols) y[j * a.ldy] = from_f32<T>(z[j] + to_f32(add[j]));
 }
 
 constexpr uint32_t kAlign = 1024;  // the swizzled tiles' alignment
@@ -104,7 +110,8 @@ __device__ __forceinline__ void tile_of(const Tc& t, int i, int& n, int& m) {
   n = group * 8 + in - m * rows;
 }
 
-template <int BN>
+// kI8: operands in fp16, which hold integers, and scales in the epilogue; else bf16.
+template <int BN, typename T, bool kI8>
 __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ Tc t) {
   using P = Pair<BN>;
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
     if (rank == 1 && !mbar_wait(&drained, 0, 2 * kSpins)) ok = false;
   } else if (warp == kPairMma && rank == 0) {
     const uint32_t lead = elect_leader();
-    constexpr uint32_t idesc = idesc_f16(256, BN, true);
+    constexpr uint32_t idesc = idesc_f16(256, BN, !kI8);
     auto wait = [&](uint64_t* bar, int parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, kSpins));
       fence_after_sync();
@@ -199,7 +206,7 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
     mbar_wait(&drained, 0, kSpins);
   } else if (warp < kPairOut) {
     // two warps per quarter of the lanes, every other 32 tokens each
-    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(t.a.bias);
+    const T* bias = static_cast<const T*>(t.a.bias);
     const int quarter = warp & 3, half = warp >> 2;
     int i = 0;
     for (int tile = first; tile < tiles; tile += step, ++i) {
@@ -211,7 +218,8 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
       const int cols = t.a.M - m0 < BN ? (int)(t.a.M - m0) : BN;
       const bool in = n < t.a.N;
       const float b = bias && in ? to_f32(bias[n]) : 0.f;
-      __nv_bfloat16 add[32], next[32];
+      const float scale = kI8 && in ? t.w_scale[n] : 0.f;
+      T add[32], next[32];
       if (in) load_residual(t.a, add, m0 + half * 32, n, cols - half * 32);
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_full[acc], (i / 2) & 1, kSpins));
       if (!ok) break;
@@ -222,8 +230,18 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
         uint32_t r[32];
         tmem_ld32(d + c, r);
         if (in && c + 64 < cols) load_residual(t.a, next, m0 + c + 64, n, cols - c - 64);
+        float z[32];
+        if constexpr (kI8) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = j < cols - c ? t.x_scale[m0 + c + j] : 0.f;
+        }
         tmem_wait_ld();
-        if (in) finish32(t.a, r, b, add, m0 + c, n, cols - c);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float sum = __uint_as_float(r[j]);
+          z[j] = kI8 ? sum * z[j] * scale : sum;
+        }
+        if (in) finish32(t.a, z, b, add, m0 + c, n, cols - c);
 #pragma unroll
         for (int j = 0; j < 32; ++j) add[j] = next[j];
       }
@@ -242,36 +260,6 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
 template <int BN, int kStages>
 constexpr uint32_t split_smem() {
   return kAlign + kStages * (kRowsA + BN) * kBlockK * 2;
-}
-
-// This rank's columns of the tile, added up over R ranks, and their epilogue: a column per warp and
-// four neighbouring channels per lane, several columns in flight.
-template <int R>
-__device__ __forceinline__ void join(const LinearArgs& a, uint32_t part, uint32_t rank, int warp, int cols,
-                                     bool wide, float4 bias, long long m0, int n) {
-  constexpr int kFlight = R == 8 ? 2 : 4;
-  uint32_t from[R];
-#pragma unroll
-  for (uint32_t r = 0; r < R; ++r) from[r] = map_to_rank(part, r);
-  for (int c0 = rank + warp * R; c0 < cols; c0 += 4 * R * kFlight) {
-    float4 v[kFlight][R];
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int c = c0 + 4 * R * i < cols ? c0 + 4 * R * i : c0;
-#pragma unroll
-      for (int r = 0; r < R; ++r) v[i][r] = ld_cluster_f32x4(from[r] + c * kRowsA * 4);
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      float4 z = v[i][0];
-#pragma unroll
-      for (int r = 1; r < R; ++r) {
-        z.x += v[i][r].x; z.y += v[i][r].y; z.z += v[i][r].z; z.w += v[i][r].w;
-      }
-      const int c = c0 + 4 * R * i;
-      if (c < cols) finish4<__nv_bfloat16>(a, wide, z, bias, m0 + c, n);
-    }
-  }
 }
 
 // The aligned 16 bytes at `at`, as far as they lie in the array [lo, hi).
@@ -454,12 +442,8 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
     const bool wide = wide4(t.a, 2);
     const float4 b = bias4<__nv_bfloat16>(t.a, n);
     const uint32_t part = smem_u32(ring) + lane * 16;
-    switch (ranks) {
-      case 1: join<1>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
-      case 2: join<2>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
-      case 4: join<4>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
-      default: join<8>(t.a, part, rank, warp, cols, wide, b, m0, n); break;
-    }
+    join(ranks, part, rank, warp, cols,
+         [&](const float4& z, int c) { finish4<__nv_bfloat16>(t.a, wide, z, b, m0 + c, n); });
   }
   fence_before_sync();
   cluster_sync();  // no CTA leaves while its sums are read
@@ -467,39 +451,66 @@ __global__ void __launch_bounds__(kTma ? kThreads : kFillThreads) linear_split_k
   if (warp == kWarpMma) tmem_dealloc(tmem, kCols);
 }
 
-// Tensor map of a [rows][K] bf16 array, rows ld elements apart: boxes of 64
+// Tensor map of a [rows][K] array in bf16 (or fp16), rows ld elements apart: boxes of 64
 // columns by `box` rows, 128-byte swizzle, zeros outside.
-bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int box) {
+bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int box, bool half = false) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
   const cuuint32_t boxes[2] = {kBlockK, (cuuint32_t)box};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes,
+  return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool fill(Tc& t, const LinearArgs& a, bool tma, int* status, int rows_w, int box_w, int rows_x, int box_x) {
+bool fill(Tc& t, const LinearArgs& a, bool tma, int* status, int rows_w, int box_w, int rows_x, int box_x,
+          bool half = false) {
   t.a = a;
+  t.x_scale = t.w_scale = nullptr;
   t.status = status;
   t.n_tiles = (a.N + rows_w - 1) / rows_w;
   t.m_tiles = (int)(((long long)a.M + rows_x - 1) / rows_x);
   t.k_blocks = (a.K + (int)kBlockK - 1) / (int)kBlockK;
-  return !tma || (encode(&t.tm_w, a.w, a.N, a.K, a.ldw, box_w) &&
-                  encode(&t.tm_x, a.x, a.M, a.K, a.ldx, box_x));
+  return !tma || (encode(&t.tm_w, a.w, a.N, a.K, a.ldw, box_w, half) &&
+                  encode(&t.tm_x, a.x, a.M, a.K, a.ldx, box_x, half));
 }
 
-template <int BN>
-cudaError_t launch_pair(const LinearArgs& a, int pairs, int* status, cudaStream_t s) {
-  const cudaError_t e = allow_smem<linear_pair_kernel<BN>>(Pair<BN>::kSmem);
+template <int BN, typename T, bool kI8>
+cudaError_t launch_pair_of(const LinearI8Args& i, int pairs, int* status, cudaStream_t s) {
+  constexpr auto kern = linear_pair_kernel<BN, T, kI8>;
+  const cudaError_t e = allow_smem<kern>(Pair<BN>::kSmem);
   if (e != cudaSuccess) return e;
   Tc t;
-  if (!fill(t, a, true, status, 256, kRowsA, BN, BN / 2)) return cudaErrorInvalidValue;
+  if (!fill(t, i.l, true, status, 256, kRowsA, BN, BN / 2, kI8)) return cudaErrorInvalidValue;
+  t.x_scale = i.x_scale;
+  t.w_scale = i.w_scale;
   const long long tiles = (long long)t.n_tiles * t.m_tiles;
-  return launch_early(linear_pair_kernel<BN>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), kPairThreads,
-                      Pair<BN>::kSmem, 1, s, t);
+  return launch_early(kern, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), kPairThreads, Pair<BN>::kSmem, 1, s,
+                      t);
+}
+template <int BN>
+cudaError_t launch_pair(const LinearArgs& a, int pairs, int* status, cudaStream_t s) {
+  return launch_pair_of<BN, __nv_bfloat16, false>({a, nullptr, nullptr}, pairs, status, s);
+}
+
+// The width of tile, of those given (widest first), whose waves of tiles cost least.  A tile's
+// time hardly falls with its width, since the rows of w have to come all the same: at
+// 8192 x 8192 x 8192 a wave took 41.5, 38.5, 36.6, 35.8, 35.2 us for 256, 224, 192, 160, 128.
+int pair_width(const LinearArgs& a, int pairs, std::initializer_list<int> widths) {
+  const long long rows = (a.N + 255LL) / 256;
+  long long best = 0;
+  int width = 0;
+  for (int bn : widths) {
+    const long long tiles = rows * ((a.M + bn - 1LL) / bn);
+    const long long cost = (tiles + pairs - 1) / pairs * (448 + bn);
+    if (!width || cost < best) {
+      best = cost;
+      width = bn;
+    }
+  }
+  return width;
 }
 
 template <int BN, int kStages, bool kTma>
@@ -536,24 +547,11 @@ bool linear_tc_takes(const LinearArgs& a, int dtype) {
 cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
   const int k_blocks = (a.K + 63) / 64;
   // Pairs of CTAs where their tiles fill half of the SMs at least (4096 x 4096 weights: 25 against
-  // 34 us with 512 tokens, 25 against 21 us with 256), with the width of tile whose waves cost least.  A
-  // tile's time hardly falls with its width, since the rows of w have to come all the same: at
-  // 8192 x 8192 x 8192 a wave took 41.5, 38.5, 36.6, 35.8, 35.2 us for 256, 224, 192, 160, 128.
-  const long long rows = (a.N + 255LL) / 256;
+  // 34 us with 512 tokens, 25 against 21 us with 256).
   const int pairs = sms / 2;
   const bool tma = tma_takes(a);
-  if (tma && rows * ((a.M + 127LL) / 128) >= pairs / 2) {
-    long long best = 0;
-    int width = 0;
-    for (int bn : {256, 224, 192, 160, 128}) {
-      const long long tiles = rows * ((a.M + bn - 1LL) / bn);
-      const long long cost = (tiles + pairs - 1) / pairs * (448 + bn);
-      if (!width || cost < best) {
-        best = cost;
-        width = bn;
-      }
-    }
-    switch (width) {
+  if (tma && (a.N + 255LL) / 256 * ((a.M + 127LL) / 128) >= pairs / 2) {
+    switch (pair_width(a, pairs, {256, 224, 192, 160, 128})) {
       case 256: return launch_pair<256>(a, pairs, status, s);
       case 224: return launch_pair<224>(a, pairs, status, s);
       case 192: return launch_pair<192>(a, pairs, status, s);
@@ -571,6 +569,22 @@ cudaError_t launch_linear_tc(const LinearArgs& a, int sms, int* status, cudaStre
     case 32: return launch_split<32, 5>(a, tma, status, split, s);
     case 64: return launch_split<64, 4>(a, tma, status, split, s);
     default: return launch_split<128, 3>(a, tma, status, split, s);
+  }
+}
+
+cudaError_t launch_linear_i8_pair(const LinearI8Args& a, int dtype, int sms, int* status, cudaStream_t s) {
+  const int pairs = sms / 2;
+  const bool f32 = dtype == KDA_F32;
+  switch (pair_width(a.l, pairs, {256, 192, 128})) {
+    case 256:
+      return f32 ? launch_pair_of<256, float, true>(a, pairs, status, s)
+                 : launch_pair_of<256, __nv_bfloat16, true>(a, pairs, status, s);
+    case 192:
+      return f32 ? launch_pair_of<192, float, true>(a, pairs, status, s)
+                 : launch_pair_of<192, __nv_bfloat16, true>(a, pairs, status, s);
+    default:
+      return f32 ? launch_pair_of<128, float, true>(a, pairs, status, s)
+                 : launch_pair_of<128, __nv_bfloat16, true>(a, pairs, status, s);
   }
 }
 
