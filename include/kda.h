@@ -467,7 +467,7 @@ size_t kda_linear_i8_workspace_size(int M, int N, int K);
  *
  * (A and b per channel, A >= 0; without input gate i: u = c x.)  States are fp32; a decay near
  * one is held as a - 1, so that a state that remembers thousands of tokens is as exact
- * as one that remembers ten.  A token that is not finite spoils its channel of its sequence
+ * as one that remembers ten; decays below 2^-126 act as 0.  A token that is not finite spoils its channel of its sequence
  * from there on (in the gradient: up to there); no other channel or sequence is touched.
  */
 enum { /* decay_from */

@@ -1,25 +1,33 @@
-// glr.cuh -- the gated linear recurrence: arguments and the per-element
-// arithmetic that its kernels share.
+// glr.cuh -- the gated linear recurrence: arguments and the arithmetic that its
+// kernels share.
 //
 //     g = min(la, 0) | -A softplus(la + b) | -A sigmoid(la + b),   a = e^g
 //     u = c sigmoid(i) x,   c = 1 | 1 - a | sqrt(1 - a^2)
 //     h_t = a_t h_{t-1} + u_t
 //
-// A decay near one is kept as a - 1, not as a: fp32 spaces values below one by
+// A decay near one is kept as a - 1, not as a: fp32 spaces numbers below one by
 // 2^-24, which for a state that remembers a thousand tokens is a systematic
 // error of 2^-25 x 1000 in it and in every gradient, while a - 1 keeps 24 bits of
-// its own.  So a decay is a `Decay`: a number whose sign bit says what it is,
-// a - 1 in [-1/2, -0] or a itself in [+0, 1/2..].  (Gradients of A and b, sums of
-// terms that nearly cancel, were 2.7e-5 of their size off with a itself.)
+// its own.  So a decay is k + t with k = 1 where it is near one and 0 where not, and
+// a h + u = t h + (k h + u).  (Gradients of A and b, sums of terms that nearly cancel,
+// were 2.7e-5 of their size off with a itself.)
+//
+// A thread has two neighbouring channels, and two numbers per instruction wherever
+// there is one (packed.cuh): the kernels are bound by the instructions issued, not
+// by memory, unless an element takes fewer than about 40 (its 8 bytes in bf16 take HBM
+// as long as that).
 #pragma once
 
+#include <type_traits>
+
 #include "gdr.cuh"
+#include "packed.cuh"
 #include "umma.cuh"
 
 namespace kda {
 
 constexpr int kGlrTile = KDA_GLR_TILE;  // tokens from one saved state to the next
-constexpr int kGlrWarps = 8, kGlrSeg = kGlrTile / kGlrWarps;
+constexpr int kGlrMaxRanks = 8;
 
 struct GlrArgs {
   const void* x;
@@ -46,103 +54,167 @@ struct GlrArgs {
   double2* partial;           // NULL, or [N][ranks][D]: the share of each CTA in dA and db
 };
 
-// ---------------------------------------------------------------- a decay
-__device__ __forceinline__ bool decay_is_near(float t) { return __float_as_int(t) < 0; }
-// e^g - 1 for g in [-0.347, 0]: the Taylor polynomial, the next term below 1.5e-8 of the value.
-__device__ __forceinline__ float expm1_near(float g) {
-  float p = 1.f / 5040;
-  p = fmaf(p, g, 1.f / 720);
-  p = fmaf(p, g, 1.f / 120);
-  p = fmaf(p, g, 1.f / 24);
-  p = fmaf(p, g, 1.f / 6);
-  p = fmaf(p, g, 0.5f);
-  return fmaf(p * g, g, g);
-}
-// The decay of log decay g <= 0 (NaN stays).
-__device__ __forceinline__ float decay_of(float g) {
-  const float near = -fabsf(expm1_near(g)), far = expf(g);
-  return g > -0.34657359f ? near : far;
-}
-__device__ __forceinline__ float decay_value(float t) { return decay_is_near(t) ? 1.f + t : t; }
-// a h + u
-__device__ __forceinline__ float decay_apply(float t, float h, float u) {
-  const float r = fmaf(t, h, u);
-  return decay_is_near(t) ? h + r : r;
-}
-
 // ---------------------------------------------------------------- the gates
-// x's sigmoid and e^-|x|, by the approximate instructions where kFast (data in bf16: their error,
-// 2^-20 for |x| up to 10, is far below the 2^-9 that x itself is rounded by).
-template <bool kFast>
-__device__ __forceinline__ float exp_of(float x) {
-  return kFast ? __expf(x) : expf(x);
-}
-template <bool kFast>
-__device__ __forceinline__ float quotient(float x, float y) {
-  return kFast ? __fdividef(x, y) : x / y;
-}
-template <bool kFast>
-__device__ __forceinline__ float sigmoid_of(float x) {
-  // e^-|x| <= 1: no quotient of infinities
-  const float e = exp_of<kFast>(-fabsf(x));
-  return quotient<kFast>(x < 0.f ? e : 1.f, 1.f + e);
-}
-// softplus(x) = max(x, 0) + log1p(e^-|x|), the logarithm as 2 artanh(s) with s = e / (2 + e) <= 1/3
-// by its series up to s^13 (the next term below 1.5e-8): no loss where e is small.
-template <bool kFast>
-__device__ __forceinline__ float softplus_of(float x) {
-  const float e = exp_of<kFast>(-fabsf(x));
-  const float s = quotient<kFast>(e, 2.f + e), q = s * s;
-  float p = 1.f / 13;
-  p = fmaf(p, q, 1.f / 11);
-  p = fmaf(p, q, 1.f / 9);
-  p = fmaf(p, q, 1.f / 7);
-  p = fmaf(p, q, 1.f / 5);
-  p = fmaf(p, q, 1.f / 3);
-  p = fmaf(p * q, s, s);
-  return fmaf(2.f, p, fmaxf(x, 0.f));  // (a NaN is one of e)
-}
-__device__ __forceinline__ float sqrt_fast(float x) {  // off by 2^-23 at most
+// kFast, for data in bf16: the approximate instructions, whose errors (2^-22 of the value, and
+// 2^-24 |x| from rounding an exponential's argument) are far below the 2^-9 that x itself is
+// rounded by.  Else the functions of CUDA's library.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2_approx(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// c of the decay t
-__device__ __forceinline__ float input_factor(int scale, float t) {
-  if (scale == KDA_GLR_INPUT_NONE) return 1.f;
-  const bool near = decay_is_near(t);
-  if (scale == KDA_GLR_INPUT_COMPLEMENT) return near ? -t : 1.f - t;
-  return sqrt_fast(near ? -t * (2.f + t) : fmaf(-t, t, 1.f));
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool kFast>
+__device__ __forceinline__ float2 exp_minus(float2 x) {  // e^-x
+  if constexpr (kFast) {
+    const float2 y = mul2(x, both(-kLog2e));
+    return make_float2(ex2_approx(y.x), ex2_approx(y.y));
+  }
+  return make_float2(expf(-x.x), expf(-x.y));
+}
+template <bool kFast>
+__device__ __forceinline__ float2 inverse(float2 x) {
+  return kFast ? make_float2(rcp_approx(x.x), rcp_approx(x.y)) : make_float2(1.f / x.x, 1.f / x.y);
+}
+template <bool kFast>
+__device__ __forceinline__ float2 sigmoid2(float2 x) {  // e^-x may be infinite: 1 / infinity = 0
+  return inverse<kFast>(add2(both(1.f), exp_minus<kFast>(x)));
+}
+// and 1 - sigmoid = e^-x sigmoid, not by a difference
+template <bool kFast>
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2& rest) {
+  const float2 e = exp_minus<kFast>(x), s = inverse<kFast>(add2(both(1.f), e)), r = mul2(e, s);
+  rest = make_float2(e.x > 1e30f ? 1.f : r.x, e.y > 1e30f ? 1.f : r.y);
+  return s;
+}
+// softplus(x) = max(x, 0) + log1p(e^-|x|), the logarithm as 2 artanh(s) with s = e / (2 + e) <= 1/3
+// by its series up to s^13 (the next term below 1.5e-8): no loss where e is small.  (A NaN is one of e.)
+template <bool kFast>
+__device__ __forceinline__ float2 softplus2(float2 x) {
+  const float2 e = exp_minus<kFast>(make_float2(fabsf(x.x), fabsf(x.y)));
+  const float2 s = mul2(e, inverse<kFast>(add2(both(2.f), e))), q = mul2(s, s);
+  float2 p = both(1.f / 13);
+  p = fma2(p, q, both(1.f / 11));
+  p = fma2(p, q, both(1.f / 9));
+  p = fma2(p, q, both(1.f / 7));
+  p = fma2(p, q, both(1.f / 5));
+  p = fma2(p, q, both(1.f / 3));
+  p = fma2(mul2(p, q), s, s);
+  return fma2(both(2.f), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+
+// ---------------------------------------------------------------- a decay
+struct Decay {
+  float2 t, k;
+};
+// 2^y - 1 for y = g log2 e in [-kNear2, 0], the Taylor polynomial of e^g - 1 in y: the first term left out
+// is below 5e-8 of the value (|g| <= 1/8, and 2^-22 beyond it from the exponential, of a decay below
+// 0.89) where kFast, else 1.5e-8 (|g| <= 0.347).
+template <bool kFast>
+struct Near {
+  static constexpr float kFrom = kFast ? -0.125f * kLog2e : -0.5f;
+  static __device__ __forceinline__ float2 poly(float2 y) {
+    constexpr double l = 0.69314718055994531;
+    float2 p;
+    if constexpr (kFast) {
+      p = both((float)(l * l * l * l * l / 120));
+    } else {
+      p = both((float)(l * l * l * l * l * l * l / 5040));
+      p = fma2(p, y, both((float)(l * l * l * l * l * l / 720)));
+      p = fma2(p, y, both((float)(l * l * l * l * l / 120)));
+    }
+    p = fma2(p, y, both((float)(l * l * l * l / 24)));
+    p = fma2(p, y, both((float)(l * l * l / 6)));
+    p = fma2(p, y, both((float)(l * l / 2)));
+    p = fma2(p, y, both((float)l));
+    return mul2(p, y);
+  }
+};
+// The decay 2^y (NaN stays).
+template <bool kFast>
+__device__ __forceinline__ Decay decay_of(float2 y) {
+  const float2 near = Near<kFast>::poly(y);
+  const bool nx = y.x > Near<kFast>::kFrom, ny = y.y > Near<kFast>::kFrom;
+  Decay d;
+  d.t.x = nx ? near.x : kFast ? ex2_approx(y.x) : exp2f(y.x);
+  d.t.y = ny ? near.y : kFast ? ex2_approx(y.y) : exp2f(y.y);
+  d.k = make_float2(nx ? 1.f : 0.f, ny ? 1.f : 0.f);
+  return d;
+}
+__device__ __forceinline__ float2 decay_value(const Decay& d) { return add2(d.k, d.t); }
+// a h + u, a h
+__device__ __forceinline__ float2 decay_apply(const Decay& d, float2 h, float2 u) {
+  return fma2(d.t, h, fma2(d.k, h, u));
+}
+__device__ __forceinline__ float2 decay_apply(const Decay& d, float2 h) { return fma2(d.t, h, mul2(d.k, h)); }
+// As one float per channel between the warps: the sign bit says whether k is 1 (t is then -0 or below).
+__device__ __forceinline__ float2 decay_pack(const Decay& d) {
+  return make_float2(d.k.x != 0.f ? -fabsf(d.t.x) : d.t.x, d.k.y != 0.f ? -fabsf(d.t.y) : d.t.y);
+}
+__device__ __forceinline__ Decay decay_unpack(float2 t) {
+  Decay d;
+  d.t = t;
+  d.k = make_float2(__int_as_float((__float_as_int(t.x) >> 31) & 0x3f800000),
+                    __int_as_float((__float_as_int(t.y) >> 31) & 0x3f800000));
+  return d;
+}
+// 1 - a
+__device__ __forceinline__ float2 decay_rest(const Decay& d) {
+  return fma2(both(-1.f), d.t, fma2(both(-1.f), d.k, both(1.f)));
+}
+// c of a decay, and 1 / c (0 where c is 0)
+template <bool kFast>
+__device__ __forceinline__ float2 input_factor(int scale, const Decay& d, float2* inv = nullptr) {
+  if (scale == KDA_GLR_INPUT_NONE) return both(1.f);
+  const float2 r = decay_rest(d);
+  if (scale == KDA_GLR_INPUT_COMPLEMENT) return r;
+  const float2 sq = fma2(r, both(2.f), mul2(mul2(r, both(-1.f)), r));  // (1 - a) (1 + a)
+  float2 i = make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y));
+  if constexpr (!kFast) {  // one step of Newton's for the instruction's 2^-22
+    const float2 e = fma2(mul2(mul2(sq, i), i), both(-0.5f), both(0.5f));
+    i = fma2(i, e, i);
+  }
+  i = make_float2(sq.x > 0x1p-126f ? i.x : sq.x * 0.f, sq.y > 0x1p-126f ? i.y : sq.y * 0.f);  // NaN stays
+  if (inv) *inv = i;
+  return mul2(sq, i);
 }
 
 // ---------------------------------------------------------------- channels of a thread
-// bf16: two neighbouring channels per lane (4 bytes a token, 128 per warp); fp32: one.
+// Two neighbouring channels of a token: in one access where rows, bases and D allow it (kPair),
+// else one by one, n of them.
 template <typename T> struct GlrLane;
 template <> struct GlrLane<__nv_bfloat16> {
-  static constexpr int kCh = 2;
   static constexpr bool kFast = true;
+  static constexpr int kSeg = 8;  // tokens of a thread
   using Raw = uint32_t;
-  static __device__ __forceinline__ void widen(Raw r, float (&v)[2]) {
-    v[0] = __uint_as_float(r << 16);
-    v[1] = __uint_as_float(r & 0xffff0000u);
+  static __device__ __forceinline__ float2 widen(Raw r) {
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   }
-  static __device__ __forceinline__ Raw narrow(const float (&v)[2]) {
-    return umma::pack_bf162(v[0], v[1]);
-  }
-  // kPair: both at once (rows and base a multiple of 4 bytes, D even); else one by one, `n` of them
+  static __device__ __forceinline__ Raw narrow(float2 v) { return umma::pack_bf162(v.x, v.y); }
+  static __device__ __forceinline__ Raw same(float v) { return umma::pack_bf162(v, v); }
   template <bool kPair>
-  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p, int n) {
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p, int n, Raw none) {
     if constexpr (kPair) {
-      return n > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+      return n > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : none;
     } else {
       const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-      uint32_t r = n > 0 ? __ldg(q) : 0u;
-      if (n > 1) r |= (uint32_t)__ldg(q + 1) << 16;
-      return r;
+      uint32_t r = n > 0 ? __ldg(q) : none & 0xffffu;
+      return r | (n > 1 ? (uint32_t)__ldg(q + 1) << 16 : none & 0xffff0000u);
     }
   }
   template <bool kPair>
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, Raw r, int n) {
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, float2 v, int n) {
+    const Raw r = narrow(v);
     if constexpr (kPair) {
       if (n > 0) *reinterpret_cast<uint32_t*>(p) = r;
     } else {
@@ -153,54 +225,69 @@ template <> struct GlrLane<__nv_bfloat16> {
   }
 };
 template <> struct GlrLane<float> {
-  static constexpr int kCh = 1;
   static constexpr bool kFast = false;
-  using Raw = float;
-  static __device__ __forceinline__ void widen(Raw r, float (&v)[1]) { v[0] = r; }
-  static __device__ __forceinline__ Raw narrow(const float (&v)[1]) { return v[0]; }
+  static constexpr int kSeg = 4;
+  using Raw = float2;
+  static __device__ __forceinline__ float2 widen(Raw r) { return r; }
+  static __device__ __forceinline__ Raw same(float v) { return both(v); }
   template <bool kPair>
-  static __device__ __forceinline__ Raw load(const float* p, int n) {
-    return n > 0 ? __ldg(p) : 0.f;
+  static __device__ __forceinline__ Raw load(const float* p, int n, Raw none) {
+    if constexpr (kPair) return n > 0 ? __ldg(reinterpret_cast<const float2*>(p)) : none;
+    return make_float2(n > 0 ? __ldg(p) : none.x, n > 1 ? __ldg(p + 1) : none.y);
   }
   template <bool kPair>
-  static __device__ __forceinline__ void store(float* p, Raw r, int n) {
-    if (n > 0) *p = r;
+  static __device__ __forceinline__ void store(float* p, float2 v, int n) {
+    if constexpr (kPair) {
+      if (n > 0) *reinterpret_cast<float2*>(p) = v;
+    } else {
+      if (n > 0) p[0] = v.x;
+      if (n > 1) p[1] = v.y;
+    }
   }
 };
-// `n` of a thread's fp32 values at p (not __ldg: a state may be written by the same kernel)
-template <int kCh>
-__device__ __forceinline__ void load_states(float (&v)[kCh], const float* p, int n) {
-#pragma unroll
-  for (int c = 0; c < kCh; ++c) v[c] = p && c < n ? p[c] : 0.f;
+// n of a thread's states at p, or zeros (not __ldg: they may be written by the same kernel)
+__device__ __forceinline__ float2 load_states(const float* p, int n) {
+  return make_float2(p && n > 0 ? p[0] : 0.f, p && n > 1 ? p[1] : 0.f);
 }
-template <int kCh>
-__device__ __forceinline__ void store_states(float* p, const float (&v)[kCh], int n) {
-#pragma unroll
-  for (int c = 0; c < kCh; ++c)
-    if (c < n) p[c] = v[c];
+__device__ __forceinline__ void store_states(float* p, float2 v, int n) {
+  if (n > 0) p[0] = v.x;
+  if (n > 1) p[1] = v.y;
 }
 
-// A channel's parameters.
-struct GlrChannel {
-  float A, b;
+// Parameters of a thread's channels.
+struct GlrChannels {
+  float2 A, b;  // A times -log2 e
 };
-__device__ __forceinline__ GlrChannel glr_channel(const GlrArgs& a, int ch, bool in) {
-  GlrChannel p;
-  p.A = a.decay_scale && in ? a.decay_scale[ch] : 1.f;
-  p.b = a.decay_bias && in ? a.decay_bias[ch] : 0.f;
+__device__ __forceinline__ GlrChannels glr_channels(const GlrArgs& a, int ch, int n) {
+  GlrChannels p;
+  p.A = a.decay_scale ? load_states(a.decay_scale + ch, n) : both(1.f);
+  p.A = mul2(p.A, both(-kLog2e));
+  p.b = load_states(a.decay_bias ? a.decay_bias + ch : nullptr, n);
   return p;
 }
-// The log decay of an element.
-template <bool kFast>
-__device__ __forceinline__ float glr_log_decay(int from, const GlrChannel& p, float la) {
-  if (from == KDA_GLR_LOG) return la > 0.f ? 0.f : la;  // NaN stays
-  return -p.A * (from == KDA_GLR_SOFTPLUS ? softplus_of<kFast>(la + p.b) : sigmoid_of<kFast>(la + p.b));
+// Log decays to base 2.
+template <int kFrom, bool kFast>
+__device__ __forceinline__ float2 glr_log_decay(const GlrChannels& p, float2 la) {
+  if constexpr (kFrom == KDA_GLR_LOG)  // above 0: 0 (NaN stays)
+    return mul2(make_float2(la.x > 0.f ? 0.f : la.x, la.y > 0.f ? 0.f : la.y), both(kLog2e));
+  const float2 v = add2(la, p.b);
+  return mul2(p.A, kFrom == KDA_GLR_SOFTPLUS ? softplus2<kFast>(v) : sigmoid2<kFast>(v));
 }
+// A log_alpha whose decay is 1, for tokens behind a sequence's end.
+__device__ __forceinline__ float glr_no_decay(int from) { return from == KDA_GLR_LOG ? 0.f : -INFINITY; }
 
 // Row of the saved states at which sequence n, whose first token is t0, starts: rows of
 // different sequences never meet, since t0' / 64 - t0 / 64 + 1 >= (t0' - t0) / 64 rounded up.
 __device__ __forceinline__ size_t glr_checkpoint_row(int t0, int n) {
   return (size_t)(t0 / kGlrTile) + n;
+}
+
+// f(std::integral_constant) of the form of the decays
+template <typename F>
+__device__ __forceinline__ void glr_decay_from(int from, const F& f) {
+  if (from == KDA_GLR_LOG) f(std::integral_constant<int, KDA_GLR_LOG>());
+  else if (from == KDA_GLR_SOFTPLUS) f(std::integral_constant<int, KDA_GLR_SOFTPLUS>());
+  else f(std::integral_constant<int, KDA_GLR_SIGMOID>());
 }
 
 // Launchers; each returns the launch's cudaError_t.  pair: see GlrLane.

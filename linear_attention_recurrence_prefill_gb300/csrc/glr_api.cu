@@ -25,7 +25,7 @@ int check_glr(int N, int T_total, int D, int dtype, const kda_glr_options* o) {
   for (const void* p : {(const void*)o->decay_scale, (const void*)o->decay_bias, (const void*)o->checkpoints})
     if (!aligned(p, 4)) return KDA_ERR_ALIGN;
   if (!aligned(o->input_gate, elem(dtype))) return KDA_ERR_ALIGN;
-  if ((D + 31LL) / 32 * N > 0x7fffffffLL) return KDA_ERR_SHAPE;  // the grid
+  if ((D + 63LL) / 64 * N > 0x7fffffffLL) return KDA_ERR_SHAPE;  // the grid
   return KDA_OK;
 }
 
@@ -45,24 +45,34 @@ GlrArgs glr_args(const void* x, const void* la, const int32_t* cu, int N, int T_
   return a;
 }
 
-// Whether two bf16 channels can be moved as one (see GlrLane).
-bool pairs(const GlrArgs& a) {
+// Whether two channels can be moved as one (see GlrLane).
+bool pairs(const GlrArgs& a, int dtype) {
   if (a.D % 2 || a.ldx % 2 || a.ldla % 2 || (a.gate && a.ldg % 2)) return false;
   for (const void* p : {a.x, a.la, a.gate, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dla,
                         (const void*)a.dgate})
-    if (!aligned(p, 4)) return false;
+    if (!aligned(p, 2 * elem(dtype))) return false;
   return true;
 }
 
-// CTAs that share a sequence's tokens, a power of two: as many as give every SM two, and no more
-// than the longest sequence has tiles.
-int glr_ranks(int T_total, int N, int D, int dtype, int max_seqlen) {
+// CTAs that share a sequence's tokens, a power of two.  As far as the host knows, T_total / longest
+// sequences are as long as the longest: their tiles in waves of two CTAs per SM, and about two
+// tiles' time for a CTA to begin and end.
+int glr_ranks(int T_total, int N, int D, int max_seqlen) {
   const long long longest = max_seqlen > 0 ? max_seqlen : T_total;
-  const long long tiles = (longest + kGlrTile - 1) / kGlrTile;
-  const long long units = (D + (dtype == KDA_BF16 ? 63LL : 31LL)) / (dtype == KDA_BF16 ? 64 : 32) * N;
-  int ranks = 1;
-  while (ranks < 8 && units * ranks * 2 <= 2LL * sm_count() && ranks * 2 <= tiles) ranks *= 2;
-  return ranks;
+  if (longest == 0) return 1;
+  const long long tiles = (longest + kGlrTile - 1) / kGlrTile, blocks = (D + 63LL) / 64, slots = 2LL * sm_count();
+  long long alike = (T_total + longest - 1) / longest;
+  if (alike > N) alike = N;
+  int best = 1;
+  long long least = 0;
+  for (int ranks = 1; ranks <= kGlrMaxRanks && ranks <= tiles; ranks *= 2) {
+    const long long cost = (alike * blocks * ranks + slots - 1) / slots * ((tiles + ranks - 1) / ranks + 2);
+    if (ranks == 1 || cost < least) {
+      least = cost;
+      best = ranks;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -99,8 +109,8 @@ int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const in
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int longest = o->max_seqlen > 0 ? o->max_seqlen : T_total;
   const cudaError_t e =
-      longest <= 16 ? launch_glr_few(a, dtype, pairs(a), s)
-                    : launch_glr_scan(a, dtype, pairs(a), glr_ranks(T_total, N, D, dtype, o->max_seqlen), s);
+      longest <= 16 ? launch_glr_few(a, dtype, pairs(a, dtype), s)
+                    : launch_glr_scan(a, dtype, pairs(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen), s);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -124,7 +134,7 @@ int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N,
   if (!status) return KDA_ERR_CUDA;
   GlrArgs a = glr_args(x, log_alpha, nullptr, N, T, D, o, status);
   a.h0 = h; a.h_T = h; a.y = y;
-  const cudaError_t e = launch_glr_few(a, dtype, pairs(a), reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_glr_few(a, dtype, pairs(a, dtype), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -134,7 +144,7 @@ size_t kda_glr_backward_workspace_size(int T_total, int N, int D, int dtype,
   if (!opt) kda_glr_options_init(&def);
   const kda_glr_options* o = opt ? opt : &def;
   if (check_glr(N, T_total, D, dtype, o) != KDA_OK) return 0;
-  return (size_t)N * glr_ranks(T_total, N, D, dtype, o->max_seqlen) * D * sizeof(double2);
+  return (size_t)N * glr_ranks(T_total, N, D, o->max_seqlen) * D * sizeof(double2);
 }
 
 int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, const void* log_alpha,
@@ -175,7 +185,7 @@ int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, cons
   GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
   a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dla = dlog_alpha; a.dgate = dinput_gate; a.dh0 = dh0;
   a.partial = static_cast<double2*>(ws);
-  const cudaError_t e = launch_glr_backward(a, dtype, pairs(a), glr_ranks(T_total, N, D, dtype, o->max_seqlen),
+  const cudaError_t e = launch_glr_backward(a, dtype, pairs(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen),
                                             ddecay_scale, ddecay_bias, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
