@@ -195,26 +195,19 @@ __device__ __forceinline__ float2 input_factor(int scale, const Decay& d, float2
 template <typename T> struct GlrLane;
 template <> struct GlrLane<__nv_bfloat16> {
   static constexpr bool kFast = true;
-  static constexpr int kSeg = 8;  // tokens of a thread
   using Raw = uint32_t;
   static __device__ __forceinline__ float2 widen(Raw r) {
     return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   }
-  static __device__ __forceinline__ Raw narrow(float2 v) { return umma::pack_bf162(v.x, v.y); }
-  static __device__ __forceinline__ Raw same(float v) { return umma::pack_bf162(v, v); }
   template <bool kPair>
-  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p, int n, Raw none) {
-    if constexpr (kPair) {
-      return n > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : none;
-    } else {
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-      uint32_t r = n > 0 ? __ldg(q) : none & 0xffffu;
-      return r | (n > 1 ? (uint32_t)__ldg(q + 1) << 16 : none & 0xffff0000u);
-    }
+  static __device__ __forceinline__ float2 load(const __nv_bfloat16* p, int n) {
+    if constexpr (kPair) return widen(n > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u);
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    return widen((n > 0 ? __ldg(q) : 0u) | (n > 1 ? (uint32_t)__ldg(q + 1) << 16 : 0u));
   }
   template <bool kPair>
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float2 v, int n) {
-    const Raw r = narrow(v);
+    const Raw r = umma::pack_bf162(v.x, v.y);
     if constexpr (kPair) {
       if (n > 0) *reinterpret_cast<uint32_t*>(p) = r;
     } else {
@@ -226,14 +219,12 @@ template <> struct GlrLane<__nv_bfloat16> {
 };
 template <> struct GlrLane<float> {
   static constexpr bool kFast = false;
-  static constexpr int kSeg = 4;
   using Raw = float2;
   static __device__ __forceinline__ float2 widen(Raw r) { return r; }
-  static __device__ __forceinline__ Raw same(float v) { return both(v); }
   template <bool kPair>
-  static __device__ __forceinline__ Raw load(const float* p, int n, Raw none) {
-    if constexpr (kPair) return n > 0 ? __ldg(reinterpret_cast<const float2*>(p)) : none;
-    return make_float2(n > 0 ? __ldg(p) : none.x, n > 1 ? __ldg(p + 1) : none.y);
+  static __device__ __forceinline__ float2 load(const float* p, int n) {
+    if constexpr (kPair) return n > 0 ? __ldg(reinterpret_cast<const float2*>(p)) : both(0.f);
+    return make_float2(n > 0 ? __ldg(p) : 0.f, n > 1 ? __ldg(p + 1) : 0.f);
   }
   template <bool kPair>
   static __device__ __forceinline__ void store(float* p, float2 v, int n) {
@@ -245,6 +236,49 @@ template <> struct GlrLane<float> {
     }
   }
 };
+
+// ---------------------------------------------------------------- tiles
+// A tile of 64 tokens by 64 channels of each array on its way to, or in, shared memory: rows of
+// [token][channel], of which a warp has eight tokens and a lane two channels.  Copied in pieces of
+// kBytes bytes: 16 and 4 asynchronously, 2 (bf16 rows at odd places) through a register.
+constexpr int kGlrSeg = 8, kGlrWarps = kGlrTile / kGlrSeg, kGlrThreads = kGlrWarps * 32, kGlrCols = 64;
+
+template <typename T, int kBytes>
+struct GlrTile {
+  static constexpr int kRow = kGlrCols * sizeof(T);
+  static constexpr int kArray = kGlrTile * kRow;  // bytes
+  static constexpr bool kPair = kBytes == 16 || (kBytes == 4 && sizeof(T) == 2);
+
+  // Rows [0, rows) and columns [0, cols) of p (rows ld apart) to shared memory at `to`; the rest of
+  // the tile gets `none` in every element.
+  static __device__ __forceinline__ void fetch(uint8_t* to, const T* p, long long ld, int rows, int cols, T none) {
+    constexpr int kPieces = kRow / kBytes, kElems = kBytes / sizeof(T), kPer = kGlrTile * kPieces / kGlrThreads;
+    const int c = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
+    const T* from = p + r0 * ld + c * kElems;
+    uint8_t* dst = to + r0 * kRow + c * kBytes;
+    constexpr int kStep = kGlrThreads / kPieces;
+    const bool in = c * kElems < cols;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (in && r0 + i * kStep < rows) {
+        if constexpr (kBytes == 16) umma::cp_async16(umma::smem_u32(dst), from, 16);
+        else if constexpr (kBytes == 4) umma::cp_async4(umma::smem_u32(dst), from);
+        else *reinterpret_cast<T*>(dst) = *from;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kElems; ++e) reinterpret_cast<T*>(dst)[e] = none;
+      }
+      from += kStep * ld;
+      dst += kStep * kRow;
+    }
+  }
+  // this thread's channels of token k of its segment
+  static __device__ __forceinline__ float2 get(const uint8_t* array, int warp, int lane, int k) {
+    using Raw = typename GlrLane<T>::Raw;
+    return GlrLane<T>::widen(*reinterpret_cast<const Raw*>(array + (warp * kGlrSeg + k) * kRow + lane * sizeof(Raw)));
+  }
+};
+
 // n of a thread's states at p, or zeros (not __ldg: they may be written by the same kernel)
 __device__ __forceinline__ float2 load_states(const float* p, int n) {
   return make_float2(p && n > 0 ? p[0] : 0.f, p && n > 1 ? p[1] : 0.f);
@@ -282,7 +316,7 @@ __device__ __forceinline__ size_t glr_checkpoint_row(int t0, int n) {
   return (size_t)(t0 / kGlrTile) + n;
 }
 
-// f(std::integral_constant) of the form of the decays
+// f(std::integral_constant) of the form of the decays, or of the inputs
 template <typename F>
 __device__ __forceinline__ void glr_decay_from(int from, const F& f) {
   if (from == KDA_GLR_LOG) f(std::integral_constant<int, KDA_GLR_LOG>());
@@ -290,10 +324,45 @@ __device__ __forceinline__ void glr_decay_from(int from, const F& f) {
   else f(std::integral_constant<int, KDA_GLR_SIGMOID>());
 }
 
-// Launchers; each returns the launch's cudaError_t.  pair: see GlrLane.
-cudaError_t launch_glr_few(const GlrArgs& a, int dtype, bool pair, cudaStream_t s);
-cudaError_t launch_glr_scan(const GlrArgs& a, int dtype, bool pair, int ranks, cudaStream_t s);
-cudaError_t launch_glr_backward(const GlrArgs& a, int dtype, bool pair, int ranks, float* dA, float* db,
+template <typename F>
+__device__ __forceinline__ void glr_input_scale(int scale, const F& f) {
+  if (scale == KDA_GLR_INPUT_NONE) f(std::integral_constant<int, KDA_GLR_INPUT_NONE>());
+  else if (scale == KDA_GLR_INPUT_COMPLEMENT) f(std::integral_constant<int, KDA_GLR_INPUT_COMPLEMENT>());
+  else f(std::integral_constant<int, KDA_GLR_INPUT_NORMALIZED>());
+}
+
+// ---------------------------------------------------------------- between the CTAs of a cluster
+// Decays and states (or gradients) of the tiles of a round, which every CTA sends to every other:
+// each write counts on a barrier of the CTA that it goes to, so that nobody waits for more than
+// what it needs.  Two sets in turn: a CTA sends those of a round only behind its own reads of the
+// round before, and nobody gets to the next round without them.
+constexpr long long kGlrSpins = 4000000000LL;  // ~2 s of clock cycles
+struct GlrExchange {
+  float4 tot[2][kGlrMaxRanks][32];
+  uint64_t arrived[2];
+
+  __device__ __forceinline__ void init() {  // one thread; before the cluster's first barrier
+    umma::mbar_init(&arrived[0], 1);
+    umma::mbar_init(&arrived[1], 1);
+    umma::mbar_fence_init();
+  }
+  // by one warp
+  __device__ __forceinline__ void send(int p, int rank, int ranks, int lane, float4 v) {
+    if (lane == 0) umma::mbar_arrive_expect_tx(&arrived[p], ranks * 512);
+    for (int r = 0; r < ranks; ++r)
+      umma::st_async_f32x4(umma::map_to_rank(umma::smem_u32(&tot[p][rank][lane]), r), v,
+                           umma::map_to_rank(umma::smem_u32(&arrived[p]), r));
+  }
+  __device__ __forceinline__ bool wait(int p, int round) {
+    return umma::mbar_wait_soon(&arrived[p], (round >> 1) & 1, kGlrSpins);
+  }
+};
+
+// Launchers; each returns the launch's cudaError_t.  bytes: what rows, bases and D allow to move at
+// once (GlrTile): 16, 4, or 2.
+cudaError_t launch_glr_few(const GlrArgs& a, int dtype, int bytes, cudaStream_t s);
+cudaError_t launch_glr_scan(const GlrArgs& a, int dtype, int bytes, int ranks, cudaStream_t s);
+cudaError_t launch_glr_backward(const GlrArgs& a, int dtype, int bytes, int ranks, float* dA, float* db,
                                 cudaStream_t s);
 
 }  // namespace kda

@@ -25,7 +25,7 @@ int check_glr(int N, int T_total, int D, int dtype, const kda_glr_options* o) {
   for (const void* p : {(const void*)o->decay_scale, (const void*)o->decay_bias, (const void*)o->checkpoints})
     if (!aligned(p, 4)) return KDA_ERR_ALIGN;
   if (!aligned(o->input_gate, elem(dtype))) return KDA_ERR_ALIGN;
-  if ((D + 63LL) / 64 * N > 0x7fffffffLL) return KDA_ERR_SHAPE;  // the grid
+  if ((D + 63LL) / 64 * N > 0x7ffffffeLL) return KDA_ERR_SHAPE;  // the grid
   return KDA_OK;
 }
 
@@ -45,13 +45,18 @@ GlrArgs glr_args(const void* x, const void* la, const int32_t* cu, int N, int T_
   return a;
 }
 
-// Whether two channels can be moved as one (see GlrLane).
-bool pairs(const GlrArgs& a, int dtype) {
-  if (a.D % 2 || a.ldx % 2 || a.ldla % 2 || (a.gate && a.ldg % 2)) return false;
-  for (const void* p : {a.x, a.la, a.gate, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dla,
-                        (const void*)a.dgate})
-    if (!aligned(p, 2 * elem(dtype))) return false;
-  return true;
+// The bytes that rows, bases and D allow to move at once (GlrTile): 16, 4, or 2.
+int piece(const GlrArgs& a, int dtype) {
+  const int e = (int)elem(dtype);
+  for (int bytes : {16, 4}) {
+    const int n = bytes / e;
+    bool fits = a.D % n == 0 && a.ldx % n == 0 && a.ldla % n == 0 && (!a.gate || a.ldg % n == 0);
+    for (const void* p : {a.x, a.la, a.gate, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dla,
+                          (const void*)a.dgate})
+      fits = fits && aligned(p, bytes);
+    if (fits) return bytes;
+  }
+  return 2;
 }
 
 // CTAs that share a sequence's tokens, a power of two.  As far as the host knows, T_total / longest
@@ -109,8 +114,8 @@ int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const in
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int longest = o->max_seqlen > 0 ? o->max_seqlen : T_total;
   const cudaError_t e =
-      longest <= 16 ? launch_glr_few(a, dtype, pairs(a, dtype), s)
-                    : launch_glr_scan(a, dtype, pairs(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen), s);
+      longest <= 16 ? launch_glr_few(a, dtype, piece(a, dtype), s)
+                    : launch_glr_scan(a, dtype, piece(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen), s);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -134,7 +139,7 @@ int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N,
   if (!status) return KDA_ERR_CUDA;
   GlrArgs a = glr_args(x, log_alpha, nullptr, N, T, D, o, status);
   a.h0 = h; a.h_T = h; a.y = y;
-  const cudaError_t e = launch_glr_few(a, dtype, pairs(a, dtype), reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_glr_few(a, dtype, piece(a, dtype), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -185,7 +190,7 @@ int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, cons
   GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
   a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dla = dlog_alpha; a.dgate = dinput_gate; a.dh0 = dh0;
   a.partial = static_cast<double2*>(ws);
-  const cudaError_t e = launch_glr_backward(a, dtype, pairs(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen),
+  const cudaError_t e = launch_glr_backward(a, dtype, piece(a, dtype), glr_ranks(T_total, N, D, o->max_seqlen),
                                             ddecay_scale, ddecay_bias, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -28,178 +28,164 @@ struct Sum {
 };
 
 // As glr_scan_kernel, walking the rounds from the last to the first.
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(kGlrTile / GlrLane<T>::kSeg * 32, 1024 / (kGlrTile / GlrLane<T>::kSeg * 64))
-    glr_backward_kernel(GlrArgs a) {
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backward_kernel(GlrArgs a) {
   using G = GlrLane<T>;
-  using Raw = typename G::Raw;
-  constexpr int kSeg = G::kSeg, kWarps = kGlrTile / kSeg;
+  using Tile = GlrTile<T, kBytes>;
   constexpr bool kFast = G::kFast;
-  __shared__ float4 seg[2][kWarps][32];        // a segment's decay (packed) and its state from zero
-  __shared__ float2 seg_grad[2][kWarps][32];   // what it hands back from zero: a G of its first token
-  __shared__ float2 seg_log[2][kWarps][32];    // its log decay
-  __shared__ float4 tot[2][kGlrMaxRanks][32];  // decays and what is handed back, of a round's tiles
+  extern __shared__ __align__(16) uint8_t stages[];  // two, of four arrays: log_alpha, x, dy, gate
+  __shared__ float4 seg[2][kGlrWarps][32];           // a segment's decay (packed) and its state from zero
+  __shared__ float2 seg_grad[2][kGlrWarps][32];      // what it hands back from zero: a G of its first token
+  __shared__ float2 seg_log[2][32 * kGlrWarps];      // its log decay
+  __shared__ float2 last[2][32];                     // what a round hands back, of a CTA alone
+  __shared__ GlrExchange others;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = gridDim.z, rank = blockIdx.z;
-  const int blocks = (a.D + 63) / 64;
-  const int n = blockIdx.x / blocks, ch = (blockIdx.x % blocks * 32 + lane) * 2;
-  const int in = max(0, min(2, a.D - ch));
+  const int blocks = (a.D + kGlrCols - 1) / kGlrCols;
+  const int n = blockIdx.x / blocks, ch0 = blockIdx.x % blocks * kGlrCols, ch = ch0 + lane * 2;
+  const int in = max(0, min(2, a.D - ch)), cols = min(kGlrCols, a.D - ch0);
   grid_launch_dependents();
   grid_wait_prerequisites();  // what ran before is complete
   int t0, t1, slot;
+  // a sequence that is left out (by the whole cluster alike) has no tokens
+  const bool live = gdr_sequence(a, n, t0, t1, slot);
+  if (!live) t0 = t1 = 0;
   double2* partial = a.partial ? a.partial + ((size_t)n * ranks + rank) * a.D + ch : nullptr;
-  if (!gdr_sequence(a, n, t0, t1, slot)) {  // the whole cluster alike
-    if (partial && warp == 0)
-      for (int c = 0; c < in; ++c) partial[c] = make_double2(0., 0.);
-    return;
-  }
   const int L = t1 - t0;
+  const int tiles = (L + kGlrTile - 1) / kGlrTile, rounds = (tiles + ranks - 1) / ranks;
+  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch0;
+  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch0;
+  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch0 : nullptr;
+  const T* dy = a.dy ? static_cast<const T*>(a.dy) + (size_t)t0 * a.D + ch0 : nullptr;
+  const uint32_t stage = (gate ? 4 : 3) * Tile::kArray;
+  auto fetch = [&](int round) {
+    const int first = (round * ranks + rank) * kGlrTile, rows = L - first;
+    uint8_t* to = stages + (round & 1) * stage;
+    Tile::fetch(to, la + (size_t)first * a.ldla, a.ldla, rows, cols, from_f32<T>(glr_no_decay(a.decay_from)));
+    Tile::fetch(to + Tile::kArray, x + (size_t)first * a.ldx, a.ldx, rows, cols, from_f32<T>(0.f));
+    Tile::fetch(to + 2 * Tile::kArray, dy + (size_t)first * a.D, a.D, dy ? rows : 0, cols, from_f32<T>(0.f));
+    if (gate)
+      Tile::fetch(to + 3 * Tile::kArray, gate + (size_t)first * a.ldg, a.ldg, rows, cols, from_f32<T>(0.f));
+  };
+  if (rounds > 0) fetch(rounds - 1);
+  cp_async_commit();
   // what the tokens behind this round hand back
-  float2 carry = load_states(a.dh_T ? a.dh_T + (size_t)n * a.D + ch : nullptr, in);
+  float2 carry = load_states(a.dh_T && live ? a.dh_T + (size_t)n * a.D + ch : nullptr, in);
   const GlrChannels par = glr_channels(a, ch, in);
   const float2 minus_A = mul2(par.A, both(1.f / kLog2e));
-  if (ranks > 1) cluster_sync();  // every CTA runs
-  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch;
-  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch;
-  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch : nullptr;
+  if (threadIdx.x == 0) others.init();
+  if (ranks > 1) cluster_sync();  // every CTA runs, and has its barriers
   const size_t out0 = (size_t)t0 * a.D + ch;
-  const T* dy = a.dy ? static_cast<const T*>(a.dy) + out0 : nullptr;
   T* dx = static_cast<T*>(a.dx) + out0;
   T* dla = static_cast<T*>(a.dla) + out0;
   T* dgate = a.dgate ? static_cast<T*>(a.dgate) + out0 : nullptr;
   const size_t saved = glr_checkpoint_row(t0, n);
-  const int tiles = (L + kGlrTile - 1) / kGlrTile, rounds = (tiles + ranks - 1) / ranks;
-  const Raw zero = G::same(0.f), stay = G::same(glr_no_decay(a.decay_from));
   Sum dA[2] = {}, db[2] = {};
+  bool ok = true;
 
-  for (int round = rounds - 1; round >= 0; --round) {
-    const int tile = round * ranks + rank, p = round & 1;
-    const int first = tile * kGlrTile + warp * kSeg;
-    Raw rx[kSeg], rl[kSeg], rg[kSeg], rd[kSeg];
-    {
-      const T *px = x + (size_t)first * a.ldx, *pl = la + (size_t)first * a.ldla;
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k) {
-        const int m = first + k < L ? in : 0;
-        rl[k] = G::template load<kPair>(pl + k * a.ldla, m, stay);
-        rx[k] = G::template load<kPair>(px + k * a.ldx, m, zero);
-        rg[k] = rd[k] = zero;
-      }
-      if (gate) {
-        const T* pg = gate + (size_t)first * a.ldg;
-#pragma unroll
-        for (int k = 0; k < kSeg; ++k) rg[k] = G::template load<kPair>(pg + k * a.ldg, first + k < L ? in : 0, zero);
-      }
-      if (dy) {
-        const T* pd = dy + (size_t)first * a.D;
-#pragma unroll
-        for (int k = 0; k < kSeg; ++k)
-          rd[k] = G::template load<kPair>(pd + (size_t)k * a.D, first + k < L ? in : 0, zero);
-      }
-    }
+  for (int i = 0; i < rounds; ++i) {
+    const int round = rounds - 1 - i, tile = round * ranks + rank, p = i & 1;
+    const int first = tile * kGlrTile + warp * kGlrSeg;
+    const uint8_t* from = stages + (round & 1) * stage;
+    const uint8_t *from_x = from + Tile::kArray, *from_dy = from + 2 * Tile::kArray, *from_gate = from + 3 * Tile::kArray;
+    cp_async_wait_all();
+    __syncthreads();  // this tile is in shared memory, and nobody reads the one before any more
+    if (round > 0) fetch(round - 1);
+    cp_async_commit();
     float2 h = load_states(a.checkpoints + (saved + tile) * a.D + ch, tile < tiles ? in : 0);
 
-    Decay d[kSeg];
-    float2 u[kSeg], lg = both(0.f);
-    glr_decay_from(a.decay_from, [&](auto from) {
+    Decay d[kGlrSeg];
+    float2 u[kGlrSeg], lg = both(0.f);
+    glr_decay_from(a.decay_from, [&](auto form) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) {
-        const float2 g = glr_log_decay<from.value, kFast>(par, G::widen(rl[k]));
+      for (int k = 0; k < kGlrSeg; ++k) {
+        const float2 g = glr_log_decay<form.value, kFast>(par, Tile::get(from, warp, lane, k));
         lg = add2(lg, g);
         d[k] = decay_of<kFast>(g);
       }
     });
-    if (a.input_scale == KDA_GLR_INPUT_NONE) {
+    auto input = [&](auto scale) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) u[k] = G::widen(rx[k]);
-    } else if (a.input_scale == KDA_GLR_INPUT_COMPLEMENT) {
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k)
-        u[k] = mul2(input_factor<kFast>(KDA_GLR_INPUT_COMPLEMENT, d[k]), G::widen(rx[k]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k)
-        u[k] = mul2(input_factor<kFast>(KDA_GLR_INPUT_NORMALIZED, d[k]), G::widen(rx[k]));
-    }
+      for (int k = 0; k < kGlrSeg; ++k) {
+        u[k] = Tile::get(from_x, warp, lane, k);
+        if (scale.value != KDA_GLR_INPUT_NONE) u[k] = mul2(input_factor<kFast>(scale.value, d[k]), u[k]);
+      }
+    };
+    glr_input_scale(a.input_scale, input);
     if (gate) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) u[k] = mul2(u[k], sigmoid2<kFast>(G::widen(rg[k])));
+      for (int k = 0; k < kGlrSeg; ++k) u[k] = mul2(u[k], sigmoid2<kFast>(Tile::get(from_gate, warp, lane, k)));
     }
     // this segment's states and gradients from zero
     float2 back = both(0.f), H = both(0.f);
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < kGlrSeg; ++k) {
       H = decay_apply(d[k], H, u[k]);
-      back = decay_apply(d[kSeg - 1 - k], add2(back, G::widen(rd[kSeg - 1 - k])));
+      back = decay_apply(d[kGlrSeg - 1 - k], add2(back, Tile::get(from_dy, warp, lane, kGlrSeg - 1 - k)));
     }
     const float2 dt = decay_pack(decay_of<kFast>(lg));
     seg[p][warp][lane] = make_float4(dt.x, dt.y, H.x, H.y);
     seg_grad[p][warp][lane] = back;
-    if (ranks > 1) seg_log[p][warp][lane] = lg;
+    if (ranks > 1) seg_log[p][threadIdx.x] = lg;
     __syncthreads();
     if (ranks > 1) {
-      if (warp < ranks) {
+      if (warp == 0) {
         float2 z = both(0.f), l = both(0.f);
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
+        for (int w = kGlrWarps - 1; w >= 0; --w) {
           const float4 s = seg[p][w][lane];
           z = decay_apply(decay_unpack(make_float2(s.x, s.y)), z, seg_grad[p][w][lane]);
-          l = add2(l, seg_log[p][w][lane]);
+          l = add2(l, seg_log[p][w * 32 + lane]);
         }
         const float2 t = decay_pack(decay_of<kFast>(l));
-        st_cluster_f32x4(map_to_rank(smem_u32(&tot[p][rank][lane]), warp), make_float4(t.x, t.y, z.x, z.y));
+        others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      cluster_sync();
+      ok = ok && others.wait(p, i);
       back = carry;
       for (int r = ranks - 1; r >= 0; --r) {
-        const float4 s = tot[p][r][lane];
+        const float4 s = others.tot[p][r][lane];
         if (r == rank) back = carry;
         carry = decay_apply(decay_unpack(make_float2(s.x, s.y)), carry, make_float2(s.z, s.w));
       }
     } else {
-      back = carry;
+      back = i > 0 ? last[1 - p][lane] : carry;
     }
     // the state before this segment, and what comes back from behind it
-    float2 all = back;
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w) {
+    for (int w = 0; w < warp; ++w) {
       const float4 s = seg[p][w][lane];
-      if (w == warp) back = all;
-      all = decay_apply(decay_unpack(make_float2(s.x, s.y)), all, seg_grad[p][w][lane]);
+      h = decay_apply(decay_unpack(make_float2(s.x, s.y)), h, make_float2(s.z, s.w));
     }
-    if (ranks == 1) carry = all;
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w) {
+    for (int w = kGlrWarps - 1; w > warp; --w) {
       const float4 s = seg[p][w][lane];
-      if (w < warp) h = decay_apply(decay_unpack(make_float2(s.x, s.y)), h, make_float2(s.z, s.w));
+      back = decay_apply(decay_unpack(make_float2(s.x, s.y)), back, seg_grad[p][w][lane]);
     }
     // the faded state before each token, in the place of its input
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < kGlrSeg; ++k) {
       const float2 faded = decay_apply(d[k], h);
       h = add2(faded, u[k]);
       u[k] = faded;
     }
     float2 tA = both(0.f), tb = both(0.f);
-    T *px = dx + (size_t)first * a.D, *pl = dla + (size_t)first * a.D;
-    T* pg = dgate ? dgate + (size_t)first * a.D : nullptr;
-    glr_decay_from(a.decay_from, [&](auto from) {
+    const size_t at = (size_t)(first + kGlrSeg - 1) * a.D;
+    T *px = dx + at, *pl = dla + at, *pg = dgate ? dgate + at : nullptr;
+    glr_decay_from(a.decay_from, [&](auto form) {
 #pragma unroll
-      for (int k = kSeg - 1; k >= 0; --k) {
-        const float2 grad = add2(G::widen(rd[k]), back), xv = G::widen(rx[k]);
-        back = decay_apply(d[k], grad);
+      for (int k = kGlrSeg - 1; k >= 0; --k) {
         const int m = first + k < L ? in : 0;
+        const float2 grad = add2(Tile::get(from_dy, warp, lane, k), back), xv = Tile::get(from_x, warp, lane, k);
+        back = decay_apply(d[k], grad);
         float2 sx = xv, inv = both(0.f);
         const float2 f = input_factor<kFast>(a.input_scale, d[k], &inv);
         float2 ox = mul2(grad, f);
         if (gate) {
           float2 rest;
-          const float2 s = sigmoid2<kFast>(G::widen(rg[k]), rest);
+          const float2 s = sigmoid2<kFast>(Tile::get(from_gate, warp, lane, k), rest);
           ox = mul2(ox, s);
           sx = mul2(s, xv);
-          if (pg) G::template store<kPair>(pg + (size_t)k * a.D, mul2(mul2(ox, xv), rest), m);
+          if (dgate) G::template store<Tile::kPair>(pg, mul2(mul2(ox, xv), rest), m);
         }
-        G::template store<kPair>(px + (size_t)k * a.D, ox, m);
+        G::template store<Tile::kPair>(px, ox, m);
         float2 dg = u[k];
         if (a.input_scale != KDA_GLR_INPUT_NONE) {
           // the slope of c: -a or -a^2 / c
@@ -209,15 +195,15 @@ __global__ void __launch_bounds__(kGlrTile / GlrLane<T>::kSeg * 32, 1024 / (kGlr
           dg = fma2(slope, sx, dg);
         }
         dg = mul2(dg, grad);
-        const float2 lv = G::widen(rl[k]);
+        const float2 lv = Tile::get(from, warp, lane, k);
         float2 ol;
-        if constexpr (from.value == KDA_GLR_LOG) {
+        if constexpr (form.value == KDA_GLR_LOG) {
           ol = make_float2(lv.x > 0.f ? 0.f : dg.x, lv.y > 0.f ? 0.f : dg.y);
         } else {
           const float2 v = add2(lv, par.b);
           float2 rest, val;
           const float2 sg = sigmoid2<kFast>(v, rest);
-          if constexpr (from.value == KDA_GLR_SOFTPLUS) {
+          if constexpr (form.value == KDA_GLR_SOFTPLUS) {
             val = softplus2<kFast>(v);
             ol = mul2(mul2(minus_A, sg), dg);
             // a decay of 0 has no gradient, however large its logarithm
@@ -231,26 +217,33 @@ __global__ void __launch_bounds__(kGlrTile / GlrLane<T>::kSeg * 32, 1024 / (kGlr
             tb = add2(tb, ol);
           }
         }
-        G::template store<kPair>(pl + (size_t)k * a.D, ol, m);
+        G::template store<Tile::kPair>(pl, ol, m);
+        px -= a.D;
+        pl -= a.D;
+        pg -= a.D;
       }
     });
+    if (warp == 0) last[p][lane] = back;
     dA[0].add(tA.x);
     dA[1].add(tA.y);
     db[0].add(tb.x);
     db[1].add(tb.y);
   }
-  if (a.dh0 && rank == 0 && warp == 0) store_states(a.dh0 + (size_t)n * a.D + ch, carry, in);
+  if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+  if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
+  else __syncthreads();
+  if (live && a.dh0 && rank == 0 && warp == 0)
+    store_states(a.dh0 + (size_t)n * a.D + ch, ranks > 1 || rounds == 0 ? carry : last[(rounds - 1) & 1][lane], in);
   if (partial) {
-    static_assert(sizeof(seg) >= kWarps * 2 * 32 * sizeof(double2), "the shares fit in its place");
+    static_assert(sizeof(seg) >= kGlrWarps * 2 * 32 * sizeof(double2), "the shares fit in its place");
     double2(*sums)[2][32] = reinterpret_cast<double2(*)[2][32]>(&seg[0][0][0]);
-    __syncthreads();  // no warp reads segments any more
 #pragma unroll
     for (int c = 0; c < 2; ++c) sums[warp][c][lane] = make_double2(dA[c].value(), db[c].value());
     __syncthreads();
     if (warp == 0)
       for (int c = 0; c < in; ++c) {
         double2 z = sums[0][c][lane];
-        for (int w = 1; w < kWarps; ++w) {
+        for (int w = 1; w < kGlrWarps; ++w) {
           z.x += sums[w][c][lane].x;
           z.y += sums[w][c][lane].y;
         }
@@ -286,20 +279,28 @@ __global__ void __launch_bounds__(256) glr_join_kernel(const double2* partial, l
   }
 }
 
-template <typename T, bool kPair>
+template <typename T, int kBytes>
 cudaError_t launch(const GlrArgs& a, int ranks, cudaStream_t s) {
-  const long long blocks = (a.D + 63LL) / 64 * a.N;
-  return launch_early(glr_backward_kernel<T, kPair>, dim3((unsigned)blocks, 1, ranks),
-                      kGlrTile / GlrLane<T>::kSeg * 32, 0, ranks, s, a);
+  constexpr auto kern = glr_backward_kernel<T, kBytes>;
+  constexpr int kArray = GlrTile<T, kBytes>::kArray;
+  const cudaError_t e = allow_smem<kern>(8 * kArray);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (a.D + kGlrCols - 1LL) / kGlrCols * a.N;
+  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 4 : 3) * kArray,
+                               ranks, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_glr_backward(const GlrArgs& a, int dtype, bool pair, int ranks, float* dA, float* db,
+cudaError_t launch_glr_backward(const GlrArgs& a, int dtype, int bytes, int ranks, float* dA, float* db,
                                 cudaStream_t s) {
-  cudaError_t e = dtype == KDA_F32 ? (pair ? launch<float, true>(a, ranks, s) : launch<float, false>(a, ranks, s))
-                  : pair           ? launch<__nv_bfloat16, true>(a, ranks, s)
-                                   : launch<__nv_bfloat16, false>(a, ranks, s);
+  cudaError_t e;
+  if (dtype == KDA_F32)
+    e = bytes == 16 ? launch<float, 16>(a, ranks, s) : launch<float, 4>(a, ranks, s);
+  else
+    e = bytes == 16  ? launch<__nv_bfloat16, 16>(a, ranks, s)
+        : bytes == 4 ? launch<__nv_bfloat16, 4>(a, ranks, s)
+                     : launch<__nv_bfloat16, 2>(a, ranks, s);
   if (e != cudaSuccess || !a.partial) return e;
   return launch_early(glr_join_kernel, dim3((unsigned)((a.D + 31LL) / 32)), 256, 0, 1, s, (const double2*)a.partial,
                       (long long)a.N * ranks, a.D, dA, db);

@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
   glr_decay_from(a.decay_from, [&](auto from) {
     for (int t = 0; t < t1 - t0; ++t) {
       if (a.checkpoints && t % kGlrTile == 0) store_states(a.checkpoints + saved++ * a.D + ch, h, in);
-      const float2 xv = G::widen(G::template load<kPair>(x, in, G::same(0.f)));
-      const float2 lv = G::widen(G::template load<kPair>(la, in, G::same(0.f)));
+      const float2 xv = G::template load<kPair>(x, in);
+      const float2 lv = G::template load<kPair>(la, in);
       const Decay d = decay_of<G::kFast>(glr_log_decay<from.value, G::kFast>(par, lv));
       float2 u = mul2(input_factor<G::kFast>(a.input_scale, d), xv);
-      if (gate) u = mul2(u, sigmoid2<G::kFast>(G::widen(G::template load<kPair>(gate, in, G::same(0.f)))));
+      if (gate) u = mul2(u, sigmoid2<G::kFast>(G::template load<kPair>(gate, in)));
       h = decay_apply(d, h, u);
       G::template store<kPair>(y, h, in);
       x += a.ldx;
@@ -50,163 +50,172 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
 }
 
 // One CTA, or a cluster of them, per sequence and 64 channels.  A tile of 64 tokens has a segment
-// of eight (four in fp32) tokens for each of the warps, a lane two channels of them in registers:
-// decays and inputs, the segment's own scan from zero, then the states before it from the other
-// segments of the tile (shared memory) and from the other CTAs' tiles of this round (distributed
-// shared memory), and the scan once more from there.  All joins are taken in the order of the
-// tokens, so that results repeat to the bit.
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(kGlrTile / GlrLane<T>::kSeg * 32, 1024 / (kGlrTile / GlrLane<T>::kSeg * 64))
-    glr_scan_kernel(GlrArgs a) {
+// of eight for each of the eight warps, a lane two channels of them in registers: decays and
+// inputs, the segment's own scan from zero, then the states before it from the other CTAs' tiles
+// of this round (distributed shared memory) and from the tile's other segments (shared memory), and
+// the scan once more from there.  All joins are taken in the order of the tokens, so that results
+// repeat to the bit.  The next tile's arrays are copied to shared memory meanwhile.
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(GlrArgs a) {
   using G = GlrLane<T>;
-  using Raw = typename G::Raw;
-  constexpr int kSeg = G::kSeg, kWarps = kGlrTile / kSeg;
+  using Tile = GlrTile<T, kBytes>;
   constexpr bool kFast = G::kFast;
-  __shared__ float4 seg[2][kWarps][32];        // a segment's decay (packed) and its state from zero
-  __shared__ float2 seg_log[2][kWarps][32];    // and its log decay
-  __shared__ float4 tot[2][kGlrMaxRanks][32];  // decays and states of the tiles of a round
+  extern __shared__ __align__(16) uint8_t stages[];  // two, of two or three arrays
+  __shared__ float4 seg[2][kGlrWarps][32];           // a segment's decay (packed) and its state from zero
+  __shared__ float2 seg_log[2][32 * kGlrWarps];      // and its log decay
+  __shared__ float2 last[2][32];                     // the state behind a round, of a CTA alone
+  __shared__ GlrExchange others;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = gridDim.z, rank = blockIdx.z;
-  const int blocks = (a.D + 63) / 64;
-  const int n = blockIdx.x / blocks, ch = (blockIdx.x % blocks * 32 + lane) * 2;
+  const int blocks = (a.D + kGlrCols - 1) / kGlrCols;
+  const int n = blockIdx.x / blocks, ch0 = blockIdx.x % blocks * kGlrCols, ch = ch0 + lane * 2;
   grid_launch_dependents();
   grid_wait_prerequisites();  // what ran before is complete
-  int t0, t1, slot;
-  if (!gdr_sequence(a, n, t0, t1, slot)) return;  // the whole cluster alike
-  const int in = max(0, min(2, a.D - ch)), L = t1 - t0;
-  // the state before this round's first tile
-  float2 carry = load_states(a.h0 ? a.h0 + (size_t)slot * a.D + ch : nullptr, in);
-  const GlrChannels par = glr_channels(a, ch, in);
-  if (ranks > 1) cluster_sync();  // every CTA runs, and has its first states
-  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch;
-  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch;
-  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch : nullptr;
-  T* y = static_cast<T*>(a.y) + (size_t)t0 * a.D + ch;
-  const size_t saved = glr_checkpoint_row(t0, n);
+  // a sequence that is left out (by the whole cluster alike) has no tokens
+  int t0 = 0, t1 = 0, slot = 0;
+  const bool live = gdr_sequence(a, n, t0, t1, slot);
+  if (!live) t0 = t1 = 0;
+  const int in = max(0, min(2, a.D - ch)), cols = min(kGlrCols, a.D - ch0), L = t1 - t0;
   const int tiles = (L + kGlrTile - 1) / kGlrTile, rounds = (tiles + ranks - 1) / ranks;
-  const Raw zero = G::same(0.f), stay = G::same(glr_no_decay(a.decay_from));
-
-  Raw rx[kSeg], rl[kSeg], rg[kSeg];
+  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch0;
+  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch0;
+  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch0 : nullptr;
+  const uint32_t stage = (gate ? 3 : 2) * Tile::kArray;
   auto fetch = [&](int round) {
-    const int first = (round * ranks + rank) * kGlrTile + warp * kSeg;
-    const T *px = x + (size_t)first * a.ldx, *pl = la + (size_t)first * a.ldla;
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-      const int m = first + k < L ? in : 0;
-      rl[k] = G::template load<kPair>(pl + k * a.ldla, m, stay);
-      rx[k] = G::template load<kPair>(px + k * a.ldx, m, zero);
-    }
-    if (gate) {
-      const T* pg = gate + (size_t)first * a.ldg;
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k) rg[k] = G::template load<kPair>(pg + k * a.ldg, first + k < L ? in : 0, zero);
-    }
+    const int first = (round * ranks + rank) * kGlrTile, rows = L - first;
+    uint8_t* to = stages + (round & 1) * stage;
+    Tile::fetch(to, la + (size_t)first * a.ldla, a.ldla, rows, cols, from_f32<T>(glr_no_decay(a.decay_from)));
+    Tile::fetch(to + Tile::kArray, x + (size_t)first * a.ldx, a.ldx, rows, cols, from_f32<T>(0.f));
+    if (gate)
+      Tile::fetch(to + 2 * Tile::kArray, gate + (size_t)first * a.ldg, a.ldg, rows, cols, from_f32<T>(0.f));
   };
   if (rounds > 0) fetch(0);
+  cp_async_commit();
+  if (rounds > 1) fetch(1);
+  cp_async_commit();
+  // the state before this round's first tile
+  float2 carry = load_states(a.h0 && live ? a.h0 + (size_t)slot * a.D + ch : nullptr, in);
+  const GlrChannels par = glr_channels(a, ch, in);
+  if (threadIdx.x == 0) others.init();
+  cp_async_wait_group<1>();
+  if (ranks > 1) cluster_sync();  // every CTA runs, and has its first states and its barriers
+  __syncthreads();                // the first tile is in shared memory
+  T* y = static_cast<T*>(a.y) + (size_t)t0 * a.D + ch;
+  const size_t saved = glr_checkpoint_row(t0, n);
+  bool ok = true;
+
   for (int round = 0; round < rounds; ++round) {
     const int tile = round * ranks + rank, p = round & 1;
-    const int first = tile * kGlrTile + warp * kSeg;
-    Decay d[kSeg];
-    float2 u[kSeg], lg = both(0.f);
+    const int first = tile * kGlrTile + warp * kGlrSeg;
+    const uint8_t* from = stages + p * stage;
+    Decay d[kGlrSeg];
+    float2 u[kGlrSeg], lg = both(0.f);
     // decays and inputs; tokens behind the end have a decay of 1 and no input
-    glr_decay_from(a.decay_from, [&](auto from) {
+    glr_decay_from(a.decay_from, [&](auto form) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) {
-        const float2 g = glr_log_decay<from.value, kFast>(par, G::widen(rl[k]));
+      for (int k = 0; k < kGlrSeg; ++k) {
+        const float2 g = glr_log_decay<form.value, kFast>(par, Tile::get(from, warp, lane, k));
         lg = add2(lg, g);
         d[k] = decay_of<kFast>(g);
       }
     });
-    if (a.input_scale == KDA_GLR_INPUT_NONE) {
+    auto input = [&](auto scale) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) u[k] = G::widen(rx[k]);
-    } else if (a.input_scale == KDA_GLR_INPUT_COMPLEMENT) {
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k)
-        u[k] = mul2(input_factor<kFast>(KDA_GLR_INPUT_COMPLEMENT, d[k]), G::widen(rx[k]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < kSeg; ++k)
-        u[k] = mul2(input_factor<kFast>(KDA_GLR_INPUT_NORMALIZED, d[k]), G::widen(rx[k]));
-    }
+      for (int k = 0; k < kGlrSeg; ++k) {
+        u[k] = Tile::get(from + Tile::kArray, warp, lane, k);
+        if (scale.value != KDA_GLR_INPUT_NONE) u[k] = mul2(input_factor<kFast>(scale.value, d[k]), u[k]);
+      }
+    };
+    glr_input_scale(a.input_scale, input);
     if (gate) {
 #pragma unroll
-      for (int k = 0; k < kSeg; ++k) u[k] = mul2(u[k], sigmoid2<kFast>(G::widen(rg[k])));
+      for (int k = 0; k < kGlrSeg; ++k)
+        u[k] = mul2(u[k], sigmoid2<kFast>(Tile::get(from + 2 * Tile::kArray, warp, lane, k)));
     }
-    if (round + 1 < rounds) fetch(round + 1);
     float2 h = both(0.f);
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) h = decay_apply(d[k], h, u[k]);
+    for (int k = 0; k < kGlrSeg; ++k) h = decay_apply(d[k], h, u[k]);
     const float2 dt = decay_pack(decay_of<kFast>(lg));
     seg[p][warp][lane] = make_float4(dt.x, dt.y, h.x, h.y);
-    if (ranks > 1) seg_log[p][warp][lane] = lg;
+    if (ranks > 1) seg_log[p][threadIdx.x] = lg;
+    cp_async_wait_all();  // the next tile
     __syncthreads();
+    if (round + 2 < rounds) fetch(round + 2);  // where this tile was
+    cp_async_commit();
     if (ranks > 1) {
       // the tile's own decay and state from zero, to every CTA of the cluster
-      if (warp < ranks) {
+      if (warp == 0) {
         float2 z = both(0.f), l = both(0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kGlrWarps; ++w) {
           const float4 s = seg[p][w][lane];
           z = decay_apply(decay_unpack(make_float2(s.x, s.y)), z, make_float2(s.z, s.w));
-          l = add2(l, seg_log[p][w][lane]);
+          l = add2(l, seg_log[p][w * 32 + lane]);
         }
         const float2 t = decay_pack(decay_of<kFast>(l));
-        st_cluster_f32x4(map_to_rank(smem_u32(&tot[p][rank][lane]), warp), make_float4(t.x, t.y, z.x, z.y));
+        others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      cluster_sync();
+      ok = ok && others.wait(p, round);
       // the state before this CTA's tile, and the one behind the round
       h = carry;
       for (int r = 0; r < ranks; ++r) {
-        const float4 s = tot[p][r][lane];
+        const float4 s = others.tot[p][r][lane];
         if (r == rank) h = carry;
         carry = decay_apply(decay_unpack(make_float2(s.x, s.y)), carry, make_float2(s.z, s.w));
       }
     } else {
-      h = carry;
+      h = round > 0 ? last[1 - p][lane] : carry;
     }
     if (a.checkpoints && warp == 0 && tile < tiles) store_states(a.checkpoints + (saved + tile) * a.D + ch, h, in);
-    float2 all = h;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < warp; ++w) {
       const float4 s = seg[p][w][lane];
-      if (w == warp) h = all;
-      all = decay_apply(decay_unpack(make_float2(s.x, s.y)), all, make_float2(s.z, s.w));
+      h = decay_apply(decay_unpack(make_float2(s.x, s.y)), h, make_float2(s.z, s.w));
     }
-    if (ranks == 1) carry = all;
     T* py = y + (size_t)first * a.D;
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < kGlrSeg; ++k) {
       h = decay_apply(d[k], h, u[k]);
-      G::template store<kPair>(py + (size_t)k * a.D, h, first + k < L ? in : 0);
+      G::template store<Tile::kPair>(py, h, first + k < L ? in : 0);
+      py += a.D;
     }
+    if (warp == kGlrWarps - 1) last[p][lane] = h;
   }
-  // (a state pool: every CTA has read its first states before the cluster's first barrier, and
-  // every warp before the first of the CTA; without a tile this warp is the only one that read)
-  if (rank == 0 && warp == 0) store_states(a.h_T + (size_t)slot * a.D + ch, carry, in);
+  if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+  if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
+  else __syncthreads();
+  // (a state pool: every warp has read its first states by now)
+  if (live && rank == 0 && warp == 0)
+    store_states(a.h_T + (size_t)slot * a.D + ch, ranks > 1 || rounds == 0 ? carry : last[(rounds - 1) & 1][lane], in);
 }
 
-template <typename T, bool kPair>
+template <typename T, int kBytes>
 cudaError_t launch_few(const GlrArgs& a, cudaStream_t s) {
   const long long blocks = (a.D + 2LL * kFewThreads - 1) / (2 * kFewThreads) * a.N;
-  return launch_early(glr_few_kernel<T, kPair>, dim3((unsigned)blocks), kFewThreads, 0, 1, s, a);
+  return launch_early(glr_few_kernel<T, GlrTile<T, kBytes>::kPair>, dim3((unsigned)blocks), kFewThreads, 0, 1, s, a);
 }
-template <typename T, bool kPair>
+template <typename T, int kBytes>
 cudaError_t launch_scan(const GlrArgs& a, int ranks, cudaStream_t s) {
-  const long long blocks = (a.D + 63LL) / 64 * a.N;
-  return launch_early(glr_scan_kernel<T, kPair>, dim3((unsigned)blocks, 1, ranks),
-                      kGlrTile / GlrLane<T>::kSeg * 32, 0, ranks, s, a);
+  constexpr auto kern = glr_scan_kernel<T, kBytes>;
+  constexpr int kArray = GlrTile<T, kBytes>::kArray;
+  const cudaError_t e = allow_smem<kern>(6 * kArray);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (a.D + kGlrCols - 1LL) / kGlrCols * a.N;
+  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 3 : 2) * kArray,
+                               ranks, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_glr_few(const GlrArgs& a, int dtype, bool pair, cudaStream_t s) {
-  if (dtype == KDA_F32) return pair ? launch_few<float, true>(a, s) : launch_few<float, false>(a, s);
-  return pair ? launch_few<__nv_bfloat16, true>(a, s) : launch_few<__nv_bfloat16, false>(a, s);
+cudaError_t launch_glr_few(const GlrArgs& a, int dtype, int bytes, cudaStream_t s) {
+  if (dtype == KDA_F32) return bytes == 16 ? launch_few<float, 16>(a, s) : launch_few<float, 4>(a, s);
+  return bytes >= 4 ? launch_few<__nv_bfloat16, 4>(a, s) : launch_few<__nv_bfloat16, 2>(a, s);
 }
-cudaError_t launch_glr_scan(const GlrArgs& a, int dtype, bool pair, int ranks, cudaStream_t s) {
-  if (dtype == KDA_F32) return pair ? launch_scan<float, true>(a, ranks, s) : launch_scan<float, false>(a, ranks, s);
-  return pair ? launch_scan<__nv_bfloat16, true>(a, ranks, s) : launch_scan<__nv_bfloat16, false>(a, ranks, s);
+cudaError_t launch_glr_scan(const GlrArgs& a, int dtype, int bytes, int ranks, cudaStream_t s) {
+  if (dtype == KDA_F32)
+    return bytes == 16 ? launch_scan<float, 16>(a, ranks, s) : launch_scan<float, 4>(a, ranks, s);
+  return bytes == 16  ? launch_scan<__nv_bfloat16, 16>(a, ranks, s)
+         : bytes == 4 ? launch_scan<__nv_bfloat16, 4>(a, ranks, s)
+                      : launch_scan<__nv_bfloat16, 2>(a, ranks, s);
 }
 
 }  // namespace kda
