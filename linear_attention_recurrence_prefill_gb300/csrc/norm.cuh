@@ -19,6 +19,10 @@ struct NormArgs {
   bool norm;  // false: n = s
 };
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_norm_bf16(const NormArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_f32(const NormArgs& a, int sms, cudaStream_t s);
+inline cudaError_t launch_norm(const NormArgs& a, int dtype, int sms, cudaStream_t s) {
+  return dtype == KDA_BF16 ? launch_norm_bf16(a, sms, s) : launch_norm_f32(a, sms, s);
+}
 
 }  // namespace kda
