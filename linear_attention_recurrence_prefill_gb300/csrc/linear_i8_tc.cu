@@ -4,10 +4,12 @@
 // This GPU multiplies 8-bit integers far below its rate for 16-bit floats, and every such
 // integer is an fp16 number: the products are taken in fp16 with fp32 sums, which are exact below
 // 2^24.  So what 8 bits save is memory, and the integers are widened on their way:
-//  * few tiles (few tokens, or a small product; bound by reading w): linear_i8_kernel, where
-//    eight warps fetch the integers into shared memory, widen them there and lay them out as the
-//    tiles that the MMAs read.  The CTAs of a cluster share a tile of 128 channels, each takes a
-//    part of K.
+//  * few tiles (few tokens, or a small product; bound by reading w): linear_i8_kernel.  w's rows go
+//    from shared memory through registers, where they are widened, into TMEM, from which the MMAs take
+//    them: a lane of TMEM is a row, so a thread widens 64 neighbouring integers of its row and
+//    stores them at once.  x, of which there is less, is widened into tiles of shared memory by
+//    warps of its own.  The CTAs of a cluster share a tile of 128 channels, each takes a part of K.
+//    (Both widened into shared memory, with its fences, took 26 us for 64 x 12288 -> 4096.)
 //  * many: both arrays are widened into the workspace first, once, and the product is that of
 //    kda_linear's pairs of CTAs.  Widened in the product, w would be taken through shared memory
 //    once more for every 256 tokens, which the tensor cores' own reads leave no room for.
@@ -21,8 +23,9 @@ namespace {
 using namespace umma;
 
 constexpr uint32_t kRowsA = kJoinRows, kBlockK = 64;
-// warps that widen, one that issues the MMAs and, where TMA can take the arrays, one that loads
-constexpr int kFill = 8, kMma = 8, kLoad = 9;
+// Warps 0-7 widen w, the even blocks of 64 columns by 0-3 and the odd ones by 4-7; then come those
+// that widen x, one that issues the MMAs and, where TMA can take the arrays, one that loads.
+constexpr int kFillW = 8;
 constexpr uint32_t kAlign = 1024;                      // the swizzled tiles' alignment
 constexpr long long kSpins = 4000000000LL;             // ~2 s of clock cycles
 
@@ -55,30 +58,49 @@ __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, uin
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The integers of a block of 64 columns: rows of w, then of x, in chunks of 16 bytes, four to a row;
-// thread t of the 256 that widen has chunks t, t + 256, ...  By TMA where it takes the arrays (rows
-// and bases at 16 bytes); else each thread copies its own, in two aligned pieces around each.
+// kTma: rows and bases at 16 bytes.  A block's integers then land in shared memory, in rows of 64
+// bytes (w's with TMA's swizzle of 64 bytes: each thread reads a row of its own); else the threads
+// read them where they are.
 template <int BN, bool kTma>
 struct Fill {
-  static constexpr int kThreads = (kFill + (kTma ? 2 : 1)) * 32;
-  static constexpr int kChunks = ((int)kRowsA + BN + 63) / 64;  // per thread
-  static constexpr int kPieces = kTma ? 1 : 2;
-  static constexpr int kRaw = kTma ? (BN > 64 ? 3 : 4) : 2;  // blocks on their way or landed
-  static constexpr uint32_t kRawBlock = kChunks * kPieces * kFill * 32 * 16;
-  static constexpr uint32_t kTile = (kRowsA + BN) * kBlockK * 2;
-  static constexpr int kTiles = 2;  // widened blocks
-  static constexpr uint32_t kSmem = kAlign + kTiles * kTile + kRaw * kRawBlock;
+  static constexpr int kFillX = BN > 32 ? 4 : 2;
+  static constexpr int kMma = kFillW + kFillX, kLoad = kMma + 1;
+  static constexpr int kThreads = (kMma + (kTma ? 2 : 1)) * 32;
+  static constexpr int kTiles = 4;                                // widened blocks
+  static constexpr int kRaw = kTma ? (BN > 64 ? 2 : 4) : 0;       // blocks on their way or landed
+  static constexpr uint32_t kRawBlock = (kRowsA + BN) * kBlockK;
+  static constexpr uint32_t kTile = BN * kBlockK * 2;             // x's part of a widened block
+  static constexpr uint32_t kUsed = kTiles * kTile + kRaw * kRawBlock, kSums = BN * kRowsA * 4;
+  static constexpr uint32_t kSmem = kAlign + (kUsed > kSums ? kUsed : kSums);
+  static constexpr uint32_t kAcc = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;  // columns of TMEM
+  static constexpr uint32_t kA = kBlockK / 2;                            // of w's part of a block
 };
 
+// 16 integers from p on, of which `left` exist (zeros behind them), `first`: of the array's first byte.
+__device__ __forceinline__ uint4 load16(const int8_t* p, long long left, const int8_t* first) {
+  const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15;
+  const int8_t* from = p - off;
+  if (left >= 16 && from >= first && (off == 0 || left >= 32)) {
+    const uint4 a = *reinterpret_cast<const uint4*>(from);
+    const uint4 b = off ? *reinterpret_cast<const uint4*>(from + 16) : a;
+    return shift_bytes(a, b, off);
+  }
+  uint4 v = make_uint4(0, 0, 0, 0);
+  uint32_t* z = &v.x;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e < left) z[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+  return v;
+}
+
 template <int BN, bool kTma, typename T>
-__global__ void __launch_bounds__(Fill<BN, kTma>::kThreads) linear_i8_kernel(const __grid_constant__ I8 t) {
+__global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(const __grid_constant__ I8 t) {
   using F = Fill<BN, kTma>;
-  constexpr uint32_t kCols = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;
-  static_assert(F::kTiles * F::kTile >= BN * kRowsA * 4, "the partial sums fit in the tiles");
+  constexpr int kRawSlots = kTma ? F::kRaw : 1;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* tiles = raw_smem + ((kAlign - (smem_u32(raw_smem) & (kAlign - 1))) & (kAlign - 1));
   uint8_t* raw = tiles + F::kTiles * F::kTile;
-  __shared__ uint64_t full[F::kTiles], empty[F::kTiles], landed[F::kRaw], taken[F::kRaw], done;
+  __shared__ uint64_t full[F::kTiles], empty[F::kTiles], landed[kRawSlots], taken[kRawSlots], done;
   __shared__ uint32_t tmem_base;
 
   const LinearArgs& l = t.a.l;
@@ -86,18 +108,18 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads) linear_i8_kernel(con
   const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::kTiles; ++i) {
-      mbar_init(&full[i], kFill);
+      mbar_init(&full[i], 4 + F::kFillX);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < F::kRaw; ++i) {
+    for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&landed[i], 1);
-      mbar_init(&taken[i], kFill);
+      mbar_init(&taken[i], 4 + F::kFillX);
     }
     mbar_init(&done, 1);
     mbar_fence_init();
   }
-  if (warp == kMma) {
-    tmem_alloc(&tmem_base, kCols);
+  if (warp == F::kMma) {
+    tmem_alloc(&tmem_base, 256);
     tmem_relinquish();
   }
   fence_before_sync();
@@ -109,123 +131,99 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads) linear_i8_kernel(con
   // this CTA's part of K: every ranks-th block (one at least)
   const int blocks = (t.k_blocks - (int)rank + (int)ranks - 1) / (int)ranks;
   const int n0 = blockIdx.x % t.n_tiles * (int)kRowsA, m0 = blockIdx.x / t.n_tiles * BN;
+  auto column = [&](int it) { return (it * (long long)ranks + rank) * kBlockK; };
 
   bool ok = true;
-  if (warp < kFill) {
-    const int tid = threadIdx.x;
-    // this thread's rows, by chunk: the address of their column 16 (tid % 4), and whether they exist
-    const int8_t* row[F::kChunks];
-    bool in[F::kChunks];
+  if (warp < kFillW) {
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const bool in = (long long)n0 + r < l.N;
+    const int8_t* row = static_cast<const int8_t*>(l.w) + (in ? (long long)n0 + r : 0) * l.ldw;
+    uint4 next[4];
     auto fetch = [&](int it) {
-      if constexpr (!kTma) {
-        if (it < blocks) {
-          const long long k = (it * (long long)ranks + rank) * kBlockK;
-          const int left = (int)min(16LL, l.K - k - tid % 4 * 16);  // columns of this thread's that exist
-          const uint32_t to = smem_u32(raw) + tid * 16 + it % F::kRaw * F::kRawBlock;
-          const int8_t* const nothing =
-              reinterpret_cast<const int8_t*>(reinterpret_cast<uintptr_t>(l.w) & ~(uintptr_t)15);
+      const long long k = column(it);
 #pragma unroll
-          for (int i = 0; i < F::kChunks; ++i) {
-            // the aligned pieces around the 16 bytes, up to the end of the row (zeros behind it): their
-            // bytes before the 16 are not used, but those before the array are not touched either
-            const int8_t* p = row[i] + k;
-            const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15;
-            const bool of_x = (tid + i * kFill * 32) / 4 >= (int)kRowsA;
-            const int8_t* lo = static_cast<const int8_t*>(of_x ? l.x : l.w);
-            const int have = in[i] && left > 0 ? (int)off + left : 0;
-            const uint32_t at = to + i * 2 * kFill * 32 * 16;
-            if (have > 0 && p - off < lo) {
-              for (int e = 0; e < 16; ++e)
-                raw[at - smem_u32(raw) + e] = e < have && p - off + e >= lo ? (uint8_t)p[e - (int)off] : 0;
-            } else {
-              cp_async16(at, have > 0 ? p - off : nothing, have > 16 ? 16 : have);
-            }
-            cp_async16(at + kFill * 32 * 16, have > 16 ? p - off + 16 : nothing, have > 16 ? have - 16 : 0);
-          }
-        }
-        cp_async_commit();
-      }
+      for (int c = 0; c < 4; ++c)
+        next[c] = load16(row + k + c * 16, in && it < blocks ? l.K - k - c * 16 : 0, static_cast<const int8_t*>(l.w));
     };
-    if constexpr (!kTma) {
+    if (!kTma) fetch(warp >> 2);
+    for (int it = warp >> 2; it < blocks; it += 2) {
+      const int s = it % F::kTiles;
+      uint32_t half[32];
+      if constexpr (kTma) {
+        const int slot = it % F::kRaw;
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&landed[slot], (it / F::kRaw) & 1, kSpins));
+        if (!ok) break;
+        const uint8_t* from = raw + slot * F::kRawBlock + r * kBlockK;
 #pragma unroll
-      for (int i = 0; i < F::kChunks; ++i) {
-        const int r = (tid + i * kFill * 32) / 4;
-        const bool of_x = r >= (int)kRowsA;
-        const long long at = of_x ? (long long)m0 + r - (int)kRowsA : (long long)n0 + r;
-        in[i] = r < (int)kRowsA + BN && at < (of_x ? l.M : l.N);
-        row[i] = (of_x ? static_cast<const int8_t*>(l.x) + at * l.ldx : static_cast<const int8_t*>(l.w) + at * l.ldw) +
-                 tid % 4 * 16;
+        for (int c = 0; c < 4; ++c) next[c] = *reinterpret_cast<const uint4*>(from + ((c ^ (r >> 1 & 3)) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[slot]);
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        widen4(next[c].x, half[8 * c], half[8 * c + 1]);
+        widen4(next[c].y, half[8 * c + 2], half[8 * c + 3]);
+        widen4(next[c].z, half[8 * c + 4], half[8 * c + 5]);
+        widen4(next[c].w, half[8 * c + 6], half[8 * c + 7]);
+      }
+      if (!kTma) fetch(it + 2);
+      if (it >= F::kTiles)
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&empty[s], (it / F::kTiles - 1) & 1, kSpins));
+      if (!ok) break;
+      fence_after_sync();
+      tmem_st32(taddr(tmem, quarter * 32, F::kAcc + s * F::kA), half);
+      tmem_wait_st();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
     }
-    for (int it = 0; it < F::kRaw - 1; ++it) fetch(it);
+  } else if (warp < F::kMma) {
+    const int tid = threadIdx.x - kFillW * 32;
+    constexpr int kThreadsX = F::kFillX * 32, kChunks = (BN * 4 + kThreadsX - 1) / kThreadsX;
+    const int c = tid % 4;
     for (int it = 0; it < blocks; ++it) {
       const int s = it % F::kTiles;
+      uint4 v[kChunks];
       if constexpr (kTma) {
-        ok = mbar_wait_soon(&landed[it % F::kRaw], (it / F::kRaw) & 1, kSpins);
-      } else {
-        fetch(it + F::kRaw - 1);
-        cp_async_wait_group<F::kRaw - 1>();  // this thread's own pieces of block `it`
-      }
-      if (ok && it >= F::kTiles) ok = mbar_wait_soon(&empty[s], (it / F::kTiles - 1) & 1, kSpins);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint8_t* from = raw + it % F::kRaw * F::kRawBlock + tid * 16;
-      uint8_t* tile = tiles + s * F::kTile;
-      const long long k = (it * (long long)ranks + rank) * kBlockK;
+        const int slot = it % F::kRaw;
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&landed[slot], (it / F::kRaw) & 1, kSpins));
+        if (!ok) break;
+        const uint8_t* from = raw + slot * F::kRawBlock + kRowsA * kBlockK;
 #pragma unroll
-      for (int i = 0; i < F::kChunks; ++i) {
-        const int r = (tid + i * kFill * 32) / 4;
-        if (((int)kRowsA + BN) % 64 != 0 && r >= (int)kRowsA + BN) break;
-        const bool of_x = r >= (int)kRowsA;
-        uint4 v = *reinterpret_cast<const uint4*>(from + i * F::kPieces * kFill * 32 * 16);
-        if (!kTma) {
-          const uint4 w = *reinterpret_cast<const uint4*>(from + (2 * i + 1) * kFill * 32 * 16);
-          v = shift_bytes(v, w, (uint32_t)(reinterpret_cast<uintptr_t>(row[i]) + k) & 15);
+        for (int i = 0; i < kChunks; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (tid + i * kThreadsX) * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[slot]);
+      } else {
+        const long long k = column(it) + c * 16;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const long long m = (long long)m0 + (tid + i * kThreadsX) / 4;
+          const bool in = m < l.M && (tid + i * kThreadsX) / 4 < BN;
+          v[i] = load16(static_cast<const int8_t*>(l.x) + (in ? m : 0) * l.ldx + k, in ? l.K - k : 0,
+                        static_cast<const int8_t*>(l.x));
         }
+      }
+      if (it >= F::kTiles)
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&empty[s], (it / F::kTiles - 1) & 1, kSpins));
+      if (!ok) break;
+      uint8_t* tile = tiles + s * F::kTile;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const uint32_t r = (tid + i * kThreadsX) / 4;
+        if (kChunks * kThreadsX != BN * 4 && r >= BN) break;
         uint4 a, b;
-        widen4(v.x, a.x, a.y);
-        widen4(v.y, a.z, a.w);
-        widen4(v.z, b.x, b.y);
-        widen4(v.w, b.z, b.w);
-        const uint32_t rr = of_x ? r - kRowsA : r;
-        uint8_t* to = tile + (of_x ? kRowsA * kBlockK * 2 : 0);
-        const uint32_t c = tid % 4 * 2;
-        *reinterpret_cast<uint4*>(to + sw128_chunk(rr, c, 0)) = a;
-        *reinterpret_cast<uint4*>(to + sw128_chunk(rr, c + 1, 0)) = b;
+        widen4(v[i].x, a.x, a.y);
+        widen4(v[i].y, a.z, a.w);
+        widen4(v[i].z, b.x, b.y);
+        widen4(v[i].w, b.z, b.w);
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(r, 2 * c, 0)) = a;
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(r, 2 * c + 1, 0)) = b;
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&full[s]);
-        if (kTma) mbar_arrive(&taken[it % F::kRaw]);
-      }
+      if (lane == 0) mbar_arrive(&full[s]);
     }
-    cp_async_wait_all();
-    // Done behind all of this CTA's blocks, each of which has a wait of its own that gives up (the
-    // MMA warp then signals all the same): a block takes some 300 to 5,000 cycles.
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(&done, 0, 3 * kSpins + (long long)blocks * 65536));
-    fence_after_sync();
-  } else if (kTma && warp == kLoad) {
-    if (lane == 0) {
-      int it = 0;
-      for (; it < blocks; ++it) {
-        const int s = it % F::kRaw, x = (it * (int)ranks + (int)rank) * (int)kBlockK;
-        if (it >= F::kRaw && !mbar_wait_soon(&taken[s], (it / F::kRaw - 1) & 1, kSpins)) {
-          ok = false;
-          break;
-        }
-        uint8_t* to = raw + s * F::kRawBlock;
-        mbar_arrive_expect_tx(&landed[s], (kRowsA + BN) * kBlockK);
-        tma_load_2d(to, &t.tm_w, x, n0, &landed[s]);
-        tma_load_2d(to + kRowsA * kBlockK, &t.tm_x, x, m0, &landed[s]);
-      }
-      // a wait that gave up, here or of the warps that widen: the loads in flight land before shared
-      // memory is released
-      for (int j = it > F::kRaw ? it - F::kRaw : 0; j < it; ++j)
-        mbar_wait(&landed[j % F::kRaw], (j / F::kRaw) & 1, kSpins);
-    }
-    __syncwarp();
-  } else {
+  } else if (warp == F::kMma) {
     const uint32_t lead = elect_leader();
     constexpr uint32_t idesc = idesc_f16(kRowsA, BN, false);
     for (int it = 0; it < blocks; ++it) {
@@ -233,18 +231,43 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads) linear_i8_kernel(con
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&full[s], (it / F::kTiles) & 1, kSpins));
       if (!ok) break;
       fence_after_sync();
-      const uint32_t at = smem_u32(tiles + s * F::kTile);
-      const uint64_t wd = desc_k_sw128(at, 0), xd = desc_k_sw128(at + kRowsA * kBlockK * 2, 0);
+      const uint64_t xd = desc_k_sw128(smem_u32(tiles + s * F::kTile), 0);
 #pragma unroll
       for (uint32_t k = 0; k < kBlockK / 16; ++k)
-        mma_ss_if(lead, tmem, wd + (k * 32 >> 4), xd + (k * 32 >> 4), idesc, it > 0 || k > 0);
+        mma_ts_if(lead, tmem, tmem + F::kAcc + s * F::kA + k * 8, xd + (k * 32 >> 4), idesc, it > 0 || k > 0);
       mma_commit_if(lead, &empty[s]);
     }
     // everything issued is complete before the tiles or TMEM are used again, or released
     mma_commit_if(lead, &done);
     mbar_wait(&done, 0, kSpins);
+  } else if (kTma) {
+    if (lane == 0) {
+      int it = 0;
+      for (; it < blocks; ++it) {
+        const int s = it % kRawSlots, x = (int)column(it);
+        if (it >= kRawSlots && !mbar_wait_soon(&taken[s], (it / kRawSlots - 1) & 1, kSpins)) {
+          ok = false;
+          break;
+        }
+        uint8_t* to = raw + s * F::kRawBlock;
+        mbar_arrive_expect_tx(&landed[s], F::kRawBlock);
+        tma_load_2d(to, &t.tm_w, x, n0, &landed[s]);
+        tma_load_2d(to + kRowsA * kBlockK, &t.tm_x, x, m0, &landed[s]);
+      }
+      // a wait that gave up, here or of the warps that widen: the loads in flight land before shared
+      // memory is released
+      for (int j = it > kRawSlots ? it - kRawSlots : 0; j < it; ++j)
+        mbar_wait(&landed[j % kRawSlots], (j / kRawSlots) & 1, kSpins);
+    }
+    __syncwarp();
   }
-  __syncthreads();  // no thread widens into the tiles any more
+  // Done behind all of this CTA's blocks, each of which has a wait of its own that gives up (the
+  // MMA warp then signals all the same): a block takes some 300 to 5,000 cycles.
+  if (warp < 4) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&done, 0, 3 * kSpins + (long long)blocks * 65536));
+    fence_after_sync();
+  }
+  __syncthreads();  // no thread widens any more, and nothing is on its way to shared memory
   if (ok && warp < 4) {
     // partial sums [column][channel] over the tiles, whose products are done
     const uint32_t d = taddr(tmem, warp * 32, 0);
@@ -285,7 +308,7 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads) linear_i8_kernel(con
   fence_before_sync();
   cluster_sync();  // no CTA leaves while its sums are read
   fence_after_sync();
-  if (warp == kMma) tmem_dealloc(tmem, kCols);
+  if (warp == F::kMma) tmem_dealloc(tmem, 256);
 }
 
 // [rows][K] integers, rows ld bytes apart, as fp16 with rows of Kp elements (a multiple of 16, zeros
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(256) no_columns_kernel(LinearI8Args a) {
 
 // Tensor map of [rows][K] integers, rows ld bytes apart: boxes of 64 columns by `box` rows, zeros
 // outside.
-bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int box) {
+bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int box, CUtensorMapSwizzle swizzle) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
@@ -367,7 +390,7 @@ bool encode(CUtensorMap* m, const void* base, int rows, int K, long long ld, int
   const cuuint32_t boxes[2] = {kBlockK, (cuuint32_t)box};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool tma_takes(const LinearArgs& l) {
@@ -387,8 +410,8 @@ cudaError_t launch_of(const LinearI8Args& a, int* status, int split, cudaStream_
   t.status = status;
   t.n_tiles = (a.l.N + (int)kRowsA - 1) / (int)kRowsA;
   t.k_blocks = (a.l.K + (int)kBlockK - 1) / (int)kBlockK;
-  if (kTma && !(encode(&t.tm_w, a.l.w, a.l.N, a.l.K, a.l.ldw, kRowsA) &&
-                encode(&t.tm_x, a.l.x, a.l.M, a.l.K, a.l.ldx, BN)))
+  if (kTma && !(encode(&t.tm_w, a.l.w, a.l.N, a.l.K, a.l.ldw, kRowsA, CU_TENSOR_MAP_SWIZZLE_64B) &&
+                encode(&t.tm_x, a.l.x, a.l.M, a.l.K, a.l.ldx, BN, CU_TENSOR_MAP_SWIZZLE_NONE)))
     return cudaErrorInvalidValue;
   const long long tiles = (long long)t.n_tiles * ((a.l.M + BN - 1LL) / BN);
   return launch_early(kern, dim3((unsigned)tiles, 1, split), F::kThreads, F::kSmem, split, s, t);
