@@ -24,7 +24,8 @@ using namespace umma;
 
 constexpr uint32_t kRowsA = kJoinRows, kBlockK = 64;
 // Warps 0-7 widen w, the even blocks of 64 columns by 0-3 and the odd ones by 4-7; then come those
-// that widen x, one that issues the MMAs and, where TMA can take the arrays, one that loads.
+// that widen x, half of them the even blocks, one that issues the MMAs and, where TMA can take the
+// arrays, one that loads.
 constexpr int kFillW = 8;
 constexpr uint32_t kAlign = 1024;                      // the swizzled tiles' alignment
 constexpr long long kSpins = 4000000000LL;             // ~2 s of clock cycles
@@ -63,8 +64,8 @@ __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, uin
 // read them where they are.
 template <int BN, bool kTma>
 struct Fill {
-  static constexpr int kFillX = BN > 32 ? 4 : 2;
-  static constexpr int kMma = kFillW + kFillX, kLoad = kMma + 1;
+  static constexpr int kFillX = BN > 32 ? 4 : 2, kFill = (kFillW + kFillX) / 2;  // the latter of a block
+  static constexpr int kMma = kFillW + kFillX;
   static constexpr int kThreads = (kMma + (kTma ? 2 : 1)) * 32;
   static constexpr int kTiles = 4;                                // widened blocks
   static constexpr int kRaw = kTma ? (BN > 64 ? 2 : 4) : 0;       // blocks on their way or landed
@@ -108,12 +109,12 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
   const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::kTiles; ++i) {
-      mbar_init(&full[i], 4 + F::kFillX);
+      mbar_init(&full[i], F::kFill);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&landed[i], 1);
-      mbar_init(&taken[i], 4 + F::kFillX);
+      mbar_init(&taken[i], F::kFill);
     }
     mbar_init(&done, 1);
     mbar_fence_init();
@@ -178,10 +179,9 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
       if (lane == 0) mbar_arrive(&full[s]);
     }
   } else if (warp < F::kMma) {
-    const int tid = threadIdx.x - kFillW * 32;
-    constexpr int kThreadsX = F::kFillX * 32, kChunks = (BN * 4 + kThreadsX - 1) / kThreadsX;
-    const int c = tid % 4;
-    for (int it = 0; it < blocks; ++it) {
+    constexpr int kThreadsX = F::kFillX * 16, kChunks = (BN * 4 + kThreadsX - 1) / kThreadsX;
+    const int tid = ((int)threadIdx.x - kFillW * 32) % kThreadsX, c = tid % 4;
+    for (int it = (warp - kFillW) / (F::kFillX / 2); it < blocks; it += 2) {
       const int s = it % F::kTiles;
       uint4 v[kChunks];
       if constexpr (kTma) {
@@ -312,10 +312,10 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
 }
 
 // [rows][K] integers, rows ld bytes apart, as fp16 with rows of Kp elements (a multiple of 16, zeros
-// behind K), x's rows and then w's: a thread takes 16 columns of four rows at a time.
-__global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, long long ldx, long long rows_x, const int8_t* w,
+// behind K), x's rows and then w's: a thread takes 16 columns of two rows at a time.
+__global__ void __launch_bounds__(256, 8) widen_kernel(const int8_t* x, long long ldx, long long rows_x, const int8_t* w,
                                                     long long ldw, long long rows_w, int K, int Kp, uint4* to) {
-  constexpr int kFlight = 4;
+  constexpr int kFlight = 2;
   grid_launch_dependents();
   grid_wait_prerequisites();
   const long long rows = rows_x + rows_w;
@@ -445,7 +445,7 @@ cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspac
                                 cudaStream_t s) {
   const LinearArgs& l = a.l;
   if (widened(l.M, l.N, sms)) {
-    const long long Kp = padded(l.K), blocks = ((long long)l.M + l.N + 3) / 4, most = 8LL * sms;
+    const long long Kp = padded(l.K), blocks = ((long long)l.M + l.N + 1) / 2, most = 8LL * sms;
     const cudaError_t e = launch_early(
         widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 1, s, static_cast<const int8_t*>(l.x),
         l.ldx, (long long)l.M, static_cast<const int8_t*>(l.w), l.ldw, (long long)l.N, l.K, (int)Kp,

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
   uint8_t* ring = raw + ((kAlign - (smem_u32(raw) & (kAlign - 1))) & (kAlign - 1));
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
+  __shared__ __align__(16) float scales[kI8 ? kPairOut : 1][32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
       const bool in = n < t.a.N;
       const float b = bias && in ? to_f32(bias[n]) : 0.f;
       const float scale = kI8 && in ? t.w_scale[n] : 0.f;
+      float scale_m = kI8 && half * 32 + lane < cols ? t.x_scale[m0 + half * 32 + lane] : 0.f;
       T add[32], next[32];
       if (in) load_residual(t.a, add, m0 + half * 32, n, cols - half * 32);
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_full[acc], (i / 2) & 1, kSpins));
@@ -231,15 +233,24 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
         tmem_ld32(d + c, r);
         if (in && c + 64 < cols) load_residual(t.a, next, m0 + c + 64, n, cols - c - 64);
         float z[32];
-        if constexpr (kI8) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = j < cols - c ? t.x_scale[m0 + c + j] : 0.f;
-        }
         tmem_wait_ld();
+        if constexpr (kI8) {
+          // the tokens' scales, a lane each, to all lanes
+          __syncwarp();
+          scales[warp][lane] = scale_m;
+          __syncwarp();
+          if (c + 64 + lane < cols) scale_m = t.x_scale[m0 + c + 64 + lane];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float sum = __uint_as_float(r[j]);
-          z[j] = kI8 ? sum * z[j] * scale : sum;
+          for (int j = 0; j < 32; j += 4) {
+            const float4 xs = *reinterpret_cast<const float4*>(&scales[warp][j]);
+            z[j] = __uint_as_float(r[j]) * xs.x * scale;
+            z[j + 1] = __uint_as_float(r[j + 1]) * xs.y * scale;
+            z[j + 2] = __uint_as_float(r[j + 2]) * xs.z * scale;
+            z[j + 3] = __uint_as_float(r[j + 3]) * xs.w * scale;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]);
         }
         if (in) finish32(t.a, z, b, add, m0 + c, n, cols - c);
 #pragma unroll
