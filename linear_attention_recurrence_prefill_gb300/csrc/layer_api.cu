@@ -257,6 +257,8 @@ int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const in
   cudaError_t e;
   if (K == 0) {
     e = launch_linear_i8_none(a, dtype, s);
+  } else if (linear_i8_few_takes(a)) {
+    e = launch_linear_i8_few(a, dtype, sm_count(), s);
   } else {
     int* status = status_word();
     if (!status) return KDA_ERR_CUDA;

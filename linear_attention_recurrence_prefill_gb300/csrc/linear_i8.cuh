@@ -15,6 +15,9 @@ struct LinearI8Args {
 
 // K = 0 only: y = act(bias) + residual.
 cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s);
+// Up to eight rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.
+bool linear_i8_few_takes(const LinearI8Args& a);
+cudaError_t launch_linear_i8_few(const LinearI8Args& a, int dtype, int sms, cudaStream_t s);
 // Any alignment and number of rows, K > 0.
 bool linear_i8_tc_takes(int M, int N);
 size_t linear_i8_workspace_bytes(int M, int N, int K, int sms);
