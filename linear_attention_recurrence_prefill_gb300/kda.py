@@ -845,6 +845,12 @@ def kda_linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, y=None, *, a
 
 
 # ------------------------------------------------- the norm before a layer
+def _like(host, x):
+    """A new dense tensor of x's shape and type."""
+    return (host.empty_like(x) if x.is_contiguous()
+            else host.empty(x.shape, dtype=x.dtype, device=x.device))
+
+
 def _norm(x, w, residual, total, y, q, scale, eps, i8):
     host = _host()
     dev = _one_device(host, x, w, residual, total, y, q, scale)
@@ -863,12 +869,12 @@ def _norm(x, w, residual, total, y, q, scale, eps, i8):
     else:
         ldr, at["residual"] = _rows(residual, "residual", M, D), residual.data_ptr()
         if total is None:
-            total = host.empty((M, D), dtype=dtype, device=x.device)
+            total = _like(host, residual)
         lds, at["sum"] = _rows(total, "total", M, D), total.data_ptr()
         if residual.dtype != dtype or total.dtype != dtype:
             raise TypeError("x, residual, total and y of one dtype")
     if y is None and not i8:
-        y = host.empty((M, D), dtype=dtype, device=x.device)
+        y = _like(host, x)
     if y is not None:
         ldy, at["y"] = _rows(y, "y", M, D), y.data_ptr()
         if y.dtype != dtype:
@@ -1025,7 +1031,7 @@ def kda_glr_scan(x, log_alpha, h0=None, cu_seqlens=None, N: int | None = None, y
     if h0 is not None and h0 is not h_T:
         _expect(h0, "h0", (n_slots, D), host.f32)
     if y is None:
-        y = host.empty((T, D), dtype=dtype, device=x.device)
+        y = _like(host, x)
     else:
         _expect(y, "y", (T, D), dtype)
     if checkpoints is not None:
@@ -1059,7 +1065,7 @@ def kda_glr_step(x, log_alpha, h, y=None, *, slots=None, decay_from="log", decay
                                 input_scale, input_gate, slots, h, N)
     _expect(h, "h", (n_slots, D), host.f32)
     if y is None:
-        y = host.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(host, x)
     else:
         _expect(y, "y", x.shape, x.dtype)
     rc = host.glr_step(x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), y.data_ptr(), N, L, D,
@@ -1096,8 +1102,8 @@ def kda_glr_scan_backward(dy, dh_T, x, log_alpha, checkpoints, cu_seqlens=None,
     _expect(checkpoints, "checkpoints", (T // GLR_TILE + N, D), host.f32)
     opt.checkpoints = checkpoints.data_ptr()
     opt.max_seqlen = max_seqlen
-    dx, dla = (host.empty((T, D), dtype=dtype, device=device) for _ in range(2))
-    dgate = host.empty((T, D), dtype=dtype, device=device) if input_gate is not None else None
+    dx, dla = _like(host, x), _like(host, x)
+    dgate = _like(host, x) if input_gate is not None else None
     dh0 = host.empty((N, D), dtype=host.f32, device=device)
     dA = db = None
     if decay_from != "log":
