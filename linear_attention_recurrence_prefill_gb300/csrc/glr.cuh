@@ -18,6 +18,8 @@
 // as long as that).
 #pragma once
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "gdr.cuh"
@@ -52,6 +54,11 @@ struct GlrArgs {
   void* dgate;                // NULL: not wanted, as the ones below
   float* dh0;
   double2* partial;           // NULL, or [N][ranks][D]: the share of each CTA in dA and db
+};
+
+// Tensor maps of the arrays that kernels read in tiles (where TMA takes them).
+struct GlrMaps {
+  CUtensorMap la, x, gate, dy;
 };
 
 // ---------------------------------------------------------------- the gates
@@ -173,19 +180,19 @@ __device__ __forceinline__ float2 decay_rest(const Decay& d) {
   return fma2(both(-1.f), d.t, fma2(both(-1.f), d.k, both(1.f)));
 }
 // c of a decay, and 1 / c (0 where c is 0)
-template <bool kFast>
+template <bool kFast, bool kInverse = false>
 __device__ __forceinline__ float2 input_factor(int scale, const Decay& d, float2* inv = nullptr) {
   if (scale == KDA_GLR_INPUT_NONE) return both(1.f);
   const float2 r = decay_rest(d);
   if (scale == KDA_GLR_INPUT_COMPLEMENT) return r;
-  const float2 sq = fma2(r, both(2.f), mul2(mul2(r, both(-1.f)), r));  // (1 - a) (1 + a)
-  float2 i = make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y));
+  const float2 sq = mul2(r, fma2(r, both(-1.f), both(2.f)));  // (1 - a) (1 + a)
+  // (the bound keeps 0 times infinity out; a NaN is still one of sq)
+  float2 i = make_float2(rsqrt_approx(fmaxf(sq.x, 0x1p-126f)), rsqrt_approx(fmaxf(sq.y, 0x1p-126f)));
   if constexpr (!kFast) {  // one step of Newton's for the instruction's 2^-22
     const float2 e = fma2(mul2(mul2(sq, i), i), both(-0.5f), both(0.5f));
     i = fma2(i, e, i);
   }
-  i = make_float2(sq.x > 0x1p-126f ? i.x : sq.x * 0.f, sq.y > 0x1p-126f ? i.y : sq.y * 0.f);  // NaN stays
-  if (inv) *inv = i;
+  if constexpr (kInverse) *inv = make_float2(sq.x > 0x1p-126f ? i.x : 0.f, sq.y > 0x1p-126f ? i.y : 0.f);
   return mul2(sq, i);
 }
 
@@ -239,19 +246,22 @@ template <> struct GlrLane<float> {
 
 // ---------------------------------------------------------------- tiles
 // A tile of 64 tokens by 64 channels of each array on its way to, or in, shared memory: rows of
-// [token][channel], of which a warp has eight tokens and a lane two channels.  Copied in pieces of
-// kBytes bytes: 16 and 4 asynchronously, 2 (bf16 rows at odd places) through a register.
+// [token][channel], of which a warp has eight tokens and a lane two channels.  By TMA where kBytes is
+// 16 (rows and bases at 16 bytes), which leaves the threads' registers to the recurrence; else copied
+// by the threads in pieces of 4 bytes, or of 2 (bf16 rows at odd places).
 constexpr int kGlrSeg = 8, kGlrWarps = kGlrTile / kGlrSeg, kGlrThreads = kGlrWarps * 32, kGlrCols = 64;
+constexpr long long kGlrSpins = 4000000000LL;  // ~2 s of clock cycles
 
 template <typename T, int kBytes>
 struct GlrTile {
   static constexpr int kRow = kGlrCols * sizeof(T);
   static constexpr int kArray = kGlrTile * kRow;  // bytes
-  static constexpr bool kPair = kBytes == 16 || (kBytes == 4 && sizeof(T) == 2);
+  static constexpr bool kTma = kBytes == 16;
+  static constexpr bool kPair = kTma || (kBytes == 4 && sizeof(T) == 2);
 
   // Rows [0, rows) and columns [0, cols) of p (rows ld apart) to shared memory at `to`; the rest of
   // the tile gets `none` in every element.
-  static __device__ __forceinline__ void fetch(uint8_t* to, const T* p, long long ld, int rows, int cols, T none) {
+  static __device__ __forceinline__ void copy(uint8_t* to, const T* p, long long ld, int rows, int cols, T none) {
     constexpr int kPieces = kRow / kBytes, kElems = kBytes / sizeof(T), kPer = kGlrTile * kPieces / kGlrThreads;
     const int c = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
     const T* from = p + r0 * ld + c * kElems;
@@ -261,8 +271,7 @@ struct GlrTile {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (in && r0 + i * kStep < rows) {
-        if constexpr (kBytes == 16) umma::cp_async16(umma::smem_u32(dst), from, 16);
-        else if constexpr (kBytes == 4) umma::cp_async4(umma::smem_u32(dst), from);
+        if constexpr (kBytes == 4) umma::cp_async4(umma::smem_u32(dst), from);
         else *reinterpret_cast<T*>(dst) = *from;
       } else {
 #pragma unroll
@@ -270,6 +279,14 @@ struct GlrTile {
       }
       from += kStep * ld;
       dst += kStep * kRow;
+    }
+  }
+  // This thread's own elements behind the end of the sequence, of which TMA brings the next one's:
+  // `none`, from token `k0` of its segment on.
+  static __device__ __forceinline__ void clear(uint8_t* array, int warp, int lane, int k0, T none) {
+    for (int k = k0 > 0 ? k0 : 0; k < kGlrSeg; ++k) {
+      T* e = reinterpret_cast<T*>(array + (warp * kGlrSeg + k) * kRow) + 2 * lane;
+      e[0] = e[1] = none;
     }
   }
   // this thread's channels of token k of its segment
@@ -336,7 +353,6 @@ __device__ __forceinline__ void glr_input_scale(int scale, const F& f) {
 // each write counts on a barrier of the CTA that it goes to, so that nobody waits for more than
 // what it needs.  Two sets in turn: a CTA sends those of a round only behind its own reads of the
 // round before, and nobody gets to the next round without them.
-constexpr long long kGlrSpins = 4000000000LL;  // ~2 s of clock cycles
 struct GlrExchange {
   float4 tot[2][kGlrMaxRanks][32];
   uint64_t arrived[2];

@@ -9,7 +9,7 @@
 //
 // The states h_{t-1} are not read back from y, which is rounded, but scanned again inside each
 // tile of 64 tokens from the states that the forward pass saved before each.
-#include "glr.cuh"
+#include "glr_maps.cuh"
 
 namespace kda {
 namespace {
@@ -29,16 +29,18 @@ struct Sum {
 
 // As glr_scan_kernel, walking the rounds from the last to the first.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backward_kernel(GlrArgs a) {
+__global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backward_kernel(const __grid_constant__ GlrArgs a, const __grid_constant__ GlrMaps maps) {
   using G = GlrLane<T>;
   using Tile = GlrTile<T, kBytes>;
   constexpr bool kFast = G::kFast;
-  extern __shared__ __align__(16) uint8_t stages[];  // two, of four arrays: log_alpha, x, dy, gate
+  extern __shared__ uint8_t smem[];
+  uint8_t* stages = smem + ((128 - (smem_u32(smem) & 127)) & 127);  // two, of four arrays: log_alpha, x, dy, gate
   __shared__ float4 seg[2][kGlrWarps][32];           // a segment's decay (packed) and its state from zero
   __shared__ float2 seg_grad[2][kGlrWarps][32];      // what it hands back from zero: a G of its first token
   __shared__ float2 seg_log[2][32 * kGlrWarps];      // its log decay
   __shared__ float2 last[2][32];                     // what a round hands back, of a CTA alone
   __shared__ GlrExchange others;
+  __shared__ uint64_t landed[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = gridDim.z, rank = blockIdx.z;
   const int blocks = (a.D + kGlrCols - 1) / kGlrCols;
@@ -53,27 +55,47 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
   double2* partial = a.partial ? a.partial + ((size_t)n * ranks + rank) * a.D + ch : nullptr;
   const int L = t1 - t0;
   const int tiles = (L + kGlrTile - 1) / kGlrTile, rounds = (tiles + ranks - 1) / ranks;
-  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch0;
-  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch0;
-  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch0 : nullptr;
-  const T* dy = a.dy ? static_cast<const T*>(a.dy) + (size_t)t0 * a.D + ch0 : nullptr;
+  const bool gate = a.gate != nullptr, dy = a.dy != nullptr;
   const uint32_t stage = (gate ? 4 : 3) * Tile::kArray;
+  const T none = from_f32<T>(glr_no_decay(a.decay_from));
+  if (threadIdx.x == 0) {
+    others.init();
+    mbar_init(&landed[0], 1);
+    mbar_init(&landed[1], 1);
+    mbar_fence_init();
+  }
   auto fetch = [&](int round) {
-    const int first = (round * ranks + rank) * kGlrTile, rows = L - first;
+    const int first = (round * ranks + rank) * kGlrTile;
     uint8_t* to = stages + (round & 1) * stage;
-    Tile::fetch(to, la + (size_t)first * a.ldla, a.ldla, rows, cols, from_f32<T>(glr_no_decay(a.decay_from)));
-    Tile::fetch(to + Tile::kArray, x + (size_t)first * a.ldx, a.ldx, rows, cols, from_f32<T>(0.f));
-    Tile::fetch(to + 2 * Tile::kArray, dy + (size_t)first * a.D, a.D, dy ? rows : 0, cols, from_f32<T>(0.f));
-    if (gate)
-      Tile::fetch(to + 3 * Tile::kArray, gate + (size_t)first * a.ldg, a.ldg, rows, cols, from_f32<T>(0.f));
+    if constexpr (Tile::kTma) {
+      if (threadIdx.x == 0) {
+        uint64_t* bar = &landed[round & 1];
+        mbar_arrive_expect_tx(bar, dy ? stage : stage - Tile::kArray);
+        tma_load_2d(to, &maps.la, ch0, t0 + first, bar);
+        tma_load_2d(to + Tile::kArray, &maps.x, ch0, t0 + first, bar);
+        if (dy) tma_load_2d(to + 2 * Tile::kArray, &maps.dy, ch0, t0 + first, bar);
+        if (gate) tma_load_2d(to + 3 * Tile::kArray, &maps.gate, ch0, t0 + first, bar);
+      }
+    } else {
+      const int rows = L - first;
+      const size_t t = (size_t)t0 + first;
+      const T zero = from_f32<T>(0.f);
+      Tile::copy(to, static_cast<const T*>(a.la) + t * a.ldla + ch0, a.ldla, rows, cols, none);
+      Tile::copy(to + Tile::kArray, static_cast<const T*>(a.x) + t * a.ldx + ch0, a.ldx, rows, cols, zero);
+      if (dy) Tile::copy(to + 2 * Tile::kArray, static_cast<const T*>(a.dy) + t * a.D + ch0, a.D, rows, cols, zero);
+      if (gate)
+        Tile::copy(to + 3 * Tile::kArray, static_cast<const T*>(a.gate) + t * a.ldg + ch0, a.ldg, rows, cols, zero);
+      cp_async_commit();
+    }
   };
+  if (!dy)  // zeros, once
+    for (int i = 0; i < 2; ++i) Tile::clear(stages + i * stage + 2 * Tile::kArray, warp, lane, 0, from_f32<T>(0.f));
+  __syncthreads();  // the barriers are there
   if (rounds > 0) fetch(rounds - 1);
-  cp_async_commit();
   // what the tokens behind this round hand back
   float2 carry = load_states(a.dh_T && live ? a.dh_T + (size_t)n * a.D + ch : nullptr, in);
   const GlrChannels par = glr_channels(a, ch, in);
   const float2 minus_A = mul2(par.A, both(1.f / kLog2e));
-  if (threadIdx.x == 0) others.init();
   if (ranks > 1) cluster_sync();  // every CTA runs, and has its barriers
   const size_t out0 = (size_t)t0 * a.D + ch;
   T* dx = static_cast<T*>(a.dx) + out0;
@@ -86,12 +108,20 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
   for (int i = 0; i < rounds; ++i) {
     const int round = rounds - 1 - i, tile = round * ranks + rank, p = i & 1;
     const int first = tile * kGlrTile + warp * kGlrSeg;
-    const uint8_t* from = stages + (round & 1) * stage;
-    const uint8_t *from_x = from + Tile::kArray, *from_dy = from + 2 * Tile::kArray, *from_gate = from + 3 * Tile::kArray;
-    cp_async_wait_all();
-    __syncthreads();  // this tile is in shared memory, and nobody reads the one before any more
+    uint8_t* from = stages + (round & 1) * stage;
+    uint8_t *from_x = from + Tile::kArray, *from_dy = from + 2 * Tile::kArray, *from_gate = from + 3 * Tile::kArray;
+    if (!Tile::kTma) cp_async_wait_all();
+    __syncthreads();  // nobody reads the tile before any more (and this one is in shared memory)
     if (round > 0) fetch(round - 1);
-    cp_async_commit();
+    if constexpr (Tile::kTma) {
+      ok = ok && mbar_wait_soon(&landed[round & 1], (i >> 1) & 1, kGlrSpins);
+      if (first + kGlrSeg > L) {
+        Tile::clear(from, warp, lane, L - first, none);
+        Tile::clear(from_x, warp, lane, L - first, from_f32<T>(0.f));
+        Tile::clear(from_dy, warp, lane, L - first, from_f32<T>(0.f));
+        fence_proxy_async();  // the next copy to this place comes behind these writes
+      }
+    }
     float2 h = load_states(a.checkpoints + (saved + tile) * a.D + ch, tile < tiles ? in : 0);
 
     Decay d[kGlrSeg];
@@ -104,6 +134,11 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
         d[k] = decay_of<kFast>(g);
       }
     });
+    // what segment w hands back of what comes from behind it
+    auto before = [&](int w, float2 behind) {
+      const float4 s = seg[p][w][lane];
+      return decay_apply(decay_unpack(make_float2(s.x, s.y)), behind, seg_grad[p][w][lane]);
+    };
     auto input = [&](auto scale) {
 #pragma unroll
       for (int k = 0; k < kGlrSeg; ++k) {
@@ -123,8 +158,8 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
       H = decay_apply(d[k], H, u[k]);
       back = decay_apply(d[kGlrSeg - 1 - k], add2(back, Tile::get(from_dy, warp, lane, kGlrSeg - 1 - k)));
     }
-    const float2 dt = decay_pack(decay_of<kFast>(lg));
-    seg[p][warp][lane] = make_float4(dt.x, dt.y, H.x, H.y);
+    const float2 ds = decay_pack(decay_of<kFast>(lg));
+    seg[p][warp][lane] = make_float4(ds.x, ds.y, H.x, H.y);
     seg_grad[p][warp][lane] = back;
     if (ranks > 1) seg_log[p][threadIdx.x] = lg;
     __syncthreads();
@@ -133,8 +168,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
         float2 z = both(0.f), l = both(0.f);
 #pragma unroll
         for (int w = kGlrWarps - 1; w >= 0; --w) {
-          const float4 s = seg[p][w][lane];
-          z = decay_apply(decay_unpack(make_float2(s.x, s.y)), z, seg_grad[p][w][lane]);
+          z = before(w, z);
           l = add2(l, seg_log[p][w * 32 + lane]);
         }
         const float2 t = decay_pack(decay_of<kFast>(l));
@@ -155,10 +189,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
       const float4 s = seg[p][w][lane];
       h = decay_apply(decay_unpack(make_float2(s.x, s.y)), h, make_float2(s.z, s.w));
     }
-    for (int w = kGlrWarps - 1; w > warp; --w) {
-      const float4 s = seg[p][w][lane];
-      back = decay_apply(decay_unpack(make_float2(s.x, s.y)), back, seg_grad[p][w][lane]);
-    }
+    for (int w = kGlrWarps - 1; w > warp; --w) back = before(w, back);
     // the faded state before each token, in the place of its input
 #pragma unroll
     for (int k = 0; k < kGlrSeg; ++k) {
@@ -169,29 +200,30 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     float2 tA = both(0.f), tb = both(0.f);
     const size_t at = (size_t)(first + kGlrSeg - 1) * a.D;
     T *px = dx + at, *pl = dla + at, *pg = dgate ? dgate + at : nullptr;
-    glr_decay_from(a.decay_from, [&](auto form) {
+    const bool whole = first + kGlrSeg <= L;
+    auto gradients = [&](auto form, auto scale) {
 #pragma unroll
       for (int k = kGlrSeg - 1; k >= 0; --k) {
-        const int m = first + k < L ? in : 0;
+        const bool here = whole || first + k < L;
         const float2 grad = add2(Tile::get(from_dy, warp, lane, k), back), xv = Tile::get(from_x, warp, lane, k);
         back = decay_apply(d[k], grad);
-        float2 sx = xv, inv = both(0.f);
-        const float2 f = input_factor<kFast>(a.input_scale, d[k], &inv);
-        float2 ox = mul2(grad, f);
+        float2 sx = xv, inv = both(0.f), ox = grad;
+        if constexpr (scale.value != KDA_GLR_INPUT_NONE)
+          ox = mul2(grad, input_factor<kFast, scale.value == KDA_GLR_INPUT_NORMALIZED>(scale.value, d[k], &inv));
         if (gate) {
           float2 rest;
           const float2 s = sigmoid2<kFast>(Tile::get(from_gate, warp, lane, k), rest);
           ox = mul2(ox, s);
           sx = mul2(s, xv);
-          if (dgate) G::template store<Tile::kPair>(pg, mul2(mul2(ox, xv), rest), m);
+          if (dgate && here) G::template store<Tile::kPair>(pg, mul2(mul2(ox, xv), rest), in);
         }
-        G::template store<Tile::kPair>(px, ox, m);
+        if (here) G::template store<Tile::kPair>(px, ox, in);
         float2 dg = u[k];
-        if (a.input_scale != KDA_GLR_INPUT_NONE) {
+        if constexpr (scale.value != KDA_GLR_INPUT_NONE) {
           // the slope of c: -a or -a^2 / c
           const float2 av = decay_value(d[k]);
           float2 slope = mul2(av, both(-1.f));
-          if (a.input_scale == KDA_GLR_INPUT_NORMALIZED) slope = mul2(mul2(slope, av), inv);
+          if constexpr (scale.value == KDA_GLR_INPUT_NORMALIZED) slope = mul2(mul2(slope, av), inv);
           dg = fma2(slope, sx, dg);
         }
         dg = mul2(dg, grad);
@@ -212,16 +244,19 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
             val = sg;
             ol = mul2(mul2(minus_A, mul2(sg, rest)), dg);
           }
-          if (m) {
+          if (here) {
             tA = fma2(mul2(val, both(-1.f)), dg, tA);
             tb = add2(tb, ol);
           }
         }
-        G::template store<Tile::kPair>(pl, ol, m);
+        if (here) G::template store<Tile::kPair>(pl, ol, in);
         px -= a.D;
         pl -= a.D;
         pg -= a.D;
       }
+    };
+    glr_decay_from(a.decay_from, [&](auto form) {
+      glr_input_scale(a.input_scale, [&](auto scale) { gradients(form, scale); });
     });
     if (warp == 0) last[p][lane] = back;
     dA[0].add(tA.x);
@@ -283,11 +318,13 @@ template <typename T, int kBytes>
 cudaError_t launch(const GlrArgs& a, int ranks, cudaStream_t s) {
   constexpr auto kern = glr_backward_kernel<T, kBytes>;
   constexpr int kArray = GlrTile<T, kBytes>::kArray;
-  const cudaError_t e = allow_smem<kern>(8 * kArray);
+  const cudaError_t e = allow_smem<kern>(8 * kArray + 128);
   if (e != cudaSuccess) return e;
+  GlrMaps maps;
+  if (kBytes == 16 && !glr_maps<T>(maps, a)) return cudaErrorInvalidValue;
   const long long blocks = (a.D + kGlrCols - 1LL) / kGlrCols * a.N;
-  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 4 : 3) * kArray,
-                               ranks, s, a);
+  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 4 : 3) * kArray + 128, ranks, s, a,
+                      maps);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // glr_scan.cu -- the gated linear recurrence forward: token by token for a few
 // tokens per sequence, and as a scan over tiles for long sequences.
-#include "glr.cuh"
+#include "glr_maps.cuh"
 
 namespace kda {
 namespace {
@@ -56,15 +56,17 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
 // the scan once more from there.  All joins are taken in the order of the tokens, so that results
 // repeat to the bit.  The next tile's arrays are copied to shared memory meanwhile.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(GlrArgs a) {
+__global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_constant__ GlrArgs a, const __grid_constant__ GlrMaps maps) {
   using G = GlrLane<T>;
   using Tile = GlrTile<T, kBytes>;
   constexpr bool kFast = G::kFast;
-  extern __shared__ __align__(16) uint8_t stages[];  // two, of two or three arrays
+  extern __shared__ uint8_t smem[];
+  uint8_t* stages = smem + ((128 - (smem_u32(smem) & 127)) & 127);  // two, of two or three arrays
   __shared__ float4 seg[2][kGlrWarps][32];           // a segment's decay (packed) and its state from zero
   __shared__ float2 seg_log[2][32 * kGlrWarps];      // and its log decay
   __shared__ float2 last[2][32];                     // the state behind a round, of a CTA alone
   __shared__ GlrExchange others;
+  __shared__ uint64_t landed[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = gridDim.z, rank = blockIdx.z;
   const int blocks = (a.D + kGlrCols - 1) / kGlrCols;
@@ -77,29 +79,47 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(GlrArgs a) {
   if (!live) t0 = t1 = 0;
   const int in = max(0, min(2, a.D - ch)), cols = min(kGlrCols, a.D - ch0), L = t1 - t0;
   const int tiles = (L + kGlrTile - 1) / kGlrTile, rounds = (tiles + ranks - 1) / ranks;
-  const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch0;
-  const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch0;
-  const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch0 : nullptr;
+  const bool gate = a.gate != nullptr;
   const uint32_t stage = (gate ? 3 : 2) * Tile::kArray;
+  const T none = from_f32<T>(glr_no_decay(a.decay_from));
+  if (threadIdx.x == 0) {
+    others.init();
+    mbar_init(&landed[0], 1);
+    mbar_init(&landed[1], 1);
+    mbar_fence_init();
+  }
   auto fetch = [&](int round) {
-    const int first = (round * ranks + rank) * kGlrTile, rows = L - first;
+    const int first = (round * ranks + rank) * kGlrTile;
     uint8_t* to = stages + (round & 1) * stage;
-    Tile::fetch(to, la + (size_t)first * a.ldla, a.ldla, rows, cols, from_f32<T>(glr_no_decay(a.decay_from)));
-    Tile::fetch(to + Tile::kArray, x + (size_t)first * a.ldx, a.ldx, rows, cols, from_f32<T>(0.f));
-    if (gate)
-      Tile::fetch(to + 2 * Tile::kArray, gate + (size_t)first * a.ldg, a.ldg, rows, cols, from_f32<T>(0.f));
+    if constexpr (Tile::kTma) {
+      if (threadIdx.x == 0) {
+        uint64_t* bar = &landed[round & 1];
+        mbar_arrive_expect_tx(bar, stage);
+        tma_load_2d(to, &maps.la, ch0, t0 + first, bar);
+        tma_load_2d(to + Tile::kArray, &maps.x, ch0, t0 + first, bar);
+        if (gate) tma_load_2d(to + 2 * Tile::kArray, &maps.gate, ch0, t0 + first, bar);
+      }
+    } else {
+      const int rows = L - first;
+      const size_t t = (size_t)t0 + first;
+      Tile::copy(to, static_cast<const T*>(a.la) + t * a.ldla + ch0, a.ldla, rows, cols, none);
+      Tile::copy(to + Tile::kArray, static_cast<const T*>(a.x) + t * a.ldx + ch0, a.ldx, rows, cols, from_f32<T>(0.f));
+      if (gate)
+        Tile::copy(to + 2 * Tile::kArray, static_cast<const T*>(a.gate) + t * a.ldg + ch0, a.ldg, rows, cols,
+                   from_f32<T>(0.f));
+      cp_async_commit();
+    }
   };
+  __syncthreads();  // the barriers are there
   if (rounds > 0) fetch(0);
-  cp_async_commit();
   if (rounds > 1) fetch(1);
-  cp_async_commit();
+  else if (!Tile::kTma) cp_async_commit();
   // the state before this round's first tile
   float2 carry = load_states(a.h0 && live ? a.h0 + (size_t)slot * a.D + ch : nullptr, in);
   const GlrChannels par = glr_channels(a, ch, in);
-  if (threadIdx.x == 0) others.init();
-  cp_async_wait_group<1>();
+  if (!Tile::kTma) cp_async_wait_group<1>();
   if (ranks > 1) cluster_sync();  // every CTA runs, and has its first states and its barriers
-  __syncthreads();                // the first tile is in shared memory
+  if (!Tile::kTma) __syncthreads();  // the first tile is in shared memory
   T* y = static_cast<T*>(a.y) + (size_t)t0 * a.D + ch;
   const size_t saved = glr_checkpoint_row(t0, n);
   bool ok = true;
@@ -107,7 +127,14 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(GlrArgs a) {
   for (int round = 0; round < rounds; ++round) {
     const int tile = round * ranks + rank, p = round & 1;
     const int first = tile * kGlrTile + warp * kGlrSeg;
-    const uint8_t* from = stages + p * stage;
+    uint8_t* from = stages + p * stage;
+    if constexpr (Tile::kTma) {
+      ok = ok && mbar_wait_soon(&landed[p], (round >> 1) & 1, kGlrSpins);
+      if (first + kGlrSeg > L) {
+        Tile::clear(from, warp, lane, L - first, none);
+        Tile::clear(from + Tile::kArray, warp, lane, L - first, from_f32<T>(0.f));
+      }
+    }
     Decay d[kGlrSeg];
     float2 u[kGlrSeg], lg = both(0.f);
     // decays and inputs; tokens behind the end have a decay of 1 and no input
@@ -138,10 +165,9 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(GlrArgs a) {
     const float2 dt = decay_pack(decay_of<kFast>(lg));
     seg[p][warp][lane] = make_float4(dt.x, dt.y, h.x, h.y);
     if (ranks > 1) seg_log[p][threadIdx.x] = lg;
-    cp_async_wait_all();  // the next tile
+    if (!Tile::kTma) cp_async_wait_all();  // the next tile
     __syncthreads();
     if (round + 2 < rounds) fetch(round + 2);  // where this tile was
-    cp_async_commit();
     if (ranks > 1) {
       // the tile's own decay and state from zero, to every CTA of the cluster
       if (warp == 0) {
@@ -197,11 +223,13 @@ template <typename T, int kBytes>
 cudaError_t launch_scan(const GlrArgs& a, int ranks, cudaStream_t s) {
   constexpr auto kern = glr_scan_kernel<T, kBytes>;
   constexpr int kArray = GlrTile<T, kBytes>::kArray;
-  const cudaError_t e = allow_smem<kern>(6 * kArray);
+  const cudaError_t e = allow_smem<kern>(6 * kArray + 128);
   if (e != cudaSuccess) return e;
+  GlrMaps maps;
+  if (kBytes == 16 && !glr_maps<T>(maps, a)) return cudaErrorInvalidValue;
   const long long blocks = (a.D + kGlrCols - 1LL) / kGlrCols * a.N;
-  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 3 : 2) * kArray,
-                               ranks, s, a);
+  return launch_early(kern, dim3((unsigned)blocks, 1, ranks), kGlrThreads, 2 * (a.gate ? 3 : 2) * kArray + 128, ranks, s, a,
+                      maps);
 }
 
 }  // namespace
