@@ -45,12 +45,14 @@ GlrArgs glr_args(const void* x, const void* la, const int32_t* cu, int N, int T_
   return a;
 }
 
-// The bytes that rows, bases and D allow to move at once (GlrTile): 16, 4, or 2.
+// The bytes that rows, bases and D allow to move at once (GlrTile): 16 (which tensor maps take, up to
+// 2^40 bytes from row to row), 4, or 2.
 int piece(const GlrArgs& a, int dtype) {
   const int e = (int)elem(dtype);
   for (int bytes : {16, 4}) {
     const int n = bytes / e;
-    bool fits = a.D % n == 0 && a.ldx % n == 0 && a.ldla % n == 0 && (!a.gate || a.ldg % n == 0);
+    bool fits = bytes < 16 || (a.ldx < (1LL << 37) && a.ldla < (1LL << 37) && a.ldg < (1LL << 37));
+    fits = fits && a.D % n == 0 && a.ldx % n == 0 && a.ldla % n == 0 && (!a.gate || a.ldg % n == 0);
     for (const void* p : {a.x, a.la, a.gate, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dla,
                           (const void*)a.dgate})
       fits = fits && aligned(p, bytes);

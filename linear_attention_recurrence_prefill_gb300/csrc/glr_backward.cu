@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     const int first = (round * ranks + rank) * kGlrTile;
     uint8_t* to = stages + (round & 1) * stage;
     if constexpr (Tile::kTma) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == kGlrThreads - 32) {  // (warp 0 has the tile's total to send)
         uint64_t* bar = &landed[round & 1];
         mbar_arrive_expect_tx(bar, dy ? stage : stage - Tile::kArray);
         tma_load_2d(to, &maps.la, ch0, t0 + first, bar);

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(Norm<T, kThreads, kI8>::kCta, Norm<T, kThreads
       const bool again = live && o.inv != 0.f && !(far < 0.5f - o.middle);
       const bool any = kWarps > 1 ? __syncthreads_or(again) : __any_sync(0xffffffffu, again);
       if (any) {
+        if (kWarps == 1) __syncwarp();  // `largest` is zero for every lane
         if (live && __uint_as_float(mine) >= next_to(big)) {
 #pragma unroll
           for (int v = 0; v < kVecs; ++v) {
