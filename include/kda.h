@@ -454,7 +454,7 @@ int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const in
                   long long ldr, void* y, long long ldy, int M, int N, int K, int act, int dtype,
                   void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
-/* Bytes of device workspace kda_linear_i8 needs on the current device. */
+/* Bytes of device workspace kda_linear_i8 needs for these sizes, whatever the alignment. */
 size_t kda_linear_i8_workspace_size(int M, int N, int K);
 
 /*

@@ -85,6 +85,23 @@ int glr_ranks(int T_total, int N, int D, int dtype, int max_seqlen) {
   return best;
 }
 
+// Whether the sequences are walked token by token, a thread per two channels: fastest where they
+// are short and so many that they fill the GPU by themselves.  In units of 10 ns, fitted to what
+// 4096 channels took: a token 0.25 us and the time of its share, a tile 3.5 us in waves as above.
+// Measured this way and in tiles, bf16, us: 1 sequence of 4, 16, 64 tokens 2.9, 6.2, 19 and 3.7 each; 32
+// of them 3.7, 7.5, 32 and 24 each; 256 of them 11, 41, 146 and 173, 188, 191, of 200 tokens 445
+// and 491, of 1000 tokens 2196 and 1700.
+bool glr_by_token(int T_total, int N, int D, int dtype, int max_seqlen) {
+  const long long longest = max_seqlen > 0 ? max_seqlen : T_total;
+  if (longest > 256) return false;
+  const long long tiles = (longest + kGlrTile - 1) / kGlrTile, blocks = (D + 63LL) / 64;
+  const long long slots = (dtype == KDA_BF16 ? 2LL : 1LL) * sm_count();
+  const long long ranks = glr_ranks(T_total, N, D, dtype, max_seqlen);
+  const double by_token = 200. + 25. * longest + (double)T_total * blocks / 60;
+  const double all = ((double)T_total / kGlrTile + N / 2.) * blocks / slots, one = (double)(tiles + ranks - 1) / ranks;
+  return by_token < 350. * (all > one ? all : one);
+}
+
 }  // namespace
 
 extern "C" {
@@ -117,10 +134,10 @@ int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const in
   GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
   a.h0 = h0; a.h_T = h_T; a.y = y;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int longest = o->max_seqlen > 0 ? o->max_seqlen : T_total;
   const cudaError_t e =
-      longest <= 16 ? launch_glr_few(a, dtype, piece(a, dtype), s)
-                    : launch_glr_scan(a, dtype, piece(a, dtype), glr_ranks(T_total, N, D, dtype, o->max_seqlen), s);
+      glr_by_token(T_total, N, D, dtype, o->max_seqlen)
+          ? launch_glr_few(a, dtype, piece(a, dtype), s)
+          : launch_glr_scan(a, dtype, piece(a, dtype), glr_ranks(T_total, N, D, dtype, o->max_seqlen), s);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

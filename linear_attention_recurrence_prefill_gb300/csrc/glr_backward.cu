@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from_x, warp, lane, L - first, from_f32<T>(0.f));
         Tile::clear(from_dy, warp, lane, L - first, from_f32<T>(0.f));
+        if (gate) Tile::clear(from_gate, warp, lane, L - first, from_f32<T>(0.f));
         fence_proxy_async();  // the next copy to this place comes behind these writes
       }
     }

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_c
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from + Tile::kArray, warp, lane, L - first, from_f32<T>(0.f));
+        if (gate) Tile::clear(from + 2 * Tile::kArray, warp, lane, L - first, from_f32<T>(0.f));
       }
     }
     Decay d[kGlrSeg];

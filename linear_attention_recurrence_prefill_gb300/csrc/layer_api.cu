@@ -217,7 +217,7 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
 
 size_t kda_linear_i8_workspace_size(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return 0;
-  return linear_i8_workspace_bytes(M, N, K, sm_count());
+  return linear_i8_workspace_bytes(M, N, K);
 }
 
 int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w,

@@ -422,16 +422,19 @@ cudaError_t launch(const LinearI8Args& a, int dtype, int* status, int split, cud
                           : launch_of<BN, kTma, __nv_bfloat16>(a, status, split, s);
 }
 
-// Whether both arrays are widened first: where pairs of CTAs have tiles for half of the SMs at least.
-bool widened(int M, int N, int sms) { return (N + 255LL) / 256 * ((M + 127LL) / 128) >= sms / 4; }
+// Whether both arrays are widened first.  That costs by M + N and pays by M N: with rows and bases at
+// 16 bytes from M N / (M + N) = 544 on (4096 channels of 4096 columns, 512 and 640 tokens: 37.5 and 40.3 us
+// this way, 29.3 and 46.6 otherwise; 12288 channels, 256 and 512 tokens: 64 and 81, 48 and 85), else from
+// 128 on (4096 channels of 4095 columns, 128 and 192 tokens: 36.8 and 37.0, 33.5 and 56.8).
+bool widened(long long M, long long N, bool tma) { return M * N >= (tma ? 544 : 128) * (M + N); }
 long long padded(int K) { return (K + 15LL) / 16 * 16; }
 
 }  // namespace
 
 bool linear_i8_tc_takes(int M, int N) { return (N + 127LL) / 128 * ((M + 15LL) / 16) <= 0x7fffffffLL; }
 
-size_t linear_i8_workspace_bytes(int M, int N, int K, int sms) {
-  return K > 0 && widened(M, N, sms) ? ((size_t)M + N) * padded(K) * 2 : 0;
+size_t linear_i8_workspace_bytes(int M, int N, int K) {
+  return K > 0 && widened(M, N, false) ? ((size_t)M + N) * padded(K) * 2 : 0;
 }
 
 cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s) {
@@ -444,7 +447,8 @@ cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t
 cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspace, int sms, int* status,
                                 cudaStream_t s) {
   const LinearArgs& l = a.l;
-  if (widened(l.M, l.N, sms)) {
+  const bool tma = tma_takes(l);
+  if (widened(l.M, l.N, tma)) {
     const long long Kp = padded(l.K), blocks = ((long long)l.M + l.N + 1) / 2, most = 8LL * sms;
     const cudaError_t e = launch_early(
         widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 1, s, static_cast<const int8_t*>(l.x),
@@ -458,8 +462,7 @@ cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspac
     return launch_linear_i8_pair(h, dtype, sms, status, s);
   }
   // K split over the CTAs of a cluster until there are two CTAs per SM.  Tiles of 64 tokens at most
-  // where threads copy the integers, so that two CTAs fit on an SM.
-  const bool tma = tma_takes(l);
+  // where threads read the integers where they are.
   const int k_blocks = (l.K + 63) / 64;
   const int bn = l.M <= 16 ? 16 : l.M <= 32 ? 32 : l.M <= 64 || !tma ? 64 : 128;
   const long long tiles = (l.N + 127LL) / 128 * ((l.M + bn - 1LL) / bn);

@@ -559,3 +559,67 @@ def test_tokens_past_two_to_the_31():
     want = glr64.backward(f, None, [300], y[-300:, cols], None)
     check(got[0][-300:, cols], *want["dx"])
     check(got[1][-300:, cols], *want["dla"])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 50])
+def test_neighbours_of_a_sequence_do_not_reach_it(dtype, D):
+    """NaN in the rows before and behind a sequence that ends inside a tile, and behind the last one."""
+    T = 150
+    x, la, form = make(3 * T + 9, D, dtype, "sigmoid", "normalized", True)
+    cu = torch.tensor([0, T, 2 * T, 3 * T], dtype=torch.int32, device="cuda")
+    dy = states(3 * T + 9, D).to(dtype)
+
+    def run():
+        y, h, saved = kda.kda_glr_scan(x, la, None, cu, checkpoints=True, **form)
+        return y, h, kda.kda_glr_scan_backward(dy, None, x, la, saved, cu, **form)
+
+    y0, h0, g0 = run()
+    for t in (x, la, form["input_gate"], dy):
+        t[:T] = float("nan")
+        t[2 * T:] = float("nan")
+    y, h, g = run()
+    middle = slice(T, 2 * T)
+    assert torch.equal(y[middle], y0[middle]) and torch.equal(h[1], h0[1])
+    assert all(torch.equal(a[middle], b[middle]) for a, b in zip(g[:3], g0[:3])) and torch.equal(g[3][1], g0[3][1])
+
+
+@gpu
+def test_many_sequences_and_slots():
+    """More sequences than a warp has lanes, of no, one and more tokens, states in a pool."""
+    lens = [(7 * i) % 5 for i in range(100)] + [90, 0, 300]
+    N, T, D = len(lens), sum(lens), 72
+    x, la, form = make(T, D, BF16, "softplus", "none", True, seed=2)
+    g = torch.Generator().manual_seed(1)
+    slots = torch.randperm(N + 5, generator=g)[:N].to(torch.int32).cuda()
+    pool = states(N + 5, D)
+    was = pool.clone()
+    first = was[slots.long()]
+    y, _ = kda.kda_glr_scan(x, la, pool, offsets(lens), h_T=pool, slots=slots, max_seqlen=300, **form)
+    ref = glr64.scan(glr64.Form(x, la, **form), first, lens)
+    check(y, ref[0], ref[2])
+    check(pool[slots.long()], ref[1], ref[3])
+    rest = [i for i in range(N + 5) if i not in slots.tolist()]
+    assert torch.equal(pool[rest], was[rest])
+
+
+@gpu
+@pytest.mark.parametrize("N, L", [(300, 5), (300, 70), (40, 200)])
+def test_by_token_and_in_tiles_agree(N, L):
+    """Many sequences are walked token by token; one of them alone is taken in tiles where it is long."""
+    D = 4096
+    x, la, form = make(N * L, D, BF16, "sigmoid", "normalized", False, seed=4)
+    y, h, saved = kda.kda_glr_scan(x, la, None, None, N, checkpoints=True, **form)
+    cols = slice(0, None, 61)
+    for n in (0, N - 1):
+        rows = slice(n * L, (n + 1) * L)
+        part = {k: v[cols] if k.startswith("decay_") and torch.is_tensor(v) else v for k, v in form.items()}
+        ref = glr64.scan(glr64.Form(x[rows, cols], la[rows, cols], **part), None, [L])
+        check(y[rows, cols], ref[0], ref[2])
+        check(h[n:n + 1, cols], ref[1], ref[3])
+    dy = states(N * L, D).to(BF16)
+    got = kda.kda_glr_scan_backward(dy, None, x, la, saved, None, N, **form)
+    want = glr64.backward(glr64.Form(x[rows, cols], la[rows, cols], **part), None, [L], dy[rows, cols], None)
+    check(got[0][rows, cols], *want["dx"])
+    check(got[1][rows, cols], *want["dla"])

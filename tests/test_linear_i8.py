@@ -295,3 +295,26 @@ def test_layer_prefill_then_decode():
         assert torch.equal(total.cpu().double(), s)
         assert plain64.rel(pool[slots.long()], h) <= 2.0 ** -7
     assert kda.kda_get_last_error() == kda.KDA_OK
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 6, 7, 8, 9])
+@pytest.mark.parametrize("K, N", [(16, 3), (1040, 67), (4100, 130), (131088, 5)])
+def test_few_rows(M, K, N):
+    """Each number of rows that is taken as a stream of w, and the next; K beyond a 32-bit sum."""
+    a = make(M, K, N, F32, seed=M)
+    check(kda.kda_linear_i8(*a, act="silu"), *plain(*a, "silu"))
+
+
+@gpu
+@pytest.mark.parametrize("M, K, N", [(640, 512, 4096), (700, 100, 5000), (130, 77, 9000), (3000, 1, 700), (200, 4095, 400)])
+def test_widened_first(M, K, N):
+    """Sizes whose integers are widened into the workspace, with one that is given and holds NaN."""
+    a = make(M, K, N, F32, seed=3)
+    need = kda.load().kda_linear_i8_workspace_size(M, N, K)
+    assert need > 0
+    ws = torch.full((need // 4 + 4,), float("nan"), device="cuda")
+    y = kda.kda_linear_i8(*a, workspace=ws)
+    check(y, *plain(*a))
+    with pytest.raises(kda.KdaError):
+        kda.kda_linear_i8(*a, workspace=ws[:need // 8])
