@@ -425,8 +425,12 @@ cudaError_t launch(const LinearI8Args& a, int dtype, int* status, int split, cud
 // Whether both arrays are widened first.  That costs by M + N and pays by M N: with rows and bases at
 // 16 bytes from M N / (M + N) = 544 on (4096 channels of 4096 columns, 512 and 640 tokens: 37.5 and 40.3 us
 // this way, 29.3 and 46.6 otherwise; 12288 channels, 256 and 512 tokens: 64 and 81, 48 and 85), else from
-// 128 on (4096 channels of 4095 columns, 128 and 192 tokens: 36.8 and 37.0, 33.5 and 56.8).
-bool widened(long long M, long long N, bool tma) { return M * N >= (tma ? 544 : 128) * (M + N); }
+// 128 on (4096 channels of 4095 columns, 128 and 192 tokens: 36.8 and 37.0, 33.5 and 56.8), but where
+// there are few columns, which are soon read, from 320 on (1499 channels of 1000 columns, 333 tokens: 18.1
+// and 17.8, with a launch more; 1001 channels of 1001, 500 tokens: 15.0 and 16.8).
+bool widened(long long M, long long N, int K, bool tma) {
+  return M * N >= (tma ? 544 : K >= 2048 ? 128 : 320) * (M + N);
+}
 long long padded(int K) { return (K + 15LL) / 16 * 16; }
 
 }  // namespace
@@ -434,7 +438,7 @@ long long padded(int K) { return (K + 15LL) / 16 * 16; }
 bool linear_i8_tc_takes(int M, int N) { return (N + 127LL) / 128 * ((M + 15LL) / 16) <= 0x7fffffffLL; }
 
 size_t linear_i8_workspace_bytes(int M, int N, int K) {
-  return K > 0 && widened(M, N, false) ? ((size_t)M + N) * padded(K) * 2 : 0;
+  return K > 0 && widened(M, N, K, false) ? ((size_t)M + N) * padded(K) * 2 : 0;
 }
 
 cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s) {
@@ -448,7 +452,7 @@ cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspac
                                 cudaStream_t s) {
   const LinearArgs& l = a.l;
   const bool tma = tma_takes(l);
-  if (widened(l.M, l.N, tma)) {
+  if (widened(l.M, l.N, l.K, tma)) {
     const long long Kp = padded(l.K), blocks = ((long long)l.M + l.N + 1) / 2, most = 8LL * sms;
     const cudaError_t e = launch_early(
         widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 1, s, static_cast<const int8_t*>(l.x),

@@ -9,9 +9,9 @@
 // reduction over the row, which stays in registers between that and the outputs: each
 // array is read once and written once, and HBM is the bound.  q is the integer nearest to
 // the quotient without rounding errors: the fp32 quotient is off by at most five
-// roundings, 127.5 * 5 * 2^-24 = 3.8e-5, so only those within 4e-5 of the middle between two
-// integers (one in 12,000) are taken again in 64 bits, with the largest product, from the
-// stored inputs.
+// roundings, 5 * 2^-24 = 3.0e-7 of itself, so only those that are nearer than 3.2e-7 of
+// themselves to the middle between two integers (one in 50,000 of normally distributed ones) are taken
+// again in 64 bits, with the largest product, from the stored inputs.
 #pragma once
 
 #include "norm.cuh"
@@ -20,7 +20,7 @@
 namespace kda {
 namespace {
 
-constexpr float kMiddle = 4e-5f;
+constexpr float kMiddle = 3.2e-7f;
 
 template <typename T>
 __device__ __forceinline__ double exact_product(const NormArgs& a, long long m, int d) {
@@ -36,7 +36,7 @@ __device__ __noinline__ int quantized_exactly(double product, double largest) {
 // What a row's threads know after the reductions.
 struct Row {
   float r, scale, inv;  // inv = 127 / largest
-  float middle;  // how near to the middle is too near; 1 where 127 / largest may overflow: every quotient
+  float always;  // 1 where 127 / largest may overflow: every quotient is taken again
 };
 __device__ __forceinline__ Row row_of(const NormArgs& a, float squares, uint32_t largest_bits) {
   Row o;
@@ -47,7 +47,7 @@ __device__ __forceinline__ Row row_of(const NormArgs& a, float squares, uint32_t
   o.scale = finite ? big * (1.f / 127.f) * o.r : big * o.r;
   if (finite && big < 0x1p-100f) o.scale = (float)((double)big * (double)o.r / 127.);
   o.inv = finite && big > 0.f ? 127.f / big : 0.f;
-  o.middle = finite && big > 0.f && big < 0x1p-100f ? 1.f : kMiddle;
+  o.always = finite && big > 0.f && big < 0x1p-100f ? 1.f : 0.f;
   return o;
 }
 // What the products are that may be the largest in 64 bits.
@@ -62,7 +62,8 @@ template <typename T>
 __device__ __forceinline__ int quantized(const NormArgs& a, const Row& o, double largest, float p, long long m, int d) {
   if (o.inv == 0.f) return 0;
   const float v = p * o.inv, k = rintf(v);
-  return !(fabsf(v - k) < 0.5f - o.middle) ? quantized_exactly(exact_product<T>(a, m, d), largest) : (int)k;
+  return !(fabsf(v - k) + kMiddle * fabsf(v) < 0.5f - o.always) ? quantized_exactly(exact_product<T>(a, m, d), largest)
+                                                                : (int)k;
 }
 
 // Rows in registers: kThreads threads per row, each kVecs vectors of eight elements, one in every
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(Norm<T, kThreads, kI8>::kCta, Norm<T, kThreads
       constexpr float kMagic = 12582912.f;
       uint32_t k[kVecs][8];
       float far = 0.f;
+      const float middle = o.inv * kMiddle;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
         float w[8];
@@ -214,10 +216,10 @@ __global__ void __launch_bounds__(Norm<T, kThreads, kI8>::kCta, Norm<T, kThreads
         for (int e = 0; e < 8; ++e) {
           const float z = s[v][e] * w[e], t = fmaf(z, o.inv, kMagic);
           k[v][e] = __float_as_uint(t);
-          far = fmaxf(far, fabsf(fmaf(z, o.inv, kMagic - t)));
+          far = fmaxf(far, fabsf(fmaf(z, o.inv, kMagic - t)) + fabsf(z * middle));
         }
       }
-      const bool again = live && o.inv != 0.f && !(far < 0.5f - o.middle);
+      const bool again = live && o.inv != 0.f && !(far < 0.5f - o.always);
       const bool any = kWarps > 1 ? __syncthreads_or(again) : __any_sync(0xffffffffu, again);
       if (any) {
         if (kWarps == 1) __syncwarp();  // `largest` is zero for every lane

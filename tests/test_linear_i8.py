@@ -307,7 +307,7 @@ def test_few_rows(M, K, N):
 
 
 @gpu
-@pytest.mark.parametrize("M, K, N", [(640, 512, 4096), (700, 100, 5000), (130, 77, 9000), (3000, 1, 700), (200, 4095, 400)])
+@pytest.mark.parametrize("M, K, N", [(640, 512, 4096), (700, 100, 5000), (330, 77, 19000), (3000, 1, 700), (400, 4095, 200)])
 def test_widened_first(M, K, N):
     """Sizes whose integers are widened into the workspace, with one that is given and holds NaN."""
     a = make(M, K, N, F32, seed=3)
