@@ -13,9 +13,9 @@
 // were 2.7e-5 of their size off with a itself.)
 //
 // A thread has two neighbouring channels, and two numbers per instruction wherever
-// there is one (packed.cuh): the kernels are bound by the instructions issued, not
-// by memory, unless an element takes fewer than about 40 (its 8 bytes in bf16 take HBM
-// as long as that).
+// there is one (packed.cuh): an element takes 44 instructions forward and 102 backward (with
+// the input gate; 110 and 251 one number at a time), while HBM brings its 8 and 14 bytes in the
+// time of some 40 and 75 at the best rate.
 #pragma once
 
 #include <cuda.h>

@@ -55,6 +55,13 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
 // of this round (distributed shared memory) and from the tile's other segments (shared memory), and
 // the scan once more from there.  All joins are taken in the order of the tokens, so that results
 // repeat to the bit.  The next tile's arrays are copied to shared memory meanwhile.
+//
+// 32,768 x 4096 in bf16 (softplus): 297 us, 0.40 of the time that its bytes take; 12,000 tokens in nine
+// prompts with an input gate 105 us (0.55).  Bound by the latency of a round, 2.3 us: two CTAs of 128
+// registers a thread per SM, 3.3 warps per scheduler, which issue in half of the cycles, and 24 SMs
+// without a CTA where 64 clusters of four fill 128.  Three CTAs of 80 registers took 419 us (they
+// load their constants again and again), one per SM 405; the clusters' barrier instead of counted
+// writes 367.
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_constant__ GlrArgs a, const __grid_constant__ GlrMaps maps) {
   using G = GlrLane<T>;

@@ -17,7 +17,9 @@
 //    PFLOP/s, 0.89 to 0.92 of the measured bf16 rate (with bias, GELU and residual 251 to 262 us;
 //    the library's plain product 208 us); 8192^3: 571 us (the library's 542).  The
 //    tensor pipe is active in 79 % of the cycles of the former; the rest is 768 tiles in waves of 76,
-//    the last one of eight tiles.
+//    the last one of eight tiles.  It also takes operands in fp16 that hold 8-bit integers, whose scales
+//    the epilogue applies (those of the tokens from shared memory: from global memory it was the epilogue
+//    that bound the product, 340 us).
 //  * linear_split_kernel, where there are too few tiles to fill the GPU (few tokens, or a small
 //    product): the CTAs of a cluster share one tile, each takes a part of K, and the partial sums
 //    meet in distributed shared memory, added in the order of the ranks, so that results repeat

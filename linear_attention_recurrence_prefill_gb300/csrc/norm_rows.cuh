@@ -12,6 +12,11 @@
 // roundings, 5 * 2^-24 = 3.0e-7 of itself, so only those that are nearer than 3.2e-7 of
 // themselves to the middle between two integers (one in 50,000 of normally distributed ones) are taken
 // again in 64 bits, with the largest product, from the stored inputs.
+//
+// 12,001 x 4096 in bf16 with the residual: 65 us (6.0 TB/s, 0.89 of the measured copy rate), 82 us with one
+// row at a time; in 8 bits 90 us (0.56), bound by the barriers and instructions of forming the integers.  One
+// row of 4096: 3.0 us.  Rows that are no multiple of 8 elements, or not at 16 bytes, go element by
+// element: 3000 x 8191 89 us (0.32).
 #pragma once
 
 #include "norm.cuh"
