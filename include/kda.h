@@ -515,10 +515,9 @@ void kda_glr_options_init(kda_glr_options* opt);
  *   y             [T_total][D] dtype out
  *   h_T           as h0, final states out (may be h0)
  *
- * opt NULL: the defaults.  Pointers need the alignment of their elements (bf16 arrays
- * are read fastest with an even D, even strides and 4-byte alignment).  y, h_T and the
- * checkpoints overlap no input and not each other, but h_T may be h0 (KDA_ERR_ARG
- * where two start at one address).
+ * opt NULL: the defaults.  Pointers need the alignment of their elements (fastest where D,
+ * strides and addresses are multiples of 16 bytes).  y, h_T and the checkpoints overlap no
+ * input and not each other, but h_T may be h0 (KDA_ERR_ARG where two start at one address).
  */
 int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const int32_t* cu_seqlens,
                  int N, void* y, float* h_T, int T_total, int D, int dtype,

@@ -9,22 +9,79 @@ using namespace umma;
 
 constexpr int kFewThreads = 128;
 
-// A thread per two channels of a sequence walks its tokens.  Bound by the states and the token
-// arrays where there are many sequences, by latency where not.
-template <typename T, bool kPair>
+// kPairs pairs of neighbouring channels of a thread: 16 bytes of a token and of a state at once where
+// there is more than one, else as in GlrLane.
+template <typename T, int kPairs, bool kPair>
+struct Wide {
+  static __device__ __forceinline__ void load(float2 (&v)[kPairs], const T* p, int n) {
+    if constexpr (kPairs == 1) {
+      v[0] = GlrLane<T>::template load<kPair>(p, n);
+    } else {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+      if constexpr (sizeof(T) == 2) {
+        v[0] = GlrLane<T>::widen(q.x); v[1] = GlrLane<T>::widen(q.y);
+        v[2] = GlrLane<T>::widen(q.z); v[3] = GlrLane<T>::widen(q.w);
+      } else {
+        v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float2 (&v)[kPairs], int n) {
+    if constexpr (kPairs == 1) {
+      GlrLane<T>::template store<kPair>(p, v[0], n);
+    } else if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf162(v[0].x, v[0].y), pack_bf162(v[1].x, v[1].y),
+                                                pack_bf162(v[2].x, v[2].y), pack_bf162(v[3].x, v[3].y));
+    } else {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+  }
+  static __device__ __forceinline__ void load_states(float2 (&v)[kPairs], const float* p, int n, float none) {
+    if constexpr (kPairs == 1) {
+      v[0] = p ? kda::load_states(p, n) : both(none);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; i += 2) {
+        const float4 q = p ? *reinterpret_cast<const float4*>(p + 2 * i) : make_float4(none, none, none, none);
+        v[i] = make_float2(q.x, q.y);
+        v[i + 1] = make_float2(q.z, q.w);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store_states(float* p, const float2 (&v)[kPairs], int n) {
+    if constexpr (kPairs == 1) {
+      kda::store_states(p, v[0], n);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; i += 2)
+        *reinterpret_cast<float4*>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+    }
+  }
+};
+
+// A thread per one to four pairs of channels of a sequence walks its tokens.  Bound by the states and
+// the token arrays where there are many sequences, by latency where not.
+template <typename T, int kPairs, bool kPair>
 __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
-  using G = GlrLane<T>;
-  const int blocks = (a.D + 2 * kFewThreads - 1) / (2 * kFewThreads);
+  using W = Wide<T, kPairs, kPair>;
+  constexpr bool kFast = GlrLane<T>::kFast;
+  constexpr int kCh = 2 * kPairs;
+  const int blocks = (a.D + kFewThreads * kCh - 1) / (kFewThreads * kCh);
   const int n = blockIdx.x / blocks;
-  const int ch = (blockIdx.x % blocks * kFewThreads + (int)threadIdx.x) * 2;
+  const int ch = (blockIdx.x % blocks * kFewThreads + (int)threadIdx.x) * kCh;
   grid_launch_dependents();
   grid_wait_prerequisites();  // what ran before is complete
   int t0, t1, slot;
   if (!gdr_sequence(a, n, t0, t1, slot)) return;
-  const int in = min(2, a.D - ch);  // this thread's channels
+  const int in = min(kCh, a.D - ch);  // this thread's channels
   if (in <= 0) return;
-  float2 h = load_states(a.h0 ? a.h0 + (size_t)slot * a.D + ch : nullptr, in);
-  const GlrChannels par = glr_channels(a, ch, in);
+  float2 h[kPairs], A[kPairs], b[kPairs];
+  W::load_states(h, a.h0 ? a.h0 + (size_t)slot * a.D + ch : nullptr, in, 0.f);
+  W::load_states(A, a.decay_scale ? a.decay_scale + ch : nullptr, in, 1.f);
+  W::load_states(b, a.decay_bias ? a.decay_bias + ch : nullptr, in, 0.f);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) A[i] = mul2(A[i], both(-kLog2e));
   const T* x = static_cast<const T*>(a.x) + (size_t)t0 * a.ldx + ch;
   const T* la = static_cast<const T*>(a.la) + (size_t)t0 * a.ldla + ch;
   const T* gate = a.gate ? static_cast<const T*>(a.gate) + (size_t)t0 * a.ldg + ch : nullptr;
@@ -32,21 +89,26 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
   size_t saved = glr_checkpoint_row(t0, n);
   glr_decay_from(a.decay_from, [&](auto from) {
     for (int t = 0; t < t1 - t0; ++t) {
-      if (a.checkpoints && t % kGlrTile == 0) store_states(a.checkpoints + saved++ * a.D + ch, h, in);
-      const float2 xv = G::template load<kPair>(x, in);
-      const float2 lv = G::template load<kPair>(la, in);
-      const Decay d = decay_of<G::kFast>(glr_log_decay<from.value, G::kFast>(par, lv));
-      float2 u = mul2(input_factor<G::kFast>(a.input_scale, d), xv);
-      if (gate) u = mul2(u, sigmoid2<G::kFast>(G::template load<kPair>(gate, in)));
-      h = decay_apply(d, h, u);
-      G::template store<kPair>(y, h, in);
+      if (a.checkpoints && t % kGlrTile == 0) W::store_states(a.checkpoints + saved++ * a.D + ch, h, in);
+      float2 xv[kPairs], lv[kPairs], gv[kPairs];
+      W::load(xv, x, in);
+      W::load(lv, la, in);
+      if (gate) W::load(gv, gate, in);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const Decay d = decay_of<kFast>(glr_log_decay<from.value, kFast>(GlrChannels{A[i], b[i]}, lv[i]));
+        float2 u = mul2(input_factor<kFast>(a.input_scale, d), xv[i]);
+        if (gate) u = mul2(u, sigmoid2<kFast>(gv[i]));
+        h[i] = decay_apply(d, h[i], u);
+      }
+      W::store(y, h, in);
       x += a.ldx;
       la += a.ldla;
       if (gate) gate += a.ldg;
       y += a.D;
     }
   });
-  store_states(a.h_T + (size_t)slot * a.D + ch, h, in);
+  W::store_states(a.h_T + (size_t)slot * a.D + ch, h, in);
 }
 
 // One CTA, or a cluster of them, per sequence and 64 channels.  A tile of 64 tokens has a segment
@@ -222,10 +284,11 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_c
     store_states(a.h_T + (size_t)slot * a.D + ch, ranks > 1 || rounds == 0 ? carry : last[(rounds - 1) & 1][lane], in);
 }
 
-template <typename T, int kBytes>
+template <typename T, int kPairs, bool kPair>
 cudaError_t launch_few(const GlrArgs& a, cudaStream_t s) {
-  const long long blocks = (a.D + 2LL * kFewThreads - 1) / (2 * kFewThreads) * a.N;
-  return launch_early(glr_few_kernel<T, GlrTile<T, kBytes>::kPair>, dim3((unsigned)blocks), kFewThreads, 0, 1, s, a);
+  constexpr int per = 2 * kPairs * kFewThreads;
+  const long long blocks = (a.D + (long long)per - 1) / per * a.N;
+  return launch_early(glr_few_kernel<T, kPairs, kPair>, dim3((unsigned)blocks), kFewThreads, 0, 1, s, a);
 }
 template <typename T, int kBytes>
 cudaError_t launch_scan(const GlrArgs& a, int ranks, cudaStream_t s) {
@@ -243,8 +306,17 @@ cudaError_t launch_scan(const GlrArgs& a, int ranks, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_glr_few(const GlrArgs& a, int dtype, int bytes, cudaStream_t s) {
-  if (dtype == KDA_F32) return bytes == 16 ? launch_few<float, 16>(a, s) : launch_few<float, 4>(a, s);
-  return bytes >= 4 ? launch_few<__nv_bfloat16, 4>(a, s) : launch_few<__nv_bfloat16, 2>(a, s);
+  // 16 bytes per thread where there are few tokens or threads enough all the same (32 sequences x 4096
+  // channels, 1 and 16 tokens: 2.5 and 10.7 us so, 2.9 and 7.5 with 4 bytes; 256 sequences: 4.6 and 39.7, 7.0 and
+  // 40.8)
+  bool wide = bytes == 16 && (a.T_total <= 4LL * a.N || (long long)a.N * a.D >= 524288);
+  for (const void* p : {(const void*)a.h0, (const void*)a.h_T, (const void*)a.decay_scale, (const void*)a.decay_bias,
+                        (const void*)a.checkpoints})
+    wide = wide && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  if (dtype == KDA_F32) return wide ? launch_few<float, 2, true>(a, s) : launch_few<float, 1, false>(a, s);
+  return wide         ? launch_few<__nv_bfloat16, 4, true>(a, s)
+         : bytes >= 4 ? launch_few<__nv_bfloat16, 1, true>(a, s)
+                      : launch_few<__nv_bfloat16, 1, false>(a, s);
 }
 cudaError_t launch_glr_scan(const GlrArgs& a, int dtype, int bytes, int ranks, cudaStream_t s) {
   if (dtype == KDA_F32)

@@ -623,3 +623,51 @@ def test_by_token_and_in_tiles_agree(N, L):
     want = glr64.backward(glr64.Form(x[rows, cols], la[rows, cols], **part), None, [L], dy[rows, cols], None)
     check(got[0][rows, cols], *want["dx"])
     check(got[1][rows, cols], *want["dla"])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_tokens(dtype):
+    """Sequences without tokens hand their states, and the gradients of those, on."""
+    D = 24
+    x, la, form = make(0, D, dtype, "sigmoid", "none", True)
+    h0 = states(3, D)
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for offs in (cu, None):
+        y, h, saved = kda.kda_glr_scan(x, la, h0, offs, 3, checkpoints=True, **form)
+        assert y.shape == (0, D) and torch.equal(h, h0)
+        got = kda.kda_glr_scan_backward(None, h, x, la, saved, offs, 3, **form)
+        assert torch.equal(got[3], h) and (got[4] == 0).all() and (got[5] == 0).all()
+    pool = states(5, D, 3)
+    was = pool.clone()
+    kda.kda_glr_scan(x, la, pool, cu, h_T=pool, slots=torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda"), **form)
+    assert torch.equal(pool, was) and kda.kda_get_last_error() == kda.KDA_OK
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [8, 1000, 1032, 4096])
+@pytest.mark.parametrize("off", [0, 1, 2])
+def test_states_at_any_place(dtype, D, off):
+    """States, parameters and saved states at 16 bytes and not, in a step and in a few tokens each."""
+    N, L = 40, 3
+    x, la, form = make(N * L, D, dtype, "softplus", "normalized", True, seed=5)
+
+    def at(t):
+        flat = torch.zeros(t.numel() + off, device="cuda")
+        flat[off:] = t.reshape(-1)
+        return flat[off:].view(t.shape)
+
+    form["decay_scale"], form["decay_bias"] = at(form["decay_scale"]), at(form["decay_bias"])
+    h = at(states(N, D))
+    ref = glr64.scan(glr64.Form(x, la, **form), h, [L] * N)
+    saved = at(torch.zeros(N * L // 64 + N, D))
+    y, end, _ = kda.kda_glr_scan(x, la, h, None, N, checkpoints=saved, **form)
+    check(y, ref[0], ref[2])
+    check(end, ref[1], ref[3])
+    rows = [n * L // 64 + n for n in range(N)]
+    assert torch.equal(saved[rows], h)
+    form["input_gate"] = form["input_gate"].view(N, L, D)
+    y = kda.kda_glr_step(x.view(N, L, D), la.view(N, L, D), h, **form)
+    check(y.view(-1, D), ref[0], ref[2])
+    check(h, ref[1], ref[3])
