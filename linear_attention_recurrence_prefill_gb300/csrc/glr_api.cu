@@ -61,22 +61,26 @@ int piece(const GlrArgs& a, int dtype) {
   return 2;
 }
 
-// CTAs that share a sequence's tokens, a power of two.  As far as the host knows, T_total / longest
-// sequences are as long as the longest: their tiles in waves of two CTAs per SM (one in fp32, whose
-// tiles take twice the shared memory), and about two tiles' time for a CTA to begin and end.
-// Forward alone, bf16, us for 1, 2, 4, 8 CTAs: 32,768 tokens x 4096 588, 464, 306, 344; nine prompts of
-// 12,000 tokens in all 116, 123, 139, 190.
+// CTAs that share a sequence's tokens, a power of two, by what they cost in tiles' times: a CTA has two
+// more to begin and end, an SM two CTAs at a time (one in fp32, whose tiles take twice the shared
+// memory), and a tile takes three tenths longer where its total goes to other CTAs.  Sequences of one length
+// go in waves; of others the host knows the longest, which one row of CTAs walks, and all tokens together.
+// Measured, bf16, us for 1, 2, 4, 8 CTAs: forward, 32,768 tokens x 4096 588, 464, 297, 344, nine prompts of
+// 12,000 tokens in all 105, 113, 132, 183; with the gradient, one sequence of 4096 381, 254, 146, 159, four of
+// 16,384 in all 939, 538, 499, 580, sixteen of 8000 in all x 2048 221, 176, 208, 317.
 int glr_ranks(int T_total, int N, int D, int dtype, int max_seqlen) {
   const long long longest = max_seqlen > 0 ? max_seqlen : T_total;
   if (longest == 0) return 1;
   const long long tiles = (longest + kGlrTile - 1) / kGlrTile, blocks = (D + 63LL) / 64;
   const long long slots = (dtype == KDA_BF16 ? 2LL : 1LL) * sm_count();
-  long long alike = (T_total + longest - 1) / longest;
-  if (alike > N) alike = N;
+  const bool alike = 5LL * T_total >= 4 * longest * N;
   int best = 1;
-  long long least = 0;
+  double least = 0.;
   for (int ranks = 1; ranks <= kGlrMaxRanks && ranks <= tiles; ranks *= 2) {
-    const long long cost = (alike * blocks * ranks + slots - 1) / slots * ((tiles + ranks - 1) / ranks + 2);
+    const double row = (double)((tiles + ranks - 1) / ranks) + 2.;
+    const double all = alike ? (double)((N * blocks * ranks + slots - 1) / slots) * row
+                             : ((double)T_total / kGlrTile + 2. * N * ranks) * blocks / slots;
+    const double cost = (all > row ? all : row) * (ranks > 1 ? 1.3 : 1.);
     if (ranks == 1 || cost < least) {
       least = cost;
       best = ranks;
