@@ -374,6 +374,15 @@ struct GlrExchange {
   }
 };
 
+// Behind a wait that gave up: what is still on its way to this CTA's shared memory lands, or has its
+// time, before that is released.  `uses`: of each pair of barriers in turn.
+__device__ __forceinline__ void glr_settle(uint64_t (&landed)[2], uint64_t (&arrived)[2], int uses, bool tma, bool shared) {
+  for (int i = uses > 2 ? uses - 2 : 0; i < uses; ++i) {
+    if (tma) umma::mbar_wait(&landed[i & 1], (i >> 1) & 1, kGlrSpins);
+    if (shared) umma::mbar_wait(&arrived[i & 1], (i >> 1) & 1, kGlrSpins);
+  }
+}
+
 // Launchers; each returns the launch's cudaError_t.  bytes: what rows, bases and D allow to move at
 // once (GlrTile): 16, 4, or 2.
 cudaError_t launch_glr_few(const GlrArgs& a, int dtype, int bytes, cudaStream_t s);

@@ -67,12 +67,12 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     mbar_init(&landed[1], 1);
     mbar_fence_init();
   }
-  auto fetch = [&](int round) {
-    const int first = (round * ranks + rank) * kGlrTile;
-    uint8_t* to = stages + (round & 1) * stage;
+  auto fetch = [&](int i) {  // the i-th round from the end
+    const int first = ((rounds - 1 - i) * ranks + rank) * kGlrTile;
+    uint8_t* to = stages + (i & 1) * stage;
     if constexpr (Tile::kTma) {
       if (threadIdx.x == kGlrThreads - 32) {  // (warp 0 has the tile's total to send)
-        uint64_t* bar = &landed[round & 1];
+        uint64_t* bar = &landed[i & 1];
         mbar_arrive_expect_tx(bar, dy ? stage : stage - Tile::kArray);
         tma_load_2d(to, &maps.la, ch0, t0 + first, bar);
         tma_load_2d(to + Tile::kArray, &maps.x, ch0, t0 + first, bar);
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
   if (!dy)  // zeros, once
     for (int i = 0; i < 2; ++i) Tile::clear(stages + i * stage + 2 * Tile::kArray, warp, lane, 0, from_f32<T>(0.f));
   __syncthreads();  // the barriers are there
-  if (rounds > 0) fetch(rounds - 1);
+  if (rounds > 0) fetch(0);
   // what the tokens behind this round hand back
   float2 carry = load_states(a.dh_T && live ? a.dh_T + (size_t)n * a.D + ch : nullptr, in);
   const GlrChannels par = glr_channels(a, ch, in);
@@ -111,13 +111,13 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
   for (int i = 0; i < rounds; ++i) {
     const int round = rounds - 1 - i, tile = round * ranks + rank, p = i & 1;
     const int first = tile * kGlrTile + warp * kGlrSeg;
-    uint8_t* from = stages + (round & 1) * stage;
+    uint8_t* from = stages + p * stage;
     uint8_t *from_x = from + Tile::kArray, *from_dy = from + 2 * Tile::kArray, *from_gate = from + 3 * Tile::kArray;
     if (!Tile::kTma) cp_async_wait_all();
     __syncthreads();  // nobody reads the tile before any more (and this one is in shared memory)
-    if (round > 0) fetch(round - 1);
+    if (i + 1 < rounds) fetch(i + 1);
     if constexpr (Tile::kTma) {
-      ok = ok && mbar_wait_soon(&landed[round & 1], (i >> 1) & 1, kGlrSpins);
+      ok = ok && mbar_wait_soon(&landed[p], (i >> 1) & 1, kGlrSpins);
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from_x, warp, lane, L - first, from_f32<T>(0.f));
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     db[1].add(tb.y);
   }
   if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+  if (!ok) glr_settle(landed, others.arrived, rounds, Tile::kTma, ranks > 1);
   if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
   else __syncthreads();
   if (live && a.dh0 && rank == 0 && warp == 0)

@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
 // load their constants again and again), one per SM 405; the clusters' barrier instead of counted
 // writes 367.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_constant__ GlrArgs a, const __grid_constant__ GlrMaps maps) {
+__global__ void __launch_bounds__(kGlrThreads, 2)
+    glr_scan_kernel(const __grid_constant__ GlrArgs a, const __grid_constant__ GlrMaps maps) {
   using G = GlrLane<T>;
   using Tile = GlrTile<T, kBytes>;
   constexpr bool kFast = G::kFast;
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2) glr_scan_kernel(const __grid_c
     if (warp == kGlrWarps - 1) last[p][lane] = h;
   }
   if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+  if (!ok) glr_settle(landed, others.arrived, rounds, Tile::kTma, ranks > 1);
   if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
   else __syncthreads();
   // (a state pool: every warp has read its first states by now)
