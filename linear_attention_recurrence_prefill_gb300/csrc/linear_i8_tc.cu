@@ -65,7 +65,9 @@ __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, uin
 
 // kTma: rows and bases at 16 bytes.  A block's integers then land in shared memory, in rows of 64
 // bytes (w's with TMA's swizzle of 64 bytes: each thread reads a row of its own); else the threads
-// read them where they are.
+// read them where they are, four neighbours a row, and those of w pass through a place of each
+// warp's own to the thread that has their row (100 x 4095 -> 4096: 30.5 us, 33.3 with a row a
+// thread; 150 x 2047 -> 1021: 15.0 and 16.5; but 12 x 1000 -> 1499: 8.9 and 8.3).
 template <int BN, bool kTma>
 struct Fill {
   static constexpr int kFillX = BN > 32 ? 4 : 2, kFill = (kFillW + kFillX) / 2;  // the latter of a block
@@ -74,8 +76,9 @@ struct Fill {
   static constexpr int kTiles = 4;                                // widened blocks
   static constexpr int kRaw = kTma ? (BN > 64 ? 2 : 4) : 0;       // blocks on their way or landed
   static constexpr uint32_t kRawBlock = (kRowsA + BN) * kBlockK;
+  static constexpr uint32_t kPass = kTma ? 0 : kFillW * 32 * kBlockK;  // bytes
   static constexpr uint32_t kTile = BN * kBlockK * 2;             // x's part of a widened block
-  static constexpr uint32_t kUsed = kTiles * kTile + kRaw * kRawBlock, kSums = BN * kRowsA * 4;
+  static constexpr uint32_t kUsed = kTiles * kTile + kRaw * kRawBlock + kPass, kSums = BN * kRowsA * 4;
   static constexpr uint32_t kSmem = kAlign + (kUsed > kSums ? kUsed : kSums);
   static constexpr uint32_t kAcc = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;  // columns of TMEM
   static constexpr uint32_t kA = kBlockK / 2;                            // of w's part of a block
@@ -141,14 +144,19 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
   bool ok = true;
   if (warp < kFillW) {
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    const bool in = (long long)n0 + r < l.N;
-    const int8_t* row = static_cast<const int8_t*>(l.w) + (in ? (long long)n0 + r : 0) * l.ldw;
+    // where they are: four neighbouring lanes a row, eight rows at a time
+    uint8_t* pass = raw + warp * 32 * kBlockK;
+    const int c4 = lane & 3;
     uint4 next[4];
     auto fetch = [&](int it) {
-      const long long k = column(it);
+      const long long k = column(it) + c4 * 16;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        next[c] = load16(row + k + c * 16, in && it < blocks ? l.K - k - c * 16 : 0, static_cast<const int8_t*>(l.w));
+      for (int j = 0; j < 4; ++j) {
+        const long long n = (long long)n0 + quarter * 32 + j * 8 + (lane >> 2);
+        const bool in = n < l.N && it < blocks;
+        next[j] = load16(static_cast<const int8_t*>(l.w) + (in ? n : 0) * l.ldw + k, in ? l.K - k : 0,
+                         static_cast<const int8_t*>(l.w));
+      }
     };
     if (!kTma) fetch(warp >> 2);
     for (int it = warp >> 2; it < blocks; it += 2) {
@@ -163,6 +171,18 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
         for (int c = 0; c < 4; ++c) next[c] = *reinterpret_cast<const uint4*>(from + ((c ^ (r >> 1 & 3)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&taken[slot]);
+      }
+      if constexpr (!kTma) {
+        __syncwarp();  // the block before has been read
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = j * 8 + (lane >> 2);
+          *reinterpret_cast<uint4*>(pass + at * kBlockK + ((c4 ^ (at >> 1 & 3)) << 4)) = next[j];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          next[c] = *reinterpret_cast<const uint4*>(pass + lane * kBlockK + ((c ^ (lane >> 1 & 3)) << 4));
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -429,11 +449,14 @@ cudaError_t launch(const LinearI8Args& a, int dtype, int* status, int split, cud
 // Whether both arrays are widened first.  That costs by M + N and pays by M N: with rows and bases at
 // 16 bytes from M N / (M + N) = 544 on (4096 channels of 4096 columns, 512 and 640 tokens: 37.5 and 40.3 us
 // this way, 29.3 and 46.6 otherwise; 12288 channels, 256 and 512 tokens: 64 and 81, 48 and 85), else from
-// 128 on (4096 channels of 4095 columns, 128 and 192 tokens: 36.8 and 37.0, 33.5 and 56.8), but where
-// there are few columns, which are soon read, from 320 on (1499 channels of 1000 columns, 333 tokens: 18.1
-// and 17.8, with a launch more; 1001 channels of 1001, 500 tokens: 15.0 and 16.8).
-bool widened(long long M, long long N, int K, bool tma) {
-  return M * N >= (tma ? 544 : K >= 2048 ? 128 : 320) * (M + N);
+// 128 on (4096 channels of 4095 columns, 128 and 160 tokens: 36.9 and 36.9, 29.9 and 49.3), but where the
+// other way has CTAs to spare for four parts of K (76 tiles of 128 x 64 or fewer), which then is near or
+// ahead with no workspace and a launch less (1021 channels of 4095, 256 and 400 tokens: 30.1 and 30.1,
+// 20.6 and 32.5; 1499 channels of 1000, 333 and 400 tokens, 72 and 84 tiles: 15.1 and 15.1, 16.4 and
+// 23.0).  What the first rule takes the second takes too: the workspace's size goes by the second.
+bool widened(long long M, long long N, bool tma) {
+  if (tma) return M * N >= 544 * (M + N);
+  return M * N >= 128 * (M + N) && (N + 127) / 128 * ((M + 63) / 64) > 76;
 }
 long long padded(int K) { return (K + 15LL) / 16 * 16; }
 
@@ -442,7 +465,7 @@ long long padded(int K) { return (K + 15LL) / 16 * 16; }
 bool linear_i8_tc_takes(int M, int N) { return (N + 127LL) / 128 * ((M + 15LL) / 16) <= 0x7fffffffLL; }
 
 size_t linear_i8_workspace_bytes(int M, int N, int K) {
-  return K > 0 && widened(M, N, K, false) ? ((size_t)M + N) * padded(K) * 2 : 0;
+  return K > 0 && widened(M, N, false) ? ((size_t)M + N) * padded(K) * 2 : 0;
 }
 
 cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s) {
@@ -456,7 +479,7 @@ cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspac
                                 cudaStream_t s) {
   const LinearArgs& l = a.l;
   const bool tma = tma_takes(l);
-  if (widened(l.M, l.N, l.K, tma)) {
+  if (widened(l.M, l.N, tma)) {
     const long long Kp = padded(l.K), blocks = ((long long)l.M + l.N + 1) / 2, most = 8LL * sms;
     const cudaError_t e = launch_early(
         widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 1, s, static_cast<const int8_t*>(l.x),

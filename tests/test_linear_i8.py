@@ -87,7 +87,8 @@ def test_binding_refuses():
 SIZES = [(1, 1, 1), (1, 64, 128), (1, 4096, 264), (2, 72, 40), (3, 200, 33), (4, 1024, 136), (5, 77, 129), (8, 512, 512),
          (15, 512, 1000), (16, 128, 128), (17, 1024, 384), (31, 8, 8), (33, 136, 72), (64, 256, 520), (65, 1008, 136),
          (100, 2000, 264), (127, 333, 511), (128, 128, 128), (129, 64, 257), (200, 96, 1499), (256, 256, 256),
-         (300, 1304, 777), (333, 1000, 1499), (513, 192, 300), (1000, 48, 130), (700, 512, 5000), (2500, 272, 2100)]
+         (300, 1304, 777), (333, 1000, 1499), (513, 192, 300), (1000, 48, 130), (700, 512, 5000), (2500, 272, 2100),
+         (400, 4095, 200)]
 
 
 @gpu
@@ -307,7 +308,7 @@ def test_few_rows(M, K, N):
 
 
 @gpu
-@pytest.mark.parametrize("M, K, N", [(640, 512, 4096), (700, 100, 5000), (330, 77, 19000), (3000, 1, 700), (400, 4095, 200)])
+@pytest.mark.parametrize("M, K, N", [(640, 512, 4096), (700, 100, 5000), (330, 77, 19000), (3000, 1, 700), (150, 4095, 4100)])
 def test_widened_first(M, K, N):
     """Sizes whose integers are widened into the workspace, with one that is given and holds NaN."""
     a = make(M, K, N, F32, seed=3)
