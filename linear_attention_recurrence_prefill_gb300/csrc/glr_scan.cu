@@ -67,9 +67,11 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
   using W = Wide<T, kPairs, kPair>;
   constexpr bool kFast = GlrLane<T>::kFast;
   constexpr int kCh = 2 * kPairs;
-  const int blocks = (a.D + kFewThreads * kCh - 1) / (kFewThreads * kCh);
+  // unsigned: rounded up to a CTA's channels (1024 at most), the largest D is 2^31; a thread's first
+  // channel is below that
+  const unsigned blocks = ((unsigned)a.D + kFewThreads * kCh - 1) / (kFewThreads * kCh);
   const int n = blockIdx.x / blocks;
-  const int ch = (blockIdx.x % blocks * kFewThreads + (int)threadIdx.x) * kCh;
+  const int ch = (blockIdx.x % blocks * kFewThreads + threadIdx.x) * kCh;
   grid_launch_dependents();
   grid_wait_prerequisites();  // what ran before is complete
   int t0, t1, slot;

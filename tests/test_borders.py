@@ -1,0 +1,43 @@
+"""Sizes next to 2^31, where an index, or a size on its way to the library, no longer fits in 32
+bits.  Arrays of such calls take some 10 to 45 GB; each test gives them back."""
+import pytest
+import torch
+
+from linear_attention_recurrence_prefill_gb300 import kda
+
+gpu = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+LARGEST = 2 ** 31 - 257  # the largest width that the library takes
+
+
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
+def everywhere(t, value):
+    """Whether all of t is `value`, without a copy of its size."""
+    flat = t.view(-1)
+    return all(bool((flat[i:i + 2 ** 28] == value).all()) for i in range(0, flat.numel(), 2 ** 28))
+
+
+@gpu
+def test_recurrence_of_the_widest_channels():
+    """Two sequences of one token, as many channels as 16-byte rows can have: h = 1 + x, with a decay
+    of 1 (each CTA has up to 1024 channels, which passes 2^31 when D is rounded up)."""
+    D = LARGEST // 8 * 8
+    assert D + 1023 >= 2 ** 31
+    x = torch.full((2, D), 2.0, dtype=BF16, device="cuda")
+    la = torch.zeros((2, D), dtype=BF16, device="cuda")
+    x[1] = 4
+    h = torch.ones((2, D), device="cuda")
+    y, end = kda.kda_glr_scan(x, la, h, N=2)
+    for t in (y, end):
+        assert everywhere(t[0], 3) and everywhere(t[1], 5)
+    del end, y
+    y = kda.kda_glr_step(x, la, h)
+    for t in (y, h):
+        assert everywhere(t[0], 3) and everywhere(t[1], 5)
+    assert kda.kda_get_last_error() == kda.KDA_OK
