@@ -302,10 +302,11 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
   const long long m = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + m * a.ldx;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr : nullptr;
-  auto at = [&](int d) { return to_f32(x[d]) + (res ? to_f32(res[d]) : 0.f); };
+  const unsigned width = a.D;  // 1024 beyond it an int would pass 2^31
+  auto at = [&](unsigned d) { return to_f32(x[d]) + (res ? to_f32(res[d]) : 0.f); };
   float sq = 0.f;
   uint32_t big = 0;
-  for (int d = threadIdx.x; d < a.D; d += 1024) {
+  for (unsigned d = threadIdx.x; d < width; d += 1024) {
     const float s = at(d), p = a.w ? s * a.w[d] : s;
     sq = fmaf(s, s, sq);
     big = max(big, __float_as_uint(fabsf(p)));
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
     big = max(big, bits[w]);
   }
   if (a.q && big < 0x7f800000u) {
-    for (int d = threadIdx.x; d < a.D; d += 1024) {
+    for (unsigned d = threadIdx.x; d < width; d += 1024) {
       const float z = at(d), p = a.w ? z * a.w[d] : z;
       if (fabsf(p) >= next_to(big)) take_larger(&largest, exact_product<T>(a, m, d));
     }
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
   const Row o = row_of(a, sq, big);
   const double exact = __longlong_as_double((long long)largest);
   if (a.q && threadIdx.x == 0) a.scale[m] = o.scale;
-  for (int d = threadIdx.x; d < a.D; d += 1024) {
+  for (unsigned d = threadIdx.x; d < width; d += 1024) {
     const float z = at(d), w = a.w ? a.w[d] : 1.f;
     if (a.q) a.q[m * a.ldq + d] = (int8_t)quantized<T>(a, o, exact, z * w, m, d);
     if (a.y) static_cast<T*>(a.y)[m * a.ldy + d] = from_f32<T>(z * o.r * w);

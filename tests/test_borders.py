@@ -41,3 +41,30 @@ def test_recurrence_of_the_widest_channels():
     for t in (y, h):
         assert everywhere(t[0], 3) and everywhere(t[1], 5)
     assert kda.kda_get_last_error() == kda.KDA_OK
+
+
+@gpu
+def test_norm_of_the_widest_row():
+    """One row of the largest width, with 4096 elements on either side of it that stay: a thread's next
+    element, 1024 on, lies past 2^31 behind the last."""
+    D, side = LARGEST, 4096
+    assert D - 1 + 1024 >= 2 ** 31
+
+    def row(dtype, value):
+        whole = torch.full((D + 2 * side,), 7, dtype=dtype, device="cuda")
+        whole[side:side + D] = value
+        return whole, whole[side:side + D].view(1, D)
+
+    _, x = row(BF16, 1)
+    x[0, 0], x[0, -1] = 4, -2  # integers 32 (31.75), 127 and -64 (-63.5, the even one)
+    (wy, y), (wq, q) = row(BF16, 0), row(torch.int8, 0)
+    kda.kda_rmsnorm(x, y=y)
+    inner = everywhere(y[0, 1:-1], 1)  # the mean is 1 + 18 / D
+    assert inner and y[0, 0] == 4 and y[0, -1] == -2
+    y.zero_()
+    _, scale = kda.kda_rmsnorm_i8(x, q=q, y=y)
+    assert everywhere(y[0, 1:-1], 1) and y[0, 0] == 4 and y[0, -1] == -2
+    assert everywhere(q[0, 1:-1], 32) and q[0, 0] == 127 and q[0, -1] == -64
+    assert abs(float(scale) * 127 - 4) < 1e-4
+    for whole in (wy, wq):
+        assert (whole[:side] == 7).all() and (whole[-side:] == 7).all()
