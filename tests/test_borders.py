@@ -6,6 +6,7 @@ import torch
 from linear_attention_recurrence_prefill_gb300 import kda
 
 gpu = pytest.mark.gpu
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="calls on stand-in tensors of the CPU")
 BF16, F32 = torch.bfloat16, torch.float32
 LARGEST = 2 ** 31 - 257  # the largest width that the library takes
 
@@ -21,6 +22,66 @@ def everywhere(t, value):
     """Whether all of t is `value`, without a copy of its size."""
     flat = t.view(-1)
     return all(bool((flat[i:i + 2 ** 28] == value).all()) for i in range(0, flat.numel(), 2 ** 28))
+
+
+MANY = 2 ** 32 + 5  # of which 32 bits are 5
+
+
+def _too_many(x):
+    """Calls with MANY rows, on x [MANY, 1], or x [MANY, 0] for the products."""
+    one, none = x[:1], x[:, :0]
+    i8 = none.to(torch.int8)
+    yield lambda: kda.kda_linear(none, none[:3])
+    yield lambda: kda.kda_linear(one[:, :0], none)
+    yield lambda: kda.kda_linear_i8(i8, None, i8[:3], None)
+    yield lambda: kda.kda_linear_i8(i8[:3], None, i8, None)
+    yield lambda: kda.kda_rmsnorm(x)
+    yield lambda: kda.kda_rmsnorm(x.view(1, MANY))
+    yield lambda: kda.kda_rmsnorm_i8(x)
+    yield lambda: kda.kda_quantize_i8(x)
+    yield lambda: kda.kda_glr_scan(x, x)
+    yield lambda: kda.kda_glr_scan(one, one, N=MANY)
+    yield lambda: kda.kda_glr_scan(one, one, max_seqlen=MANY)
+    yield lambda: kda.kda_glr_step(x, x, x)
+    yield lambda: kda.kda_glr_step(x.view(1, MANY, 1), x.view(1, MANY, 1), x)
+    yield lambda: kda.kda_glr_scan_backward(x, None, x, x, x)
+    yield lambda: kda.kda_glr_scan_backward(None, None, one, one, one, N=MANY)
+
+
+def test_sizes_beyond_32_bits_do_not_fit():
+    kda._sizes("call", 2 ** 31 - 1, 0)
+    with pytest.raises(kda.KdaError) as e:
+        kda._sizes("call", 1, 2 ** 31)
+    assert e.value.status == kda.KDA_ERR_SHAPE
+
+
+@no_gpu
+def test_sizes_beyond_32_bits_are_refused_on_the_host(monkeypatch):
+    """Before anything of their size is allocated: stand-ins without memory, the device not asked for."""
+    monkeypatch.setattr(kda, "_one_device", lambda *a: 0)
+    for call in _too_many(torch.empty(MANY, 1, dtype=BF16, device="meta")):
+        with pytest.raises(kda.KdaError) as e:
+            call()
+        assert e.value.status == kda.KDA_ERR_SHAPE
+
+
+@gpu
+def test_sizes_beyond_32_bits_are_refused():
+    for call in _too_many(torch.empty(MANY, 1, dtype=BF16, device="cuda")):
+        with pytest.raises(kda.KdaError) as e:
+            call()
+        assert e.value.status == kda.KDA_ERR_SHAPE
+
+
+@gpu
+def test_a_pool_of_more_rows_than_32_bits():
+    pool = torch.zeros(MANY, 1, device="cuda")
+    slots = torch.tensor([7], dtype=torch.int32, device="cuda")
+    x = torch.full((1, 1), 3.0, device="cuda")
+    y, _ = kda.kda_glr_scan(x, x, pool, h_T=pool, slots=slots)
+    assert y[0, 0] == 3 and pool[7, 0] == 3
+    y = kda.kda_glr_step(x, x, pool, slots=slots)
+    assert y[0, 0] == 6 and pool[7, 0] == 6 and kda.kda_get_last_error() == kda.KDA_OK
 
 
 @gpu
