@@ -529,6 +529,8 @@ int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const in
  *   x, log_alpha  [N][L][D] dtype (token strides in opt)
  *   h             [N or n_slots][D] fp32, read and overwritten
  *   y             [N][L][D] dtype out
+ *
+ * y and h overlap no input and not each other (KDA_ERR_ARG where two start at one address).
  */
 int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N, int L, int D,
                  int dtype, const kda_glr_options* opt, kda_stream_t stream);
@@ -545,7 +547,8 @@ int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N,
  *   ddecay_scale, ddecay_bias  [D] fp32 out, or NULL (not with KDA_GLR_LOG): summed over
  *                 all tokens, in an order of its own that does not change
  *
- * Rows of outputs behind the last sequence are left as they are.  Where the decay is 1
+ * Outputs and the workspace overlap no input and not each other (KDA_ERR_ARG where two start at
+ * one address).  Rows of outputs behind the last sequence are left as they are.  Where the decay is 1
  * to the last bit, the slope of sqrt(1 - a^2), which is infinite there, is taken as 0.
  */
 int kda_glr_scan_backward(const void* dy, const float* dh_T, const void* x, const void* log_alpha,

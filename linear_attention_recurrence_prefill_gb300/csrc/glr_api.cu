@@ -130,9 +130,9 @@ int kda_glr_scan(const void* x, const void* log_alpha, const float* h0, const in
     if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
   if (!aligned(h0, 4) || !aligned(h_T, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_ALIGN;
   if (!cu_seqlens && T_total % N != 0) return KDA_ERR_SHAPE;
-  if (same(y, {x, log_alpha, o->input_gate, h0, h_T, o->checkpoints})) return KDA_ERR_ARG;
-  if (same(h_T, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias})) return KDA_ERR_ARG;
-  if (same(o->checkpoints, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias, h0, h_T})) return KDA_ERR_ARG;
+  for (const void* out : {(const void*)y, (const void*)h_T, (const void*)o->checkpoints})
+    if (same(out, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias, cu_seqlens, o->slots})) return KDA_ERR_ARG;
+  if (same(y, {h0, h_T, o->checkpoints}) || same(o->checkpoints, {h0, h_T})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GlrArgs a = glr_args(x, log_alpha, cu_seqlens, N, T_total, D, o, status);
@@ -159,8 +159,9 @@ int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N,
   for (const void* p : {x, log_alpha, (const void*)y})
     if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
   if (!aligned(h, 4)) return KDA_ERR_ALIGN;
-  if (same(y, {x, log_alpha, o->input_gate, h})) return KDA_ERR_ARG;
-  if (same(h, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias})) return KDA_ERR_ARG;
+  for (const void* out : {(const void*)y, (const void*)h})
+    if (same(out, {x, log_alpha, o->input_gate, o->decay_scale, o->decay_bias, o->slots})) return KDA_ERR_ARG;
+  if (same(y, {h})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GlrArgs a = glr_args(x, log_alpha, nullptr, N, T, D, o, status);

@@ -671,3 +671,20 @@ def test_states_at_any_place(dtype, D, off):
     y = kda.kda_glr_step(x.view(N, L, D), la.view(N, L, D), h, **form)
     check(y.view(-1, D), ref[0], ref[2])
     check(h, ref[1], ref[3])
+
+
+@no_gpu
+@pytest.mark.parametrize("out", ["y", "h", "checkpoints"])
+@pytest.mark.parametrize("at", ["x", "la", "cu", "input_gate", "decay_scale", "decay_bias", "slots"])
+def test_an_output_at_an_input_is_refused(out, at):
+    """Other CTAs still read the parameters, offsets and slots when one writes its outputs."""
+    if at in ("x", "la", "cu"):
+        kw, opt = {at: 8 * A}, {}
+    else:
+        kw, opt = {}, {at: 8 * A} | (dict(n_slots=4) if at == "slots" else {})
+    opt["decay_from"] = 1
+    where = opt if out == "checkpoints" else kw
+    where[out] = 8 * A
+    assert _scan(opt, **kw) == kda.KDA_ERR_ARG
+    if at != "cu" and out != "checkpoints":
+        assert _step(opt, **kw) == kda.KDA_ERR_ARG
