@@ -141,6 +141,8 @@ int kda_gdr_prefill(const void* q, const void* k, const void* v, const float* lo
   }
   if (same(o, {q, k, v, log_alpha, beta, S0, S_T, op->workspace})) return KDA_ERR_ARG;
   if (same(S_T, {q, k, v, log_alpha, beta, op->workspace})) return KDA_ERR_ARG;
+  for (const void* out : {(const void*)o, (const void*)S_T})
+    if (same(out, {cu_seqlens, op->slots, op->decay_scale, op->decay_bias})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GdrArgs a = gdr_args(q, k, v, log_alpha, beta, S0, S_T, o, N, T_total, H_k, H_v, d_k, d_v, op,
@@ -169,6 +171,8 @@ int kda_gdr_decode_step(const void* q, const void* k, const void* v, const float
   if (same(o, {q, k, v, log_alpha, beta, S, op->snapshots})) return KDA_ERR_ARG;
   if (same(S, {q, k, v, log_alpha, beta})) return KDA_ERR_ARG;
   if (same(op->snapshots, {q, k, v, log_alpha, beta, S})) return KDA_ERR_ARG;
+  for (const void* out : {(const void*)o, (const void*)S, (const void*)op->snapshots})
+    if (same(out, {op->slots, op->decay_scale, op->decay_bias})) return KDA_ERR_ARG;
   int* status = status_word();
   if (!status) return KDA_ERR_CUDA;
   GdrArgs a = gdr_args(q, k, v, log_alpha, beta, S, S, o, N, T, H_k, H_v, d_k, d_v, op, status);

@@ -5,7 +5,7 @@ import torch
 
 from linear_attention_recurrence_prefill_gb300 import kda
 from tests import plain64
-from tests.test_gdr import BF16, TOL, check, cu_of, draw, expect_prefill, pool
+from tests.test_gdr import A, BF16, TOL, _prefill, _step, apart, check, cu_of, draw, expect_prefill, no_gpu, pool
 
 gpu = pytest.mark.gpu
 
@@ -133,3 +133,19 @@ def test_one_token_whatever_its_stride(impl):
     o_ref, S_ref = expect_prefill((q, k, v, la, beta), [1], None)
     check(o, o_ref, TOL[impl], "o")
     check(S, S_ref, TOL[impl], "S_T")
+
+
+@no_gpu
+@pytest.mark.parametrize("out", ["o", "S", "snapshots"])
+@pytest.mark.parametrize("at", ["cu", "slots", "decay_scale", "decay_bias"])
+def test_refuses_an_output_on_offsets_slots_or_parameters(out, at):
+    """Other CTAs still read them when one writes its outputs."""
+    kw, opt = apart(), dict(decay_from_logit=1)
+    (kw if at == "cu" else opt)[at] = 9 * A
+    if at == "slots":
+        opt["n_slots"] = 4
+    (opt if out == "snapshots" else kw)[out] = 9 * A
+    if out != "snapshots":
+        assert _prefill(kda.kda_gdr_options_init(impl="simt", **opt), **kw) == kda.KDA_ERR_ARG
+    if at != "cu":
+        assert _step(kda.kda_gdr_options_init(**opt), **kw) == kda.KDA_ERR_ARG
