@@ -54,6 +54,9 @@ struct GlrArgs {
   void* dgate;                // NULL: not wanted, as the ones below
   float* dh0;
   double2* partial;           // NULL, or [N][ranks][D]: the share of each CTA in dA and db
+  // after how many cycles a wait gives up, for a tile and for the other CTAs' totals; below 0: at
+  // once, without a look
+  long long wait_tile, wait_totals;
 };
 
 // Tensor maps of the arrays that kernels read in tiles (where TMA takes them).
@@ -348,6 +351,10 @@ __device__ __forceinline__ void glr_input_scale(int scale, const F& f) {
   else f(std::integral_constant<int, KDA_GLR_INPUT_NORMALIZED>());
 }
 
+__device__ __forceinline__ bool glr_wait(uint64_t* bar, int parity, long long limit) {
+  return limit >= 0 && umma::mbar_wait_soon(bar, parity, limit);
+}
+
 // ---------------------------------------------------------------- between the CTAs of a cluster
 // Decays and states (or gradients) of the tiles of a round, which every CTA sends to every other:
 // each write counts on a barrier of the CTA that it goes to, so that nobody waits for more than
@@ -369,18 +376,17 @@ struct GlrExchange {
       umma::st_async_f32x4(umma::map_to_rank(umma::smem_u32(&tot[p][rank][lane]), r), v,
                            umma::map_to_rank(umma::smem_u32(&arrived[p]), r));
   }
-  __device__ __forceinline__ bool wait(int p, int round) {
-    return umma::mbar_wait_soon(&arrived[p], (round >> 1) & 1, kGlrSpins);
+  __device__ __forceinline__ bool wait(int p, int round, long long limit) {
+    return glr_wait(&arrived[p], (round >> 1) & 1, limit);
   }
 };
 
-// Behind a wait that gave up: what is still on its way to this CTA's shared memory lands, or has its
-// time, before that is released.  `uses`: of each pair of barriers in turn.
-__device__ __forceinline__ void glr_settle(uint64_t (&landed)[2], uint64_t (&arrived)[2], int uses, bool tma, bool shared) {
-  for (int i = uses > 2 ? uses - 2 : 0; i < uses; ++i) {
-    if (tma) umma::mbar_wait(&landed[i & 1], (i >> 1) & 1, kGlrSpins);
-    if (shared) umma::mbar_wait(&arrived[i & 1], (i >> 1) & 1, kGlrSpins);
-  }
+// Behind a wait that gave up, which the whole CTA has agreed on before it expects anything more on a
+// barrier: what is still on its way to this CTA's shared memory lands, or has its time, before that is
+// released.  `fetched`, `sent`: how often the barriers of either pair, in turn, were told what to expect.
+__device__ __forceinline__ void glr_settle(uint64_t (&landed)[2], int fetched, uint64_t (&arrived)[2], int sent) {
+  for (int i = fetched > 2 ? fetched - 2 : 0; i < fetched; ++i) umma::mbar_wait(&landed[i & 1], (i >> 1) & 1, kGlrSpins);
+  for (int i = sent > 2 ? sent - 2 : 0; i < sent; ++i) umma::mbar_wait(&arrived[i & 1], (i >> 1) & 1, kGlrSpins);
 }
 
 // Launchers; each returns the launch's cudaError_t.  bytes: what rows, bases and D allow to move at

@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
   T* dgate = a.dgate ? static_cast<T*>(a.dgate) + out0 : nullptr;
   const size_t saved = glr_checkpoint_row(t0, n);
   Sum dA[2] = {}, db[2] = {};
-  bool ok = true;
+  bool ok = true;  // of this thread, and of all behind the second barrier in the loop
+  int i = 0;
 
-  for (int i = 0; i < rounds; ++i) {
+  for (; i < rounds; ++i) {
     const int round = rounds - 1 - i, tile = round * ranks + rank, p = i & 1;
     const int first = tile * kGlrTile + warp * kGlrSeg;
     uint8_t* from = stages + p * stage;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     __syncthreads();  // nobody reads the tile before any more (and this one is in shared memory)
     if (i + 1 < rounds) fetch(i + 1);
     if constexpr (Tile::kTma) {
-      ok = ok && mbar_wait_soon(&landed[p], (i >> 1) & 1, kGlrSpins);
+      ok = ok && glr_wait(&landed[p], (i >> 1) & 1, a.wait_tile);
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from_x, warp, lane, L - first, from_f32<T>(0.f));
@@ -166,7 +167,8 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     seg[p][warp][lane] = make_float4(ds.x, ds.y, H.x, H.y);
     seg_grad[p][warp][lane] = back;
     if (ranks > 1) seg_log[p][threadIdx.x] = lg;
-    __syncthreads();
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
     if (ranks > 1) {
       if (warp == 0) {
         float2 z = both(0.f), l = both(0.f);
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
         const float2 t = decay_pack(decay_of<kFast>(l));
         others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      ok = ok && others.wait(p, i);
+      ok = others.wait(p, i, a.wait_totals);
       back = carry;
       for (int r = ranks - 1; r >= 0; --r) {
         const float4 s = others.tot[p][r][lane];
@@ -268,11 +270,14 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     db[0].add(tb.x);
     db[1].add(tb.y);
   }
-  if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
-  if (!ok) glr_settle(landed, others.arrived, rounds, Tile::kTma, ranks > 1);
+  ok = __syncthreads_and(ok);
+  if (!ok) {
+    if (threadIdx.x == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+    if (!Tile::kTma) cp_async_wait_all();
+    glr_settle(landed, Tile::kTma ? min(i + 2, rounds) : 0, others.arrived, ranks > 1 ? i : 0);
+  }
   if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
-  else __syncthreads();
-  if (live && a.dh0 && rank == 0 && warp == 0)
+  if (live && ok && a.dh0 && rank == 0 && warp == 0)
     store_states(a.dh0 + (size_t)n * a.D + ch, ranks > 1 || rounds == 0 ? carry : last[(rounds - 1) & 1][lane], in);
   if (partial) {
     static_assert(sizeof(seg) >= kGlrWarps * 2 * 32 * sizeof(double2), "the shares fit in its place");

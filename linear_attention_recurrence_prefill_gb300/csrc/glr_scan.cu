@@ -194,14 +194,15 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
   if (!Tile::kTma) __syncthreads();  // the first tile is in shared memory
   T* y = static_cast<T*>(a.y) + (size_t)t0 * a.D + ch;
   const size_t saved = glr_checkpoint_row(t0, n);
-  bool ok = true;
+  bool ok = true;  // of this thread, and of all behind the barrier in the loop
+  int round = 0;
 
-  for (int round = 0; round < rounds; ++round) {
+  for (; round < rounds; ++round) {
     const int tile = round * ranks + rank, p = round & 1;
     const int first = tile * kGlrTile + warp * kGlrSeg;
     uint8_t* from = stages + p * stage;
     if constexpr (Tile::kTma) {
-      ok = ok && mbar_wait_soon(&landed[p], (round >> 1) & 1, kGlrSpins);
+      ok = ok && glr_wait(&landed[p], (round >> 1) & 1, a.wait_tile);
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from + Tile::kArray, warp, lane, L - first, from_f32<T>(0.f));
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
     seg[p][warp][lane] = make_float4(dt.x, dt.y, h.x, h.y);
     if (ranks > 1) seg_log[p][threadIdx.x] = lg;
     if (!Tile::kTma) cp_async_wait_all();  // the next tile
-    __syncthreads();
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
     if (round + 2 < rounds) fetch(round + 2);  // where this tile was
     if (ranks > 1) {
       // the tile's own decay and state from zero, to every CTA of the cluster
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
         const float2 t = decay_pack(decay_of<kFast>(l));
         others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      ok = ok && others.wait(p, round);
+      ok = others.wait(p, round, a.wait_totals);
       // the state before this CTA's tile, and the one behind the round
       h = carry;
       for (int r = 0; r < ranks; ++r) {
@@ -279,12 +281,14 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
     }
     if (warp == kGlrWarps - 1) last[p][lane] = h;
   }
-  if (!ok && lane == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
-  if (!ok) glr_settle(landed, others.arrived, rounds, Tile::kTma, ranks > 1);
+  ok = __syncthreads_and(ok);
+  if (!ok) {
+    if (threadIdx.x == 0) atomicExch(a.status, KDA_ERR_TIMEOUT);
+    glr_settle(landed, Tile::kTma ? min(round + 2, rounds) : 0, others.arrived, ranks > 1 ? round : 0);
+  }
   if (ranks > 1) cluster_sync();  // no CTA leaves while another may write to it
-  else __syncthreads();
   // (a state pool: every warp has read its first states by now)
-  if (live && rank == 0 && warp == 0)
+  if (live && ok && rank == 0 && warp == 0)
     store_states(a.h_T + (size_t)slot * a.D + ch, ranks > 1 || rounds == 0 ? carry : last[(rounds - 1) & 1][lane], in);
 }
 
