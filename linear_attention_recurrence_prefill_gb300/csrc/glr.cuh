@@ -54,9 +54,6 @@ struct GlrArgs {
   void* dgate;                // NULL: not wanted, as the ones below
   float* dh0;
   double2* partial;           // NULL, or [N][ranks][D]: the share of each CTA in dA and db
-  // after how many cycles a wait gives up, for a tile and for the other CTAs' totals; below 0: at
-  // once, without a look
-  long long wait_tile, wait_totals;
 };
 
 // Tensor maps of the arrays that kernels read in tiles (where TMA takes them).
@@ -351,8 +348,15 @@ __device__ __forceinline__ void glr_input_scale(int scale, const F& f) {
   else f(std::integral_constant<int, KDA_GLR_INPUT_NORMALIZED>());
 }
 
-__device__ __forceinline__ bool glr_wait(uint64_t* bar, int parity, long long limit) {
-  return limit >= 0 && umma::mbar_wait_soon(bar, parity, limit);
+// A wait for a tile, or for the other CTAs' totals.  A build of these kernels for tests defines which of
+// them give up at once (limits as arguments instead took 3 us of the 105 that nine packed prompts take).
+enum GlrWait { kGlrWaitTile, kGlrWaitTotals };
+#ifndef KDA_GLR_GIVES_UP
+#define KDA_GLR_GIVES_UP(what) false
+#endif
+template <GlrWait kWhat>
+__device__ __forceinline__ bool glr_wait(uint64_t* bar, int parity) {
+  return !(KDA_GLR_GIVES_UP(kWhat)) && umma::mbar_wait_soon(bar, parity, kGlrSpins);
 }
 
 // ---------------------------------------------------------------- between the CTAs of a cluster
@@ -376,8 +380,8 @@ struct GlrExchange {
       umma::st_async_f32x4(umma::map_to_rank(umma::smem_u32(&tot[p][rank][lane]), r), v,
                            umma::map_to_rank(umma::smem_u32(&arrived[p]), r));
   }
-  __device__ __forceinline__ bool wait(int p, int round, long long limit) {
-    return glr_wait(&arrived[p], (round >> 1) & 1, limit);
+  __device__ __forceinline__ bool wait(int p, int round) {
+    return glr_wait<kGlrWaitTotals>(&arrived[p], (round >> 1) & 1);
   }
 };
 

@@ -41,7 +41,6 @@ GlrArgs glr_args(const void* x, const void* la, const int32_t* cu, int N, int T_
   a.checkpoints = o->checkpoints; a.status = status;
   a.N = N; a.T_total = T_total; a.D = D;
   a.decay_from = o->decay_from; a.input_scale = o->input_scale;
-  a.wait_tile = a.wait_totals = kGlrSpins;
   a.ldx = o->ldx ? o->ldx : D; a.ldla = o->ldla ? o->ldla : D; a.ldg = o->ldg ? o->ldg : D;
   return a;
 }

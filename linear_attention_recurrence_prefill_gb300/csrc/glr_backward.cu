@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
     __syncthreads();  // nobody reads the tile before any more (and this one is in shared memory)
     if (i + 1 < rounds) fetch(i + 1);
     if constexpr (Tile::kTma) {
-      ok = ok && glr_wait(&landed[p], (i >> 1) & 1, a.wait_tile);
+      ok = ok && glr_wait<kGlrWaitTile>(&landed[p], (i >> 1) & 1);
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from_x, warp, lane, L - first, from_f32<T>(0.f));
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kGlrThreads, sizeof(T) == 2 ? 2 : 1) glr_backw
         const float2 t = decay_pack(decay_of<kFast>(l));
         others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      ok = others.wait(p, i, a.wait_totals);
+      ok = others.wait(p, i);
       back = carry;
       for (int r = ranks - 1; r >= 0; --r) {
         const float4 s = others.tot[p][r][lane];

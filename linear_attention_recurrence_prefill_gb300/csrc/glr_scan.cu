@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
     const int first = tile * kGlrTile + warp * kGlrSeg;
     uint8_t* from = stages + p * stage;
     if constexpr (Tile::kTma) {
-      ok = ok && glr_wait(&landed[p], (round >> 1) & 1, a.wait_tile);
+      ok = ok && glr_wait<kGlrWaitTile>(&landed[p], (round >> 1) & 1);
       if (first + kGlrSeg > L) {
         Tile::clear(from, warp, lane, L - first, none);
         Tile::clear(from + Tile::kArray, warp, lane, L - first, from_f32<T>(0.f));
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
         const float2 t = decay_pack(decay_of<kFast>(l));
         others.send(p, rank, ranks, lane, make_float4(t.x, t.y, z.x, z.y));
       }
-      ok = others.wait(p, round, a.wait_totals);
+      ok = others.wait(p, round);
       // the state before this CTA's tile, and the one behind the round
       h = carry;
       for (int r = 0; r < ranks; ++r) {

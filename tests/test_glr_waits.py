@@ -1,5 +1,5 @@
 """What the gated linear recurrence does behind a wait that gives up: the kernels, built once more
-with the limits of their waits as arguments, on the GPU.  The status word is set, no state is
+with waits that give up at once where the test says so, on the GPU.  The status word is set, no state is
 written, nothing is on its way any more, and the next call is right."""
 import ctypes
 import os
@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc", "glr_waits.cu")
 OUT = os.path.join(HERE, "_build", "libglr_waits.so")
 BF16 = torch.bfloat16
-WAIT, GIVE_UP = 0, -1
+WAIT, GIVE_UP = 0, 1
 
 
 @pytest.fixture(scope="module")
@@ -31,9 +31,9 @@ def lib():
         cmd = [libbuild.nvcc(), *libbuild.flags(), "-shared", "-cudart", "shared", SRC, "-o", OUT]
         subprocess.run(cmd, check=True)
     l = ctypes.CDLL(OUT)
-    vp, ci, cl = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
-    l.glr_waits_scan.argtypes = [vp] * 6 + [ci] * 4 + [cl] * 2
-    l.glr_waits_backward.argtypes = [vp] * 8 + [ci] * 4 + [cl] * 2
+    vp, ci = ctypes.c_void_p, ctypes.c_int
+    l.glr_waits_scan.argtypes = [vp] * 6 + [ci] * 4
+    l.glr_waits_backward.argtypes = [vp] * 8 + [ci] * 4
     return l
 
 
@@ -47,8 +47,9 @@ def fives(*shape, dtype=torch.float32):
     return torch.full(shape, 5.0, dtype=dtype, device="cuda")
 
 
-def call(f, tensors, *numbers):
+def call(lib, f, tensors, *numbers, waits):
     torch.cuda.synchronize()
+    assert lib.glr_waits_set(*waits) == 0
     start = time.monotonic()
     assert f(*(t.data_ptr() for t in tensors), *numbers) == 0
     assert time.monotonic() - start < 1.5  # (a wait for something that never comes takes 2 s)
@@ -68,8 +69,8 @@ def test_scan(lib, T, bytes, ranks, tile, totals):
     for give_up in (False, True, False):
         y, h, cp = fives(T, D, dtype=BF16), fives(1, D), fives(T // 64 + 1, D)
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        limits = (tile, totals) if give_up else (WAIT, WAIT)
-        call(lib.glr_waits_scan, (x, la, y, h, cp, status), *sizes, *limits)
+        waits = (tile, totals) if give_up else (WAIT, WAIT)
+        call(lib, lib.glr_waits_scan, (x, la, y, h, cp, status), *sizes, waits=waits)
         if give_up:
             assert status.item() == kda.KDA_ERR_TIMEOUT
             assert (h == 5).all()
@@ -94,8 +95,8 @@ def test_backward(lib, T, bytes, ranks, tile, totals):
     for give_up in (False, True, False):
         dx, dla, dh0 = fives(T, D, dtype=BF16), fives(T, D, dtype=BF16), fives(1, D)
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        limits = (tile, totals) if give_up else (WAIT, WAIT)
-        call(lib.glr_waits_backward, (dy, x, la, saved, dx, dla, dh0, status), *sizes, *limits)
+        waits = (tile, totals) if give_up else (WAIT, WAIT)
+        call(lib, lib.glr_waits_backward, (dy, x, la, saved, dx, dla, dh0, status), *sizes, waits=waits)
         if give_up:
             assert status.item() == kda.KDA_ERR_TIMEOUT
             assert (dh0 == 5).all()
