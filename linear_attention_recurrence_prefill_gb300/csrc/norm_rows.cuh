@@ -51,7 +51,7 @@ __device__ __forceinline__ Row row_of(const NormArgs& a, float squares, uint32_t
   const bool finite = largest_bits < 0x7f800000u;
   o.scale = finite ? big * (1.f / 127.f) * o.r : big * o.r;
   if (finite && big < 0x1p-100f) o.scale = (float)((double)big * (double)o.r / 127.);
-  o.inv = finite && big > 0.f ? 127.f / big : 0.f;
+  o.inv = finite && big > 0.f && o.r != 0.f ? 127.f / big : 0.f;  // (r = 0: the squares vanished)
   o.always = finite && big > 0.f && big < 0x1p-100f ? 1.f : 0.f;
   return o;
 }

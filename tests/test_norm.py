@@ -259,3 +259,25 @@ def test_rows_past_two_to_the_31():
     check(y[-5:], n, 41)
     check(scale[-5:], sc, 40)
     assert torch.equal(q[-5:].cpu().double(), want) and (q[:-5:1009] == 0).all() and (scale[:-5:1009] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [40, 4096, 20000])
+def test_small_rows_without_eps(dtype, D):
+    """Squares down to a mean of 2^-100: what is lost of one below 2^-126 is 2^-24 of the mean at most."""
+    x, w, _ = make(4, D, dtype, 5, residual=False)
+    x *= 2.0 ** -50 * 1.5  # (the mean of the squares of normal numbers is one, and 2.25 here)
+    y = kda.kda_rmsnorm(x, w, eps=0.0)
+    q, scale = kda.kda_rmsnorm_i8(x, w, eps=0.0)
+    s, n, want, sc = plain(x, w, None, eps=0.0)
+    assert (s * s).mean(1).min() >= 2.0 ** -100
+    check(y, n, 42)
+    check(scale, sc, 41)
+    assert torch.equal(q.cpu().double(), want)
+    x[1:3] = 1e-30  # squares that vanish
+    x[2] *= -1
+    y = kda.kda_rmsnorm(x, w, eps=0.0)
+    q, scale = kda.kda_rmsnorm_i8(x, w, eps=0.0)
+    for t in (y, q, scale):
+        assert (t[1:3] == 0).all() and (t[[0, 3]] != 0).any()
