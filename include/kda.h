@@ -417,7 +417,7 @@ int kda_linear(const void* x, long long ldx, const void* w, long long ldw, const
  *
  * At least one of y and q is given; outputs overlap no input (but sum) and not
  * each other (KDA_ERR_ARG where two start at one address).  q is the integer nearest
- * to 127 n / max |n| as it is without rounding errors, ties to the even one.  A row of
+ * to 127 n / max |n| formed in 64 bits from x, the residual and w, ties to the even one.  A row of
  * zeros has scale 0 and q = 0; one with an infinity or a NaN in n a scale that is not
  * finite and q = 0.  Squares are summed in fp32: their sum must stay below 3.4e38
  * and, with an eps below 2^-100, their mean above that (a row whose squares all vanish counts as zeros).

@@ -8,10 +8,12 @@
 // q does not depend on r, so the squares' sum and the largest |p| are found in one
 // reduction over the row, which stays in registers between that and the outputs: each
 // array is read once and written once, and HBM is the bound.  q is the integer nearest to
-// the quotient without rounding errors: the fp32 quotient is off by at most five
-// roundings, 5 * 2^-24 = 3.0e-7 of itself, so only those that are nearer than 3.2e-7 of
-// themselves to the middle between two integers (one in 50,000 of normally distributed ones) are taken
-// again in 64 bits, with the largest product, from the stored inputs.
+// the quotient as 64 bits have it: the product of p and 127 / max |p| is off by the five roundings of
+// s, p, the largest s and p, and the division, 5 * 2^-24 of itself, and its distance to an integer, formed
+// by one fma, by 2^-26 more, which is 2^-25 of a quotient of 1/2 or above: 3.28e-7 in all.  So
+// only those that are nearer than 3.3e-7 of themselves to the middle between two integers (one in
+// 48,000 of normally distributed ones) are taken again in 64 bits, with the largest product, from the
+// stored inputs.
 //
 // 12,001 x 4096 in bf16 with the residual: 65 us (6.0 TB/s, 0.89 of the measured copy rate), 82 us with one
 // row at a time; in 8 bits 90 us (0.56), bound by the barriers and instructions of forming the integers.  One
@@ -25,7 +27,7 @@
 namespace kda {
 namespace {
 
-constexpr float kMiddle = 3.2e-7f;
+constexpr float kMiddle = 3.3e-7f;
 
 template <typename T>
 __device__ __forceinline__ double exact_product(const NormArgs& a, long long m, int d) {
@@ -67,8 +69,9 @@ template <typename T>
 __device__ __forceinline__ int quantized(const NormArgs& a, const Row& o, double largest, float p, long long m, int d) {
   if (o.inv == 0.f) return 0;
   const float v = p * o.inv, k = rintf(v);
-  return !(fabsf(v - k) + kMiddle * fabsf(v) < 0.5f - o.always) ? quantized_exactly(exact_product<T>(a, m, d), largest)
-                                                                : (int)k;
+  return !(fabsf(fmaf(p, o.inv, -k)) + kMiddle * fabsf(v) < 0.5f - o.always)
+             ? quantized_exactly(exact_product<T>(a, m, d), largest)
+             : (int)k;
 }
 
 // Rows in registers: kThreads threads per row, each kVecs vectors of eight elements, one in every

@@ -281,3 +281,21 @@ def test_small_rows_without_eps(dtype, D):
     q, scale = kda.kda_rmsnorm_i8(x, w, eps=0.0)
     for t in (y, q, scale):
         assert (t[1:3] == 0).all() and (t[[0, 3]] != 0).any()
+
+
+@gpu
+@pytest.mark.parametrize("M, D", [(40, 520), (8, 8192), (3, 20000)])
+def test_products_between_two_integers(M, D):
+    """Products of a rounded sum and a weight whose quotients lie a few steps of fp32 on either side of
+    the middle between two integers: every rounding that the fp32 quotient has counts."""
+    g = torch.Generator().manual_seed(11)
+    w = 1 + torch.rand(D, generator=g)
+    res = torch.randn(M, D, generator=g)
+    big = 1 + torch.rand(M, 1, generator=g)
+    half = torch.randint(-126, 126, (M, D), generator=g) + 0.5
+    s = half.double() / 127 * big.double() / w.double() * (1 + torch.randint(-6, 7, (M, D), generator=g) * 2.0 ** -24)
+    s[:, 0] = big[:, 0].double() / w[0].double()
+    x = (s - res.double()).float()
+    x, w, res = x.cuda(), w.cuda(), res.cuda()
+    q, _, _ = kda.kda_rmsnorm_i8(x, w, res)
+    assert torch.equal(q.cpu().double(), plain(x, w, res)[2])
