@@ -469,7 +469,8 @@ size_t kda_linear_i8_workspace_size(int M, int N, int K);
  * (A and b per channel, A >= 0; without input gate i: u = c x.)  States are fp32; a decay near
  * one is held as a - 1, so that a state that remembers thousands of tokens is as exact
  * as one that remembers ten; decays below 2^-126 act as 0.  A token that is not finite spoils its channel of its sequence
- * from there on (in the gradient: up to there); no other channel or sequence is touched.
+ * from there on; no other channel or sequence is touched.  (What that does to the gradient stands at
+ * kda_glr_scan_backward.)
  */
 enum { /* decay_from */
   KDA_GLR_LOG = 0,     /* log_alpha holds log decays, above 0 taken as 0 */
@@ -547,6 +548,13 @@ int kda_glr_step(const void* x, const void* log_alpha, float* h, void* y, int N,
  *   dh0           [N][D] fp32 out, or NULL
  *   ddecay_scale, ddecay_bias  [D] fp32 out, or NULL (not with KDA_GLR_LOG): summed over
  *                 all tokens, in an order of its own that does not change
+ *
+ * What is not finite spoils, in its channel of its sequence, ddecay_scale and ddecay_bias and
+ *   dy at token t            dx, dinput_gate, dlog_alpha up to t, and dh0 (dh_T: all of them)
+ *   x at token t             dinput_gate at t, dlog_alpha from t on (the states); nothing of dx
+ *   input_gate at token t    dx and dinput_gate at t, dlog_alpha from t on
+ *   log_alpha at token t     dx and dinput_gate up to t, dlog_alpha everywhere, and dh0
+ * (at t itself some of these stay finite without an input_scale).
  *
  * Outputs and the workspace overlap no input and not each other (KDA_ERR_ARG where two start at
  * one address).  Rows of outputs behind the last sequence are left as they are.  Where the decay is 1

@@ -688,3 +688,39 @@ def test_an_output_at_an_input_is_refused(out, at):
     assert _scan(opt, **kw) == kda.KDA_ERR_ARG
     if at != "cu" and out != "checkpoints":
         assert _step(opt, **kw) == kda.KDA_ERR_ARG
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [15, 700, 3000])
+def test_what_nan_spoils_of_the_gradient(dtype, T):
+    """The table in the header, for a NaN in each input; everything else is the same to the bit."""
+    D, at, ch = 72, T // 2, 5
+    x, la, form = make(2 * T, D, dtype, "sigmoid", "normalized", True)
+    dy, dh = states(2 * T, D).to(dtype), states(2, D, 3)
+
+    def run(x, la, gate, dy, dh):
+        f = form | dict(input_gate=gate)
+        *_, saved = kda.kda_glr_scan(x, la, None, None, 2, checkpoints=True, **f)
+        return kda.kda_glr_scan_backward(dy, dh, x, la, saved, None, 2, **f)
+
+    inputs = dict(x=x, la=la, gate=form["input_gate"], dy=dy, dh=dh)
+    clean = run(*inputs.values())
+    upto, behind, here, every, none = slice(0, at + 1), slice(at, T), slice(at, at + 1), slice(0, T), slice(0, 0)
+    #               dx     dla     dgate  dh0
+    spoiled = dict(x=(none, behind, here, False), la=(upto, every, upto, True), gate=(here, behind, here, False),
+                   dy=(upto, upto, upto, True), dh=(every, every, every, True))
+    for name, (*rows, first) in spoiled.items():
+        bad = {k: v.clone() for k, v in inputs.items()}
+        bad[name][0 if name == "dh" else at, ch] = float("nan")
+        got = run(*bad.values())
+        for g, c, r in zip(got[:3], clean[:3], rows):
+            nan = torch.zeros(2 * T, D, dtype=torch.bool, device="cuda")
+            nan[r, ch] = True
+            assert torch.equal(g.isnan(), nan) and torch.equal(g[~nan], c[~nan])
+        nan = torch.zeros(2, D, dtype=torch.bool, device="cuda")
+        nan[0, ch] = first
+        assert torch.equal(got[3].isnan(), nan) and torch.equal(got[3][~nan], clean[3][~nan])
+        for g, c in zip(got[4:], clean[4:]):
+            nan = torch.arange(D, device="cuda") == ch
+            assert torch.equal(g.isnan(), nan) and torch.equal(g[~nan], c[~nan])
