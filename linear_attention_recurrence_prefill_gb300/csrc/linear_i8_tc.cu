@@ -3,7 +3,8 @@
 //
 // This GPU multiplies 8-bit integers far below its rate for 16-bit floats, and every such
 // integer is an fp16 number: the products are taken in fp16 with fp32 sums, which are exact below
-// 2^24.  So what 8 bits save is memory, and the integers are widened on their way:
+// 2^24 and lose up to 2^-23 of themselves in each of K / 16 additions beyond (the header gives the
+// bound).  So what 8 bits save is memory, and the integers are widened on their way:
 //  * few tiles (few tokens, or a small product; bound by reading w): linear_i8_kernel.  w's rows go
 //    from shared memory through registers, where they are widened, into TMEM, from which the MMAs take
 //    them: a lane of TMEM is a row, so a thread widens 64 neighbouring integers of its row and

@@ -815,7 +815,8 @@ def kda_linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, y=None, *, a
     x [M, K], w [N, K] int8, rows contiguous, any distance apart; x_scale [M], w_scale
     [N] fp32; bias [N], residual [M, N] of ``dtype`` (None: y's, the residual's or the
     bias's, else bfloat16) or None.  ``act``: a key of ``ACTS``.  y [M, N] may be the residual
-    itself.  ``stream`` as in kda_gdr_prefill."""
+    itself.  The integer sum is exact up to K = 1024, and up to 2^24 for any K; the header says what
+    it loses beyond.  ``stream`` as in kda_gdr_prefill."""
     host = _host()
     dev = _one_device(host, x, x_scale, w, w_scale, bias, residual, y, workspace)
     if x.dim() != 2 or w.dim() != 2:

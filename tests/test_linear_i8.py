@@ -319,3 +319,24 @@ def test_widened_first(M, K, N):
     check(y, *plain(*a))
     with pytest.raises(kda.KdaError):
         kda.kda_linear_i8(*a, workspace=ws[:need // 8])
+
+
+@gpu
+@pytest.mark.parametrize("K", [1040, 4096, 12288, 40000])
+@pytest.mark.parametrize("M, N", [(1, 300), (8, 300), (9, 300), (64, 300), (200, 300), (1500, 2600)])
+def test_bound_of_sums_beyond_two_to_the_24(M, N, K):
+    """Integers of one sign: up to eight rows the sum itself, rounded once; beyond, low by at most
+    K / 16 additions' 2^-23 of it (and a rounding of each of up to eight parts of K, and the last one).
+    Integers of either sign: the sum, which stays below 2^24 at these K."""
+    g = torch.Generator().manual_seed(K)
+    one = torch.ones(max(M, N), device="cuda")
+    for low in (100, -128):
+        x, w = (torch.randint(low, 128, (rows, K), generator=g).to(torch.int8).cuda() for rows in (M, N))
+        y = kda.kda_linear_i8(x, one[:M], w, one[:N], dtype=F32).double()
+        z = x.double() @ w.double().T  # (exact: below 2^53)
+        if M <= 8:
+            assert torch.equal(y, z.float().double())
+        elif low < 0:
+            assert z.abs().max() < 2 ** 24 and torch.equal(y, z)
+        else:
+            assert ((y - z) <= 9 * E * z).all() and ((z - y) <= (K * 2.0 ** -27 + 9 * E) * z).all()
