@@ -13,6 +13,13 @@ struct LinearI8Args {
   const float* w_scale;
 };
 
+// A sum with its scales and the bias, in two roundings.  Every kernel has it from here, so that a token's
+// row is the same to the bit whatever kernel the number of rows chooses (the compiler fused the
+// bias's addition in some of them and not in others).
+__device__ __forceinline__ float scaled(float sum, float x_scale, float w_scale, float bias) {
+  return __fmaf_rn(__fmul_rn(sum, x_scale), w_scale, bias);
+}
+
 // K = 0 only: y = act(bias) + residual.
 cudaError_t launch_linear_i8_none(const LinearI8Args& a, int dtype, cudaStream_t s);
 // Up to eight rows of x; x and w 16-byte aligned, rows a multiple of 16 bytes apart, K > 0.

@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kWarps * 32) linear_i8_few_kernel(LinearI8Args
     if (n < l.N) {
       int z = 0;
       for (int p = 0; p < parts; ++p) z += sums[warp + p][lane];
-      finish<T>(l, (float)z * a.x_scale[m] * a.w_scale[n], l.bias ? to_f32(static_cast<const T*>(l.bias)[n]) : 0.f, m,
-                (int)n);
+      const float bias = l.bias ? to_f32(static_cast<const T*>(l.bias)[n]) : 0.f;
+      finish<T>(l, scaled((float)z, a.x_scale[m], a.w_scale[n], bias), 0.f, m, (int)n);
     }
   }
 }

@@ -323,11 +323,11 @@ __global__ void __launch_bounds__(Fill<BN, kTma>::kThreads, 2) linear_i8_kernel(
     ws.w = n + 3 < l.N ? t.a.w_scale[n + 3] : 0.f;
     join(ranks, smem_u32(tiles) + lane * 16, rank, warp, cols, [&](float4 z, int c) {
       const float xs = t.a.x_scale[(long long)m0 + c];
-      z.x = z.x * xs * ws.x;
-      z.y = z.y * xs * ws.y;
-      z.z = z.z * xs * ws.z;
-      z.w = z.w * xs * ws.w;
-      finish4<T>(l, wide, z, b, (long long)m0 + c, n);
+      z.x = scaled(z.x, xs, ws.x, b.x);
+      z.y = scaled(z.y, xs, ws.y, b.y);
+      z.z = scaled(z.z, xs, ws.z, b.z);
+      z.w = scaled(z.w, xs, ws.w, b.w);
+      finish4<T>(l, wide, z, make_float4(0.f, 0.f, 0.f, 0.f), (long long)m0 + c, n);
     });
   }
   fence_before_sync();

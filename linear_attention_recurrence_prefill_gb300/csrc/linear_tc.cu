@@ -56,7 +56,7 @@ struct Tc {
 };
 
 // The epilogue of output channel n for the 32 tokens from m on, of which `cols` exist: the
-// residual, fetched ahead of the sums, then the rest.  T: the type of residual and y.
+// residual, fetched ahead of the sums, then the rest behind the bias.  T: the type of residual and y.
 template <typename T>
 __device__ __forceinline__ void load_residual(const LinearArgs& a, T (&add)[32], long long m, int n, int cols) {
   const T* res = static_cast<const T*>(a.residual) + m * a.ldr + n;
@@ -65,11 +65,9 @@ __device__ __forceinline__ void load_residual(const LinearArgs& a, T (&add)[32],
 }
 
 template <typename T>
-__device__ __forceinline__ void finish32(const LinearArgs& a, float (&z)[32], float bias, const T (&add)[32],
-                                         long long m, int n, int cols) {
+__device__ __forceinline__ void finish32(const LinearArgs& a, float (&z)[32], const T (&add)[32], long long m, int n,
+                                         int cols) {
   constexpr bool kFast = sizeof(T) == 2;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) z[j] += bias;
   // the activation chosen once for all
   auto all = [&](auto f) {
 #pragma unroll
@@ -245,16 +243,16 @@ __global__ void __launch_bounds__(kPairThreads) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 xs = *reinterpret_cast<const float4*>(&scales[warp][j]);
-            z[j] = __uint_as_float(r[j]) * xs.x * scale;
-            z[j + 1] = __uint_as_float(r[j + 1]) * xs.y * scale;
-            z[j + 2] = __uint_as_float(r[j + 2]) * xs.z * scale;
-            z[j + 3] = __uint_as_float(r[j + 3]) * xs.w * scale;
+            z[j] = scaled(__uint_as_float(r[j]), xs.x, scale, b);
+            z[j + 1] = scaled(__uint_as_float(r[j + 1]), xs.y, scale, b);
+            z[j + 2] = scaled(__uint_as_float(r[j + 2]), xs.z, scale, b);
+            z[j + 3] = scaled(__uint_as_float(r[j + 3]), xs.w, scale, b);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]);
+          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(r[j]) + b;
         }
-        if (in) finish32(t.a, z, b, add, m0 + c, n, cols - c);
+        if (in) finish32(t.a, z, add, m0 + c, n, cols - c);
 #pragma unroll
         for (int j = 0; j < 32; ++j) add[j] = next[j];
       }

@@ -340,3 +340,13 @@ def test_bound_of_sums_beyond_two_to_the_24(M, N, K):
             assert z.abs().max() < 2 ** 24 and torch.equal(y, z)
         else:
             assert ((y - z) <= 9 * E * z).all() and ((z - y) <= (K * 2.0 ** -27 + 9 * E) * z).all()
+
+
+@gpu
+def test_a_token_alone_and_in_a_batch():
+    """Up to K = 1024 a token's row does not depend on how many others are in the batch, or on the kernel."""
+    x, sx, w, sw, b, r = make(1500, 1024, 2600, F32, seed=12)
+    x[0] = w[0] = -128
+    whole = kda.kda_linear_i8(x, sx, w, sw, b, r)
+    for M in (1, 8, 9, 40, 200):
+        assert torch.equal(kda.kda_linear_i8(x[:M], sx[:M], w, sw, b, r[:M]), whole[:M])
