@@ -453,8 +453,10 @@ int kda_quantize_i8(const void* x, long long ldx, int8_t* q, long long ldq, floa
  *
  * (sum x_scale) w_scale, bias, activation and residual are in fp32, rounded once to
  * dtype.  M, N and K are from 0 to 2^31 - 257 (K = 0: y = act(bias) + residual).  The
- * workspace (kda_linear_i8_workspace_size bytes, none where that is 0; 16-byte aligned)
- * holds nothing between calls, but calls that can overlap on the GPU need one each.
+ * workspace (kda_linear_i8_workspace_size bytes, 16-byte aligned) is for products whose arrays are
+ * widened first: KDA_ERR_WORKSPACE where one is missing or too small.  With x and w at 16 bytes and
+ * rows a multiple of 16 bytes apart those have 400 rows and 400 channels at least.  It holds nothing
+ * between calls, but calls that can overlap on the GPU need one each.
  */
 int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w,
                   long long ldw, const float* w_scale, const void* bias, const void* residual,

@@ -242,26 +242,26 @@ int kda_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const in
   if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return KDA_ERR_ALIGN;
   for (const void* p : {bias, residual, (const void*)y})
     if (!aligned(p, elem(dtype))) return KDA_ERR_ALIGN;
-  const size_t need = kda_linear_i8_workspace_size(M, N, K);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;
-  }
-  // in place only where every element is read and written by the same thread
-  if (residual == y && ldr != ldy) return KDA_ERR_ARG;
-  void* const ws = need > 0 ? workspace : nullptr;
-  if (same(y, {bias, x_scale, w_scale, ws}) || (K > 0 && same(y, {x, w}))) return KDA_ERR_ARG;
-  if (same(ws, {x, w, x_scale, w_scale, bias, residual})) return KDA_ERR_ARG;
   LinearI8Args a;
   a.l.x = x; a.l.w = w; a.l.bias = bias; a.l.residual = residual; a.l.y = y;
   a.l.ldx = ldx; a.l.ldw = ldw; a.l.ldr = ldr; a.l.ldy = ldy;
   a.l.M = M; a.l.N = N; a.l.K = K; a.l.act = act;
   a.x_scale = x_scale; a.w_scale = w_scale;
+  const bool few = linear_i8_few_takes(a), needed = K > 0 && !few && linear_i8_tc_needs_workspace(a.l);
+  if (needed) {
+    if (!workspace || workspace_bytes < linear_i8_workspace_bytes(M, N, K)) return KDA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;
+  }
+  // in place only where every element is read and written by the same thread
+  if (residual == y && ldr != ldy) return KDA_ERR_ARG;
+  void* const ws = needed ? workspace : nullptr;
+  if (same(y, {bias, x_scale, w_scale, ws}) || (K > 0 && same(y, {x, w}))) return KDA_ERR_ARG;
+  if (same(ws, {x, w, x_scale, w_scale, bias, residual})) return KDA_ERR_ARG;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (K == 0) {
     e = launch_linear_i8_none(a, dtype, s);
-  } else if (linear_i8_few_takes(a)) {
+  } else if (few) {
     e = launch_linear_i8_few(a, dtype, sm_count(), s);
   } else {
     int* status = status_word();

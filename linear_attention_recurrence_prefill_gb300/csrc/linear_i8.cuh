@@ -27,7 +27,8 @@ bool linear_i8_few_takes(const LinearI8Args& a);
 cudaError_t launch_linear_i8_few(const LinearI8Args& a, int dtype, int sms, cudaStream_t s);
 // Any alignment and number of rows, K > 0.
 bool linear_i8_tc_takes(int M, int N);
-size_t linear_i8_workspace_bytes(int M, int N, int K);
+size_t linear_i8_workspace_bytes(int M, int N, int K);  // whatever the alignment
+bool linear_i8_tc_needs_workspace(const LinearArgs& l);
 cudaError_t launch_linear_i8_tc(const LinearI8Args& a, int dtype, void* workspace, int sms, int* status,
                                 cudaStream_t s);
 // linear_tc.cu: l.x and l.w are fp16 arrays that hold the integers, rows 16-byte aligned.

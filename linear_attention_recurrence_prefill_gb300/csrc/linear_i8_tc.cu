@@ -447,23 +447,31 @@ cudaError_t launch(const LinearI8Args& a, int dtype, int* status, int split, cud
                           : launch_of<BN, kTma, __nv_bfloat16>(a, status, split, s);
 }
 
-// Whether both arrays are widened first.  That costs by M + N and pays by M N: with rows and bases at
-// 16 bytes from M N / (M + N) = 544 on (4096 channels of 4096 columns, 512 and 640 tokens: 37.5 and 40.3 us
-// this way, 29.3 and 46.6 otherwise; 12288 channels, 256 and 512 tokens: 64 and 81, 48 and 85), else from
-// 128 on (4096 channels of 4095 columns, 128 and 160 tokens: 36.9 and 36.9, 29.9 and 49.3), but where the
-// other way has CTAs to spare for four parts of K (76 tiles of 128 x 64 or fewer), which then is near or
-// ahead with no workspace and a launch less (1021 channels of 4095, 256 and 400 tokens: 30.1 and 30.1,
-// 20.6 and 32.5; 1499 channels of 1000, 333 and 400 tokens, 72 and 84 tiles: 15.1 and 15.1, 16.4 and
-// 23.0).  What the first rule takes the second takes too: the workspace's size goes by the second.
+// Whether both arrays are widened first.  That costs by M + N and pays by M N, and the other way goes in
+// waves of 304 CTAs, two to each of 152 SMs (constants, since the workspace's size must not depend on the
+// device).  All with inputs that were not in L2, us, widened first and not:
+//  * Rows and bases at 16 bytes: from M N / (M + N) = 544 on (columns 4096, channels 4096: 512 and 640 rows
+//    36.4 and 40.1, 33.5 and 59.2; channels 8192: 54.8 and 70.7, 59.2 and 103), from 400 on where the tiles of
+//    128 x 128 take a second wave (12288 channels, 384 and 512 rows: 76.6 and 82.5, 60.2 and 117; 24576:
+//    134 and 140, 121 and 179).  Few channels of many columns would stay longer (2048 of 12288,
+//    1024 rows: 91 and 68), 1024 columns go sooner (4096 channels, 320 rows: 15.5 and 20.6).
+//  * Else, where a thread reads its own integers and tiles have 64 tokens: from 65 rows on with more
+//    tiles than give four CTAs each, 76 (4095 columns, 12288 channels, 96 and 128 rows: 58 and 59, 122 and 122;
+//    4096 channels, 128 and 160 rows, 64 and 96 tiles: 36.8 and 37.0, 36.9 and 65.7; 1499 channels of 1000, 333 and 400
+//    rows, 72 and 84 tiles: 15.3 and 14.8, 18.9 and 28.8; 100 channels of 1000, 20,000 rows: 45 and 90).  Up to 64 rows the widened weights would
+//    pass through memory for at most a quarter of the time (12288 channels, 64 rows: 55.6 and 70.9).
+// What the first rule takes the second takes too: the workspace's size goes by the second.
 bool widened(long long M, long long N, bool tma) {
-  if (tma) return M * N >= 544 * (M + N);
-  return M * N >= 128 * (M + N) && (N + 127) / 128 * ((M + 63) / 64) > 76;
+  if (!tma) return M > 64 && (N + 127) / 128 * ((M + 63) / 64) > 76;
+  return M * N >= 544 * (M + N) || (M * N >= 400 * (M + N) && (N + 127) / 128 * ((M + 127) / 128) > 304);
 }
 long long padded(int K) { return (K + 15LL) / 16 * 16; }
 
 }  // namespace
 
 bool linear_i8_tc_takes(int M, int N) { return (N + 127LL) / 128 * ((M + 15LL) / 16) <= 0x7fffffffLL; }
+
+bool linear_i8_tc_needs_workspace(const LinearArgs& l) { return widened(l.M, l.N, tma_takes(l)); }
 
 size_t linear_i8_workspace_bytes(int M, int N, int K) {
   return K > 0 && widened(M, N, false) ? ((size_t)M + N) * padded(K) * 2 : 0;

@@ -847,10 +847,13 @@ def kda_linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, y=None, *, a
         ldy = _rows(y, "y", M, N)
         if y.dtype != dtype:
             raise TypeError("bias, residual and y of one dtype")
-    at, size, workspace = _workspace(host, workspace, host.linear_i8_size(M, N, K), x.device)
-    rc = host.linear_i8(x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
-                        w_scale.data_ptr(), b, r, ldr, y.data_ptr(), ldy, M, N, K, ACTS[act], code,
-                        at, size, host.current_stream(dev))
+    args = (x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), b, r, ldr,
+            y.data_ptr(), ldy, M, N, K, ACTS[act], code)
+    at, size, _ = _workspace(host, workspace, 0 if workspace is None else 1, x.device)
+    rc = host.linear_i8(*args, at, size, host.current_stream(dev))
+    if rc == KDA_ERR_WORKSPACE and workspace is None:  # only some products need one
+        at, size, workspace = _workspace(host, None, host.linear_i8_size(M, N, K), x.device)
+        rc = host.linear_i8(*args, at, size, host.current_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_linear_i8")
     return y

@@ -350,3 +350,34 @@ def test_a_token_alone_and_in_a_batch():
     whole = kda.kda_linear_i8(x, sx, w, sw, b, r)
     for M in (1, 8, 9, 40, 200):
         assert torch.equal(kda.kda_linear_i8(x[:M], sx[:M], w, sw, b, r[:M]), whole[:M])
+
+
+@no_gpu
+@pytest.mark.parametrize("M, N, K, ldx, need", [
+    (8, 12288, 4096, 0, False), (64, 12288, 4095, 0, False), (65, 12288, 4095, 0, True), (65, 12288, 4096, 0, False),
+    (65, 12288, 4096, 4100, True), (400, 2 ** 20, 4096, 0, False), (384, 12288, 4096, 0, False), (512, 12288, 4096, 0, True),
+    (512, 4096, 4096, 0, False), (640, 4096, 4096, 0, True), (128, 4096, 1000, 0, False), (129, 4096, 1000, 0, True),
+    (20000, 100, 1000, 0, True), (20000, 100, 1024, 0, False), (5, 12288, 4095, 0, False), (640, 4096, 0, 0, False)])
+def test_which_products_need_a_workspace(M, N, K, ldx, need):
+    """Arrays at 16 bytes go by another rule than others, and bring a workspace only where it is used."""
+    kw = dict(M=M, N=N, K=K, ldx=ldx)
+    size = kda.load().kda_linear_i8_workspace_size(M, N, K)
+    assert (_linear(**kw, ws=None, size=0) == kda.KDA_ERR_WORKSPACE) == need
+    assert _linear(**kw, ws=6 * A, size=size) != kda.KDA_ERR_WORKSPACE
+    if need:
+        assert size == (M + N) * (-(-K // 16) * 16) * 2
+        assert _linear(**kw, ws=6 * A, size=size - 1) == kda.KDA_ERR_WORKSPACE
+        assert _linear(**kw, ws=6 * A + 8, size=size) == kda.KDA_ERR_ALIGN
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M, K, N", [(65, 100, 9800), (96, 333, 12288), (5000, 77, 65), (512, 128, 12288), (384, 128, 12288),
+                                     (70, 96, 10000)])
+def test_either_side_of_the_rule(dtype, M, K, N):
+    """Few rows of many channels, many rows of few; a second wave of tiles; with and without a workspace."""
+    a = make(M, K, N, dtype, seed=13)
+    want = plain(*a, "silu")
+    check(kda.kda_linear_i8(*a, act="silu"), *want)
+    ws = torch.full((kda.load().kda_linear_i8_workspace_size(M, N, K),), 255, dtype=torch.uint8, device="cuda")
+    check(kda.kda_linear_i8(*a, act="silu", workspace=ws if len(ws) else None), *want)
