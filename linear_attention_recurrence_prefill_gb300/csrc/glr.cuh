@@ -13,7 +13,7 @@
 // were 2.7e-5 of their size off with a itself.)
 //
 // A thread has two neighbouring channels, and two numbers per instruction wherever
-// there is one (packed.cuh): an element takes 44 instructions forward and 102 backward (with
+// there is one (packed.cuh): an element takes 44 instructions forward and 104 backward (with
 // the input gate; 110 and 251 one number at a time), while HBM brings its 8 and 14 bytes in the
 // time of some 40 and 75 at the best rate.
 #pragma once

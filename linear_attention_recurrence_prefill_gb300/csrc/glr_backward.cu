@@ -10,8 +10,9 @@
 // The states h_{t-1} are not read back from y, which is rounded, but scanned again inside each
 // tile of 64 tokens from the states that the forward pass saved before each.
 //
-// 8192 x 4096 in bf16 with an input gate: 185 us of 470 MB, 0.37 of the measured copy rate; the forward
-// pass before it 86 us.  Bound as glr_scan_kernel is, with 102 instructions an element.
+// 8192 x 4096 in bf16 with an input gate: 186 us of 470 MB, 0.37 of the measured copy rate; the forward
+// pass before it 83 us.  Both passes over 16,384 x 4096 in fp32: 1325 us (0.33).  Bound as glr_scan_kernel is,
+// with 104 instructions an element.
 #include "glr_maps.cuh"
 
 namespace kda {

@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(kFewThreads) glr_few_kernel(GlrArgs a) {
 // the scan once more from there.  All joins are taken in the order of the tokens, so that results
 // repeat to the bit.  The next tile's arrays are copied to shared memory meanwhile.
 //
-// 32,768 x 4096 in bf16 (softplus): 297 us, 0.40 of the time that its bytes take; 12,000 tokens in nine
-// prompts with an input gate 105 us (0.55).  Bound by the latency of a round, 2.3 us: two CTAs of 128
+// 32,768 x 4096 in bf16 (softplus): 290 us, 0.41 of the rate of its bytes; 12,000 tokens in nine
+// prompts with an input gate 104 us (0.56); 16,384 x 4096 in fp32 338 us (0.35), with a gate 433 (0.37).
+// Bound by the latency of a round, 2.3 us: two CTAs of 128
 // registers a thread per SM, 3.3 warps per scheduler, which issue in half of the cycles, and 24 SMs
 // without a CTA where 64 clusters of four fill 128.  Three CTAs of 80 registers took 419 us (they
 // load their constants again and again), one per SM 405; the clusters' barrier instead of counted

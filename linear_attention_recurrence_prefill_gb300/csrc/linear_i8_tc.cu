@@ -18,6 +18,11 @@
 //    once more for every 256 tokens, which the tensor cores' own reads leave no room for.
 //    4096 x 4096 -> 12288 with bias, GELU and residual: 282 to 297 us, of which the widening 38 (201 MB, a part of
 //    which stays in L2) and the product 250 (1.65 PFLOP/s, as kda_linear's).
+// So 8 bits are faster than kda_linear in bf16 up to some 16 to 64 rows and save memory beyond (with the
+// residual, 8 bits and bf16, us: 4096 -> 12288, 1, 16, 64, 512, 4096 rows 10.6 and 18.2, 18.9 and 22.0, 24.9 and 22.7,
+// 83 and 48, 275 and 248; 12288 -> 4096 12.1 and 21.4, 16.3 and 19.1, 19.4 and 21.3, 69 and 59, 300 and 237).
+// linear_i8_kernel has 72 or 80 registers a thread, two CTAs to an SM, and spills 20 to 88 bytes of them, widen_kernel
+// 16, the pairs' kernel 12.
 #include "linear_i8.cuh"
 #include "linear_join.cuh"
 #include "tensor_map.cuh"

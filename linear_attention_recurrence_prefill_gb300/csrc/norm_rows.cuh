@@ -16,9 +16,14 @@
 // stored inputs.
 //
 // 12,001 x 4096 in bf16 with the residual: 65 us (6.0 TB/s, 0.89 of the measured copy rate), 82 us with one
-// row at a time; in 8 bits 90 us (0.56), bound by the barriers and instructions of forming the integers.  One
-// row of 4096: 3.0 us.  Rows that are no multiple of 8 elements, or not at 16 bytes, go element by
-// element: 3000 x 8191 89 us (0.32).
+// row at a time; in fp32 129 us (0.90).  In 8 bits, bound by the barriers and instructions of forming the
+// integers, 90 us (0.56) with weights that differ, 110 us (0.86) in fp32.  Where bf16 rows have no weights,
+// or equal ones, nearly every row has elements of half its largest, whose quotient is 63.5 exactly, and takes some
+// of its quotients again: 200 to 215 us (0.24), without a residual 225, kda_quantize_i8 195 (0.11; in fp32,
+// where such elements are rare, 68, 0.53).  One row of 4096: 2.8 us.  Rows that are no multiple of 8
+// elements, or not at 16 bytes, go element by element: 3000 x 8191 89 us (0.32).  The 8-bit forms for 8,193 to 16,384
+// elements spill (up to 704 bytes a thread in bf16, 868 in fp32, whose 1024 threads have 64 registers): 4000 x 12288
+// without differing weights 335 and 241 us.
 #pragma once
 
 #include "norm.cuh"
@@ -370,7 +375,8 @@ cudaError_t launch_t(const NormArgs& a, int sms, cudaStream_t s) {
                     on16(a.sum, a.lds, sizeof(T), 16) && on16(a.y, a.ldy, sizeof(T), 16) && on16(a.w, 0, 4, 16) &&
                     on16(a.q, a.ldq, 1, 8);
   // Eight elements per thread where there are few rows, for the latency, sixteen where rows fill the
-  // GPU; a warp at least.
+  // GPU; a warp at least.  (Eight for one row of 512 to 2048 elements would take 2.1 us and not 2.75, for 64 rows
+  // the same as sixteen; for one of 8192 3.5 and not 2.8.)
   if (a.D <= 256) return launch_of<T, 32, 1>(a, wide, sms, s);
   if (a.D <= 512) return launch_of<T, 32, 2>(a, wide, sms, s);
   if (a.D <= 1024) return launch_of<T, 64, 2>(a, wide, sms, s);

@@ -1029,7 +1029,8 @@ def kda_glr_scan(x, log_alpha, h0=None, cu_seqlens=None, N: int | None = None, y
     (c = 1), "complement" (1 - a) or "normalized" (sqrt(1 - a^2)).  h0 [N, D] fp32 or None
     (zeros); cu_seqlens, N, max_seqlen, slots (h0 and h_T are pools [n_slots, D] then) and
     stream as in kda_gdr_prefill.  Returns (y, h_T); with ``checkpoints`` (True, or a tensor
-    [T // 64 + N, D] fp32) (y, h_T, checkpoints), which kda_glr_scan_backward takes."""
+    [T // 64 + N, D] fp32) (y, h_T, checkpoints), which kda_glr_scan_backward takes.  Like every
+    call here it records nothing for autograd: the gradient is that call's, made by the caller."""
     host = _host()
     if checkpoints is False:
         checkpoints = None
